@@ -15,6 +15,7 @@ Names match the C ABI in include/lrc.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -26,7 +27,8 @@ __all__ = [
     "LRC_SCORE_FISHER", "LRC_SCORE_KFAC", "LRC_RANKSCORE_UNIRANK", "LRC_RANKSCORE_SWIFT", "LrcError", "lib",
     "library_path", "lrc_accumulate_cov", "lrc_whiten_decompose", "lrc_score_components", "lrc_allocate_ranks",
     "lrc_rank_scores", "lrc_rotate_quantize", "lrc_quantize_rows", "lrc_lowrank_ffn", "lrc_ffn_select_channels",
-    "lrc_hybrid_ffn",
+    "lrc_hybrid_ffn", "LRC_CKPT_BLOCK", "lrc_pack_activations", "lrc_unpack_activations", "lrc_layer_norm",
+    "lrc_layer_norm_backward", "lrc_linear", "lrc_linear_backward",
     "lrc_status_string", "lrc_profile_start", "lrc_profile_stop", "lrc_profile_kernels",
 ]
 
@@ -37,6 +39,8 @@ LRC_SCORE_FISHER = 0x1
 LRC_SCORE_KFAC = 0x2
 LRC_RANKSCORE_UNIRANK = 0x1
 LRC_RANKSCORE_SWIFT = 0x2
+LRC_CKPT_BLOCK = 64                     # channels that share one checkpoint exponent
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "liblrc.so")
@@ -72,6 +76,19 @@ _SIGS = {
     "lrc_hybrid_ffn": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
                               _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "lrc_hybrid_ffn_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "lrc_pack_activations": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "lrc_unpack_activations": (_i32, [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "lrc_layer_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _vp, _vp,
+                              _vp, _vp]),
+    "lrc_layer_norm_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                       _vp, _vp, _vp, _sz, _vp]),
+    "lrc_layer_norm_backward_workspace": (_sz, [_i64, _i64]),
+    "lrc_linear": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64,
+                          _vp, _vp, _vp, _vp, _sz, _vp]),
+    "lrc_linear_workspace": (_sz, [_i32, _i64, _i64, _i64]),
+    "lrc_linear_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64,
+                                   _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _sz, _vp]),
+    "lrc_linear_backward_workspace": (_sz, [_i32, _i64, _i64, _i64]),
     "lrc_status_string": (ctypes.c_char_p, [_i32]),
     "lrc_last_hip_error": (_i32, []),
     "lrc_profile_start": (_i32, []),
@@ -514,6 +531,218 @@ def lrc_lowrank_ffn(x: torch.Tensor, gate, up, down):
                                _ptr(dn[2]), _ptr(dn[3]), rd, _ptr(y), _ptr(ws), ws.numel(), _stream()),
            "lrc_lowrank_ffn")
     return y
+
+
+def _on(device):
+    """Context in which `device` is current (a launch needs its stream's device current)."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream_of(device):
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _rows(t, name, shape, dtype=None, device=None):
+    """Check a 2-D GPU tensor and return (tensor, leading dim); rows that are not contiguous
+    or overlap are copied."""
+    _tensor(t, name, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype, shape, device)
+    n, d = t.shape
+    if d > 0 and n > 0 and ((d > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < d)):
+        t = t.contiguous()
+    return t, (max(t.stride(0), d, 1) if n > 1 else max(d, 1))
+
+
+def _vector(t, name, n, device):
+    return None if t is None else _tensor(t, name, torch.float32, (n,), device).contiguous()
+
+
+def _checkpoint(ck, name, n, d, device):
+    """Check a (codes, exps) pair of n rows of d channels."""
+    if len(ck) != 2:
+        raise ValueError(f"{name} must be a tensor or a (codes, exps) pair")
+    codes = _tensor(ck[0], f"{name} codes", torch.int8, (n, d), device).contiguous()
+    exps = _tensor(ck[1], f"{name} exps", torch.int8, (n, -(-d // LRC_CKPT_BLOCK)), device).contiguous()
+    return codes, exps
+
+
+def _kept(t, name, n, d, dtype, device):
+    """(tensor, leading dim, codes, exps) of an activation given in full or as a checkpoint."""
+    if t is None:
+        return None, max(d, 1), None, None
+    if isinstance(t, (tuple, list)):
+        codes, exps = _checkpoint(t, name, n, d, device)
+        return None, max(d, 1), codes, exps
+    t, ld = _rows(t, name, (n, d), dtype, device)
+    return t, ld, None, None
+
+
+def _new_checkpoint(n, d, device):
+    return (torch.empty(n, d, dtype=torch.int8, device=device),
+            torch.empty(n, -(-d // LRC_CKPT_BLOCK), dtype=torch.int8, device=device))
+
+
+def lrc_pack_activations(x: torch.Tensor, info=None):
+    """8-bit checkpoint of token rows.  x: (n_tokens, d) bf16 or fp32.
+
+    Returns (codes int8 (n_tokens, d), exps int8 (n_tokens, ceil(d / 64)), info int32 (1,)):
+    the values held are codes * 2^exps per 64 channels.  info (sticky, optional) receives
+    LRC_ENONFINITE when an entry is NaN or Inf."""
+    x, ldx = _rows(x, "x", (None, None))
+    dt, dev = _dtype_code(x), x.device
+    n, d = x.shape
+    codes, exps = _new_checkpoint(n, d, dev)
+    info = _info(info, dev)
+    with _on(dev):
+        _check(lib.lrc_pack_activations(_ptr(x), dt, n, d, ldx, _ptr(codes), _ptr(exps), _ptr(info),
+                                        _stream_of(dev)), "lrc_pack_activations")
+    return codes, exps, info
+
+
+def lrc_unpack_activations(codes: torch.Tensor, exps: torch.Tensor, dtype=torch.bfloat16):
+    """The values an 8-bit checkpoint holds, as bf16 or fp32 (both exact)."""
+    _dev(codes, "codes")
+    if codes.dim() != 2:
+        raise ValueError("codes must be (n_tokens, d)")
+    n, d = codes.shape
+    dev = codes.device
+    codes, exps = _checkpoint((codes, exps), "checkpoint", n, d, dev)
+    x = torch.empty(n, d, dtype=dtype, device=dev)
+    with _on(dev):
+        _check(lib.lrc_unpack_activations(_ptr(codes), _ptr(exps), n, d, _ptr(x), _dtype_code(x), max(d, 1),
+                                          _stream_of(dev)), "lrc_unpack_activations")
+    return x
+
+
+def lrc_layer_norm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, checkpoint: bool = False, info=None):
+    """Layer norm of token rows.  x: (n_tokens, d) bf16 or fp32; gamma, beta: (d,) fp32 or None.
+
+    Returns (y, mean, rstd, kept, info): y like x, mean and rstd fp32 (n_tokens,), kept the
+    (codes, exps) checkpoint of x when `checkpoint` (else None, and info None unless given)."""
+    x, ldx = _rows(x, "x", (None, None))
+    dt, dev = _dtype_code(x), x.device
+    n, d = x.shape
+    gamma, beta = _vector(gamma, "gamma", d, dev), _vector(beta, "beta", d, dev)
+    y = torch.empty(n, d, dtype=x.dtype, device=dev)
+    mean = torch.empty(n, dtype=torch.float32, device=dev)
+    rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    kept = _new_checkpoint(n, d, dev) if checkpoint else None
+    if checkpoint or info is not None:
+        info = _info(info, dev)
+    codes, exps = kept or (None, None)
+    with _on(dev):
+        _check(lib.lrc_layer_norm(_ptr(x), dt, n, d, ldx, _ptr(gamma), _ptr(beta), float(eps), _ptr(y), max(d, 1),
+                                  _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(exps), _ptr(info), _stream_of(dev)),
+               "lrc_layer_norm")
+    return y, mean, rstd, kept, info
+
+
+def lrc_layer_norm_backward(dy: torch.Tensor, x, mean: torch.Tensor, rstd: torch.Tensor, gamma=None,
+                            need_dx: bool = True, need_dparams: bool = True):
+    """Gradients of lrc_layer_norm.  dy: (n_tokens, d); x: the input like dy, or its
+    (codes, exps) checkpoint; mean, rstd: (n_tokens,) fp32 as lrc_layer_norm returned them.
+
+    Returns (dx like dy, dgamma fp32 (d,), dbeta fp32 (d,)), None where not needed."""
+    dy, lddy = _rows(dy, "dy", (None, None))
+    dt, dev = _dtype_code(dy), dy.device
+    n, d = dy.shape
+    if x is None:
+        raise ValueError("x must be a tensor or a (codes, exps) pair")
+    xt, ldx, codes, exps = _kept(x, "x", n, d, dy.dtype, dev)
+    mean, rstd = _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev)
+    gamma = _vector(gamma, "gamma", d, dev)
+    dx = torch.empty(n, d, dtype=dy.dtype, device=dev) if need_dx else None
+    dgamma = torch.empty(d, dtype=torch.float32, device=dev) if need_dparams else None
+    dbeta = torch.empty(d, dtype=torch.float32, device=dev) if need_dparams else None
+    with _on(dev):
+        ws = _workspace(lib.lrc_layer_norm_backward_workspace(n, d), dev)
+        _check(lib.lrc_layer_norm_backward(_ptr(dy), dt, n, d, lddy, _ptr(xt), ldx, _ptr(codes), _ptr(exps),
+                                           _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dx), max(d, 1), _ptr(dgamma),
+                                           _ptr(dbeta), _ptr(ws), ws.numel(), _stream_of(dev)),
+               "lrc_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def _act_code(act):
+    if act not in _ACTS:
+        raise ValueError(f"act is one of {', '.join(_ACTS)}")
+    return _ACTS[act]
+
+
+def lrc_linear(x: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", residual=None, save: str = "none",
+               info=None):
+    """y = act(x W^T + bias) + residual.  x: (n_tokens, d_in), W: (d_out, d_in), residual:
+    (n_tokens, d_out), all bf16 or all fp32; bias: (d_out,) fp32; act: none, relu, gelu
+    (exact) or silu.  save keeps the pre-activation z = x W^T + bias for the backward pass:
+    "z" in full, "checkpoint" in 8 bits, "none" not at all.
+
+    Returns (y, saved, info): saved is z, (codes, exps) or None; info (int32 (1,), sticky
+    LRC_ENONFINITE) is None unless given or save is "checkpoint"."""
+    x, ldx = _rows(x, "x", (None, None))
+    dt, dev = _dtype_code(x), x.device
+    n, d_in = x.shape
+    W, ldw = _rows(W, "W", (None, d_in), x.dtype, dev)
+    d_out = W.shape[0]
+    code = _act_code(act)
+    bias = _vector(bias, "bias", d_out, dev)
+    ldr = d_out
+    if residual is not None:
+        residual, ldr = _rows(residual, "residual", (n, d_out), x.dtype, dev)
+    y = torch.empty(n, d_out, dtype=x.dtype, device=dev)
+    z, codes, exps = None, None, None
+    if save == "z":
+        z = torch.empty(n, d_out, dtype=x.dtype, device=dev)
+    elif save == "checkpoint":
+        codes, exps = _new_checkpoint(n, d_out, dev)
+    elif save != "none":
+        raise ValueError("save is none, z or checkpoint")
+    if codes is not None or info is not None:
+        info = _info(info, dev)
+    with _on(dev):
+        ws = _workspace(lib.lrc_linear_workspace(dt, n, d_in, d_out), dev)
+        _check(lib.lrc_linear(_ptr(x), dt, n, d_in, d_out, ldx, _ptr(W), ldw, _ptr(bias), code, _ptr(residual), ldr,
+                              _ptr(y), max(d_out, 1), _ptr(z), max(d_out, 1), _ptr(codes), _ptr(exps), _ptr(info),
+                              _ptr(ws), ws.numel(), _stream_of(dev)), "lrc_linear")
+    return y, (codes, exps) if codes is not None else z, info
+
+
+def lrc_linear_backward(dy: torch.Tensor, x, W: torch.Tensor, act: str = "none", z=None, need_dx: bool = True,
+                        need_dw: bool = True, need_db: bool = True, dw_dtype=None):
+    """Gradients of lrc_linear.  dy: (n_tokens, d_out); x: the input (n_tokens, d_in) like dy,
+    or its (codes, exps) checkpoint (may be None without need_dw); W: (d_out, d_in); z: the
+    pre-activation like dy or its (codes, exps) checkpoint (needed unless act is none).
+
+    Returns (dz, dx, dW, db): dz = dy * act'(z), the layer's output-gradient stream (dy itself
+    for act none), dx (n_tokens, d_in), dW (d_out, d_in) in dw_dtype (default dy's; torch.float32
+    allowed), db fp32 (d_out,); None where not needed."""
+    dy, lddy = _rows(dy, "dy", (None, None))
+    dt, dev = _dtype_code(dy), dy.device
+    n, d_out = dy.shape
+    W, ldw = _rows(W, "W", (d_out, None), dy.dtype, dev)
+    d_in = W.shape[1]
+    code = _act_code(act)
+    if need_dw and x is None:
+        raise ValueError("dW needs x or its checkpoint")
+    if code and z is None:
+        raise ValueError("the gradient of an activation needs z or its checkpoint")
+    xt, ldx, xcodes, xexps = _kept(x if need_dw else None, "x", n, d_in, dy.dtype, dev)
+    zt, ldz, zcodes, zexps = _kept(z if code else None, "z", n, d_out, dy.dtype, dev)
+    dw_dtype = dw_dtype or dy.dtype
+    if dw_dtype not in (dy.dtype, torch.float32):
+        raise ValueError("dw_dtype is dy's dtype or torch.float32")
+    dz = torch.empty(n, d_out, dtype=dy.dtype, device=dev) if code else None
+    dx = torch.empty(n, d_in, dtype=dy.dtype, device=dev) if need_dx else None
+    dW = torch.empty(d_out, d_in, dtype=dw_dtype, device=dev) if need_dw else None
+    db = torch.empty(d_out, dtype=torch.float32, device=dev) if need_db else None
+    dw_dt = LRC_F32 if dw_dtype == torch.float32 else LRC_BF16
+    with _on(dev):
+        ws = _workspace(lib.lrc_linear_backward_workspace(dt, n, d_in, d_out), dev)
+        _check(lib.lrc_linear_backward(_ptr(dy), dt, n, d_in, d_out, lddy, _ptr(W), ldw, _ptr(xt), ldx, _ptr(xcodes),
+                                       _ptr(xexps), code, _ptr(zt), ldz, _ptr(zcodes), _ptr(zexps), _ptr(dz),
+                                       max(d_out, 1), _ptr(dx), max(d_in, 1), _ptr(dW), dw_dt, max(d_in, 1),
+                                       _ptr(db), _ptr(ws), ws.numel(), _stream_of(dev)), "lrc_linear_backward")
+    return dz if code else dy, dx, dW, db
 
 
 def lrc_profile_start() -> None:

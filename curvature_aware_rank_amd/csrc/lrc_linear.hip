@@ -1,0 +1,431 @@
+// Linear layer of a token block: y = act(x W^T + b) + residual, and its gradients from
+// activations kept in full or in 8 bits.
+//
+// All three products are D[m][n] = sum_k A(m, k) B(n, k):
+//   forward  m = token, n = output channel, k = input channel;   A = x, B = W: rows along k
+//   dx       m = token, n = input channel,  k = output channel;  A = dz rows, B = W's columns
+//   dW       m = output channel, n = input channel, k = token;   A, B = columns of dz and x
+// An operand is therefore a row-major matrix whose rows run along k (K_ROWS) or whose rows
+// are the k steps (K_COLS), or a checkpoint of the latter kind (K_CODES).
+#include "lrc_train.h"
+
+#include <algorithm>
+
+namespace lrc {
+namespace {
+
+constexpr int LT = 256;
+
+enum OperandKind { K_ROWS, K_COLS, K_CODES };
+
+struct Operand {
+  const void* p;        // elements, or int8 codes
+  int64_t ld;
+  const int8_t* exps;   // K_CODES: block exponents, nb per row
+  int64_t nb;
+  bool vec;             // 16-byte (codes: 8-byte) pieces allowed
+};
+
+// What happens to a finished row piece of D.
+struct Epilogue {
+  const float* bias = nullptr;
+  int act = LRC_ACT_NONE;
+  const void* res = nullptr;
+  int64_t ldr = 0;
+  void* y = nullptr;
+  int64_t ldy = 0;
+  void* z = nullptr;
+  int64_t ldz = 0;
+  int8_t* codes = nullptr;
+  int8_t* exps = nullptr;
+  int64_t nb = 0;
+  int32_t* info = nullptr;
+  bool vec_y = false, vec_r = false, vec_z = false, vec_c = false;
+};
+
+// Eight consecutive columns of one row.  Lanes 8 i .. 8 i + 7 of a wave hold the 64 columns
+// of one block of the row and call this together; `cnt` of the lane's columns exist.
+template <class TO>
+__device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t col, int cnt, float (&v)[8], int lane,
+                                        bool& bad) {
+  if (ep.bias != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += e < cnt ? ep.bias[col + e] : 0.f;
+  }
+  if (ep.z != nullptr && cnt > 0) st8(static_cast<TO*>(ep.z) + row * ep.ldz + col, ep.vec_z, cnt, v);
+  if (ep.codes != nullptr) {
+    const int64_t n = ep.nb;
+    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * n + (col >> 6), ep.vec_c, cnt, v, lane, bad);
+  }
+  if (cnt <= 0) return;
+  if (ep.act != LRC_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value(ep.act, v[e]);
+  }
+  if (ep.res != nullptr) {
+    float r[8];
+    ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, ep.vec_r, cnt, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += r[e];
+  }
+  st8(static_cast<TO*>(ep.y) + row * ep.ldy + col, ep.vec_y, cnt, v);
+}
+
+// ---- any size, stride and alignment: 64 x 64 tiles, four waves of 32 x 32 ---------------
+constexpr int GT = 64;    // tile edge
+constexpr int GK = 32;    // k per step
+
+template <class T>
+struct GTile {
+  static constexpr int PITCH = sizeof(T) == 2 ? GK + 8 : GK + 4;
+};
+
+// Eight values of an operand as T bits: for K_ROWS along k at (row, k), for the others along
+// the rows at step k.
+template <class T, int KIND>
+__device__ __forceinline__ void operand8(const Operand& o, int64_t row, int64_t k, int64_t rows, int64_t kk,
+                                         float (&v)[8]) {
+  if (KIND == K_ROWS) {
+    const int64_t left = row < rows ? kk - k : 0;
+    ld8(static_cast<const T*>(o.p) + row * o.ld + k, o.vec, int(left < 0 ? 0 : left > 8 ? 8 : left), v);
+    return;
+  }
+  const int64_t left = k < kk ? rows - row : 0;
+  const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
+  if (KIND == K_COLS) {
+    ld8(static_cast<const T*>(o.p) + k * o.ld + row, o.vec, cnt, v);
+  } else {   // eight channels from a multiple of eight: one block
+    const float step = cnt > 0 ? pow2f(o.exps[k * o.nb + (row >> 6)]) : 0.f;
+    ld8_codes(static_cast<const int8_t*>(o.p) + k * o.ld + row, o.vec, cnt, step, v);
+  }
+}
+
+__device__ __forceinline__ void lds_put8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void lds_put8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// One step of an operand into LDS as [row][k].
+template <class T, int KIND>
+__device__ __forceinline__ void stage_any(const Operand& o, T* lds, int64_t row0, int64_t k0, int64_t rows, int64_t kk) {
+  constexpr int P = GTile<T>::PITCH;
+  float v[8];
+  if (KIND == K_ROWS) {
+    const int r = threadIdx.x >> 2, k = (threadIdx.x & 3) * 8;
+    operand8<T, KIND>(o, row0 + r, k0 + k, rows, kk, v);
+    lds_put8(lds + r * P + k, v);
+  } else {
+    const int k = threadIdx.x >> 3, r = (threadIdx.x & 7) * 8;
+    operand8<T, KIND>(o, row0 + r, k0 + k, rows, kk, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) st_elem(lds + (r + e) * P + k, v[e]);
+  }
+}
+
+__device__ __forceinline__ void mma_any(const uint16_t* a, const uint16_t* b, int lane, f32x4& acc) {
+  const int off = (lane & 15) * GTile<uint16_t>::PITCH + 8 * (lane >> 4);
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(a + off),
+                                                *reinterpret_cast<const bf16x8*>(b + off), acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma_any(const float* a, const float* b, int lane, f32x4& acc) {
+  const int off = (lane & 15) * GTile<float>::PITCH + (lane >> 4);
+#pragma unroll
+  for (int s = 0; s < GK / 4; ++s)
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[off + 4 * s], b[off + 4 * s], acc, 0, 0, 0);
+}
+
+template <class T, class TO, int KA, int KB>
+__global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
+                                                        int64_t tiles_n, Epilogue ep) {
+  constexpr int P = GTile<T>::PITCH;
+  constexpr int EP = GT + 4;   // epilogue tile pitch
+  __shared__ __attribute__((aligned(16))) uint8_t lds[GT * EP * 4 > 2 * GT * P * int(sizeof(T))
+                                                          ? GT * EP * 4
+                                                          : 2 * GT * P * int(sizeof(T))];
+  T* la = reinterpret_cast<T*>(lds);
+  T* lb = la + GT * P;
+  const int64_t m0 = int64_t(blockIdx.x) / tiles_n * GT, n0 = int64_t(blockIdx.x) % tiles_n * GT;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
+  f32x4 acc[2][2] = {};
+  for (int64_t k0 = 0; k0 < K; k0 += GK) {
+    stage_any<T, KA>(A, la, m0, k0, M, K);
+    stage_any<T, KB>(B, lb, n0, k0, N, K);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mma_any(la + (wr + 16 * i) * P, lb + (wc + 16 * j) * P, lane, acc[i][j]);
+    __syncthreads();
+  }
+  float* tile = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        tile[(wr + 16 * i + 4 * (lane >> 4) + e) * EP + wc + 16 * j + (lane & 15)] = acc[i][j][e];
+  __syncthreads();
+  bool bad = false;
+  for (int r = threadIdx.x >> 3; r < GT; r += LT / 8) {
+    const int64_t row = m0 + r, col = n0 + 8 * (lane & 7);
+    const int64_t left = row < M ? N - col : 0;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = tile[r * EP + 8 * (lane & 7) + e];
+    finish8<TO>(ep, row, col, int(left < 0 ? 0 : left > 8 ? 8 : left), v, lane, bad);
+  }
+  if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
+}
+
+// ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
+constexpr int DZ_ROWS = 64;   // tokens per chunk at least
+struct ColPlan {
+  int64_t rows, chunks;
+};
+ColPlan col_plan(int64_t n) {
+  ColPlan p;
+  p.rows = std::max<int64_t>(DZ_ROWS, cdiv(n, 1024));
+  p.chunks = cdiv(n, p.rows);
+  return p;
+}
+
+template <class T, bool CK>
+__global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_t lddy, int64_t n, int64_t d,
+                                                const T* __restrict__ z, int64_t ldz,
+                                                const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
+                                                int64_t nb, int act, T* __restrict__ dz, int64_t lddz, int64_t rows,
+                                                float* __restrict__ partial) {
+  const int64_t j = int64_t(blockIdx.x) * LT + threadIdx.x;
+  if (j >= d) return;
+  const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
+  float s = 0.f;
+  for (int64_t t = t0; t < t1; ++t) {
+    float g = ld_elem(dy + t * lddy + j);
+    if (act != LRC_ACT_NONE) {
+      const float zv = CK ? float(codes[t * d + j]) * pow2f(exps[t * nb + (j >> 6)]) : ld_elem(z + t * ldz + j);
+      g *= act_slope(act, zv);
+      st_elem(dz + t * lddz + j, g);
+    }
+    s += g;
+  }
+  if (partial != nullptr) partial[int64_t(blockIdx.y) * d + j] = s;
+}
+
+// rows of `halves` 16-bit words, pitch `ld`, set to zero
+__global__ __launch_bounds__(LT) void zero_rows_kernel(uint16_t* p, int64_t rows, int64_t halves, int64_t ld) {
+  const int64_t step = int64_t(gridDim.x) * LT;
+  for (int64_t i = int64_t(blockIdx.x) * LT + threadIdx.x; i < rows * halves; i += step)
+    p[i / halves * ld + i % halves] = 0;
+}
+
+constexpr int64_t DMAX = int64_t(1) << 24;
+bool sizes_ok(int64_t n, int64_t i, int64_t o) {
+  return n >= 0 && n < (int64_t(1) << 31) && i >= 1 && i <= DMAX && o >= 1 && o <= DMAX;
+}
+bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
+
+template <class T, class TO, int KA, int KB>
+lrc_status product(hipStream_t st, const char* name, const Operand& A, const Operand& B, int64_t M, int64_t N,
+                   int64_t K, const Epilogue& ep, double bytes) {
+  const int64_t tn = cdiv(N, GT), grid = cdiv(M, GT) * tn;
+  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  ProfScope scope(name, st, 2.0 * double(M) * double(N) * double(K), bytes);
+  linear_any_kernel<T, TO, KA, KB><<<unsigned(grid), LT, 0, st>>>(A, B, M, N, K, tn, ep);
+  LRC_LAUNCHED();
+  return LRC_OK;
+}
+
+template <class T>
+Operand plain(const void* p, int64_t ld) {
+  return {p, ld, nullptr, 0, rows_vec16(p, ld, sizeof(T))};
+}
+template <class T>
+void set_out(Epilogue& ep, void* y, int64_t ldy) {
+  ep.y = y;
+  ep.ldy = ldy;
+  ep.vec_y = rows_vec16(y, ldy, sizeof(T));
+}
+
+template <class T>
+lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, int64_t dn, int64_t ldx, const void* W,
+                          int64_t ldw, const float* bias, int act, const void* res, int64_t ldr, void* y, int64_t ldy,
+                          void* z, int64_t ldz, int8_t* zcodes, int8_t* zexps, int32_t* info) {
+  Epilogue ep;
+  ep.bias = bias;
+  ep.act = act;
+  ep.res = res;
+  ep.ldr = ldr;
+  ep.vec_r = rows_vec16(res, ldr, sizeof(T));
+  set_out<T>(ep, y, ldy);
+  ep.z = z;
+  ep.ldz = zcodes != nullptr ? dn : ldz;
+  ep.vec_z = rows_vec16(z, ldz, sizeof(T));
+  ep.codes = zcodes;
+  ep.exps = zexps;
+  ep.nb = cdiv(dn, CKB);
+  ep.vec_c = dn % 8 == 0 && (reinterpret_cast<uintptr_t>(zcodes) & 7) == 0;
+  ep.info = info;
+  const double bytes = double(sizeof(T)) * (double(n) * di + double(dn) * di + double(n) * dn * (res ? 2 : 1));
+  return product<T, T, K_ROWS, K_ROWS>(st, "linear_kernel", plain<T>(x, ldx), plain<T>(W, ldw), n, dn, di, ep, bytes);
+}
+
+}  // namespace
+}  // namespace lrc
+
+using namespace lrc;
+
+extern "C" size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out) {
+  (void)dt;
+  if (!sizes_ok(n_tokens, d_in, d_out)) return 0;
+  return 0;
+}
+
+extern "C" lrc_status lrc_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,
+                                 int64_t ldx, const void* W, int64_t ldw, const float* bias, lrc_act act,
+                                 const void* residual, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz,
+                                 int8_t* zcodes, int8_t* zexps, int32_t* info, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  if ((dt != LRC_F32 && dt != LRC_BF16) || !act_ok(act)) return LRC_EDTYPE;
+  if (!sizes_ok(n_tokens, d_in, d_out) || ldx < d_in || ldw < d_in || ldy < d_out) return LRC_EINVAL;
+  if ((residual != nullptr && ldr < d_out) || (z != nullptr && ldz < d_out)) return LRC_EINVAL;
+  if ((zcodes == nullptr) != (zexps == nullptr) || (z != nullptr && zcodes != nullptr)) return LRC_EINVAL;
+  if (n_tokens == 0) return LRC_OK;
+  if (x == nullptr || W == nullptr || y == nullptr) return LRC_EINVAL;
+  const size_t need = lrc_linear_workspace(dt, n_tokens, d_in, d_out);
+  if (ws_bytes < need || (need > 0 && ws == nullptr)) return LRC_EWORKSPACE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (dt == LRC_BF16)
+    return linear_forward<uint16_t>(st, x, n_tokens, d_in, d_out, ldx, W, ldw, bias, act, residual, ldr, y, ldy, z,
+                                    ldz, zcodes, zexps, info);
+  return linear_forward<float>(st, x, n_tokens, d_in, d_out, ldx, W, ldw, bias, act, residual, ldr, y, ldy, z, ldz,
+                               zcodes, zexps, info);
+}
+
+extern "C" size_t lrc_linear_backward_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out) {
+  (void)dt;
+  if (!sizes_ok(n_tokens, d_in, d_out)) return 0;
+  Carve cv(nullptr);
+  cv.take<float>(size_t(col_plan(n_tokens).chunks) * d_out);
+  return cv.bytes();
+}
+
+namespace lrc {
+namespace {
+struct BackArgs {
+  int64_t n, di, dn;
+  const void* dy;
+  int64_t lddy;
+  const void* W;
+  int64_t ldw;
+  const void* x;
+  int64_t ldx;
+  const int8_t *xcodes, *xexps;
+  int act;
+  const void* z;
+  int64_t ldz;
+  const int8_t *zcodes, *zexps;
+  void* dz;
+  int64_t lddz;
+  void* dx;
+  int64_t lddx;
+  void* dW;
+  int dw_dt;
+  int64_t lddw;
+  float* db;
+};
+
+template <class T>
+lrc_status linear_back(hipStream_t st, const BackArgs& a, float* partial) {
+  const int64_t n = a.n, di = a.di, dn = a.dn;
+  const void* g = a.dy;
+  int64_t ldg = a.lddy;
+  if (a.act != LRC_ACT_NONE || a.db != nullptr) {
+    const ColPlan p = col_plan(n);
+    {
+      ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
+      const dim3 grid(unsigned(cdiv(dn, LT)), unsigned(p.chunks));
+      float* part = a.db != nullptr ? partial : nullptr;
+      const T *dy = static_cast<const T*>(a.dy), *z = static_cast<const T*>(a.z);
+      T* dz = static_cast<T*>(a.dz);
+      if (a.z == nullptr && a.act != LRC_ACT_NONE)
+        dz_kernel<T, true><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, cdiv(dn, CKB), a.act,
+                                                dz, a.lddz, p.rows, part);
+      else
+        dz_kernel<T, false><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, nullptr, nullptr, 0, a.act, dz, a.lddz,
+                                                 p.rows, part);
+      LRC_LAUNCHED();
+    }
+    if (a.db != nullptr) LRC_TRY(reduce_partials(st, partial, p.chunks, dn, dn, a.db));
+    if (a.act != LRC_ACT_NONE) {
+      g = a.dz;
+      ldg = a.lddz;
+    }
+  }
+  const double e = sizeof(T);
+  if (a.dx != nullptr) {
+    Epilogue ep;
+    set_out<T>(ep, a.dx, a.lddx);
+    LRC_TRY((product<T, T, K_ROWS, K_COLS>(st, "linear_dx_kernel", plain<T>(g, ldg), plain<T>(a.W, a.ldw), n, di, dn,
+                                           ep, e * (double(n) * dn + double(dn) * di + double(n) * di))));
+  }
+  if (a.dW == nullptr) return LRC_OK;
+  Epilogue ep;
+  const Operand ga = plain<T>(g, ldg);
+  const double bytes = e * (double(n) * dn + double(dn) * di) + double(n) * di * (a.x ? e : 1.0);
+  auto go = [&](auto tag) -> lrc_status {
+    using TO = decltype(tag);
+    set_out<TO>(ep, a.dW, a.lddw);
+    if (a.x != nullptr)
+      return product<T, TO, K_COLS, K_COLS>(st, "linear_dw_kernel", ga, plain<T>(a.x, a.ldx), dn, di, n, ep, bytes);
+    const Operand q = {a.xcodes, di, a.xexps, cdiv(di, CKB),
+                       di % 8 == 0 && (reinterpret_cast<uintptr_t>(a.xcodes) & 7) == 0};
+    return product<T, TO, K_COLS, K_CODES>(st, "linear_dw_kernel", ga, q, dn, di, n, ep, bytes);
+  };
+  if (a.dw_dt == LRC_F32) return go(float{});
+  return go(uint16_t{});
+}
+}  // namespace
+}  // namespace lrc
+
+extern "C" lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,
+                                          int64_t lddy, const void* W, int64_t ldw, const void* x, int64_t ldx,
+                                          const int8_t* xcodes, const int8_t* xexps, lrc_act act, const void* z,
+                                          int64_t ldz, const int8_t* zcodes, const int8_t* zexps, void* dz,
+                                          int64_t lddz, void* dx, int64_t lddx, void* dW, lrc_dtype dw_dt,
+                                          int64_t lddw, float* db, void* ws, size_t ws_bytes, void* stream) {
+  if ((dt != LRC_F32 && dt != LRC_BF16) || !act_ok(act)) return LRC_EDTYPE;
+  if (dW != nullptr && dw_dt != LRC_F32 && dw_dt != dt) return LRC_EDTYPE;
+  if (!sizes_ok(n_tokens, d_in, d_out) || lddy < d_out) return LRC_EINVAL;
+  if ((dx != nullptr && (lddx < d_in || ldw < d_in)) || (dW != nullptr && lddw < d_in)) return LRC_EINVAL;
+  if (x != nullptr && ldx < d_in) return LRC_EINVAL;
+  if (act != LRC_ACT_NONE && ((z != nullptr && ldz < d_out) || lddz < d_out)) return LRC_EINVAL;
+  if (n_tokens > 0) {
+    if (dy == nullptr || (dx != nullptr && W == nullptr)) return LRC_EINVAL;
+    if (dW != nullptr && x == nullptr && (xcodes == nullptr || xexps == nullptr)) return LRC_EINVAL;
+    if (act != LRC_ACT_NONE && (dz == nullptr || (z == nullptr && (zcodes == nullptr || zexps == nullptr))))
+      return LRC_EINVAL;
+  }
+  const size_t need = lrc_linear_backward_workspace(dt, n_tokens, d_in, d_out);
+  if (ws_bytes < need || (need > 0 && ws == nullptr)) return LRC_EWORKSPACE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n_tokens == 0) {   // sums over nothing
+    if (dW != nullptr) {
+      const int64_t half = dw_dt == LRC_F32 ? 2 : 1;
+      const int64_t grid = std::min<int64_t>(cdiv(d_out * d_in * half, LT), 16384);
+      zero_rows_kernel<<<unsigned(grid), LT, 0, st>>>(static_cast<uint16_t*>(dW), d_out, d_in * half, lddw * half);
+      LRC_LAUNCHED();
+    }
+    if (db != nullptr) LRC_TRY(reduce_partials(st, nullptr, 0, 0, d_out, db));
+    return LRC_OK;
+  }
+  const BackArgs a = {n_tokens, d_in, d_out, dy,  lddy,  W,     ldw, x,    ldx, xcodes, xexps, act,
+                      z,        ldz,  zcodes, zexps, dz, lddz, dx,  lddx, dW,  int(dw_dt), lddw, db};
+  float* partial = static_cast<float*>(ws);
+  return dt == LRC_BF16 ? linear_back<uint16_t>(st, a, partial) : linear_back<float>(st, a, partial);
+}

@@ -1,0 +1,177 @@
+// Device helpers shared by the layer-norm, linear and 8-bit checkpoint kernels.
+#pragma once
+
+#include "lrc_internal.h"
+
+namespace lrc {
+
+constexpr int CKB = LRC_CKPT_BLOCK;   // channels that share one checkpoint exponent
+
+// ---- element types: bf16 held as raw bits (uint16_t) or fp32 -------------------------
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float ld_elem(const float* p) { return *p; }
+__device__ __forceinline__ float ld_elem(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+
+// two fp32 -> two bf16 in one word, round to nearest even (NaN stays NaN)
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  const f32x2 v = {a, b};
+  const bf16x2 h = __builtin_convertvector(v, bf16x2);
+  uint32_t u;
+  __builtin_memcpy(&u, &h, 4);
+  return u;
+}
+__device__ __forceinline__ void st_elem(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st_elem(uint16_t* p, float v) { *p = uint16_t(pack_bf16x2(v, v)); }
+__device__ __forceinline__ float round_to(float v, const float*) { return v; }
+__device__ __forceinline__ float round_to(float v, const uint16_t*) {
+  return bf16_bits_to_f32(pack_bf16x2(v, v) & 0xffffu);
+}
+
+// eight consecutive elements; `vec`: 16-byte accesses allowed, `cnt`: elements in range
+__device__ __forceinline__ void ld8(const float* p, bool vec, int cnt, float (&v)[8]) {
+  if (vec && cnt >= 8) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? p[e] : 0.f;
+}
+__device__ __forceinline__ void ld8(const uint16_t* p, bool vec, int cnt, float (&v)[8]) {
+  if (vec && cnt >= 8) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? bf16_bits_to_f32(p[e]) : 0.f;
+}
+__device__ __forceinline__ void st8(float* p, bool vec, int cnt, const float (&v)[8]) {
+  if (vec && cnt >= 8) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) p[e] = v[e];
+}
+__device__ __forceinline__ void st8(uint16_t* p, bool vec, int cnt, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  if (vec && cnt >= 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+}
+
+// rows of `ld` elements of `size` bytes starting at p can be read 16 bytes at a time
+inline bool rows_vec16(const void* p, int64_t ld, int size) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * size) % 16 == 0;
+}
+
+// ---- 8-bit checkpoints ---------------------------------------------------------------
+// A block of 64 channels of a token shares the exponent e, the smallest integer with
+// max|x| <= 127 * 2^e, held to [-126, 121] so that 2^e is a normal number and 127 * 2^e is
+// finite; the codes are q = clamp(rint(x * 2^-e), -127, 127), ties to even.  The scaling by
+// a power of two is exact, so there is one rounding per value, and q * 2^e has at most seven
+// significant bits: it is exact in bf16.
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+__device__ __forceinline__ int ckpt_exponent(float m) {   // m: largest finite magnitude
+  const uint32_t u = __float_as_uint(m);
+  // m = f 2^(E - 127), 1 <= f < 2: 64 f <= 127 exactly when the mantissa field is <= 0x7E0000
+  const int e = int(u >> 23) - 133 + ((u & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return max(-126, min(121, e));
+}
+__device__ __forceinline__ bool finite_f(float v) { return fabsf(v) < __builtin_inff(); }
+__device__ __forceinline__ float finite_mag(float v) { return finite_f(v) ? fabsf(v) : 0.f; }
+// code of one value (inv = 2^-e); an infinity becomes +-127, NaN becomes 0
+__device__ __forceinline__ int ckpt_code(float v, float inv) {
+  const float q = fminf(fmaxf(rintf(v * inv), -127.f), 127.f);
+  return v == v ? int(q) : 0;
+}
+__device__ __forceinline__ uint32_t pack_codes4(int a, int b, int c, int d) {
+  return uint32_t(a & 255) | (uint32_t(b & 255) << 8) | (uint32_t(c & 255) << 16) | (uint32_t(d) << 24);
+}
+// eight codes times their block's step
+__device__ __forceinline__ void ld8_codes(const int8_t* p, bool vec, int cnt, float step, float (&v)[8]) {
+  if (vec && cnt >= 8) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = float(int8_t(u.x >> (8 * e))) * step;
+      v[4 + e] = float(int8_t(u.y >> (8 * e))) * step;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? float(p[e]) * step : 0.f;
+}
+// Codes of eight consecutive values held by each of the eight lanes that share a block
+// (lanes 8 i .. 8 i + 7; every lane of the group takes part, `cnt` of its values exist).
+__device__ __forceinline__ void st8_codes(int8_t* p, int8_t* pe, bool vec, int cnt, const float (&v)[8], int lane,
+                                          bool& bad) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) {
+      m = fmaxf(m, finite_mag(v[e]));
+      bad |= !finite_f(v[e]);
+    }
+  m = fmaxf(m, __shfl_xor(m, 1));
+  m = fmaxf(m, __shfl_xor(m, 2));
+  m = fmaxf(m, __shfl_xor(m, 4));
+  const int ex = ckpt_exponent(m);
+  const float inv = pow2f(-ex);
+  if (cnt <= 0) return;
+  int q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = ckpt_code(v[e], inv);
+  if (vec && cnt >= 8) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(pack_codes4(q[0], q[1], q[2], q[3]), pack_codes4(q[4], q[5], q[6], q[7]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < cnt) p[e] = int8_t(q[e]);
+  }
+  if ((lane & 7) == 0) *pe = int8_t(ex);
+}
+
+// ---- activations and their derivatives -----------------------------------------------
+__device__ __forceinline__ float act_value(int act, float z) {
+  if (act == LRC_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
+  if (act == LRC_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == LRC_ACT_SILU) return z / (1.f + expf(-z));
+  return z;
+}
+__device__ __forceinline__ float act_slope(int act, float z) {
+  if (act == LRC_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
+  if (act == LRC_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+  if (act == LRC_ACT_SILU) {
+    const float s = 1.f / (1.f + expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  return 1.f;
+}
+
+// ---- column sums ---------------------------------------------------------------------
+// out[c] = sum over p < parts of partial[p * stride + c], in the order of p.
+lrc_status reduce_partials(hipStream_t st, const float* partial, int64_t parts, int64_t stride, int64_t cols,
+                           float* out);
+
+}  // namespace lrc

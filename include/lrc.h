@@ -56,6 +56,11 @@ typedef enum {
 
 typedef enum { LRC_F32 = 0, LRC_BF16 = 1 } lrc_dtype;
 
+/* activation of lrc_linear: z, max(z, 0), z Phi(z) (the exact GELU), z / (1 + exp(-z)) */
+typedef enum { LRC_ACT_NONE = 0, LRC_ACT_RELU = 1, LRC_ACT_GELU = 2, LRC_ACT_SILU = 3 } lrc_act;
+
+#define LRC_CKPT_BLOCK 64              /* channels that share one checkpoint exponent */
+
 /* lrc_accumulate_cov flags */
 #define LRC_COV_QUANT_INT8_TOKEN 0x1u  /* fake-quantise each token to int8 first (QAW) */
 
@@ -375,6 +380,105 @@ lrc_status lrc_hybrid_ffn(const float* x, int64_t n_tok, int64_t d, int64_t n_lr
                           const int8_t* q_gd, const float* s_gd, const int8_t* q_ud, const float* s_ud,
                           const int8_t* q_dd, const float* s_dd, float* y, void* ws, size_t ws_bytes, void* stream);
 size_t lrc_hybrid_ffn_workspace(int64_t n_tok, int64_t n_lr, int64_t rg, int64_t ru, int64_t rd, int64_t n_dense);
+
+/*
+ * lrc_pack_activations / lrc_unpack_activations -- activation checkpoints in 8 bits.
+ * The covariances and Fisher scores above are taken from a forward and a backward pass over
+ * the calibration tokens; between the two, the activations the backward pass needs are kept
+ * as int8 codes, 64 channels of a token sharing one power-of-two step:
+ *   e = smallest integer with max|x| <= 127 * 2^e over the block, held to [-126, 121],
+ *   q = clamp(round_half_even(x * 2^-e), -127, 127),    the value held is q * 2^e
+ * (the symmetric int8 quantiser of LASER Methodology 1, QAW, with a step per block instead of
+ * per token, so that an outlier channel costs only its own block precision, and with a step
+ * that is a power of two, so that a held value is exact in bf16 and goes to the matrix cores
+ * without another rounding).  A block of zeros has e = -126.
+ * x: n_tokens x d, dtype `dt`, leading dim ldx >= d.  codes: n_tokens x d int8 (leading dim
+ * d).  exps: n_tokens x ceil(d / 64) int8 (packed).  1 <= d <= 2^24, n_tokens < 2^31.
+ * info: device int32 or NULL; set to LRC_ENONFINITE when an entry is NaN or Inf, never
+ * cleared.  Such an entry does not count for e; an infinity is held as +-127 * 2^e, NaN as 0.
+ * Unpacking writes q * 2^e in dtype `dt` (exact in both).  n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_pack_activations(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t ldx,
+                                int8_t* codes, int8_t* exps, int32_t* info, void* stream);
+lrc_status lrc_unpack_activations(const int8_t* codes, const int8_t* exps, int64_t n_tokens, int64_t d, void* x,
+                                  lrc_dtype dt, int64_t ldx, void* stream);
+
+/*
+ * lrc_layer_norm -- layer norm of every token, optionally keeping its input in 8 bits.
+ *   mean = sum_j x_j / d,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / d + eps),
+ *   y = (x - mean) * rstd * gamma + beta
+ * x, y: n_tokens x d, dtype `dt`, leading dims ldx, ldy >= d.  gamma, beta: float[d], or
+ * NULL for 1 and 0.  eps >= 0.  mean, rstd: float[n_tokens] (written; lrc_layer_norm_backward
+ * takes them).  codes, exps: both given or both NULL; when given they receive the checkpoint
+ * of x, the same bits as lrc_pack_activations of x, and `info` is used as there (NULL for
+ * no check).  Statistics are fp32 over values centred first (two passes over registers).
+ * 1 <= d <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_layer_norm(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t ldx,
+                          const float* gamma, const float* beta, float eps, void* y, int64_t ldy, float* mean,
+                          float* rstd, int8_t* codes, int8_t* exps, int32_t* info, void* stream);
+
+/*
+ * lrc_layer_norm_backward -- gradients of lrc_layer_norm.
+ *   xh = (x - mean) * rstd,  g = dy * gamma,
+ *   dx = rstd * (g - sum_j g_j / d - xh * sum_j g_j xh_j / d),
+ *   dgamma = sum_t dy xh,  dbeta = sum_t dy
+ * dy: n_tokens x d, dtype `dt`, leading dim lddy.  The input is x (dtype `dt`, leading dim
+ * ldx), or, with x NULL, its checkpoint codes and exps; mean and rstd are those
+ * lrc_layer_norm wrote.  gamma: float[d] or NULL for 1.  Outputs: dx (n_tokens x d, dtype
+ * `dt`, leading dim lddx), dgamma, dbeta (float[d]); any of the three may be NULL.
+ * The token sums run over fixed chunks in a fixed order (equal inputs give equal bits).
+ * n_tokens == 0 writes zeros to dgamma and dbeta.  Sizes as lrc_layer_norm.
+ */
+lrc_status lrc_layer_norm_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t lddy,
+                                   const void* x, int64_t ldx, const int8_t* codes, const int8_t* exps,
+                                   const float* mean, const float* rstd, const float* gamma, void* dx,
+                                   int64_t lddx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                   void* stream);
+size_t lrc_layer_norm_backward_workspace(int64_t n_tokens, int64_t d);
+
+/*
+ * lrc_linear -- matrix product with bias, activation and residual in its epilogue.
+ *   z = x W^T + bias,  y = act(z) + residual
+ * x: n_tokens x d_in (leading dim ldx), W: d_out x d_in (leading dim ldw), residual and y:
+ * n_tokens x d_out (leading dims ldr, ldy), all dtype `dt`; bias: float[d_out] or NULL;
+ * residual may be NULL, and may be y itself.  A rank-r layer is two calls, the first with
+ * Right (r x d_in), the second with Left (d_out x r).
+ * The pre-activation z that the backward pass needs is kept on request: z (n_tokens x d_out,
+ * dtype `dt`, leading dim ldz), or zcodes and zexps, its 8-bit checkpoint taken from the
+ * fp32 z (`info` as in lrc_pack_activations); at most one of the two, NULL otherwise.
+ * bf16: products exact, sums fp32.  fp32: products and sums to fp32 accuracy.  The order of
+ * every sum depends on the sizes only, so equal inputs give equal bits.
+ * 1 <= d_in, d_out <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out, int64_t ldx,
+                      const void* W, int64_t ldw, const float* bias, lrc_act act, const void* residual,
+                      int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz, int8_t* zcodes, int8_t* zexps,
+                      int32_t* info, void* ws, size_t ws_bytes, void* stream);
+size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out);
+
+/*
+ * lrc_linear_backward -- gradients of lrc_linear from kept activations.
+ *   dz = dy * act'(z),  dx = dz W,  dW = dz^T x,  db = sum_t dz
+ * dz is the output-gradient stream B that lrc_accumulate_cov and lrc_score_components take
+ * (the residual's gradient is dy itself).  dy: n_tokens x d_out (leading dim lddy), W as in
+ * lrc_linear.  The input is x (leading dim ldx), or, with x NULL, its checkpoint xcodes and
+ * xexps (needed for dW only).  With an activation other than LRC_ACT_NONE, z (leading dim
+ * ldz) or, with z NULL, zcodes and zexps are needed, and dz (n_tokens x d_out, dtype `dt`,
+ * leading dim lddz) is written; with LRC_ACT_NONE dz is dy and the argument is ignored.
+ * relu'(0) = 0.  dx: n_tokens x d_in (leading dim lddx); dW: d_out x d_in (leading dim
+ * lddw), dtype dw_dt (LRC_F32, or `dt`); db: float[d_out]; any of the three may be NULL.
+ * With dtype bf16, dx and dW are products of the rounded dz, as the stream holds it; db sums
+ * the unrounded one.  Sums fp32 in an order that depends on the sizes only.
+ * n_tokens == 0 writes zeros to dW and db.  Sizes as lrc_linear.
+ */
+lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,
+                               int64_t lddy, const void* W, int64_t ldw, const void* x, int64_t ldx,
+                               const int8_t* xcodes, const int8_t* xexps, lrc_act act, const void* z, int64_t ldz,
+                               const int8_t* zcodes, const int8_t* zexps, void* dz, int64_t lddz, void* dx,
+                               int64_t lddx, void* dW, lrc_dtype dw_dt, int64_t lddw, float* db, void* ws,
+                               size_t ws_bytes, void* stream);
+size_t lrc_linear_backward_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out);
 
 /*
  * Measurement support (benchmarks and profilers; not needed for results).
