@@ -16,60 +16,13 @@ namespace {
 
 constexpr int LT = 256;
 
-enum OperandKind { K_ROWS, K_COLS, K_CODES };
-
 struct Operand {
-  const void* p;        // elements, or int8 codes
+  const void* p;        // elements, or int8 codes (leading dim ld)
   int64_t ld;
   const int8_t* exps;   // K_CODES: block exponents, nb per row
   int64_t nb;
   bool vec;             // 16-byte (codes: 8-byte) pieces allowed
 };
-
-// What happens to a finished row piece of D.
-struct Epilogue {
-  const float* bias = nullptr;
-  int act = LRC_ACT_NONE;
-  const void* res = nullptr;
-  int64_t ldr = 0;
-  void* y = nullptr;
-  int64_t ldy = 0;
-  void* z = nullptr;
-  int64_t ldz = 0;
-  int8_t* codes = nullptr;
-  int8_t* exps = nullptr;
-  int64_t nb = 0;
-  int32_t* info = nullptr;
-  bool vec_y = false, vec_r = false, vec_z = false, vec_c = false;
-};
-
-// Eight consecutive columns of one row.  Lanes 8 i .. 8 i + 7 of a wave hold the 64 columns
-// of one block of the row and call this together; `cnt` of the lane's columns exist.
-template <class TO>
-__device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t col, int cnt, float (&v)[8], int lane,
-                                        bool& bad) {
-  if (ep.bias != nullptr) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += e < cnt ? ep.bias[col + e] : 0.f;
-  }
-  if (ep.z != nullptr && cnt > 0) st8(static_cast<TO*>(ep.z) + row * ep.ldz + col, ep.vec_z, cnt, v);
-  if (ep.codes != nullptr) {
-    const int64_t n = ep.nb;
-    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * n + (col >> 6), ep.vec_c, cnt, v, lane, bad);
-  }
-  if (cnt <= 0) return;
-  if (ep.act != LRC_ACT_NONE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = act_value(ep.act, v[e]);
-  }
-  if (ep.res != nullptr) {
-    float r[8];
-    ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, ep.vec_r, cnt, r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += r[e];
-  }
-  st8(static_cast<TO*>(ep.y) + row * ep.ldy + col, ep.vec_y, cnt, v);
-}
 
 // ---- any size, stride and alignment: 64 x 64 tiles, four waves of 32 x 32 ---------------
 constexpr int GT = 64;    // tile edge
@@ -140,7 +93,8 @@ __device__ __forceinline__ void mma_any(const float* a, const float* b, int lane
 
 template <class T, class TO, int KA, int KB>
 __global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
-                                                        int64_t tiles_n, Epilogue ep) {
+                                                        int64_t tiles_n, Epilogue ep, const int32_t* __restrict__ only) {
+  if (only != nullptr && *only == 0) return;
   constexpr int P = GTile<T>::PITCH;
   constexpr int EP = GT + 4;   // epilogue tile pitch
   __shared__ __attribute__((aligned(16))) uint8_t lds[GT * EP * 4 > 2 * GT * P * int(sizeof(T))
@@ -230,13 +184,130 @@ bool sizes_ok(int64_t n, int64_t i, int64_t o) {
 }
 bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
 
+// ---- operands for the matrix cores ------------------------------------------------------
+// An operand the bf16 product cannot read where it lies is first written to the workspace as
+// rows of `planes` pieces of w8 = 8 ceil(cols / 8) bf16 (zeros behind the columns):
+//   bf16 whose rows are not whole 16-byte pieces, and checkpoints (exact in bf16): one piece;
+//   fp32: three pieces with x = h + m + l exactly (8 + 8 + 8 significant bits).  A product of
+//   two such operands is h h + h m + m h + h l + m m + l h, the terms left out are below
+//   2^-24 of it: six bf16 products give fp32 accuracy at more than the fp32 matrix rate.  An
+//   entry that is not finite raises `flag`; the product is then done on fp32 tiles instead.
+template <class T>
+__device__ __forceinline__ void split_store(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag);
+template <>
+__device__ __forceinline__ void split_store<uint16_t>(uint16_t* o, int64_t, float (&v)[8], int32_t*) {
+  st8(o, true, 8, v);
+}
+template <>
+__device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag) {
+  float h[8], m[8];
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    bad |= !finite_f(v[e]);
+    h[e] = round_to(v[e], static_cast<const uint16_t*>(nullptr));
+    if (!finite_f(h[e])) h[e] = __uint_as_float(__float_as_uint(v[e]) & 0xffff0000u);   // rounded past the largest
+    const float r = v[e] - h[e];
+    m[e] = round_to(r, static_cast<const uint16_t*>(nullptr));
+    v[e] = r - m[e];
+  }
+  st8(o, true, 8, h);
+  st8(o + w8, true, 8, m);
+  st8(o + 2 * w8, true, 8, v);
+  if (bad) *flag = 1;
+}
+template <class T, bool CODES>
+__global__ __launch_bounds__(LT) void operand_kernel(const void* __restrict__ p, int64_t ld,
+                                                     const int8_t* __restrict__ exps, int64_t nb, bool vec,
+                                                     int64_t rows, int64_t cols, int64_t w8, int planes,
+                                                     uint16_t* __restrict__ out, int32_t* __restrict__ flag) {
+  const int64_t i = int64_t(blockIdx.x) * LT + threadIdx.x, per = w8 / 8;
+  if (i >= rows * per) return;
+  const int64_t r = i / per, c = i % per * 8;
+  const int cnt = int(cols - c > 8 ? 8 : cols - c);
+  float v[8];
+  uint16_t* o = out + r * planes * w8 + c;
+  if (CODES) {
+    ld8_codes(static_cast<const int8_t*>(p) + r * ld + c, vec, cnt, pow2f(exps[r * nb + (c >> 6)]), v);
+    split_store<uint16_t>(o, w8, v, flag);
+  } else {
+    ld8(static_cast<const T*>(p) + r * ld + c, vec, cnt, v);
+    split_store<T>(o, w8, v, flag);
+  }
+}
+__global__ void clear_flag_kernel(int32_t* flag) { *flag = 0; }
+
+int64_t round8(int64_t v) { return (v + 7) & ~int64_t(7); }
+
+// Room in the workspace for one such operand, in bf16.
+template <class T>
+size_t operand_room(int64_t rows, int64_t cols) {
+  return size_t(rows) * (sizeof(T) == 4 ? 3 : 1) * round8(cols);
+}
+
+struct Prepared {
+  GemmOperand op;
+  int planes;
+};
+
+template <class T>
+lrc_status prepare_operand(hipStream_t st, const Operand& o, bool codes, int64_t rows, int64_t cols, uint16_t* room,
+                           int32_t* flag, Prepared& out) {
+  if (sizeof(T) == 2 && !codes && o.vec && cols % 8 == 0) {   // read in place
+    out = {{static_cast<const uint16_t*>(o.p), o.ld, 0}, 1};
+    return LRC_OK;
+  }
+  const int64_t w8 = round8(cols), grid = cdiv(rows * (w8 / 8), LT);
+  const int planes = sizeof(T) == 4 && !codes ? 3 : 1;
+  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  ProfScope scope("linear_operand_kernel", st, 0.0,
+                  double(rows) * double(cols) * ((codes ? 1.0 : double(sizeof(T))) + 2.0 * planes));
+  if (codes)
+    operand_kernel<T, true><<<unsigned(grid), LT, 0, st>>>(o.p, o.ld, o.exps, o.nb, o.vec, rows, cols, w8, planes,
+                                                           room, flag);
+  else
+    operand_kernel<T, false><<<unsigned(grid), LT, 0, st>>>(o.p, o.ld, nullptr, 0, o.vec, rows, cols, w8, planes, room,
+                                                            flag);
+  LRC_LAUNCHED();
+  out = {{room, planes * w8, w8}, planes};
+  return LRC_OK;
+}
+
+// segments of a product of operands with so many planes (h, m, l), smallest terms first
+GemmSegments segments(int pa, int pb) {
+  GemmSegments s;
+  auto add = [&](int i, uint32_t a, uint32_t b) {
+    s.pa |= a << (2 * i);
+    s.pb |= b << (2 * i);
+    s.count = i + 1;
+  };
+  if (pa == 3 && pb == 3) {
+    add(0, 2, 0), add(1, 0, 2), add(2, 1, 1), add(3, 1, 0), add(4, 0, 1), add(5, 0, 0);
+  } else if (pa == 3) {
+    add(0, 2, 0), add(1, 1, 0), add(2, 0, 0);
+  } else if (pb == 3) {
+    add(0, 0, 2), add(1, 0, 1), add(2, 0, 0);
+  }
+  return s;
+}
+
+// Whether a product goes to the matrix-core path for large tiles.  Below this much work the
+// passes that prepare its operands cost more than they save.
+bool large_product(int64_t M, int64_t N, int64_t K) {
+  return double(M) * double(N) * double(K) >= double(1 << 24);
+}
+template <class T>
+bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two operands
+  return std::max(round8(rows_a), round8(rows_b)) * (sizeof(T) == 4 ? 3 : 1) <= GEMM_MAX_LD;
+}
+
 template <class T, class TO, int KA, int KB>
-lrc_status product(hipStream_t st, const char* name, const Operand& A, const Operand& B, int64_t M, int64_t N,
-                   int64_t K, const Epilogue& ep, double bytes) {
+lrc_status product_any(hipStream_t st, const char* name, const Operand& A, const Operand& B, int64_t M, int64_t N,
+                       int64_t K, const Epilogue& ep, const int32_t* only, double bytes) {
   const int64_t tn = cdiv(N, GT), grid = cdiv(M, GT) * tn;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-  ProfScope scope(name, st, 2.0 * double(M) * double(N) * double(K), bytes);
-  linear_any_kernel<T, TO, KA, KB><<<unsigned(grid), LT, 0, st>>>(A, B, M, N, K, tn, ep);
+  ProfScope scope(name, st, only ? 0.0 : 2.0 * double(M) * double(N) * double(K), only ? 0.0 : bytes);
+  linear_any_kernel<T, TO, KA, KB><<<unsigned(grid), LT, 0, st>>>(A, B, M, N, K, tn, ep, only);
   LRC_LAUNCHED();
   return LRC_OK;
 }
@@ -252,10 +323,55 @@ void set_out(Epilogue& ep, void* y, int64_t ldy) {
   ep.vec_y = rows_vec16(y, ldy, sizeof(T));
 }
 
+// Workspace of the three products.
+struct LinearRoom {
+  int32_t* flag = nullptr;      // an fp32 operand holds an entry that is not finite
+  float* partial = nullptr;     // split products
+  float* sums = nullptr;        // db chunks
+  uint16_t *a = nullptr, *b = nullptr;   // operands
+  size_t bytes = 0;
+};
+template <class T>
+LinearRoom forward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
+  LinearRoom r;
+  Carve cv(ws);
+  if (large_product(n, dn, di) && gemm_fits<T>(di, di)) {
+    r.flag = cv.take<int32_t>(1);
+    r.partial = cv.take<float>(gemm_bf16_workspace(n, dn, di) / 4);
+    if (sizeof(T) == 4 || di % 8 != 0) {
+      r.a = cv.take<uint16_t>(operand_room<T>(n, di));
+      r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
+    }
+  }
+  r.bytes = cv.bytes();
+  return r;
+}
+template <class T>
+LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
+  LinearRoom r;
+  Carve cv(ws);
+  r.sums = cv.take<float>(size_t(col_plan(n).chunks) * dn);
+  if (large_product(n, dn, di) && gemm_fits<T>(di, dn)) {
+    r.flag = cv.take<int32_t>(1);
+    r.partial = cv.take<float>(std::max(gemm_bf16_workspace(n, di, dn), gemm_bf16_workspace(dn, di, n)) / 4);
+    if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
+    // W for dx, then x (a checkpoint becomes one bf16 piece) for dW
+    r.b = cv.take<uint16_t>(sizeof(T) == 4 || di % 8 != 0 ? operand_room<T>(std::max(n, dn), di)
+                                                          : operand_room<T>(n, di));
+  }
+  r.bytes = cv.bytes();
+  return r;
+}
+// whether an operand is read in place or has its room
+template <class T>
+bool has_room(const Operand& o, int64_t cols) {
+  return sizeof(T) == 4 || cols % 8 != 0 || o.vec;
+}
+
 template <class T>
 lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, int64_t dn, int64_t ldx, const void* W,
                           int64_t ldw, const float* bias, int act, const void* res, int64_t ldr, void* y, int64_t ldy,
-                          void* z, int64_t ldz, int8_t* zcodes, int8_t* zexps, int32_t* info) {
+                          void* z, int64_t ldz, int8_t* zcodes, int8_t* zexps, int32_t* info, void* ws) {
   Epilogue ep;
   ep.bias = bias;
   ep.act = act;
@@ -272,7 +388,23 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
   ep.vec_c = dn % 8 == 0 && (reinterpret_cast<uintptr_t>(zcodes) & 7) == 0;
   ep.info = info;
   const double bytes = double(sizeof(T)) * (double(n) * di + double(dn) * di + double(n) * dn * (res ? 2 : 1));
-  return product<T, T, K_ROWS, K_ROWS>(st, "linear_kernel", plain<T>(x, ldx), plain<T>(W, ldw), n, dn, di, ep, bytes);
+  const Operand ox = plain<T>(x, ldx), ow = plain<T>(W, ldw);
+  const LinearRoom room = forward_room<T>(ws, n, di, dn);
+  if (room.flag == nullptr || !has_room<T>(ox, di) || !has_room<T>(ow, di) || std::max(ldx, ldw) > GEMM_MAX_LD)
+    return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, nullptr, bytes);
+  const int32_t* flag = sizeof(T) == 4 ? room.flag : nullptr;
+  if (flag) {
+    clear_flag_kernel<<<1, 1, 0, st>>>(room.flag);
+    LRC_LAUNCHED();
+  }
+  Prepared a, b;
+  LRC_TRY(prepare_operand<T>(st, ox, false, n, di, room.a, room.flag, a));
+  LRC_TRY(prepare_operand<T>(st, ow, false, dn, di, room.b, room.flag, b));
+  LRC_TRY((gemm_bf16<T, K_ROWS, K_ROWS>(st, "linear_kernel", a.op, b.op, n, dn, di,
+                                        segments(a.planes, b.planes), ep, room.partial, flag,
+                                        2.0 * double(n) * double(dn) * double(di), bytes)));
+  if (!flag) return LRC_OK;
+  return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, flag, bytes);
 }
 
 }  // namespace
@@ -281,9 +413,9 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
 using namespace lrc;
 
 extern "C" size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out) {
-  (void)dt;
   if (!sizes_ok(n_tokens, d_in, d_out)) return 0;
-  return 0;
+  return dt == LRC_BF16 ? forward_room<uint16_t>(nullptr, n_tokens, d_in, d_out).bytes
+                        : forward_room<float>(nullptr, n_tokens, d_in, d_out).bytes;
 }
 
 extern "C" lrc_status lrc_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,
@@ -302,17 +434,15 @@ extern "C" lrc_status lrc_linear(const void* x, lrc_dtype dt, int64_t n_tokens, 
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (dt == LRC_BF16)
     return linear_forward<uint16_t>(st, x, n_tokens, d_in, d_out, ldx, W, ldw, bias, act, residual, ldr, y, ldy, z,
-                                    ldz, zcodes, zexps, info);
+                                    ldz, zcodes, zexps, info, ws);
   return linear_forward<float>(st, x, n_tokens, d_in, d_out, ldx, W, ldw, bias, act, residual, ldr, y, ldy, z, ldz,
-                               zcodes, zexps, info);
+                               zcodes, zexps, info, ws);
 }
 
 extern "C" size_t lrc_linear_backward_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out) {
-  (void)dt;
   if (!sizes_ok(n_tokens, d_in, d_out)) return 0;
-  Carve cv(nullptr);
-  cv.take<float>(size_t(col_plan(n_tokens).chunks) * d_out);
-  return cv.bytes();
+  return dt == LRC_BF16 ? backward_room<uint16_t>(nullptr, n_tokens, d_in, d_out).bytes
+                        : backward_room<float>(nullptr, n_tokens, d_in, d_out).bytes;
 }
 
 namespace lrc {
@@ -341,7 +471,8 @@ struct BackArgs {
 };
 
 template <class T>
-lrc_status linear_back(hipStream_t st, const BackArgs& a, float* partial) {
+lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
+  const LinearRoom room = backward_room<T>(ws, a.n, a.di, a.dn);
   const int64_t n = a.n, di = a.di, dn = a.dn;
   const void* g = a.dy;
   int64_t ldg = a.lddy;
@@ -350,7 +481,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, float* partial) {
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
       const dim3 grid(unsigned(cdiv(dn, LT)), unsigned(p.chunks));
-      float* part = a.db != nullptr ? partial : nullptr;
+      float* part = a.db != nullptr ? room.sums : nullptr;
       const T *dy = static_cast<const T*>(a.dy), *z = static_cast<const T*>(a.z);
       T* dz = static_cast<T*>(a.dz);
       if (a.z == nullptr && a.act != LRC_ACT_NONE)
@@ -361,31 +492,61 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, float* partial) {
                                                  p.rows, part);
       LRC_LAUNCHED();
     }
-    if (a.db != nullptr) LRC_TRY(reduce_partials(st, partial, p.chunks, dn, dn, a.db));
+    if (a.db != nullptr) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db));
     if (a.act != LRC_ACT_NONE) {
       g = a.dz;
       ldg = a.lddz;
     }
   }
+  if (a.dx == nullptr && a.dW == nullptr) return LRC_OK;
   const double e = sizeof(T);
+  const Operand og = plain<T>(g, ldg), ow = plain<T>(a.W, a.ldw);
+  const bool held = a.x == nullptr;
+  const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB),
+                                    di % 8 == 0 && (reinterpret_cast<uintptr_t>(a.xcodes) & 7) == 0}
+                          : plain<T>(a.x, a.ldx);
+  const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
+  const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD;
+  const bool fast_dw = fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD));
+  const int32_t* flag = sizeof(T) == 4 && (fast_dx || fast_dw) ? room.flag : nullptr;
+  Prepared pg, pw;
+  if (flag) {
+    clear_flag_kernel<<<1, 1, 0, st>>>(room.flag);
+    LRC_LAUNCHED();
+  }
+  if (fast_dx || fast_dw) LRC_TRY(prepare_operand<T>(st, og, false, n, dn, room.a, room.flag, pg));
   if (a.dx != nullptr) {
     Epilogue ep;
     set_out<T>(ep, a.dx, a.lddx);
-    LRC_TRY((product<T, T, K_ROWS, K_COLS>(st, "linear_dx_kernel", plain<T>(g, ldg), plain<T>(a.W, a.ldw), n, di, dn,
-                                           ep, e * (double(n) * dn + double(dn) * di + double(n) * di))));
+    const double bytes = e * (double(n) * dn + double(dn) * di + double(n) * di);
+    if (fast_dx) {
+      LRC_TRY(prepare_operand<T>(st, ow, false, dn, di, room.b, room.flag, pw));
+      LRC_TRY((gemm_bf16<T, K_ROWS, K_COLS>(st, "linear_dx_kernel", pg.op, pw.op, n, di, dn,
+                                            segments(pg.planes, pw.planes), ep, room.partial, flag,
+                                            2.0 * double(n) * double(dn) * double(di), bytes)));
+    }
+    if (!fast_dx || flag)
+      LRC_TRY((product_any<T, T, K_ROWS, K_COLS>(st, "linear_dx_any_kernel", og, ow, n, di, dn, ep,
+                                                 fast_dx ? flag : nullptr, bytes)));
   }
   if (a.dW == nullptr) return LRC_OK;
-  Epilogue ep;
-  const Operand ga = plain<T>(g, ldg);
-  const double bytes = e * (double(n) * dn + double(dn) * di) + double(n) * di * (a.x ? e : 1.0);
+  const double bytes = e * (double(n) * dn + double(dn) * di) + double(n) * di * (held ? 1.0 : e);
   auto go = [&](auto tag) -> lrc_status {
     using TO = decltype(tag);
+    Epilogue ep;
     set_out<TO>(ep, a.dW, a.lddw);
-    if (a.x != nullptr)
-      return product<T, TO, K_COLS, K_COLS>(st, "linear_dw_kernel", ga, plain<T>(a.x, a.ldx), dn, di, n, ep, bytes);
-    const Operand q = {a.xcodes, di, a.xexps, cdiv(di, CKB),
-                       di % 8 == 0 && (reinterpret_cast<uintptr_t>(a.xcodes) & 7) == 0};
-    return product<T, TO, K_COLS, K_CODES>(st, "linear_dw_kernel", ga, q, dn, di, n, ep, bytes);
+    if (fast_dw) {
+      Prepared px;
+      LRC_TRY(prepare_operand<T>(st, ox, held, n, di, room.b, room.flag, px));
+      LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n,
+                                             segments(pg.planes, px.planes), ep, room.partial, flag,
+                                             2.0 * double(n) * double(dn) * double(di), bytes)));
+      if (!flag) return LRC_OK;
+    }
+    const int32_t* only = fast_dw ? flag : nullptr;
+    if (held)
+      return product_any<T, TO, K_COLS, K_CODES>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, only, bytes);
+    return product_any<T, TO, K_COLS, K_COLS>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, only, bytes);
   };
   if (a.dw_dt == LRC_F32) return go(float{});
   return go(uint16_t{});
@@ -426,6 +587,5 @@ extern "C" lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t 
   }
   const BackArgs a = {n_tokens, d_in, d_out, dy,  lddy,  W,     ldw, x,    ldx, xcodes, xexps, act,
                       z,        ldz,  zcodes, zexps, dz, lddz, dx,  lddx, dW,  int(dw_dt), lddw, db};
-  float* partial = static_cast<float*>(ws);
-  return dt == LRC_BF16 ? linear_back<uint16_t>(st, a, partial) : linear_back<float>(st, a, partial);
+  return dt == LRC_BF16 ? linear_back<uint16_t>(st, a, ws) : linear_back<float>(st, a, ws);
 }

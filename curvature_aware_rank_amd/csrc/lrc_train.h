@@ -169,6 +169,79 @@ __device__ __forceinline__ float act_slope(int act, float z) {
   return 1.f;
 }
 
+// ---- products of the linear layer: D[m][n] = sum_k A(m, k) B(n, k) ----------------------
+// An operand is a row-major matrix whose rows run along k (K_ROWS) or whose rows are the k
+// steps (K_COLS), or a checkpoint of the latter kind (K_CODES).
+enum OperandKind { K_ROWS, K_COLS, K_CODES };
+
+// What happens to a finished row piece of D.
+struct Epilogue {
+  const float* bias = nullptr;
+  int act = LRC_ACT_NONE;
+  const void* res = nullptr;
+  int64_t ldr = 0;
+  void* y = nullptr;
+  int64_t ldy = 0;
+  void* z = nullptr;
+  int64_t ldz = 0;
+  int8_t* codes = nullptr;
+  int8_t* exps = nullptr;
+  int64_t nb = 0;
+  int32_t* info = nullptr;
+  bool vec_y = false, vec_r = false, vec_z = false, vec_c = false;
+};
+
+// Eight consecutive columns of one row.  Lanes 8 i .. 8 i + 7 of a wave hold the 64 columns
+// of one block of the row and call this together; `cnt` of the lane's columns exist.
+template <class TO>
+__device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t col, int cnt, float (&v)[8], int lane,
+                                        bool& bad) {
+  if (ep.bias != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += e < cnt ? ep.bias[col + e] : 0.f;
+  }
+  if (ep.z != nullptr && cnt > 0) st8(static_cast<TO*>(ep.z) + row * ep.ldz + col, ep.vec_z, cnt, v);
+  if (ep.codes != nullptr) {
+    const int64_t n = ep.nb;
+    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * n + (col >> 6), ep.vec_c, cnt, v, lane, bad);
+  }
+  if (cnt <= 0) return;
+  if (ep.act != LRC_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value(ep.act, v[e]);
+  }
+  if (ep.res != nullptr) {
+    float r[8];
+    ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, ep.vec_r, cnt, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += r[e];
+  }
+  st8(static_cast<TO*>(ep.y) + row * ep.ldy + col, ep.vec_y, cnt, v);
+}
+
+// bf16 operands with 16-byte rows on the matrix cores (lrc_gemm.hip).
+struct GemmOperand {
+  const uint16_t* p;   // 16-byte aligned
+  int64_t ld;          // elements, a multiple of 8
+  int64_t plane;       // elements between the planes of a split fp32 operand
+};
+// The reduction may run over several pairs of planes, one after the other: segment s
+// multiplies plane (pa >> 2 s) & 3 of A with plane (pb >> 2 s) & 3 of B.
+struct GemmSegments {
+  int count = 1;
+  uint32_t pa = 0, pb = 0;
+};
+constexpr int64_t GEMM_MAX_LD = int64_t(1) << 21;   // tile offsets stay below 2^31 bytes
+// The rows of a K_ROWS operand are whole 16-byte pieces, zeros behind K where K is not a
+// multiple of 8; the other extent of a K_COLS operand is a multiple of 8 or padded likewise.
+// TO: type of the epilogue's matrices.  `partial`: workspace of gemm_bf16_workspace bytes.
+// `skip`: NULL, or a device word that makes the product a no-op when it is not zero.
+template <class TO, int KA, int KB>
+lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperand B, int64_t M, int64_t N, int64_t K,
+                     const GemmSegments& seg, const Epilogue& ep, float* partial, const int32_t* skip, double flops,
+                     double bytes);
+size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K);
+
 // ---- column sums ---------------------------------------------------------------------
 // out[c] = sum over p < parts of partial[p * stride + c], in the order of p.
 lrc_status reduce_partials(hipStream_t st, const float* partial, int64_t parts, int64_t stride, int64_t cols,

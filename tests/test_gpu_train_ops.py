@@ -296,6 +296,62 @@ def test_linear_exact_on_small_integers(lrc, dtype, n, d_in, d_out):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d_in,d_out", [(4096, 160, 4104), (3900, 2100, 2500), (5001, 1500, 5011)])
+def test_linear_large_tiles_exact(lrc, dtype, n, d_in, d_out):
+    """As the tests on small integers, at sizes that fill the chip with large tiles; ragged ones among them."""
+    g = torch.Generator().manual_seed(n)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).to(dtype).to(dev())   # noqa: E731
+    x, w, dy = ints(n, d_in), ints(d_out, d_in), ints(n, d_out)
+    b = torch.randint(-9, 10, (d_out,), generator=g).float().to(dev())
+    y, kept, _ = lrc.lrc_linear(x, w, b, act="relu", residual=dy, save="checkpoint")
+    z = x.double() @ w.double().T + b.double()
+    codes, exps, _ = lrc.lrc_pack_activations(z.float())
+    assert torch.equal(y, (z.clamp_min(0) + dy.double()).to(dtype))
+    assert torch.equal(kept[0], codes) and torch.equal(kept[1], exps)
+    for held in (False, True):
+        xa = lrc.lrc_pack_activations(x)[:2] if held else x
+        _, dx, dw, db = lrc.lrc_linear_backward(dy, xa, w, dw_dtype=torch.float32)
+        assert torch.equal(dx, (dy.double() @ w.double()).to(dtype))
+        assert torch.equal(dw.double(), dy.double().T.contiguous() @ x.double())
+        assert torch.equal(db.double(), dy.double().sum(0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 3000, 600), (70, 1024, 1500), (1100, 1100, 1100)])
+def test_linear_accuracy_at_long_sums(lrc, dtype, n, d_in, d_out):
+    """Against fp64 within the norm-wise accuracy of fp32 sums: with random signs the error of a K-term fp32 sum is
+    about sqrt(K) u of the terms' root mean square, i.e. about u sqrt(K) / sqrt(K) = u of the result per add; 24 u
+    of the 2-norm leaves room for the adds inside a matrix instruction and a biased rounding.  bf16 results add
+    2^-8 / sqrt(3)."""
+    g = torch.Generator().manual_seed(d_in)
+    x, dy = stream(n, d_in, dtype, 1).to(dev()), stream(n, d_out, dtype, 2).to(dev())
+    w = (torch.randn(d_out, d_in, generator=g) / math.sqrt(d_in)).to(dtype).to(dev())
+    bound = 24 * U + (2.0 ** -8 / math.sqrt(3) if dtype == torch.bfloat16 else 0)
+    off = lambda got, want: float((got.double() - want).norm() / want.norm())   # noqa: E731
+    assert off(lrc.lrc_linear(x, w)[0], x.double() @ w.double().T) < bound
+    _, dx, dw, _ = lrc.lrc_linear_backward(dy, x, w, dw_dtype=torch.float32)
+    assert off(dx, dy.double() @ w.double()) < bound
+    assert off(dw, dy.double().T.contiguous() @ x.double()) < 24 * U
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("where", ["x", "w", "dy"])
+def test_nonfinite_entries_in_a_large_product(lrc, dtype, where):
+    """Infinities and NaN at sizes that go to the large tiles: what the plain products give."""
+    n, d_in, d_out = 520, 264, 392
+    ones = lambda *s: torch.ones(*s, dtype=dtype)   # noqa: E731
+    t = {"x": ones(n, d_in), "w": ones(d_out, d_in), "dy": ones(n, d_out)}
+    t[where][3, 5], t[where][40, 77], t[where][41, 77] = float("inf"), float("-inf"), float("nan")
+    x, w, dy = (t[k].to(dev()) for k in ("x", "w", "dy"))
+    res = ones(n, d_out).to(dev())
+    same = lambda p, q: torch.equal(torch.nan_to_num(p.double(), 9e9, 8e8, 7e7),   # noqa: E731
+                                    torch.nan_to_num(q.to(p.dtype).double(), 9e9, 8e8, 7e7))
+    assert same(lrc.lrc_linear(x, w, residual=res)[0], x.double() @ w.double().T + 1)
+    _, dx, dw, _ = lrc.lrc_linear_backward(dy, x, w)
+    assert same(dx, dy.double() @ w.double()) and same(dw, dy.double().T.contiguous() @ x.double())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n,d_in,d_out", LINEAR_SHAPES)
 @pytest.mark.parametrize("held", [False, True])
 def test_linear_backward(lrc, dtype, n, d_in, d_out, held):
