@@ -15,6 +15,7 @@
 #include "lrc_train.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace lrc {
 namespace gemm {
@@ -46,7 +47,7 @@ struct Stager {
   int64_t ld, plane;
   unsigned voff[LOADS];
   int kk[LOADS];          // K_ROWS: first k of the lane's granule within the stage
-  int extent;             // bytes behind base a K_ROWS row tile or a K_COLS k step's rows may reach
+  int rows_rec;           // K_ROWS: bytes to the start of the tile's last row; K_COLS: bytes of a k step
 
   __device__ void init(const GemmOperand& o, int64_t row0, int64_t rows, int wave, int lane) {
     ld = o.ld;
@@ -61,7 +62,7 @@ struct Stager {
         kk[j] = 8 * g;
         voff[j] = r < left ? unsigned(r * ld * 2) + 16 * g : OOB;
       }
-      extent = left;
+      rows_rec = int((left - 1) * ld * 2);
     } else {
       base = o.p + row0;
       constexpr int LPR = EDGE / 8;        // lanes (16-byte granules) per k step
@@ -69,37 +70,35 @@ struct Stager {
       for (int j = 0; j < LOADS; ++j) {
         const int t = (64 / LPR) * (LOADS * wave + j) + lane / LPR;
         const int g = (lane % LPR) ^ (4 * (t & 3));
-        kk[j] = t;
+        kk[j] = 0;
         voff[j] = 8 * g < left ? unsigned(t * ld * 2) + 16 * g : OOB;
       }
-      extent = (left + 7) & ~7;
+      rows_rec = 2 * ((left + 7) & ~7);
     }
   }
 
-  // stage of k steps [k, k + 32) of plane `pl`, of which those below k_end exist
-  __device__ void issue(uint8_t* dst, int wave, int pl, int64_t k, int64_t k_end) const {
-    const int64_t left = k_end - k;
-    const int kl = int(left < 0 ? 0 : left > KS ? KS : left);
-    if (KIND == K_ROWS) {
-      const uint16_t* p = base + pl * plane + k;
-      // rows are whole granules (zeros behind k_end where k_end is not)
-      const int nrec = kl > 0 ? int(((extent - 1) * ld + ((kl + 7) & ~7)) * 2) : 0;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          uniform_ptr(p), 0, __builtin_amdgcn_readfirstlane(nrec), 0x00020000);
+  // The loads of one stage: k steps [k, k + 32) of plane `pl`, of which `left` or all 32 exist.
+  struct Stage {
+    __amdgpu_buffer_rsrc_t r;
+    unsigned v[LOADS];
+  };
+  __device__ __forceinline__ Stage stage(int pl, int k, int left) const {
+    const int kl = max(0, min(left, KS));
+    // K_ROWS: rows are whole granules (zeros behind the last k where that is not one)
+    const int rec = KIND == K_ROWS ? rows_rec + 2 * ((kl + 7) & ~7) : (kl - 1) * int(ld) * 2 + rows_rec;
+    const uint16_t* p = base + pl * plane + (KIND == K_ROWS ? k : k * ld);
+    Stage s;
+    s.r = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(p), 0, __builtin_amdgcn_readfirstlane(kl > 0 ? rec : 0),
+                                            0x00020000);
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(dst + (LOADS * wave + j) * 1024), 16,
-                                                 kk[j] < kl ? voff[j] : OOB, 0, 0, 0);
-    } else {
-      const uint16_t* p = base + pl * plane + k * ld;
-      const int nrec = kl > 0 ? int(((kl - 1) * ld + extent) * 2) : 0;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          uniform_ptr(p), 0, __builtin_amdgcn_readfirstlane(nrec), 0x00020000);
+    for (int j = 0; j < LOADS; ++j) s.v[j] = KIND == K_ROWS && kk[j] >= kl ? OOB : voff[j];
+    return s;
+  }
+  static __device__ __forceinline__ void issue(const Stage& s, uint8_t* dst, int wave) {
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(dst + (LOADS * wave + j) * 1024), 16, voff[j], 0, 0,
-                                                 0);
-    }
+    for (int j = 0; j < LOADS; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.r, (lds_void_t*)(dst + (LOADS * wave + j) * 1024), 16, s.v[j], 0, 0,
+                                               0);
   }
 
   // byte offset of the lane's fragment of tile rows row .. row + 31, k half 0
@@ -129,8 +128,8 @@ struct Stager {
 struct TileGrid {
   int64_t nm, nn, tiles;
   int per_xcd, splits;
-  int64_t steps_per_split;   // stages of one split
-  int64_t steps;             // stages of one segment
+  int steps_per_split;   // stages of one split
+  int steps;             // stages of one segment
 };
 
 // Tile of linear index i: groups of eight tile rows, column after column inside a group, so
@@ -142,7 +141,7 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
   tn = r / rows;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN>
+template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, bool SEG>
 __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N, int64_t K,
                                           const GemmSegments& seg, const TileGrid& tg, const Epilogue& ep,
                                           float* __restrict__ partial, const int32_t* __restrict__ skip) {
@@ -174,19 +173,30 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   sb.init(B, n0, N, wave, lane);
 
   // stages of this split, counted over all segments
-  const int64_t total = tg.steps * seg.count;
-  const int64_t first = int64_t(split) * tg.steps_per_split;
-  const int nsteps = int(min(tg.steps_per_split, total - first));
-  int sg = __builtin_amdgcn_readfirstlane(int(first / tg.steps));
-  int64_t k = (first - int64_t(sg) * tg.steps) * KS;   // next stage to issue
-  auto issue = [&](uint8_t* dst, bool live) {
-    sa.issue(dst, wave, int((seg.pa >> (2 * sg)) & 3), k, live ? K : 0);
-    sb.issue(dst + AB, wave, int((seg.pb >> (2 * sg)) & 3), k, live ? K : 0);
+  const int total = tg.steps * (SEG ? seg.count : 1);
+  const int first = split * tg.steps_per_split;
+  const int nsteps = min(tg.steps_per_split, total - first);
+  int sg = SEG ? first / tg.steps : 0;
+  int k = (first - sg * tg.steps) * KS;   // next stage to issue
+  const int kend = int(K);
+  typename SA::Stage ga;
+  typename SB::Stage gb;
+  // resources and offsets of the next stage, then (after the barrier that frees its buffer) its
+  // loads
+  auto next_stage = [&](bool live) {
+    const int left = live ? kend - k : 0;
+    ga = sa.stage(SEG ? int((seg.pa >> (2 * sg)) & 3) : 0, k, left);
+    gb = sb.stage(SEG ? int((seg.pb >> (2 * sg)) & 3) : 0, k, left);
     k += KS;
-    if (k >= K) {
-      k = 0;
-      ++sg;
+    if (SEG) {
+      const bool next = k >= kend;
+      sg += next ? 1 : 0;
+      k = next ? 0 : k;
     }
+  };
+  auto issue = [&](uint8_t* dst) {
+    SA::issue(ga, dst, wave);
+    SB::issue(gb, dst + AB, wave);
   };
 
   int offa[FM], offb[FN];
@@ -216,6 +226,23 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
       for (int j = 0; j < FN; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
   };
+  // Issue orders of the two halves of a step: the fragment reads (and the next stage's loads)
+  // go out between the products, which hide them.
+  constexpr int RD = (FM * (KA == K_ROWS ? 1 : 2) + FN * (KB == K_ROWS ? 1 : 2) + FM * FN - 1) / (FM * FN);
+  auto interleave_reads = [&]() {
+#define LRC_PAIR                                         \
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     \
+  __builtin_amdgcn_sched_group_barrier(0x100, RD, 0);
+    LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR
+    if constexpr (FM * FN == 8) { LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR }
+  };
+  auto interleave_loads = [&]() {
+#define LRC_TRIPLE LRC_PAIR __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE
+    if constexpr (FM * FN == 8) { LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR }
+#undef LRC_TRIPLE
+#undef LRC_PAIR
+  };
   auto buf = [&](int st) -> uint8_t* {
     const int q = st & 3;
     return q == 0 ? sb0 : q == 1 ? sb1 : q == 2 ? sb2 : sb3;
@@ -227,33 +254,43 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   // buffer takes stage s + 4; read the first half of stage s + 1, multiply the second half of
   // stage s.  Stages past the end are issued with empty resources (zeros, never multiplied), so
   // that the count of loads in flight stays the same to the end.
-  issue(sb0, nsteps > 0);
-  issue(sb1, nsteps > 1);
-  issue(sb2, nsteps > 2);
-  issue(sb3, nsteps > 3);
+  next_stage(nsteps > 0);
+  issue(sb0);
+  next_stage(nsteps > 1);
+  issue(sb1);
+  next_stage(nsteps > 2);
+  issue(sb2);
+  next_stage(nsteps > 3);
+  issue(sb3);
   LRC_WAIT_BARRIER(12);
   read_half(sb0, 0, fa0, fb0);
   int s = 0;
-#define LRC_STEP(CUR, NXT, LIVE)       \
+#define LRC_STEP(CUR, NXT)             \
+  next_stage(true);                    \
   read_half(CUR, 1, fa1, fb1);         \
   mma(fa0, fb0);                       \
-  LRC_WAIT_BARRIER(8);                 \
-  issue(CUR, LIVE);                    \
+  interleave_reads();                  \
   __builtin_amdgcn_sched_barrier(0);   \
+  LRC_WAIT_BARRIER(8);                 \
+  __builtin_amdgcn_sched_barrier(0);   \
+  issue(CUR);                          \
   read_half(NXT, 0, fa0, fb0);         \
-  mma(fa1, fb1);
+  mma(fa1, fb1);                       \
+  interleave_loads();                  \
+  __builtin_amdgcn_sched_barrier(0);
   for (; s + 7 < nsteps; s += 4) {
-    LRC_STEP(sb0, sb1, true)
-    LRC_STEP(sb1, sb2, true)
-    LRC_STEP(sb2, sb3, true)
-    LRC_STEP(sb3, sb0, true)
+    LRC_STEP(sb0, sb1)
+    LRC_STEP(sb1, sb2)
+    LRC_STEP(sb2, sb3)
+    LRC_STEP(sb3, sb0)
   }
 #undef LRC_STEP
   for (; s < nsteps; ++s) {
     read_half(buf(s), 1, fa1, fb1);
     mma(fa0, fb0);
     LRC_WAIT_BARRIER(8);
-    issue(buf(s), s + 4 < nsteps);
+    next_stage(s + 4 < nsteps);
+    issue(buf(s));
     read_half(buf(s + 1), 0, fa0, fb0);   // zeros behind the last stage
     mma(fa1, fb1);
   }
@@ -299,12 +336,12 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN>
+template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, bool SEG>
 __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_bf16_kernel(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                                     int64_t K, GemmSegments seg, TileGrid tg,
                                                                     Epilogue ep, float* __restrict__ partial,
                                                                     const int32_t* __restrict__ skip) {
-  gemm_tile<TO, KA, KB, WM, WN, FM, FN>(A, B, M, N, K, seg, tg, ep, partial, skip);
+  gemm_tile<TO, KA, KB, WM, WN, FM, FN, SEG>(A, B, M, N, K, seg, tg, ep, partial, skip);
 }
 
 // Sum of the splits' tiles in split order, then the epilogue.  One lane per eight columns, the
@@ -364,7 +401,7 @@ static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count) {
       if (c < cost * 0.999) {
         cost = c;
         best.big = big;
-        best.tg = {nm, nn, tiles, int(cdiv(tiles, NXCD)), int(s), per, steps};
+        best.tg = {nm, nn, tiles, int(cdiv(tiles, NXCD)), int(s), int(per), int(steps)};
       }
     }
   }
@@ -392,10 +429,20 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   const int64_t grid = int64_t(NXCD) * p.tg.per_xcd * p.tg.splits;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   ProfScope scope(name, st, flops, bytes);
-  if (p.big)
-    gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, p.tg, ep, partial, skip);
-  else
-    gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, p.tg, ep, partial, skip);
+  auto launch = [&](auto many) {
+    constexpr bool SEG = decltype(many)::value;
+    if (p.big)
+      gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, SEG><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, p.tg, ep,
+                                                                                   partial, skip);
+    else
+      gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, SEG><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, p.tg, ep,
+                                                                                   partial, skip);
+  };
+  // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
+  if (std::is_same<TO, uint16_t>::value || seg.count == 1)
+    launch(std::false_type{});
+  else if constexpr (!std::is_same<TO, uint16_t>::value)
+    launch(std::true_type{});
   LRC_LAUNCHED();
   if (p.tg.splits == 1) return LRC_OK;
   const int64_t np = (N + 7) & ~int64_t(7), blocks = cdiv(N, CKB), threads = M * blocks * 8;

@@ -138,13 +138,15 @@ __global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, in
 }
 
 // ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
-constexpr int DZ_ROWS = 64;   // tokens per chunk at least
+// Bound by memory: dy and z read, dz written once.  A lane takes eight consecutive channels,
+// the workgroup's four waves take the chunk's tokens in turn; db's share of the chunk is the
+// waves' sums added in order.
 struct ColPlan {
-  int64_t rows, chunks;
+  int64_t rows, chunks;   // tokens per chunk
 };
 ColPlan col_plan(int64_t n) {
   ColPlan p;
-  p.rows = std::max<int64_t>(DZ_ROWS, cdiv(n, 1024));
+  p.rows = std::max<int64_t>(n <= 4096 ? 8 : 32, cdiv(n, 1024));
   p.chunks = cdiv(n, p.rows);
   return p;
 }
@@ -154,21 +156,45 @@ __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_
                                                 const T* __restrict__ z, int64_t ldz,
                                                 const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
                                                 int64_t nb, int act, T* __restrict__ dz, int64_t lddz, int64_t rows,
-                                                float* __restrict__ partial) {
-  const int64_t j = int64_t(blockIdx.x) * LT + threadIdx.x;
-  if (j >= d) return;
+                                                bool vec, bool vec_z, float* __restrict__ partial) {
+  __shared__ float sums[3][64][9];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t(blockIdx.x) * 64 + lane) * 8;
+  const int64_t left = d - c;
+  const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
   const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
-  float s = 0.f;
-  for (int64_t t = t0; t < t1; ++t) {
-    float g = ld_elem(dy + t * lddy + j);
-    if (act != LRC_ACT_NONE) {
-      const float zv = CK ? float(codes[t * d + j]) * pow2f(exps[t * nb + (j >> 6)]) : ld_elem(z + t * ldz + j);
-      g *= act_slope(act, zv);
-      st_elem(dz + t * lddz + j, g);
+  float s[8] = {};
+  if (cnt > 0) {
+#pragma unroll 2
+    for (int64_t t = t0 + wave; t < t1; t += 4) {
+      float g[8];
+      ld8(dy + t * lddy + c, vec, cnt, g);
+      if (act != LRC_ACT_NONE) {
+        float zv[8];
+        if (CK)
+          ld8_codes(codes + t * d + c, vec_z, cnt, pow2f(exps[t * nb + (c >> 6)]), zv);
+        else
+          ld8(z + t * ldz + c, vec_z, cnt, zv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= act_slope(act, zv[e]);
+        st8(dz + t * lddz + c, vec, cnt, g);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += g[e];
     }
-    s += g;
   }
-  if (partial != nullptr) partial[int64_t(blockIdx.y) * d + j] = s;
+  if (partial == nullptr) return;
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wave - 1][lane][e] = s[e];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    s[e] = ((s[e] + sums[0][lane][e]) + sums[1][lane][e]) + sums[2][lane][e];
+    if (e < cnt) partial[int64_t(blockIdx.y) * d + c + e] = s[e];
+  }
 }
 
 // rows of `halves` 16-bit words, pitch `ld`, set to zero
@@ -293,8 +319,8 @@ GemmSegments segments(int pa, int pb) {
 
 // Whether a product goes to the matrix-core path for large tiles.  Below this much work the
 // passes that prepare its operands cost more than they save.
-bool large_product(int64_t M, int64_t N, int64_t K) {
-  return double(M) * double(N) * double(K) >= double(1 << 24);
+bool large_product(int64_t n, int64_t di, int64_t dn) {
+  return double(n) * double(di) * double(dn) >= double(1 << 24) && n <= GEMM_MAX_K;
 }
 template <class T>
 bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two operands
@@ -335,7 +361,7 @@ template <class T>
 LinearRoom forward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   LinearRoom r;
   Carve cv(ws);
-  if (large_product(n, dn, di) && gemm_fits<T>(di, di)) {
+  if (large_product(n, di, dn) && gemm_fits<T>(di, di)) {
     r.flag = cv.take<int32_t>(1);
     r.partial = cv.take<float>(gemm_bf16_workspace(n, dn, di) / 4);
     if (sizeof(T) == 4 || di % 8 != 0) {
@@ -351,7 +377,7 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   LinearRoom r;
   Carve cv(ws);
   r.sums = cv.take<float>(size_t(col_plan(n).chunks) * dn);
-  if (large_product(n, dn, di) && gemm_fits<T>(di, dn)) {
+  if (large_product(n, di, dn) && gemm_fits<T>(di, dn)) {
     r.flag = cv.take<int32_t>(1);
     r.partial = cv.take<float>(std::max(gemm_bf16_workspace(n, di, dn), gemm_bf16_workspace(dn, di, n)) / 4);
     if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
@@ -480,19 +506,23 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     const ColPlan p = col_plan(n);
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
-      const dim3 grid(unsigned(cdiv(dn, LT)), unsigned(p.chunks));
+      const dim3 grid(unsigned(cdiv(dn, 512)), unsigned(p.chunks));
       float* part = a.db != nullptr ? room.sums : nullptr;
       const T *dy = static_cast<const T*>(a.dy), *z = static_cast<const T*>(a.z);
       T* dz = static_cast<T*>(a.dz);
-      if (a.z == nullptr && a.act != LRC_ACT_NONE)
+      const bool vec = rows_vec16(dy, a.lddy, sizeof(T)) &&
+                       (a.act == LRC_ACT_NONE || rows_vec16(dz, a.lddz, sizeof(T)));
+      if (a.z == nullptr && a.act != LRC_ACT_NONE) {
+        const bool vec_z = dn % 8 == 0 && (reinterpret_cast<uintptr_t>(a.zcodes) & 7) == 0;
         dz_kernel<T, true><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, cdiv(dn, CKB), a.act,
-                                                dz, a.lddz, p.rows, part);
-      else
+                                                dz, a.lddz, p.rows, vec, vec_z, part);
+      } else {
         dz_kernel<T, false><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, nullptr, nullptr, 0, a.act, dz, a.lddz,
-                                                 p.rows, part);
+                                                 p.rows, vec, rows_vec16(z, a.ldz, sizeof(T)), part);
+      }
       LRC_LAUNCHED();
     }
-    if (a.db != nullptr) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db));
+    if (a.db != nullptr) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db, nullptr));
     if (a.act != LRC_ACT_NONE) {
       g = a.dz;
       ldg = a.lddz;
@@ -582,7 +612,7 @@ extern "C" lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t 
       zero_rows_kernel<<<unsigned(grid), LT, 0, st>>>(static_cast<uint16_t*>(dW), d_out, d_in * half, lddw * half);
       LRC_LAUNCHED();
     }
-    if (db != nullptr) LRC_TRY(reduce_partials(st, nullptr, 0, 0, d_out, db));
+    if (db != nullptr) LRC_TRY(reduce_partials(st, nullptr, 0, d_out, d_out, db, nullptr));
     return LRC_OK;
   }
   const BackArgs a = {n_tokens, d_in, d_out, dy,  lddy,  W,     ldw, x,    ldx, xcodes, xexps, act,

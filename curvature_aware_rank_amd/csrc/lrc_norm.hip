@@ -2,6 +2,7 @@
 #include "lrc_train.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace lrc {
 namespace {
@@ -126,36 +127,379 @@ __global__ __launch_bounds__(NT) void ln_bwd_cols_kernel(const T* __restrict__ d
   partial[(int64_t(blockIdx.y) * 2 + 1) * d + j] = b;
 }
 
-// chunks of tokens of a column sum: at most 1024 of them, 64 tokens at least in each
+// ---- rows of at most 16384 channels, held in registers ---------------------------------
+// WPR waves share a token, each lane holds 8 V of its channels: the token is read from memory
+// once, the statistics are taken from the registers (values centred before they are squared),
+// and gamma, beta and the running sums of dgamma and dbeta stay in registers over all tokens of
+// the workgroup.  The next token's loads are in flight while the present one is worked on.
+//   VEC: 16-byte pieces (d a multiple of 8, rows aligned); lane l holds channels
+//        8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint block;
+//   else lane l holds channels i LANES + l, so a wave holds one block per i.
+constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }   // tokens of a workgroup at a time
+constexpr int row_threads(int wpr) { return 64 * wpr * row_groups(wpr); }
+
+template <class T, int WPR, int V, bool VEC>
+struct RowShape {
+  static constexpr int E = 8 * V, LANES = 64 * WPR, GROUPS = row_groups(WPR), THREADS = row_threads(WPR);
+  static __device__ __forceinline__ int col(int i, int l) {
+    return VEC ? ((i >> 3) * LANES + l) * 8 + (i & 7) : i * LANES + l;
+  }
+};
+
+// a token's elements as they lie in memory
+template <class T, int WPR, int V, bool VEC>
+struct RawRow {
+  using S = RowShape<T, WPR, V, VEC>;
+  static constexpr int WORDS = 8 * V * int(sizeof(T)) / 16;
+  uint4 q[VEC ? WORDS : 1];
+  T s[VEC ? 1 : 8 * V];
+  __device__ __forceinline__ void load(const T* row, int d, int l, bool live) {
+    if (VEC) {
+      constexpr int W = sizeof(T) == 2 ? 1 : 2;   // 16-byte words per piece
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * S::LANES + l) * 8;
+        const bool ok = live && c < d;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          q[W * k + w] = ok ? reinterpret_cast<const uint4*>(row + c)[w] : make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8 * V; ++i) {
+        const int c = i * S::LANES + l;
+        s[i] = live && c < d ? row[c] : T(0);
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if (!VEC) return ld_elem(&s[i]);
+    const int word = sizeof(T) == 2 ? i >> 1 : i;
+    const uint4& u = q[word >> 2];
+    const uint32_t w = (word & 3) == 0 ? u.x : (word & 3) == 1 ? u.y : (word & 3) == 2 ? u.z : u.w;
+    if (sizeof(T) == 4) return __uint_as_float(w);
+    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+};
+// a token's codes and exponents
+template <int WPR, int V, bool VEC>
+struct RawCodes {
+  using S = RowShape<uint16_t, WPR, V, VEC>;
+  uint2 q[VEC ? V : 1];
+  int8_t s[VEC ? 1 : 8 * V];
+  int8_t e[VEC ? V : 8 * V];
+  __device__ __forceinline__ void load(const int8_t* codes, const int8_t* exps, int d, int l, bool live) {
+    if (VEC) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * S::LANES + l) * 8;
+        const bool ok = live && c < d;
+        q[k] = ok ? *reinterpret_cast<const uint2*>(codes + c) : make_uint2(0u, 0u);
+        e[k] = ok ? exps[c >> 6] : int8_t(0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8 * V; ++i) {
+        const int c = i * S::LANES + l;
+        const bool ok = live && c < d;
+        s[i] = ok ? codes[c] : int8_t(0);
+        e[i] = ok ? exps[c >> 6] : int8_t(0);
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if (!VEC) return float(s[i]) * pow2f(e[i]);
+    const uint32_t w = (i & 4) ? q[i >> 3].y : q[i >> 3].x;
+    return float(int8_t(w >> (8 * (i & 3)))) * pow2f(e[i >> 3]);
+  }
+};
+
+// Sums of the token's WPR waves, the same in all its lanes; one barrier when waves share a
+// token (`red`: a slot per wave, not reused before the barrier after the next one).
+template <int WPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int wave_in_row, int lane, int group) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+  if (WPR == 1) return;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[group * WPR + wave_in_row][k] = v[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) s += red[group * WPR + w][k];
+    v[k] = s;
+  }
+}
+
+template <class T, int WPR, int V, bool VEC>
+__global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
+    const T* __restrict__ x, int64_t ldx, int64_t n, int d, const float* __restrict__ gamma,
+    const float* __restrict__ beta, float eps, T* __restrict__ y, int64_t ldy, float* __restrict__ mean,
+    float* __restrict__ rstd, int8_t* __restrict__ codes, int8_t* __restrict__ exps, int64_t nb,
+    int32_t* __restrict__ info) {
+  using S = RowShape<T, WPR, V, VEC>;
+  constexpr int E = S::E;
+  __shared__ float red[2][WPR > 1 ? S::GROUPS * WPR : 1][1];
+  const int lane = threadIdx.x & 63, group = threadIdx.x / S::LANES, l = threadIdx.x % S::LANES;
+  const int wave = l >> 6;
+  float ga[E], be[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = S::col(i, l);
+    ga[i] = gamma != nullptr && c < d ? gamma[c] : 1.f;
+    be[i] = beta != nullptr && c < d ? beta[c] : 0.f;
+  }
+  const float inv_d = 1.f / float(d);
+  const int64_t step = int64_t(gridDim.x) * S::GROUPS;
+  int64_t t = int64_t(blockIdx.x) * S::GROUPS + group;
+  RawRow<T, WPR, V, VEC> raw;
+  raw.load(x + t * ldx, d, l, t < n);
+  bool bad = false;
+  for (int64_t t0 = int64_t(blockIdx.x) * S::GROUPS; t0 < n; t0 += step, t += step) {
+    float v[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = raw.at(i);
+    raw.load(x + (t + step) * ldx, d, l, t + step < n);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) s[0] += v[i];
+    row_sums<WPR, 1>(s, red[0], wave, lane, group);
+    const float mu = s[0] * inv_d;
+    if (codes != nullptr) {   // before v is centred
+      if (VEC) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int c = (k * S::LANES + l) * 8;
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = v[8 * k + e];
+          st8_codes(codes + t * d + c, exps + t * nb + (c >> 6), true, t < n && c < d ? 8 : 0, p, lane, bad);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int c = S::col(i, l);
+          float m = finite_mag(v[i]);
+          bad |= !finite_f(v[i]);
+#pragma unroll
+          for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+          const int e = ckpt_exponent(m);
+          if (t < n && c < d) {
+            codes[t * d + c] = int8_t(ckpt_code(v[i], pow2f(-e)));
+            if (lane == 0) exps[t * nb + (c >> 6)] = int8_t(e);
+          }
+        }
+      }
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      v[i] -= mu;
+      q[0] = S::col(i, l) < d ? fmaf(v[i], v[i], q[0]) : q[0];
+    }
+    row_sums<WPR, 1>(q, red[1], wave, lane, group);
+    const float rs = 1.f / sqrtf(q[0] * inv_d + eps);
+    if (t >= n) continue;
+    if (l == 0) {
+      mean[t] = mu;
+      rstd[t] = rs;
+    }
+    T* o = y + t * ldy;
+    if (VEC) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * S::LANES + l) * 8;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = fmaf(v[8 * k + e] * rs, ga[8 * k + e], be[8 * k + e]);
+        if (c < d) st8(o + c, true, 8, p);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = S::col(i, l);
+        if (c < d) st_elem(o + c, fmaf(v[i] * rs, ga[i], be[i]));
+      }
+    }
+  }
+  if (info != nullptr && bad) *info = LRC_ENONFINITE;
+}
+
+// dx of every token and the workgroup's share of dgamma and dbeta (partial[2 b], partial[2 b + 1]
+// of workgroup b; not written when NULL, and no dx when that is NULL).
+template <class T, int WPR, int V, bool VEC, bool CK>
+__global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
+    const T* __restrict__ dy, int64_t lddy, int64_t n, int d, const T* __restrict__ x, int64_t ldx,
+    const int8_t* __restrict__ codes, const int8_t* __restrict__ exps, int64_t nb, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const float* __restrict__ gamma, T* __restrict__ dx, int64_t lddx,
+    float* __restrict__ partial) {
+  using S = RowShape<T, WPR, V, VEC>;
+  constexpr int E = S::E;
+  __shared__ float red[2][WPR > 1 ? S::GROUPS * WPR : 1][2];
+  __shared__ float sums[S::GROUPS > 1 ? (S::GROUPS - 1) * 2 * E * S::LANES : 1];
+  const int lane = threadIdx.x & 63, group = threadIdx.x / S::LANES, l = threadIdx.x % S::LANES;
+  const int wave = l >> 6;
+  float ga[E], dg[E], db[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = S::col(i, l);
+    ga[i] = gamma != nullptr && c < d ? gamma[c] : 1.f;
+    dg[i] = 0.f;
+    db[i] = 0.f;
+  }
+  const float inv_d = 1.f / float(d);
+  const int64_t step = int64_t(gridDim.x) * S::GROUPS;
+  int64_t t = int64_t(blockIdx.x) * S::GROUPS + group;
+  RawRow<T, WPR, V, VEC> rg, rx;
+  RawCodes<WPR, V, VEC> rc;
+  float mu = 0.f, rs = 0.f;
+  auto load = [&](int64_t u) {
+    const bool live = u < n;
+    rg.load(dy + u * lddy, d, l, live);
+    if (CK)
+      rc.load(codes + u * d, exps + u * nb, d, l, live);
+    else
+      rx.load(x + u * ldx, d, l, live);
+    mu = live ? mean[u] : 0.f;
+    rs = live ? rstd[u] : 0.f;
+  };
+  load(t);
+  int odd = 0;
+  for (int64_t t0 = int64_t(blockIdx.x) * S::GROUPS; t0 < n; t0 += step, t += step, odd ^= 1) {
+    float g[E], xh[E];
+    const float r = rs;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      g[i] = rg.at(i);
+      const float xv = CK ? rc.at(i) : rx.at(i);
+      xh[i] = S::col(i, l) < d ? (xv - mu) * r : 0.f;
+    }
+    load(t + step);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      dg[i] = fmaf(g[i], xh[i], dg[i]);
+      db[i] += g[i];
+      g[i] *= ga[i];
+      s[0] += g[i];
+      s[1] = fmaf(g[i], xh[i], s[1]);
+    }
+    if (dx == nullptr) continue;
+    row_sums<WPR, 2>(s, red[odd], wave, lane, group);
+    if (t >= n) continue;
+    const float c1 = s[0] * inv_d, c2 = s[1] * inv_d;
+    T* o = dx + t * lddx;
+    if (VEC) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * S::LANES + l) * 8;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = r * (g[8 * k + e] - c1 - xh[8 * k + e] * c2);
+        if (c < d) st8(o + c, true, 8, p);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = S::col(i, l);
+        if (c < d) st_elem(o + c, r * (g[i] - c1 - xh[i] * c2));
+      }
+    }
+  }
+  if (partial == nullptr) return;
+  if (S::GROUPS > 1) {   // the workgroup's tokens of one pass, added in order
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        sums[((group - 1) * 2 * E + i) * S::LANES + l] = dg[i];
+        sums[((group - 1) * 2 * E + E + i) * S::LANES + l] = db[i];
+      }
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int k = 0; k < S::GROUPS - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        dg[i] += sums[(k * 2 * E + i) * S::LANES + l];
+        db[i] += sums[(k * 2 * E + E + i) * S::LANES + l];
+      }
+  }
+  float* p = partial + int64_t(blockIdx.x) * 2 * d;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = S::col(i, l);
+    if (c < d) {
+      p[c] = dg[i];
+      p[d + c] = db[i];
+    }
+  }
+}
+
+constexpr int ROW_MAX = 16384;        // widest row held in registers
+constexpr int MAX_PARTS = 1024;       // partials of dgamma and dbeta
+
+// chunks of tokens of a column sum of wider rows
 struct ColPlan {
   int64_t rows, chunks;
 };
 ColPlan col_plan(int64_t n) {
   ColPlan p;
-  p.rows = std::max<int64_t>(ROWS_PER_CHUNK, cdiv(n, 1024));
+  p.rows = std::max<int64_t>(ROWS_PER_CHUNK, cdiv(n, MAX_PARTS));
   p.chunks = cdiv(n, p.rows);
   return p;
 }
 
-// out[c] = sum_p partial[p stride + c]: 16 columns x 16 slices of the parts per workgroup,
-// the slices added in order
+// Workgroups of the backward kernel: each takes at least four tokens per group, so that the
+// partials stay a small part of the traffic, and 512 fill the chip (two per compute unit, each
+// with a token's loads ahead).
+int64_t bwd_groups(int64_t n, int64_t d) {
+  const int64_t at_once = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
+  return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(n, 4 * at_once)));
+}
+int64_t bwd_parts(int64_t n, int64_t d) { return d <= ROW_MAX ? bwd_groups(n, d) : col_plan(n).chunks; }
+
+// 32 columns x 8 slices of the parts per workgroup, the slices added in order
 __global__ __launch_bounds__(NT) void reduce_partials_kernel(const float* __restrict__ partial, int64_t parts,
-                                                             int64_t stride, int64_t cols, float* __restrict__ out) {
-  __shared__ float acc[16][17];
-  const int cx = threadIdx.x & 15, sl = threadIdx.x >> 4;
-  const int64_t c = int64_t(blockIdx.x) * 16 + cx;
+                                                             int64_t cols, int64_t split, float* __restrict__ out0,
+                                                             float* __restrict__ out1) {
+  __shared__ float acc[8][33];
+  const int cx = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t c = int64_t(blockIdx.x) * 32 + cx;
   float s = 0.f;
-  if (c < cols)
-    for (int64_t p = sl; p < parts; p += 16) s += partial[p * stride + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t p = sl; p < parts; p += 8) s += partial[p * cols + c];
+  }
   acc[sl][cx] = s;
   __syncthreads();
   if (sl == 0 && c < cols) {
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += acc[i][cx];
-    out[c] = v;
+    for (int i = 0; i < 8; ++i) v += acc[i][cx];
+    float* out = c < split ? out0 : out1;
+    if (out != nullptr) out[c < split ? c : c - split] = v;
   }
 }
+
+// Calls f(waves per token, 8-channel pieces per lane) as compile-time constants for rows of d
+// channels; a lane holds 8 or 16 channels.
+template <class F>
+lrc_status with_row_shape(int64_t d, F f) {
+  using std::integral_constant;
+  if (d <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  if (d <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+  if (d <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+  if (d <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  if (d <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+}
+
+bool codes_vec(const int8_t* codes) { return (reinterpret_cast<uintptr_t>(codes) & 7) == 0; }
 
 template <class T>
 lrc_status norm_forward(hipStream_t st, const T* x, int64_t n, int64_t d, int64_t ldx, const float* gamma,
@@ -164,10 +508,26 @@ lrc_status norm_forward(hipStream_t st, const T* x, int64_t n, int64_t d, int64_
   const int64_t nb = cdiv(d, CKB);
   ProfScope scope("ln_fwd_kernel", st, 8.0 * double(n) * double(d),
                   double(n) * double(d) * (2 * sizeof(T) + (codes ? 1 : 0)) + 8.0 * double(n + d));
-  ln_fwd_rows_kernel<T><<<unsigned(n), NT, 0, st>>>(x, ldx, int(d), gamma, beta, eps, y, ldy, mean, rstd, codes, exps,
-                                                    nb, info);
-  LRC_LAUNCHED();
-  return LRC_OK;
+  if (d > ROW_MAX) {
+    ln_fwd_rows_kernel<T><<<unsigned(n), NT, 0, st>>>(x, ldx, int(d), gamma, beta, eps, y, ldy, mean, rstd, codes,
+                                                      exps, nb, info);
+    LRC_LAUNCHED();
+    return LRC_OK;
+  }
+  const bool vec = d % 8 == 0 && rows_vec16(x, ldx, sizeof(T)) && rows_vec16(y, ldy, sizeof(T)) && codes_vec(codes);
+  return with_row_shape(d, [&](auto w, auto v) -> lrc_status {
+    constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
+    using S = RowShape<T, WPR, V, true>;
+    const unsigned grid = unsigned(std::min<int64_t>(cdiv(n, S::GROUPS), 2048 / std::max(1, WPR / 4)));
+    if (vec)
+      ln_fwd_kernel<T, WPR, V, true><<<grid, S::THREADS, 0, st>>>(x, ldx, n, int(d), gamma, beta, eps, y, ldy, mean,
+                                                                  rstd, codes, exps, nb, info);
+    else
+      ln_fwd_kernel<T, WPR, V, false><<<grid, S::THREADS, 0, st>>>(x, ldx, n, int(d), gamma, beta, eps, y, ldy, mean,
+                                                                   rstd, codes, exps, nb, info);
+    LRC_LAUNCHED();
+    return LRC_OK;
+  });
 }
 
 template <class T, bool CK>
@@ -175,32 +535,52 @@ lrc_status norm_backward(hipStream_t st, const T* dy, int64_t n, int64_t d, int6
                          const int8_t* codes, const int8_t* exps, const float* mean, const float* rstd,
                          const float* gamma, T* dx, int64_t lddx, float* dgamma, float* dbeta, float* partial) {
   const int64_t nb = cdiv(d, CKB);
-  const ColPlan p = col_plan(n);
+  const bool params = dgamma != nullptr || dbeta != nullptr;
+  if (dx == nullptr && !params) return LRC_OK;
   {
     ProfScope scope("ln_bwd_kernel", st, 14.0 * double(n) * double(d),
                     double(n) * double(d) * (2 * sizeof(T) + (CK ? 1 : sizeof(T))) + 8.0 * double(n) + 12.0 * d);
-    if (dx != nullptr) {
-      ln_bwd_rows_kernel<T, CK><<<unsigned(n), NT, 0, st>>>(dy, lddy, int(d), x, ldx, codes, exps, nb, mean, rstd,
-                                                            gamma, dx, lddx);
-      LRC_LAUNCHED();
+    if (d <= ROW_MAX) {
+      const bool vec = d % 8 == 0 && rows_vec16(dy, lddy, sizeof(T)) && (dx == nullptr || rows_vec16(dx, lddx, sizeof(T))) &&
+                       (CK ? codes_vec(codes) : rows_vec16(x, ldx, sizeof(T)));
+      const unsigned grid = unsigned(bwd_groups(n, d));
+      float* part = params ? partial : nullptr;
+      LRC_TRY(with_row_shape(d, [&](auto w, auto v) -> lrc_status {
+        constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
+        using S = RowShape<T, WPR, V, true>;
+        if (vec)
+          ln_bwd_kernel<T, WPR, V, true, CK><<<grid, S::THREADS, 0, st>>>(dy, lddy, n, int(d), x, ldx, codes, exps, nb,
+                                                                          mean, rstd, gamma, dx, lddx, part);
+        else
+          ln_bwd_kernel<T, WPR, V, false, CK><<<grid, S::THREADS, 0, st>>>(dy, lddy, n, int(d), x, ldx, codes, exps, nb,
+                                                                           mean, rstd, gamma, dx, lddx, part);
+        LRC_LAUNCHED();
+        return LRC_OK;
+      }));
+    } else {
+      if (dx != nullptr) {
+        ln_bwd_rows_kernel<T, CK><<<unsigned(n), NT, 0, st>>>(dy, lddy, int(d), x, ldx, codes, exps, nb, mean, rstd,
+                                                              gamma, dx, lddx);
+        LRC_LAUNCHED();
+      }
+      if (params) {
+        const ColPlan p = col_plan(n);
+        ln_bwd_cols_kernel<T, CK><<<dim3(unsigned(cdiv(d, NT)), unsigned(p.chunks)), NT, 0, st>>>(
+            dy, lddy, n, int(d), x, ldx, codes, exps, nb, mean, rstd, p.rows, partial);
+        LRC_LAUNCHED();
+      }
     }
-    if (dgamma == nullptr && dbeta == nullptr) return LRC_OK;
-    ln_bwd_cols_kernel<T, CK><<<dim3(unsigned(cdiv(d, NT)), unsigned(p.chunks)), NT, 0, st>>>(
-        dy, lddy, n, int(d), x, ldx, codes, exps, nb, mean, rstd, p.rows, partial);
-    LRC_LAUNCHED();
   }
-  if (dgamma != nullptr) LRC_TRY(reduce_partials(st, partial, p.chunks, 2 * d, d, dgamma));
-  if (dbeta != nullptr) LRC_TRY(reduce_partials(st, partial + d, p.chunks, 2 * d, d, dbeta));
-  return LRC_OK;
+  return params ? reduce_partials(st, partial, bwd_parts(n, d), 2 * d, d, dgamma, dbeta) : LRC_OK;
 }
 
 bool sizes_ok(int64_t n, int64_t d) { return n >= 0 && n < (int64_t(1) << 31) && d >= 1 && d <= (int64_t(1) << 24); }
 
 }  // namespace
 
-lrc_status reduce_partials(hipStream_t st, const float* partial, int64_t parts, int64_t stride, int64_t cols,
-                           float* out) {
-  reduce_partials_kernel<<<unsigned(cdiv(cols, 16)), NT, 0, st>>>(partial, parts, stride, cols, out);
+lrc_status reduce_partials(hipStream_t st, const float* partial, int64_t parts, int64_t cols, int64_t split,
+                           float* out0, float* out1) {
+  reduce_partials_kernel<<<unsigned(cdiv(cols, 32)), NT, 0, st>>>(partial, parts, cols, split, out0, out1);
   LRC_LAUNCHED();
   return LRC_OK;
 }
@@ -229,7 +609,7 @@ extern "C" lrc_status lrc_layer_norm(const void* x, lrc_dtype dt, int64_t n_toke
 extern "C" size_t lrc_layer_norm_backward_workspace(int64_t n_tokens, int64_t d) {
   if (!sizes_ok(n_tokens, d)) return 0;
   Carve cv(nullptr);
-  cv.take<float>(size_t(col_plan(n_tokens).chunks) * 2 * d);
+  cv.take<float>(size_t(bwd_parts(n_tokens, d)) * 2 * d);
   return cv.bytes();
 }
 
@@ -248,9 +628,7 @@ extern "C" lrc_status lrc_layer_norm_backward(const void* dy, lrc_dtype dt, int6
   const size_t need = lrc_layer_norm_backward_workspace(n_tokens, d);
   if (ws_bytes < need || (need > 0 && ws == nullptr)) return LRC_EWORKSPACE;
   if (n_tokens == 0) {   // sums over nothing
-    if (dgamma != nullptr) LRC_TRY(reduce_partials(st, nullptr, 0, 0, d, dgamma));
-    if (dbeta != nullptr) LRC_TRY(reduce_partials(st, nullptr, 0, 0, d, dbeta));
-    return LRC_OK;
+    return reduce_partials(st, nullptr, 0, 2 * d, d, dgamma, dbeta);
   }
   float* partial = static_cast<float*>(ws);
   auto go = [&](auto tag) -> lrc_status {
