@@ -15,7 +15,6 @@ Names match the C ABI in include/lrc.h.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -133,7 +132,7 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
@@ -533,38 +532,56 @@ def lrc_lowrank_ffn(x: torch.Tensor, gate, up, down):
     return y
 
 
-def _on(device):
-    """Context in which `device` is current (a launch needs its stream's device current)."""
+def _run(where, device, fn, *args):
+    """Call fn(*args, stream) with `device` current, on its current stream (a launch needs its
+    stream's device current), and turn a failure into an exception."""
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if st != LRC_OK:
+        raise LrcError(st, where)
 
 
-def _stream_of(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _rows(t, name, shape, dtype=None, device=None):
-    """Check a 2-D GPU tensor and return (tensor, leading dim); rows that are not contiguous
-    or overlap are copied."""
-    _tensor(t, name, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype, shape, device)
-    n, d = t.shape
-    if d > 0 and n > 0 and ((d > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < d)):
-        t = t.contiguous()
-    return t, (max(t.stride(0), d, 1) if n > 1 else max(d, 1))
+def _rows(t, name, n=None, d=None, dtype=None, device=None):
+    """Check a 2-D GPU tensor (its dtype, its device and, where given, its n rows and d columns)
+    and return (tensor, leading dim); rows that are not contiguous or overlap are copied."""
+    _dev(t, name)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    rows, cols = t.shape
+    if (n is not None and rows != n) or (d is not None and cols != d):
+        raise ValueError(f"{name} must have shape {(n, d)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    s0, s1 = t.stride()
+    if rows <= 1 or cols == 0:
+        return t if s1 == 1 or cols <= 1 else t.contiguous(), max(cols, 1)
+    if (cols > 1 and s1 != 1) or s0 < cols:
+        return t.contiguous(), cols
+    return t, s0
 
 
 def _vector(t, name, n, device):
-    return None if t is None else _tensor(t, name, torch.float32, (n,), device).contiguous()
+    if t is None:
+        return None
+    _dev(t, name)
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != device:
+        raise ValueError(f"{name} must be fp32 of shape ({n},) on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.contiguous()
 
 
 def _checkpoint(ck, name, n, d, device):
     """Check a (codes, exps) pair of n rows of d channels."""
     if len(ck) != 2:
         raise ValueError(f"{name} must be a tensor or a (codes, exps) pair")
-    codes = _tensor(ck[0], f"{name} codes", torch.int8, (n, d), device).contiguous()
-    exps = _tensor(ck[1], f"{name} exps", torch.int8, (n, -(-d // LRC_CKPT_BLOCK)), device).contiguous()
-    return codes, exps
+    codes, ldc = _rows(ck[0], f"{name} codes", n, d, torch.int8, device)
+    blocks = -(-d // LRC_CKPT_BLOCK)
+    exps, lde = _rows(ck[1], f"{name} exps", n, blocks, torch.int8, device)
+    return codes if ldc == max(d, 1) else codes.contiguous(), exps if lde == max(blocks, 1) else exps.contiguous()
 
 
 def _kept(t, name, n, d, dtype, device):
@@ -574,7 +591,7 @@ def _kept(t, name, n, d, dtype, device):
     if isinstance(t, (tuple, list)):
         codes, exps = _checkpoint(t, name, n, d, device)
         return None, max(d, 1), codes, exps
-    t, ld = _rows(t, name, (n, d), dtype, device)
+    t, ld = _rows(t, name, n, d, dtype, device)
     return t, ld, None, None
 
 
@@ -589,14 +606,13 @@ def lrc_pack_activations(x: torch.Tensor, info=None):
     Returns (codes int8 (n_tokens, d), exps int8 (n_tokens, ceil(d / 64)), info int32 (1,)):
     the values held are codes * 2^exps per 64 channels.  info (sticky, optional) receives
     LRC_ENONFINITE when an entry is NaN or Inf."""
-    x, ldx = _rows(x, "x", (None, None))
+    x, ldx = _rows(x, "x")
     dt, dev = _dtype_code(x), x.device
     n, d = x.shape
     codes, exps = _new_checkpoint(n, d, dev)
     info = _info(info, dev)
-    with _on(dev):
-        _check(lib.lrc_pack_activations(_ptr(x), dt, n, d, ldx, _ptr(codes), _ptr(exps), _ptr(info),
-                                        _stream_of(dev)), "lrc_pack_activations")
+    _run("lrc_pack_activations", dev, lib.lrc_pack_activations, _ptr(x), dt, n, d, ldx, _ptr(codes), _ptr(exps),
+         _ptr(info))
     return codes, exps, info
 
 
@@ -609,9 +625,8 @@ def lrc_unpack_activations(codes: torch.Tensor, exps: torch.Tensor, dtype=torch.
     dev = codes.device
     codes, exps = _checkpoint((codes, exps), "checkpoint", n, d, dev)
     x = torch.empty(n, d, dtype=dtype, device=dev)
-    with _on(dev):
-        _check(lib.lrc_unpack_activations(_ptr(codes), _ptr(exps), n, d, _ptr(x), _dtype_code(x), max(d, 1),
-                                          _stream_of(dev)), "lrc_unpack_activations")
+    _run("lrc_unpack_activations", dev, lib.lrc_unpack_activations, _ptr(codes), _ptr(exps), n, d, _ptr(x),
+         _dtype_code(x), max(d, 1))
     return x
 
 
@@ -620,7 +635,7 @@ def lrc_layer_norm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, ch
 
     Returns (y, mean, rstd, kept, info): y like x, mean and rstd fp32 (n_tokens,), kept the
     (codes, exps) checkpoint of x when `checkpoint` (else None, and info None unless given)."""
-    x, ldx = _rows(x, "x", (None, None))
+    x, ldx = _rows(x, "x")
     dt, dev = _dtype_code(x), x.device
     n, d = x.shape
     gamma, beta = _vector(gamma, "gamma", d, dev), _vector(beta, "beta", d, dev)
@@ -631,10 +646,8 @@ def lrc_layer_norm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5, ch
     if checkpoint or info is not None:
         info = _info(info, dev)
     codes, exps = kept or (None, None)
-    with _on(dev):
-        _check(lib.lrc_layer_norm(_ptr(x), dt, n, d, ldx, _ptr(gamma), _ptr(beta), float(eps), _ptr(y), max(d, 1),
-                                  _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(exps), _ptr(info), _stream_of(dev)),
-               "lrc_layer_norm")
+    _run("lrc_layer_norm", dev, lib.lrc_layer_norm, _ptr(x), dt, n, d, ldx, _ptr(gamma), _ptr(beta), float(eps),
+         _ptr(y), max(d, 1), _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(exps), _ptr(info))
     return y, mean, rstd, kept, info
 
 
@@ -644,7 +657,7 @@ def lrc_layer_norm_backward(dy: torch.Tensor, x, mean: torch.Tensor, rstd: torch
     (codes, exps) checkpoint; mean, rstd: (n_tokens,) fp32 as lrc_layer_norm returned them.
 
     Returns (dx like dy, dgamma fp32 (d,), dbeta fp32 (d,)), None where not needed."""
-    dy, lddy = _rows(dy, "dy", (None, None))
+    dy, lddy = _rows(dy, "dy")
     dt, dev = _dtype_code(dy), dy.device
     n, d = dy.shape
     if x is None:
@@ -655,12 +668,10 @@ def lrc_layer_norm_backward(dy: torch.Tensor, x, mean: torch.Tensor, rstd: torch
     dx = torch.empty(n, d, dtype=dy.dtype, device=dev) if need_dx else None
     dgamma = torch.empty(d, dtype=torch.float32, device=dev) if need_dparams else None
     dbeta = torch.empty(d, dtype=torch.float32, device=dev) if need_dparams else None
-    with _on(dev):
-        ws = _workspace(lib.lrc_layer_norm_backward_workspace(n, d), dev)
-        _check(lib.lrc_layer_norm_backward(_ptr(dy), dt, n, d, lddy, _ptr(xt), ldx, _ptr(codes), _ptr(exps),
-                                           _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dx), max(d, 1), _ptr(dgamma),
-                                           _ptr(dbeta), _ptr(ws), ws.numel(), _stream_of(dev)),
-               "lrc_layer_norm_backward")
+    ws = _workspace(lib.lrc_layer_norm_backward_workspace(n, d), dev)
+    _run("lrc_layer_norm_backward", dev, lib.lrc_layer_norm_backward, _ptr(dy), dt, n, d, lddy, _ptr(xt), ldx,
+         _ptr(codes), _ptr(exps), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dx), max(d, 1), _ptr(dgamma), _ptr(dbeta),
+         _ptr(ws), ws.numel())
     return dx, dgamma, dbeta
 
 
@@ -679,16 +690,16 @@ def lrc_linear(x: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
 
     Returns (y, saved, info): saved is z, (codes, exps) or None; info (int32 (1,), sticky
     LRC_ENONFINITE) is None unless given or save is "checkpoint"."""
-    x, ldx = _rows(x, "x", (None, None))
+    x, ldx = _rows(x, "x")
     dt, dev = _dtype_code(x), x.device
     n, d_in = x.shape
-    W, ldw = _rows(W, "W", (None, d_in), x.dtype, dev)
+    W, ldw = _rows(W, "W", None, d_in, x.dtype, dev)
     d_out = W.shape[0]
     code = _act_code(act)
     bias = _vector(bias, "bias", d_out, dev)
     ldr = d_out
     if residual is not None:
-        residual, ldr = _rows(residual, "residual", (n, d_out), x.dtype, dev)
+        residual, ldr = _rows(residual, "residual", n, d_out, x.dtype, dev)
     y = torch.empty(n, d_out, dtype=x.dtype, device=dev)
     z, codes, exps = None, None, None
     if save == "z":
@@ -699,11 +710,10 @@ def lrc_linear(x: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", r
         raise ValueError("save is none, z or checkpoint")
     if codes is not None or info is not None:
         info = _info(info, dev)
-    with _on(dev):
-        ws = _workspace(lib.lrc_linear_workspace(dt, n, d_in, d_out), dev)
-        _check(lib.lrc_linear(_ptr(x), dt, n, d_in, d_out, ldx, _ptr(W), ldw, _ptr(bias), code, _ptr(residual), ldr,
-                              _ptr(y), max(d_out, 1), _ptr(z), max(d_out, 1), _ptr(codes), _ptr(exps), _ptr(info),
-                              _ptr(ws), ws.numel(), _stream_of(dev)), "lrc_linear")
+    ws = _workspace(lib.lrc_linear_workspace(dt, n, d_in, d_out), dev)
+    _run("lrc_linear", dev, lib.lrc_linear, _ptr(x), dt, n, d_in, d_out, ldx, _ptr(W), ldw, _ptr(bias), code,
+         _ptr(residual), ldr, _ptr(y), max(d_out, 1), _ptr(z), max(d_out, 1), _ptr(codes), _ptr(exps), _ptr(info),
+         _ptr(ws), ws.numel())
     return y, (codes, exps) if codes is not None else z, info
 
 
@@ -716,10 +726,10 @@ def lrc_linear_backward(dy: torch.Tensor, x, W: torch.Tensor, act: str = "none",
     Returns (dz, dx, dW, db): dz = dy * act'(z), the layer's output-gradient stream (dy itself
     for act none), dx (n_tokens, d_in), dW (d_out, d_in) in dw_dtype (default dy's; torch.float32
     allowed), db fp32 (d_out,); None where not needed."""
-    dy, lddy = _rows(dy, "dy", (None, None))
+    dy, lddy = _rows(dy, "dy")
     dt, dev = _dtype_code(dy), dy.device
     n, d_out = dy.shape
-    W, ldw = _rows(W, "W", (d_out, None), dy.dtype, dev)
+    W, ldw = _rows(W, "W", d_out, None, dy.dtype, dev)
     d_in = W.shape[1]
     code = _act_code(act)
     if need_dw and x is None:
@@ -736,12 +746,10 @@ def lrc_linear_backward(dy: torch.Tensor, x, W: torch.Tensor, act: str = "none",
     dW = torch.empty(d_out, d_in, dtype=dw_dtype, device=dev) if need_dw else None
     db = torch.empty(d_out, dtype=torch.float32, device=dev) if need_db else None
     dw_dt = LRC_F32 if dw_dtype == torch.float32 else LRC_BF16
-    with _on(dev):
-        ws = _workspace(lib.lrc_linear_backward_workspace(dt, n, d_in, d_out), dev)
-        _check(lib.lrc_linear_backward(_ptr(dy), dt, n, d_in, d_out, lddy, _ptr(W), ldw, _ptr(xt), ldx, _ptr(xcodes),
-                                       _ptr(xexps), code, _ptr(zt), ldz, _ptr(zcodes), _ptr(zexps), _ptr(dz),
-                                       max(d_out, 1), _ptr(dx), max(d_in, 1), _ptr(dW), dw_dt, max(d_in, 1),
-                                       _ptr(db), _ptr(ws), ws.numel(), _stream_of(dev)), "lrc_linear_backward")
+    ws = _workspace(lib.lrc_linear_backward_workspace(dt, n, d_in, d_out), dev)
+    _run("lrc_linear_backward", dev, lib.lrc_linear_backward, _ptr(dy), dt, n, d_in, d_out, lddy, _ptr(W), ldw,
+         _ptr(xt), ldx, _ptr(xcodes), _ptr(xexps), code, _ptr(zt), ldz, _ptr(zcodes), _ptr(zexps), _ptr(dz),
+         max(d_out, 1), _ptr(dx), max(d_in, 1), _ptr(dW), dw_dt, max(d_in, 1), _ptr(db), _ptr(ws), ws.numel())
     return dz if code else dy, dx, dW, db
 
 

@@ -20,14 +20,17 @@
 namespace lrc {
 namespace gemm {
 
-constexpr int KS = 32;      // k steps per stage
 constexpr int NXCD = 8;
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-#define LRC_WAIT_BARRIER(N) asm volatile("s_waitcnt vmcnt(" #N ") lgkmcnt(0)\n\ts_barrier" ::: "memory")
+// wait until at most N loads of this wave are in flight and its LDS reads are done, then the workgroup
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void* uniform_ptr(const void* p) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
@@ -37,7 +40,7 @@ __device__ __forceinline__ void* uniform_ptr(const void* p) {
 }
 
 // One operand's stages: EDGE tile rows (channels for K_COLS), NW waves.
-template <int KIND, int EDGE, int NW>
+template <int KIND, int EDGE, int NW, int KS>
 struct Stager {
   static constexpr int LOADS = EDGE * KS * 2 / 1024 / NW;   // 1 KB loads per wave and stage
   static constexpr int ROWB = EDGE * 2;                     // K_COLS: bytes per k step
@@ -57,8 +60,9 @@ struct Stager {
       base = o.p + row0 * ld;
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) {
-        const int r = 16 * (LOADS * wave + j) + (lane >> 2);
-        const int g = (lane & 3) ^ ((r >> 2) & 3);
+        constexpr int GPR = KS / 8;          // granules per row
+        const int r = (64 / GPR) * (LOADS * wave + j) + lane / GPR;
+        const int g = (lane % GPR) ^ row_swizzle(r);
         kk[j] = 8 * g;
         voff[j] = r < left ? unsigned(r * ld * 2) + 16 * g : OOB;
       }
@@ -101,21 +105,24 @@ struct Stager {
                                                0);
   }
 
-  // byte offset of the lane's fragment of tile rows row .. row + 31, k half 0
+  // K_ROWS: rows 16 apart in a fragment read fall on every bank once
+  static __device__ __forceinline__ int row_swizzle(int r) { return KS == 32 ? (r >> 2) & 3 : (r >> 1) & 7; }
+
+  // byte offset of the lane's fragment of tile rows row .. row + 31, first 16 k steps
   static __device__ int frag_off(int row, int lane) {
     if (KIND == K_ROWS) {
       const int r = row + (lane & 31);
-      return r * 64 + (((lane >> 5) ^ ((r >> 2) & 3)) << 4);
+      return r * (2 * KS) + (((lane >> 5) ^ row_swizzle(r)) << 4);
     }
     const int g = lane >> 4, sl = lane & 15;
     const int ch = row + 16 * (g & 1) + 4 * (sl & 3);
     const int tk = 8 * (g >> 1) + (sl >> 2);
     return tk * ROWB + (((ch >> 3) ^ (4 * (tk & 3))) << 4) + (ch & 7) * 2;
   }
-  // fragment of k half `half` (16 steps)
-  static __device__ bf16x8 frag(const uint8_t* lds, int off, int half) {
-    if (KIND == K_ROWS) return *reinterpret_cast<const bf16x8*>(lds + (half ? off ^ 32 : off));
-    const uint8_t* p = lds + off + half * 16 * ROWB;
+  // fragment of the stage's k steps [16 q, 16 q + 16)
+  static __device__ bf16x8 frag(const uint8_t* lds, int off, int q) {
+    if (KIND == K_ROWS) return *reinterpret_cast<const bf16x8*>(lds + (off ^ (32 * q)));
+    const uint8_t* p = lds + off + q * 16 * ROWB;
     const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p));
     const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * ROWB));
     const short tmp[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -126,6 +133,7 @@ struct Stager {
 };
 
 struct TileGrid {
+  int64_t m_base, n_base;    // first row and column of the part of D that the tiles cover
   int64_t nm, nn, tiles;
   int per_xcd, splits;
   int steps_per_split;   // stages of one split
@@ -141,18 +149,21 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
   tn = r / rows;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, bool SEG>
+template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG>
 __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N, int64_t K,
                                           const GemmSegments& seg, const TileGrid& tg, const Epilogue& ep,
                                           float* __restrict__ partial, const int32_t* __restrict__ skip) {
   constexpr int NW = WM * WN, BM = WM * FM * 32, BN = WN * FN * 32;
   constexpr int AB = BM * KS * 2, STB = (BM + BN) * KS * 2;
-  using SA = Stager<KA, BM, NW>;
-  using SB = Stager<KB, BN, NW>;
-  static_assert(SA::LOADS + SB::LOADS == 4, "the stage barrier counts four loads per wave and stage");
+  using SA = Stager<KA, BM, NW, KS>;
+  using SB = Stager<KB, BN, NW, KS>;
+  constexpr int L = SA::LOADS + SB::LOADS;      // loads of a wave per stage
   // one LDS object per stage, so that a read of one stage does not wait for the loads of others
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[STB], sb1[STB], sb2[STB], sb3[STB];
-  static_assert(2 * 32 * FN * 32 * 4 <= STB && NW <= 8, "two waves' epilogue rows per stage buffer");
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[STB], sb1[STB], sb2[NST > 2 ? STB : 16],
+      sb3[NST > 3 ? STB : 16];
+  constexpr int PART = 32 * FN * 32 * 4;        // a wave's epilogue rows
+  constexpr int FIT = STB / PART;               // of them in a stage buffer
+  static_assert(NST >= 2 && NST <= 4 && KS % 32 == 0 && FIT >= 1 && FIT * NST >= NW, "the epilogue rows fit the stage buffers");
 
   if (skip != nullptr && *skip != 0) return;
   const int b = blockIdx.x;
@@ -162,7 +173,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   if (ti >= tg.tiles) return;
   int64_t tm, tn;
   tile_at(ti, tg.nm, tg.nn, tm, tn);
-  const int64_t m0 = tm * BM, n0 = tn * BN;
+  const int64_t m0 = tg.m_base + tm * BM, n0 = tg.n_base + tn * BN;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -213,11 +224,11 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
   bf16x8 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
-  auto read_half = [&](const uint8_t* s, int half, bf16x8* fa, bf16x8* fb) {
+  auto read_frags = [&](const uint8_t* s, int q, bf16x8* fa, bf16x8* fb) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[i] = SA::frag(s, offa[i], half);
+    for (int i = 0; i < FM; ++i) fa[i] = SA::frag(s, offa[i], q);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = SB::frag(s + AB, offb[j], half);
+    for (int j = 0; j < FN; ++j) fb[j] = SB::frag(s + AB, offb[j], q);
   };
   auto mma = [&](const bf16x8* fa, const bf16x8* fb) {
 #pragma unroll
@@ -237,72 +248,90 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     if constexpr (FM * FN == 8) { LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR }
   };
   auto interleave_loads = [&]() {
-#define LRC_TRIPLE LRC_PAIR __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+#define LRC_TRIPLE LRC_PAIR __builtin_amdgcn_sched_group_barrier(0x020, (L + FM * FN - 1) / (FM * FN), 0);
     LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE
-    if constexpr (FM * FN == 8) { LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR }
+    if constexpr (FM * FN == 8) { LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE }
 #undef LRC_TRIPLE
 #undef LRC_PAIR
   };
   auto buf = [&](int st) -> uint8_t* {
-    const int q = st & 3;
+    const int q = st % NST;
     return q == 0 ? sb0 : q == 1 ? sb1 : q == 2 ? sb2 : sb3;
   };
 
-  // Schedule, stage s in buffer s % 4.  Iteration s: read the second half of stage s, multiply
-  // its first half, then a barrier that leaves the loads of stages s + 2 and s + 3 (four each
-  // per wave) in flight: stage s + 1 is then in LDS and nobody reads stage s any more, so its
-  // buffer takes stage s + 4; read the first half of stage s + 1, multiply the second half of
-  // stage s.  Stages past the end are issued with empty resources (zeros, never multiplied), so
-  // that the count of loads in flight stays the same to the end.
+  // Schedule, stage s in buffer s % NST.  Iteration s: read the second half of stage s, multiply
+  // its first half, then a barrier that leaves the loads of the stages behind s + 1 (L each per
+  // wave) in flight: stage s + 1 is then in LDS and nobody reads stage s any more, so its buffer
+  // takes stage s + NST; read the first half of stage s + 1, multiply the second half of stage s.
+  // Stages past the end are issued with empty resources (zeros, never multiplied), so that the
+  // count of loads in flight stays the same to the end.
   next_stage(nsteps > 0);
   issue(sb0);
   next_stage(nsteps > 1);
   issue(sb1);
-  next_stage(nsteps > 2);
-  issue(sb2);
-  next_stage(nsteps > 3);
-  issue(sb3);
-  LRC_WAIT_BARRIER(12);
-  read_half(sb0, 0, fa0, fb0);
-  int s = 0;
-#define LRC_STEP(CUR, NXT)             \
-  next_stage(true);                    \
-  read_half(CUR, 1, fa1, fb1);         \
-  mma(fa0, fb0);                       \
-  interleave_reads();                  \
-  __builtin_amdgcn_sched_barrier(0);   \
-  LRC_WAIT_BARRIER(8);                 \
-  __builtin_amdgcn_sched_barrier(0);   \
-  issue(CUR);                          \
-  read_half(NXT, 0, fa0, fb0);         \
-  mma(fa1, fb1);                       \
-  interleave_loads();                  \
-  __builtin_amdgcn_sched_barrier(0);
-  for (; s + 7 < nsteps; s += 4) {
-    LRC_STEP(sb0, sb1)
-    LRC_STEP(sb1, sb2)
-    LRC_STEP(sb2, sb3)
-    LRC_STEP(sb3, sb0)
+  if constexpr (NST > 2) {
+    next_stage(nsteps > 2);
+    issue(sb2);
   }
-#undef LRC_STEP
-  for (; s < nsteps; ++s) {
-    read_half(buf(s), 1, fa1, fb1);
-    mma(fa0, fb0);
-    LRC_WAIT_BARRIER(8);
-    next_stage(s + 4 < nsteps);
-    issue(buf(s));
-    read_half(buf(s + 1), 0, fa0, fb0);   // zeros behind the last stage
+  if constexpr (NST > 3) {
+    next_stage(nsteps > 3);
+    issue(sb3);
+  }
+  wait_barrier<(NST - 1) * L>();
+  read_frags(sb0, 0, fa0, fb0);
+  auto step = [&](uint8_t* cur, const uint8_t* nxt, bool live) {
+    next_stage(live);
+#pragma unroll
+    for (int q = 0; q < KS / 16 - 1; q += 2) {
+      read_frags(cur, q + 1, fa1, fb1);
+      mma(fa0, fb0);
+      interleave_reads();
+      __builtin_amdgcn_sched_barrier(0);
+      if (q + 2 < KS / 16) {
+        read_frags(cur, q + 2, fa0, fb0);
+        mma(fa1, fb1);
+        interleave_reads();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_barrier<(NST - 2) * L>();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(cur);
+    read_frags(nxt, 0, fa0, fb0);
     mma(fa1, fb1);
+    interleave_loads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int s = 0;
+  for (; s + 2 * NST - 1 < nsteps; s += NST) {
+    if constexpr (NST == 2) {
+      step(sb0, sb1, true);
+      step(sb1, sb0, true);
+    } else if constexpr (NST == 3) {
+      step(sb0, sb1, true);
+      step(sb1, sb2, true);
+      step(sb2, sb0, true);
+    } else {
+      step(sb0, sb1, true);
+      step(sb1, sb2, true);
+      step(sb2, sb3, true);
+      step(sb3, sb0, true);
+    }
   }
-  LRC_WAIT_BARRIER(0);   // every load has landed and every read is done: the buffers are free
+  // the last stages choose their buffers at run time; behind the last one only zeros are read
+  for (; s < nsteps; ++s) step(buf(s), buf(s + 1), s + NST < nsteps);
+  wait_barrier<0>();   // every load has landed and every read is done: the buffers are free
 
   // Epilogue: a wave's 32 rows x (32 FN) columns pass through its own part of LDS, so that a
   // lane holds eight consecutive columns of a row and the accesses to memory are whole pieces.
   // Accumulator element e of lane l is row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
-  float* tile = reinterpret_cast<float*>(buf(wave >> 1) + (wave & 1) * (32 * FN * 32 * 4));
+  float* tile = reinterpret_cast<float*>(buf(wave / FIT) + (wave % FIT) * PART);
   constexpr int TW = FN * 32;          // tile columns
   constexpr int LPR = TW / 8;          // lanes per row
   bool bad = false;
+  const int64_t col = n0 + wc * TW + 8 * (lane % LPR);   // the lane's columns
+  float bias[8];
+  bias8(ep, col, int(min(N - col, int64_t(8))), bias);
   auto emit = [&](const f32x16 (&rows)[FN], int i) {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -312,36 +341,40 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
         tile[r * TW + ((j * 32 + (lane & 31)) ^ ((r & 4) << 3))] = rows[j][e];
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 1
+#pragma unroll 2
     for (int q = 0; q < 32 * LPR / 64; ++q) {
       const int r = q * (64 / LPR) + lane / LPR, c = 8 * (lane % LPR);
       const float* src = tile + r * TW + (c ^ ((r & 4) << 3));
       const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      const int64_t row = m0 + (wr * FM + i) * 32 + r, col = n0 + wc * TW + c;
+      const int64_t row = m0 + (wr * FM + i) * 32 + r;
       const int64_t left = row < M ? N - col : 0;
       const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
       if (tg.splits > 1) {
         const int64_t np = (N + 7) & ~int64_t(7);
         if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, true, 8, v);
       } else {
-        finish8<TO>(ep, row, col, cnt, v, lane, bad);
+        finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
-  static_assert(FM == 2, "the accumulator rows are named, so that they stay in registers");
+  static_assert(FM == 2 || FM == 4, "the accumulator rows are named, so that they stay in registers");
   emit(acc[0], 0);
   emit(acc[1], 1);
+  if constexpr (FM == 4) {
+    emit(acc[2], 2);
+    emit(acc[3], 3);
+  }
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, bool SEG>
-__global__ __launch_bounds__(64 * WM * WN, 1) void gemm_bf16_kernel(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
+template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_bf16_kernel(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                                     int64_t K, GemmSegments seg, TileGrid tg,
                                                                     Epilogue ep, float* __restrict__ partial,
                                                                     const int32_t* __restrict__ skip) {
-  gemm_tile<TO, KA, KB, WM, WN, FM, FN, SEG>(A, B, M, N, K, seg, tg, ep, partial, skip);
+  gemm_tile<TO, KA, KB, WM, WN, FM, FN, KS, NST, SEG>(A, B, M, N, K, seg, tg, ep, partial, skip);
 }
 
 // Sum of the splits' tiles in split order, then the epilogue.  One lane per eight columns, the
@@ -359,65 +392,114 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
   float v[8] = {};
   if (cnt > 0) {
     const float* p = partial + row * np + col;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(p + int64_t(s) * M * np);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(p + int64_t(s) * M * np + 4);
+    const int64_t plane = M * np;
+    for (int s0 = 0; s0 < splits; s0 += 8) {   // eight splits' loads in flight, added in order
+      f32x4 lo[8], hi[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += lo[e];
-        v[4 + e] += hi[e];
+      for (int u = 0; u < 8; ++u) {
+        const float* q = p + min(s0 + u, splits - 1) * plane;
+        lo[u] = *reinterpret_cast<const f32x4*>(q);
+        hi[u] = *reinterpret_cast<const f32x4*>(q + 4);
       }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += s0 + u < splits ? lo[u][e] : 0.f;
+          v[4 + e] += s0 + u < splits ? hi[u][e] : 0.f;
+        }
     }
   }
   bool bad = false;
-  finish8<TO>(ep, row, col, cnt, v, lane, bad);
+  float bias[8];
+  bias8(ep, col, cnt, bias);
+  finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
 
 // Tiles and splits from the sizes alone (256 compute units), so that workspace sizes are known
-// without a device and equal inputs give equal bits.
-struct Plan {
-  bool big;
+// without a device and equal inputs give equal bits.  Large tiles (256 x 256, one workgroup per
+// compute unit, 1250 TFLOP/s at 4096^3) for products that fill the chip in whole rounds; small
+// ones (128 x 128, two per unit, 1060) otherwise, with k split when they are few, and for what a
+// last round of large tiles would leave most units idle on.  Times below in microseconds, taken
+// at 256 x 4096 x 4096 to 8192 x 4096 x 11008.
+struct Part {
+  bool large;
   TileGrid tg;
 };
-static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count) {
-  Plan best{};
+struct Plan {
+  int parts = 0;
+  Part part[2];
+};
+// 64 k steps of every workgroup of a round; a round's first loads and its epilogue
+constexpr double LARGE_STEP = 1.65, SMALL_STEP_FULL = 1.0, SMALL_STEP_HALF = 0.68, ROUND = 7.0, MEMORY = 4.5e6;
+
+static TileGrid tiles_of(int64_t m_base, int64_t m, int64_t n_base, int64_t n, int edge, int splits, int64_t per,
+                         int64_t steps) {
+  const int64_t nm = cdiv(m, edge), nn = cdiv(n, edge);
+  return {m_base, n_base, nm, nn, nm * nn, int(cdiv(nm * nn, NXCD)), splits, int(per), int(steps)};
+}
+static double large_cost(int64_t tiles, double steps64) {
+  return double(cdiv(tiles, 256)) * (steps64 * LARGE_STEP + ROUND);
+}
+static double small_cost(int64_t groups, double steps64) {
+  const int64_t full = groups / 512, rest = groups % 512;
+  double c = double(full) * (steps64 * SMALL_STEP_FULL + ROUND);
+  if (rest > 0) c += steps64 * (rest > 256 ? SMALL_STEP_FULL : SMALL_STEP_HALF) + ROUND;
+  return c;
+}
+// KL: k steps per stage of a large tile
+static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL) {
+  Plan best;
   double cost = 1e300;
-  for (int big = 0; big < 2; ++big) {
-    const int64_t edge = big ? 256 : 128;
-    const int64_t nm = cdiv(M, edge), nn = cdiv(N, edge), tiles = nm * nn;
-    const int64_t steps = std::max<int64_t>(1, cdiv(K, KS)), total = steps * count;
-    // workgroups that run at once: one big tile or two small ones per compute unit; a stage of a
-    // big tile costs 1, of a small one 0.3 (two of them share a unit), a split's partial tile
-    // about 12 stages
-    const double slots = big ? 256 : 512, stage = big ? 1.0 : 0.6, fixed = big ? 20.0 : 12.0;
-    for (int64_t s = 1; s <= std::min<int64_t>(32, total); ++s) {
-      const int64_t per = cdiv(total, s), real = cdiv(total, per);
-      if (real != s) continue;
-      const double rounds = std::ceil(double(cdiv(tiles, NXCD) * NXCD * s) / slots);
-      const double extra = s > 1 ? double(s) * double(M) * double(N) * 8.0 / 4e6 / 1.3 * 0.5 + 8.0 : 0.0;
-      const double c = rounds * (double(per) * stage + fixed) + extra;
-      if (c < cost * 0.999) {
-        cost = c;
-        best.big = big;
-        best.tg = {nm, nn, tiles, int(cdiv(tiles, NXCD)), int(s), int(per), int(steps)};
-      }
+  const int64_t steps_l = cdiv(K, KL), steps_s = cdiv(K, 64);
+  const double s64 = double(steps_s) * count;
+  const double floor_us = 2.0 * double(K) * double(M + N) * (count > 1 ? 3 : 1) / MEMORY;
+  const int64_t nm = cdiv(M, 256), nn = cdiv(N, 256), tiles = nm * nn;
+  auto take = [&](double c, int parts, const Part& a, const Part& b) {
+    if (c >= cost) return;
+    cost = c;
+    best.parts = parts;
+    best.part[0] = a;
+    best.part[1] = b;
+  };
+  const Part whole = {true, tiles_of(0, M, 0, N, 256, 1, steps_l * count, steps_l)};
+  take(std::max(floor_us, large_cost(tiles, s64)), 1, whole, whole);
+  const int64_t full = tiles / 256 * 256;   // tiles of whole rounds
+  if (full > 0 && full < tiles) {           // columns, or rows, of tiles that fill whole rounds; small tiles behind
+    for (int rows = 0; rows < 2; ++rows) {
+      const int64_t keep = full / (rows ? nn : nm);
+      if (keep <= 0 || keep >= (rows ? nm : nn)) continue;
+      const int64_t at = keep * 256, m = rows ? M - at : M, n = rows ? N : N - at;
+      const Part a = {true, rows ? tiles_of(0, at, 0, N, 256, 1, steps_l * count, steps_l)
+                                 : tiles_of(0, M, 0, at, 256, 1, steps_l * count, steps_l)};
+      const Part b = {false, tiles_of(rows ? at : 0, m, rows ? 0 : at, n, 128, 1, steps_s * count, steps_s)};
+      take(large_cost(a.tg.tiles, s64) + small_cost(b.tg.tiles, s64), 2, a, b);
     }
+  }
+  const int64_t total = steps_s * count;
+  for (int64_t s = 1; s <= std::min<int64_t>(32, total); ++s) {
+    const int64_t per = cdiv(total, s);
+    if (cdiv(total, per) != s) continue;
+    const Part p = {false, tiles_of(0, M, 0, N, 128, int(s), per, steps_s)};
+    double c = std::max(floor_us, small_cost(p.tg.tiles * s, double(per)));
+    if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
+    take(c, 1, p, p);
   }
   return best;
 }
+static size_t plan_bytes(const Plan& p, int64_t M, int64_t N) {
+  return p.part[0].tg.splits > 1 ? size_t(p.part[0].tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
+}
+constexpr int large_stage(int ka, int kb) { return ka == K_ROWS && kb == K_ROWS ? 64 : 32; }
 
 }  // namespace gemm
 
 using namespace gemm;
 
-size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K) {
+size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB) {
   size_t most = 0;
-  for (int count : {1, 3, 6}) {
-    const Plan p = plan_gemm(M, N, K, count);
-    if (p.tg.splits > 1) most = std::max(most, size_t(p.tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4);
-  }
+  for (int count : {1, 3, 6}) most = std::max(most, plan_bytes(plan_gemm(M, N, K, count, large_stage(KA, KB)), M, N));
   return most;
 }
 
@@ -425,30 +507,38 @@ template <class TO, int KA, int KB>
 lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperand B, int64_t M, int64_t N, int64_t K,
                      const GemmSegments& seg, const Epilogue& ep, float* partial, const int32_t* skip, double flops,
                      double bytes) {
-  const Plan p = plan_gemm(M, N, K, seg.count);
-  const int64_t grid = int64_t(NXCD) * p.tg.per_xcd * p.tg.splits;
-  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  // Stages of a large tile: 64 k steps in two buffers where both operands' rows run along k (a
+  // row's piece is then a whole 128-byte line: 8192 x 4096 x 11008 678 us against 712), else 32
+  // in four (dx 560 against 579, dW 581 against 610).  Small tiles: 64 in two (785 against 954).
+  constexpr int KL = large_stage(KA, KB), NL = KL == 64 ? 2 : 4;
+  const Plan p = plan_gemm(M, N, K, seg.count, KL);
   ProfScope scope(name, st, flops, bytes);
-  auto launch = [&](auto many) {
+  auto launch = [&](auto many, const Part& part) -> lrc_status {
     constexpr bool SEG = decltype(many)::value;
-    if (p.big)
-      gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, SEG><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, p.tg, ep,
-                                                                                   partial, skip);
+    const TileGrid& tg = part.tg;
+    const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
+    if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+    if (part.large)
+      gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, KL, NL, SEG><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, tg, ep,
+                                                                                            partial, skip);
     else
-      gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, SEG><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, p.tg, ep,
-                                                                                   partial, skip);
+      gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, 64, 2, SEG><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, tg, ep,
+                                                                                           partial, skip);
+    LRC_LAUNCHED();
+    return LRC_OK;
   };
-  // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
-  if (std::is_same<TO, uint16_t>::value || seg.count == 1)
-    launch(std::false_type{});
-  else if constexpr (!std::is_same<TO, uint16_t>::value)
-    launch(std::true_type{});
-  LRC_LAUNCHED();
-  if (p.tg.splits == 1) return LRC_OK;
+  for (int i = 0; i < p.parts; ++i) {
+    // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
+    if (std::is_same<TO, uint16_t>::value || seg.count == 1)
+      LRC_TRY(launch(std::false_type{}, p.part[i]));
+    else if constexpr (!std::is_same<TO, uint16_t>::value)
+      LRC_TRY(launch(std::true_type{}, p.part[i]));
+  }
+  const int splits = p.part[0].tg.splits;
+  if (splits == 1) return LRC_OK;
   const int64_t np = (N + 7) & ~int64_t(7), blocks = cdiv(N, CKB), threads = M * blocks * 8;
   if (cdiv(threads, 256) >= (int64_t(1) << 31)) return LRC_EINVAL;
-  gemm_finish_kernel<TO><<<unsigned(cdiv(threads, 256)), 256, 0, st>>>(partial, p.tg.splits, M, N, np, blocks, ep,
-                                                                          skip);
+  gemm_finish_kernel<TO><<<unsigned(cdiv(threads, 256)), 256, 0, st>>>(partial, splits, M, N, np, blocks, ep, skip);
   LRC_LAUNCHED();
   return LRC_OK;
 }

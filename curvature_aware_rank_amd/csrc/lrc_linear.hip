@@ -10,6 +10,7 @@
 #include "lrc_train.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace lrc {
 namespace {
@@ -126,15 +127,141 @@ __global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, in
         tile[(wr + 16 * i + 4 * (lane >> 4) + e) * EP + wc + 16 * j + (lane & 15)] = acc[i][j][e];
   __syncthreads();
   bool bad = false;
+  const int64_t col = n0 + 8 * (lane & 7);
+  float bias[8];
+  bias8(ep, col, int(min(N - col, int64_t(8))), bias);
   for (int r = threadIdx.x >> 3; r < GT; r += LT / 8) {
-    const int64_t row = m0 + r, col = n0 + 8 * (lane & 7);
+    const int64_t row = m0 + r;
     const int64_t left = row < M ? N - col : 0;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = tile[r * EP + 8 * (lane & 7) + e];
-    finish8<TO>(ep, row, col, int(left < 0 ? 0 : left > 8 ? 8 : left), v, lane, bad);
+    finish8<TO>(ep, row, col, int(left < 0 ? 0 : left > 8 ? 8 : left), bias, v, lane, bad);
   }
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
+}
+
+// ---- few tokens: the weight streamed once ------------------------------------------------
+// Up to 64 tokens.  Bound by reading W: a wave holds 16 output channels x 16 G tokens and takes
+// a share of k; its W fragments come straight from memory (a lane reads 16 bytes of one weight
+// row, the four lanes of a row 64 bytes, four such pieces in flight), x comes from the caches.
+// The waves' sums are added in order in LDS, then the epilogue.  fp32: a 16-byte piece holds
+// four k steps, one matrix instruction takes one of them from every lane (any order of k serves
+// as long as both operands agree on it).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <class T>
+struct RowsPiece;
+template <>
+struct RowsPiece<uint16_t> {
+  static constexpr int K = 32;
+  static __device__ __forceinline__ void mma(const u32x4& w, const u32x4& x, f32x4& acc) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0,
+                                                  0, 0);
+  }
+};
+template <>
+struct RowsPiece<float> {
+  static constexpr int K = 16;
+  static __device__ __forceinline__ void mma(const u32x4& w, const u32x4& x, f32x4& acc) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[0]), __uint_as_float(x[0]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[1]), __uint_as_float(x[1]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[2]), __uint_as_float(x[2]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[3]), __uint_as_float(x[3]), acc, 0, 0, 0);
+  }
+};
+
+template <class T, int G, int NW>
+__global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restrict__ x, int64_t ldx,
+                                                              const T* __restrict__ W, int64_t ldw, int n, int64_t N,
+                                                              int K, Epilogue ep) {
+  using P = RowsPiece<T>;
+  constexpr int U = 4, EL = 16 / int(sizeof(T));   // pieces in flight, elements of a piece
+  __shared__ __attribute__((aligned(16))) float part[NW * G * 256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  // rows past the end repeat the last one, their results are not written
+  const T* w = W + min(n0 + (lane & 15), N - 1) * ldw;
+  const T* xr[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) xr[g] = x + int64_t(min(16 * g + (lane & 15), n - 1)) * ldx;
+  const int pieces = (K + P::K - 1) / P::K, per = (pieces + NW - 1) / NW;
+  const int p0 = wave * per, p1 = min(pieces, p0 + per), k0 = EL * (lane >> 4);
+  f32x4 acc[G] = {};
+  int p = p0;
+  for (; (p + U) * P::K <= K && p + U <= p1; p += U) {
+    u32x4 wv[U], xv[U][G];
+#pragma unroll
+    for (int u = 0; u < U; ++u) wv[u] = *reinterpret_cast<const u32x4*>(w + (p + u) * P::K + k0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int g = 0; g < G; ++g) xv[u][g] = *reinterpret_cast<const u32x4*>(xr[g] + (p + u) * P::K + k0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int g = 0; g < G; ++g) P::mma(wv[u], xv[u][g], acc[g]);
+  }
+  for (; p < p1; ++p) {   // k past the end reads as zero on both sides
+    const int k = p * P::K + k0;
+    const bool in = k < K;
+    const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
+    const u32x4 wv = in ? *reinterpret_cast<const u32x4*>(w + k) : zero;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const u32x4 xv = in ? *reinterpret_cast<const u32x4*>(xr[g] + k) : zero;
+      P::mma(wv, xv, acc[g]);
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) *reinterpret_cast<f32x4*>(part + ((wave * G + g) * 64 + lane) * 4) = acc[g];
+  __syncthreads();
+  // accumulator element e of lane l: channel 4 (l / 16) + e, token l % 16
+  for (int i = threadIdx.x; i < G * 256; i += 64 * NW) {
+    const int t = i >> 4, c = i & 15;
+    const int64_t col = n0 + c;
+    if (t >= n || col >= N) continue;
+    const int at = (t >> 4) * 256 + ((c >> 2) * 16 + (t & 15)) * 4 + (c & 3);
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) v += part[q * G * 256 + at];
+    if (ep.bias != nullptr) v += ep.bias[col];
+    if (ep.z != nullptr) st_elem(static_cast<T*>(ep.z) + t * ep.ldz + col, v);
+    v = act_value(ep.act, v);
+    if (ep.res != nullptr) v += ld_elem(static_cast<const T*>(ep.res) + t * ep.ldr + col);
+    st_elem(static_cast<T*>(ep.y) + t * ep.ldy + col, v);
+  }
+}
+
+// Up to 16 tokens always; up to 64 where x, which every 16 channels read again, is small beside
+// a launch: bf16 weights up to 2^24 entries (4096 x 4096: 24 tokens 13 us against 22 on tiles
+// with split k, 64 tokens 23 against 22; 11008 x 4096: 24 tokens 36 against 25).  fp32 weights
+// would be split into three pieces first: always (4096 x 11008, 64 tokens: 124 us against 191).
+bool few_tokens(int64_t n, int64_t di, int64_t dn, size_t size) {
+  return n <= 16 || (n <= 64 && (size == 4 || di * dn <= (int64_t(1) << 24)));
+}
+
+template <class T>
+lrc_status linear_rows(hipStream_t st, const Operand& x, const Operand& W, int64_t n, int64_t dn, int64_t di,
+                       const Epilogue& ep, double bytes) {
+  ProfScope scope("linear_rows_kernel", st, 2.0 * double(n) * double(dn) * double(di), bytes);
+  const unsigned grid = unsigned(cdiv(dn, 16));
+  auto go = [&](auto groups) {
+    constexpr int G = decltype(groups)::value;
+    const T *xp = static_cast<const T*>(x.p), *wp = static_cast<const T*>(W.p);
+    // few channels: more waves share the k of each
+    if (grid <= 256)
+      linear_rows_kernel<T, G, 16><<<grid, 1024, 0, st>>>(xp, x.ld, wp, W.ld, int(n), dn, int(di), ep);
+    else
+      linear_rows_kernel<T, G, 8><<<grid, 512, 0, st>>>(xp, x.ld, wp, W.ld, int(n), dn, int(di), ep);
+  };
+  if (n <= 16)
+    go(std::integral_constant<int, 1>{});
+  else if (n <= 32)
+    go(std::integral_constant<int, 2>{});
+  else
+    go(std::integral_constant<int, 4>{});
+  LRC_LAUNCHED();
+  return LRC_OK;
 }
 
 // ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
@@ -363,7 +490,7 @@ LinearRoom forward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   Carve cv(ws);
   if (large_product(n, di, dn) && gemm_fits<T>(di, di)) {
     r.flag = cv.take<int32_t>(1);
-    r.partial = cv.take<float>(gemm_bf16_workspace(n, dn, di) / 4);
+    r.partial = cv.take<float>(gemm_bf16_workspace(n, dn, di, K_ROWS, K_ROWS) / 4);
     if (sizeof(T) == 4 || di % 8 != 0) {
       r.a = cv.take<uint16_t>(operand_room<T>(n, di));
       r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
@@ -379,7 +506,8 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   r.sums = cv.take<float>(size_t(col_plan(n).chunks) * dn);
   if (large_product(n, di, dn) && gemm_fits<T>(di, dn)) {
     r.flag = cv.take<int32_t>(1);
-    r.partial = cv.take<float>(std::max(gemm_bf16_workspace(n, di, dn), gemm_bf16_workspace(dn, di, n)) / 4);
+    r.partial = cv.take<float>(std::max(gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS),
+                                          gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS)) / 4);
     if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
     // W for dx, then x (a checkpoint becomes one bf16 piece) for dW
     r.b = cv.take<uint16_t>(sizeof(T) == 4 || di % 8 != 0 ? operand_room<T>(std::max(n, dn), di)
@@ -415,6 +543,9 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
   ep.info = info;
   const double bytes = double(sizeof(T)) * (double(n) * di + double(dn) * di + double(n) * dn * (res ? 2 : 1));
   const Operand ox = plain<T>(x, ldx), ow = plain<T>(W, ldw);
+  // the kept pre-activation's blocks of 64 channels need a tile that holds them
+  if (few_tokens(n, di, dn, sizeof(T)) && di % (16 / int(sizeof(T))) == 0 && ox.vec && ow.vec && zcodes == nullptr)
+    return linear_rows<T>(st, ox, ow, n, dn, di, ep, bytes);
   const LinearRoom room = forward_room<T>(ws, n, di, dn);
   if (room.flag == nullptr || !has_room<T>(ox, di) || !has_room<T>(ow, di) || std::max(ldx, ldw) > GEMM_MAX_LD)
     return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, nullptr, bytes);

@@ -103,9 +103,6 @@ __device__ __forceinline__ int ckpt_code(float v, float inv) {
   const float q = fminf(fmaxf(rintf(v * inv), -127.f), 127.f);
   return v == v ? int(q) : 0;
 }
-__device__ __forceinline__ uint32_t pack_codes4(int a, int b, int c, int d) {
-  return uint32_t(a & 255) | (uint32_t(b & 255) << 8) | (uint32_t(c & 255) << 16) | (uint32_t(d) << 24);
-}
 // eight codes times their block's step
 __device__ __forceinline__ void ld8_codes(const int8_t* p, bool vec, int cnt, float step, float (&v)[8]) {
   if (vec && cnt >= 8) {
@@ -120,29 +117,52 @@ __device__ __forceinline__ void ld8_codes(const int8_t* p, bool vec, int cnt, fl
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = e < cnt ? float(p[e]) * step : 0.f;
 }
+// Largest of the values of the eight lanes 8 i .. 8 i + 7, in each of them (three lane
+// permutations inside the vector unit: neighbours, pairs, mirrored halves).
+__device__ __forceinline__ uint32_t max_of_8(uint32_t u) {
+  u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0xb1, 0xf, 0xf, true)));
+  u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x4e, 0xf, 0xf, true)));
+  return max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x141, 0xf, 0xf, true)));
+}
 // Codes of eight consecutive values held by each of the eight lanes that share a block
 // (lanes 8 i .. 8 i + 7; every lane of the group takes part, `cnt` of its values exist).
+// Magnitudes are compared as integers, where NaN and infinities come out above every finite
+// one: a block without them, and below the exponent's upper end, needs no test per value, and
+// v * 2^-e + 1.5 * 2^23 has the code in its low byte (one rounding, ties to even).
 __device__ __forceinline__ void st8_codes(int8_t* p, int8_t* pe, bool vec, int cnt, const float (&v)[8], int lane,
                                           bool& bad) {
-  float m = 0.f;
+  uint32_t u = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < cnt) {
-      m = fmaxf(m, finite_mag(v[e]));
-      bad |= !finite_f(v[e]);
-    }
-  m = fmaxf(m, __shfl_xor(m, 1));
-  m = fmaxf(m, __shfl_xor(m, 2));
-  m = fmaxf(m, __shfl_xor(m, 4));
-  const int ex = ckpt_exponent(m);
-  const float inv = pow2f(-ex);
+  for (int e = 0; e < 8; ++e) u = max(u, e < cnt ? __float_as_uint(v[e]) & 0x7fffffffu : 0u);
+  u = max_of_8(u);
+  uint32_t q[8];
+  int ex;
+  if (u <= 0x7bfe0000u) {   // 127 * 2^121
+    ex = ckpt_exponent(__uint_as_float(u));
+    const float inv = pow2f(-ex);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(fmaf(v[e], inv, 12582912.f));
+  } else {
+    uint32_t f = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < cnt) {
+        f = max(f, __float_as_uint(finite_mag(v[e])));
+        bad |= !finite_f(v[e]);
+      }
+    ex = ckpt_exponent(__uint_as_float(max_of_8(f)));
+    const float inv = pow2f(-ex);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = uint32_t(ckpt_code(v[e], inv));
+  }
   if (cnt <= 0) return;
-  int q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = ckpt_code(v[e], inv);
   if (vec && cnt >= 8) {
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(pack_codes4(q[0], q[1], q[2], q[3]), pack_codes4(q[4], q[5], q[6], q[7]));
+    // the low bytes of four words in one
+    auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+      return lo | hi;
+    };
+    *reinterpret_cast<uint2*>(p) = make_uint2(four(q[0], q[1], q[2], q[3]), four(q[4], q[5], q[6], q[7]));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -218,28 +238,31 @@ struct Epilogue {
   bool vec_y = false, vec_r = false, vec_z = false, vec_c = false;
 };
 
+// the bias of eight consecutive columns, of which `cnt` exist
+__device__ __forceinline__ void bias8(const Epilogue& ep, int64_t col, int cnt, float (&b)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = ep.bias != nullptr && e < cnt ? ep.bias[col + e] : 0.f;
+}
 // Eight consecutive columns of one row.  Lanes 8 i .. 8 i + 7 of a wave hold the 64 columns
 // of one block of the row and call this together; `cnt` of the lane's columns exist.
 template <class TO>
-__device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t col, int cnt, float (&v)[8], int lane,
-                                        bool& bad) {
+__device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t col, int cnt, const float (&b)[8],
+                                        float (&v)[8], int lane, bool& bad) {
+  float r[8];
+  if (ep.res != nullptr) ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, ep.vec_r, cnt, r);
   if (ep.bias != nullptr) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += e < cnt ? ep.bias[col + e] : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] += b[e];
   }
   if (ep.z != nullptr && cnt > 0) st8(static_cast<TO*>(ep.z) + row * ep.ldz + col, ep.vec_z, cnt, v);
-  if (ep.codes != nullptr) {
-    const int64_t n = ep.nb;
-    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * n + (col >> 6), ep.vec_c, cnt, v, lane, bad);
-  }
+  if (ep.codes != nullptr)
+    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * ep.nb + (col >> 6), ep.vec_c, cnt, v, lane, bad);
   if (cnt <= 0) return;
   if (ep.act != LRC_ACT_NONE) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = act_value(ep.act, v[e]);
   }
   if (ep.res != nullptr) {
-    float r[8];
-    ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, ep.vec_r, cnt, r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
@@ -268,7 +291,7 @@ template <class TO, int KA, int KB>
 lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperand B, int64_t M, int64_t N, int64_t K,
                      const GemmSegments& seg, const Epilogue& ep, float* partial, const int32_t* skip, double flops,
                      double bytes);
-size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K);
+size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB);
 
 // ---- column sums ---------------------------------------------------------------------
 // out0[c] (c < split) and out1[c - split] (c >= split) = sum over p < parts of
