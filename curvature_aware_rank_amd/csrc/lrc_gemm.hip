@@ -133,7 +133,6 @@ struct Stager {
 };
 
 struct TileGrid {
-  int64_t m_base, n_base;    // first row and column of the part of D that the tiles cover
   int64_t nm, nn, tiles;
   int per_xcd, splits;
   int steps_per_split;   // stages of one split
@@ -173,7 +172,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   if (ti >= tg.tiles) return;
   int64_t tm, tn;
   tile_at(ti, tg.nm, tg.nn, tm, tn);
-  const int64_t m0 = tg.m_base + tm * BM, n0 = tg.n_base + tn * BN;
+  const int64_t m0 = tm * BM, n0 = tn * BN;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -419,25 +418,21 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
 
 // Tiles and splits from the sizes alone (256 compute units), so that workspace sizes are known
 // without a device and equal inputs give equal bits.  Large tiles (256 x 256, one workgroup per
-// compute unit, 1250 TFLOP/s at 4096^3) for products that fill the chip in whole rounds; small
-// ones (128 x 128, two per unit, 1060) otherwise, with k split when they are few, and for what a
-// last round of large tiles would leave most units idle on.  Times below in microseconds, taken
-// at 256 x 4096 x 4096 to 8192 x 4096 x 11008.
-struct Part {
+// compute unit, 1200 TFLOP/s at 4096^3) for products that fill the chip; small ones (128 x 128, two
+// per unit, 1060) otherwise, with k split when they are few.  Small tiles for what a last, part
+// full round of large ones holds gained nothing (8192 x 4096 x 11008, 5.4 rounds: 695 us against
+// 690): the chip is then at its power limit, and units that idle let the others run faster.  Times
+// below in microseconds, taken at 256 x 4096 x 4096 to 8192 x 4096 x 11008.
+struct Plan {
   bool large;
   TileGrid tg;
-};
-struct Plan {
-  int parts = 0;
-  Part part[2];
 };
 // 64 k steps of every workgroup of a round; a round's first loads and its epilogue
 constexpr double LARGE_STEP = 1.65, SMALL_STEP_FULL = 1.0, SMALL_STEP_HALF = 0.68, ROUND = 7.0, MEMORY = 4.5e6;
 
-static TileGrid tiles_of(int64_t m_base, int64_t m, int64_t n_base, int64_t n, int edge, int splits, int64_t per,
-                         int64_t steps) {
+static TileGrid tiles_of(int64_t m, int64_t n, int edge, int splits, int64_t per, int64_t steps) {
   const int64_t nm = cdiv(m, edge), nn = cdiv(n, edge);
-  return {m_base, n_base, nm, nn, nm * nn, int(cdiv(nm * nn, NXCD)), splits, int(per), int(steps)};
+  return {nm, nn, nm * nn, int(cdiv(nm * nn, NXCD)), splits, int(per), int(steps)};
 }
 static double large_cost(int64_t tiles, double steps64) {
   return double(cdiv(tiles, 256)) * (steps64 * LARGE_STEP + ROUND);
@@ -451,45 +446,28 @@ static double small_cost(int64_t groups, double steps64) {
 // KL: k steps per stage of a large tile
 static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL) {
   Plan best;
-  double cost = 1e300;
   const int64_t steps_l = cdiv(K, KL), steps_s = cdiv(K, 64);
   const double s64 = double(steps_s) * count;
   const double floor_us = 2.0 * double(K) * double(M + N) * (count > 1 ? 3 : 1) / MEMORY;
-  const int64_t nm = cdiv(M, 256), nn = cdiv(N, 256), tiles = nm * nn;
-  auto take = [&](double c, int parts, const Part& a, const Part& b) {
-    if (c >= cost) return;
-    cost = c;
-    best.parts = parts;
-    best.part[0] = a;
-    best.part[1] = b;
-  };
-  const Part whole = {true, tiles_of(0, M, 0, N, 256, 1, steps_l * count, steps_l)};
-  take(std::max(floor_us, large_cost(tiles, s64)), 1, whole, whole);
-  const int64_t full = tiles / 256 * 256;   // tiles of whole rounds
-  if (full > 0 && full < tiles) {           // columns, or rows, of tiles that fill whole rounds; small tiles behind
-    for (int rows = 0; rows < 2; ++rows) {
-      const int64_t keep = full / (rows ? nn : nm);
-      if (keep <= 0 || keep >= (rows ? nm : nn)) continue;
-      const int64_t at = keep * 256, m = rows ? M - at : M, n = rows ? N : N - at;
-      const Part a = {true, rows ? tiles_of(0, at, 0, N, 256, 1, steps_l * count, steps_l)
-                                 : tiles_of(0, M, 0, at, 256, 1, steps_l * count, steps_l)};
-      const Part b = {false, tiles_of(rows ? at : 0, m, rows ? 0 : at, n, 128, 1, steps_s * count, steps_s)};
-      take(large_cost(a.tg.tiles, s64) + small_cost(b.tg.tiles, s64), 2, a, b);
-    }
-  }
+  best.large = true;
+  best.tg = tiles_of(M, N, 256, 1, steps_l * count, steps_l);
+  double cost = std::max(floor_us, large_cost(best.tg.tiles, s64));
   const int64_t total = steps_s * count;
   for (int64_t s = 1; s <= std::min<int64_t>(32, total); ++s) {
     const int64_t per = cdiv(total, s);
     if (cdiv(total, per) != s) continue;
-    const Part p = {false, tiles_of(0, M, 0, N, 128, int(s), per, steps_s)};
-    double c = std::max(floor_us, small_cost(p.tg.tiles * s, double(per)));
+    const TileGrid tg = tiles_of(M, N, 128, int(s), per, steps_s);
+    double c = std::max(floor_us, small_cost(tg.tiles * s, double(per)));
     if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
-    take(c, 1, p, p);
+    if (c < cost) {
+      cost = c;
+      best = {false, tg};
+    }
   }
   return best;
 }
 static size_t plan_bytes(const Plan& p, int64_t M, int64_t N) {
-  return p.part[0].tg.splits > 1 ? size_t(p.part[0].tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
+  return p.tg.splits > 1 ? size_t(p.tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
 }
 constexpr int large_stage(int ka, int kb) { return ka == K_ROWS && kb == K_ROWS ? 64 : 32; }
 
@@ -503,6 +481,19 @@ size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB) {
   return most;
 }
 
+template <class TO>
+lrc_status gemm_finish(hipStream_t st, const float* partial, int splits, int64_t M, int64_t N, const Epilogue& ep,
+                       const int32_t* skip) {
+  const int64_t np = (N + 7) & ~int64_t(7), blocks = cdiv(N, CKB), threads = M * blocks * 8;
+  if (cdiv(threads, 256) >= (int64_t(1) << 31)) return LRC_EINVAL;
+  gemm_finish_kernel<TO><<<unsigned(cdiv(threads, 256)), 256, 0, st>>>(partial, splits, M, N, np, blocks, ep, skip);
+  LRC_LAUNCHED();
+  return LRC_OK;
+}
+template lrc_status gemm_finish<float>(hipStream_t, const float*, int, int64_t, int64_t, const Epilogue&, const int32_t*);
+template lrc_status gemm_finish<uint16_t>(hipStream_t, const float*, int, int64_t, int64_t, const Epilogue&,
+                                          const int32_t*);
+
 template <class TO, int KA, int KB>
 lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperand B, int64_t M, int64_t N, int64_t K,
                      const GemmSegments& seg, const Epilogue& ep, float* partial, const int32_t* skip, double flops,
@@ -513,34 +504,27 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   constexpr int KL = large_stage(KA, KB), NL = KL == 64 ? 2 : 4;
   const Plan p = plan_gemm(M, N, K, seg.count, KL);
   ProfScope scope(name, st, flops, bytes);
-  auto launch = [&](auto many, const Part& part) -> lrc_status {
+  const TileGrid& tg = p.tg;
+  const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
+  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  auto launch = [&](auto many) {
     constexpr bool SEG = decltype(many)::value;
-    const TileGrid& tg = part.tg;
-    const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
-    if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-    if (part.large)
+    if (p.large)
       gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, KL, NL, SEG><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, tg, ep,
                                                                                             partial, skip);
     else
       gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, 64, 2, SEG><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, tg, ep,
                                                                                            partial, skip);
-    LRC_LAUNCHED();
-    return LRC_OK;
   };
-  for (int i = 0; i < p.parts; ++i) {
-    // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
-    if (std::is_same<TO, uint16_t>::value || seg.count == 1)
-      LRC_TRY(launch(std::false_type{}, p.part[i]));
-    else if constexpr (!std::is_same<TO, uint16_t>::value)
-      LRC_TRY(launch(std::true_type{}, p.part[i]));
-  }
-  const int splits = p.part[0].tg.splits;
-  if (splits == 1) return LRC_OK;
-  const int64_t np = (N + 7) & ~int64_t(7), blocks = cdiv(N, CKB), threads = M * blocks * 8;
-  if (cdiv(threads, 256) >= (int64_t(1) << 31)) return LRC_EINVAL;
-  gemm_finish_kernel<TO><<<unsigned(cdiv(threads, 256)), 256, 0, st>>>(partial, splits, M, N, np, blocks, ep, skip);
+  // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
+  if (std::is_same<TO, uint16_t>::value || seg.count == 1)
+    launch(std::false_type{});
+  else if constexpr (!std::is_same<TO, uint16_t>::value)
+    launch(std::true_type{});
   LRC_LAUNCHED();
-  return LRC_OK;
+  if (tg.splits == 1) return LRC_OK;
+  const int splits = tg.splits;
+  return gemm_finish<TO>(st, partial, splits, M, N, ep, skip);
 }
 
 #define LRC_GEMM(TO, KA, KB)                                                                                   \

@@ -26,12 +26,16 @@ struct Operand {
 };
 
 // ---- any size, stride and alignment: 64 x 64 tiles, four waves of 32 x 32 ---------------
+// Operands pass through registers into LDS as [row][k], a step ahead of the products; two LDS
+// buffers, one barrier a step.  Bound by the latency of a step's loads where tiles are few, so k
+// is then split over workgroups and the splits' tiles are added in order by a second kernel.
 constexpr int GT = 64;    // tile edge
-constexpr int GK = 32;    // k per step
 
 template <class T>
 struct GTile {
-  static constexpr int PITCH = sizeof(T) == 2 ? GK + 8 : GK + 4;
+  static constexpr int K = sizeof(T) == 2 ? 64 : 32;   // k per step: 128 bytes of a row
+  static constexpr int PITCH = sizeof(T) == 2 ? K + 8 : K + 4;
+  static constexpr int PIECES = GT * K / 8 / LT;       // pieces of eight of a thread and step
 };
 
 // Eight values of an operand as T bits: for K_ROWS along k at (row, k), for the others along
@@ -63,80 +67,143 @@ __device__ __forceinline__ void lds_put8(uint16_t* p, const float (&v)[8]) {
                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// One step of an operand into LDS as [row][k].
+// Piece i of a thread: its tile row and k (K_ROWS: along k, else along the rows).
 template <class T, int KIND>
-__device__ __forceinline__ void stage_any(const Operand& o, T* lds, int64_t row0, int64_t k0, int64_t rows, int64_t kk) {
-  constexpr int P = GTile<T>::PITCH;
-  float v[8];
+__device__ __forceinline__ void piece_at(int i, int& row, int& k) {
+  const int p = threadIdx.x + LT * i;
   if (KIND == K_ROWS) {
-    const int r = threadIdx.x >> 2, k = (threadIdx.x & 3) * 8;
-    operand8<T, KIND>(o, row0 + r, k0 + k, rows, kk, v);
-    lds_put8(lds + r * P + k, v);
+    row = p / (GTile<T>::K / 8);
+    k = p % (GTile<T>::K / 8) * 8;
   } else {
-    const int k = threadIdx.x >> 3, r = (threadIdx.x & 7) * 8;
-    operand8<T, KIND>(o, row0 + r, k0 + k, rows, kk, v);
+    k = p >> 3;
+    row = (p & 7) * 8;
+  }
+}
+template <class T, int KIND>
+__device__ __forceinline__ void fetch_any(const Operand& o, int64_t row0, int64_t k0, int64_t rows, int64_t kk,
+                                          float (&v)[GTile<T>::PIECES][8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) st_elem(lds + (r + e) * P + k, v[e]);
+  for (int i = 0; i < GTile<T>::PIECES; ++i) {
+    int row, k;
+    piece_at<T, KIND>(i, row, k);
+    operand8<T, KIND>(o, row0 + row, k0 + k, rows, kk, v[i]);
+  }
+}
+template <class T, int KIND>
+__device__ __forceinline__ void store_any(T* lds, const float (&v)[GTile<T>::PIECES][8]) {
+  constexpr int P = GTile<T>::PITCH;
+#pragma unroll
+  for (int i = 0; i < GTile<T>::PIECES; ++i) {
+    int row, k;
+    piece_at<T, KIND>(i, row, k);
+    if (KIND == K_ROWS) {
+      lds_put8(lds + row * P + k, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) st_elem(lds + (row + e) * P + k, v[i][e]);
+    }
   }
 }
 
 __device__ __forceinline__ void mma_any(const uint16_t* a, const uint16_t* b, int lane, f32x4& acc) {
   const int off = (lane & 15) * GTile<uint16_t>::PITCH + 8 * (lane >> 4);
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(a + off),
-                                                *reinterpret_cast<const bf16x8*>(b + off), acc, 0, 0, 0);
+#pragma unroll
+  for (int s = 0; s < GTile<uint16_t>::K; s += 32)
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(a + off + s),
+                                                  *reinterpret_cast<const bf16x8*>(b + off + s), acc, 0, 0, 0);
 }
 __device__ __forceinline__ void mma_any(const float* a, const float* b, int lane, f32x4& acc) {
   const int off = (lane & 15) * GTile<float>::PITCH + (lane >> 4);
 #pragma unroll
-  for (int s = 0; s < GK / 4; ++s)
-    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[off + 4 * s], b[off + 4 * s], acc, 0, 0, 0);
+  for (int s = 0; s < GTile<float>::K; s += 4)
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[off + s], b[off + s], acc, 0, 0, 0);
 }
 
+struct AnyPlan {
+  int64_t tiles_n, tiles;
+  int splits;
+  int64_t k_per_split;
+};
+template <class T>
+AnyPlan plan_any(int64_t M, int64_t N, int64_t K) {
+  AnyPlan p;
+  p.tiles_n = cdiv(N, GT);
+  p.tiles = cdiv(M, GT) * p.tiles_n;
+  const int64_t steps = std::max<int64_t>(1, cdiv(K, GTile<T>::K));
+  // up to two workgroups per compute unit, eight steps at least in each split (a second launch
+  // and the partial tiles cost about as much as eight steps)
+  const int64_t s = std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, p.tiles), steps / 8, 16}));
+  const int64_t per = cdiv(steps, s);
+  p.splits = int(cdiv(steps, per));
+  p.k_per_split = per * GTile<T>::K;
+  return p;
+}
+
+// `only`: NULL, or a device word without which the product is not wanted.  The workgroups take
+// tiles in turn, so that a product that is not wanted costs few of them.
 template <class T, class TO, int KA, int KB>
 __global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
-                                                        int64_t tiles_n, Epilogue ep, const int32_t* __restrict__ only) {
+                                                        AnyPlan plan, Epilogue ep, float* __restrict__ partial,
+                                                        const int32_t* __restrict__ only) {
   if (only != nullptr && *only == 0) return;
-  constexpr int P = GTile<T>::PITCH;
+  constexpr int P = GTile<T>::PITCH, PC = GTile<T>::PIECES, BK = GTile<T>::K;
   constexpr int EP = GT + 4;   // epilogue tile pitch
-  __shared__ __attribute__((aligned(16))) uint8_t lds[GT * EP * 4 > 2 * GT * P * int(sizeof(T))
-                                                          ? GT * EP * 4
-                                                          : 2 * GT * P * int(sizeof(T))];
-  T* la = reinterpret_cast<T*>(lds);
-  T* lb = la + GT * P;
-  const int64_t m0 = int64_t(blockIdx.x) / tiles_n * GT, n0 = int64_t(blockIdx.x) % tiles_n * GT;
+  constexpr int STAGE = 2 * GT * P * int(sizeof(T));
+  __shared__ __attribute__((aligned(16))) uint8_t lds[GT * EP * 4 > 2 * STAGE ? GT * EP * 4 : 2 * STAGE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
-  f32x4 acc[2][2] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += GK) {
-    stage_any<T, KA>(A, la, m0, k0, M, K);
-    stage_any<T, KB>(B, lb, n0, k0, N, K);
+  const int split = blockIdx.y;
+  const int64_t k_begin = int64_t(split) * plan.k_per_split, k_end = min(K, k_begin + plan.k_per_split);
+  bool bad = false;
+  for (int64_t tile_i = blockIdx.x; tile_i < plan.tiles; tile_i += gridDim.x) {
+    const int64_t m0 = tile_i / plan.tiles_n * GT, n0 = tile_i % plan.tiles_n * GT;
+    f32x4 acc[2][2] = {};
+    float va[PC][8], vb[PC][8];
+    fetch_any<T, KA>(A, m0, k_begin, M, k_end, va);
+    fetch_any<T, KB>(B, n0, k_begin, N, k_end, vb);
+    int buf = 0;
+    for (int64_t k0 = k_begin; k0 < k_end; k0 += BK, buf ^= 1) {
+      T* la = reinterpret_cast<T*>(lds + buf * STAGE);
+      T* lb = la + GT * P;
+      store_any<T, KA>(la, va);
+      store_any<T, KB>(lb, vb);
+      if (k0 + BK < k_end) {
+        fetch_any<T, KA>(A, m0, k0 + BK, M, k_end, va);
+        fetch_any<T, KB>(B, n0, k0 + BK, N, k_end, vb);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma_any(la + (wr + 16 * i) * P, lb + (wc + 16 * j) * P, lane, acc[i][j]);
+    }
     __syncthreads();
+    float* tile = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) mma_any(la + (wr + 16 * i) * P, lb + (wc + 16 * j) * P, lane, acc[i][j]);
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          tile[(wr + 16 * i + 4 * (lane >> 4) + e) * EP + wc + 16 * j + (lane & 15)] = acc[i][j][e];
     __syncthreads();
-  }
-  float* tile = reinterpret_cast<float*>(lds);
+    const int64_t col = n0 + 8 * (lane & 7), np = (N + 7) & ~int64_t(7);
+    float bias[8];
+    bias8(ep, col, int(min(N - col, int64_t(8))), bias);
+    for (int r = threadIdx.x >> 3; r < GT; r += LT / 8) {
+      const int64_t row = m0 + r;
+      const int64_t left = row < M ? N - col : 0;
+      const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
+      float v[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        tile[(wr + 16 * i + 4 * (lane >> 4) + e) * EP + wc + 16 * j + (lane & 15)] = acc[i][j][e];
-  __syncthreads();
-  bool bad = false;
-  const int64_t col = n0 + 8 * (lane & 7);
-  float bias[8];
-  bias8(ep, col, int(min(N - col, int64_t(8))), bias);
-  for (int r = threadIdx.x >> 3; r < GT; r += LT / 8) {
-    const int64_t row = m0 + r;
-    const int64_t left = row < M ? N - col : 0;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[r * EP + 8 * (lane & 7) + e];
-    finish8<TO>(ep, row, col, int(left < 0 ? 0 : left > 8 ? 8 : left), bias, v, lane, bad);
+      for (int e = 0; e < 8; ++e) v[e] = tile[r * EP + 8 * (lane & 7) + e];
+      if (plan.splits > 1) {
+        if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, true, 8, v);
+      } else {
+        finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);
+      }
+    }
+    __syncthreads();   // the tile is read before the next one's steps
   }
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
@@ -283,8 +350,10 @@ __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_
                                                 const T* __restrict__ z, int64_t ldz,
                                                 const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
                                                 int64_t nb, int act, T* __restrict__ dz, int64_t lddz, int64_t rows,
-                                                bool vec, bool vec_z, float* __restrict__ partial) {
+                                                bool vec, bool vec_z, float* __restrict__ partial,
+                                                int32_t* __restrict__ clear) {
   __shared__ float sums[3][64][9];
+  if (clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *clear = 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t(blockIdx.x) * 64 + lane) * 8;
   const int64_t left = d - c;
@@ -369,23 +438,36 @@ __device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, floa
   st8(o + 2 * w8, true, 8, v);
   if (bad) *flag = 1;
 }
-template <class T, bool CODES>
-__global__ __launch_bounds__(LT) void operand_kernel(const void* __restrict__ p, int64_t ld,
-                                                     const int8_t* __restrict__ exps, int64_t nb, bool vec,
-                                                     int64_t rows, int64_t cols, int64_t w8, int planes,
-                                                     uint16_t* __restrict__ out, int32_t* __restrict__ flag) {
-  const int64_t i = int64_t(blockIdx.x) * LT + threadIdx.x, per = w8 / 8;
-  if (i >= rows * per) return;
+// Up to three operands in one launch: a workgroup belongs to the job its index falls into.
+struct OperandJob {
+  const void* p = nullptr;
+  const int8_t* exps = nullptr;   // codes if not NULL
+  uint16_t* out = nullptr;
+  int64_t ld = 0, nb = 0, rows = 0, cols = 0, w8 = 0, blocks = 0;
+  int planes = 1;
+  bool vec = false;
+};
+struct OperandJobs {
+  OperandJob job[3];
+};
+template <class T>
+__global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* __restrict__ flag) {
+  int64_t block = blockIdx.x;
+  int q = 0;
+  while (q < 2 && block >= jobs.job[q].blocks) block -= jobs.job[q++].blocks;
+  const OperandJob& j = jobs.job[q];
+  const int64_t i = block * LT + threadIdx.x, per = j.w8 / 8;
+  if (i >= j.rows * per) return;
   const int64_t r = i / per, c = i % per * 8;
-  const int cnt = int(cols - c > 8 ? 8 : cols - c);
+  const int cnt = int(j.cols - c > 8 ? 8 : j.cols - c);
   float v[8];
-  uint16_t* o = out + r * planes * w8 + c;
-  if (CODES) {
-    ld8_codes(static_cast<const int8_t*>(p) + r * ld + c, vec, cnt, pow2f(exps[r * nb + (c >> 6)]), v);
-    split_store<uint16_t>(o, w8, v, flag);
+  uint16_t* o = j.out + r * j.planes * j.w8 + c;
+  if (j.exps != nullptr) {
+    ld8_codes(static_cast<const int8_t*>(j.p) + r * j.ld + c, j.vec, cnt, pow2f(j.exps[r * j.nb + (c >> 6)]), v);
+    split_store<uint16_t>(o, j.w8, v, flag);
   } else {
-    ld8(static_cast<const T*>(p) + r * ld + c, vec, cnt, v);
-    split_store<T>(o, w8, v, flag);
+    ld8(static_cast<const T*>(j.p) + r * j.ld + c, j.vec, cnt, v);
+    split_store<T>(o, j.w8, v, flag);
   }
 }
 __global__ void clear_flag_kernel(int32_t* flag) { *flag = 0; }
@@ -403,26 +485,40 @@ struct Prepared {
   int planes;
 };
 
+// Adds the operand to the jobs if it cannot be read where it lies.
 template <class T>
-lrc_status prepare_operand(hipStream_t st, const Operand& o, bool codes, int64_t rows, int64_t cols, uint16_t* room,
-                           int32_t* flag, Prepared& out) {
-  if (sizeof(T) == 2 && !codes && o.vec && cols % 8 == 0) {   // read in place
-    out = {{static_cast<const uint16_t*>(o.p), o.ld, 0}, 1};
-    return LRC_OK;
+Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t rows, int64_t cols, uint16_t* room) {
+  const bool codes = o.exps != nullptr;
+  if (sizeof(T) == 2 && !codes && o.vec && cols % 8 == 0)
+    return {{static_cast<const uint16_t*>(o.p), o.ld, 0}, 1};
+  OperandJob& j = jobs.job[count++];
+  j.p = o.p;
+  j.exps = o.exps;
+  j.out = room;
+  j.ld = o.ld;
+  j.nb = o.nb;
+  j.rows = rows;
+  j.cols = cols;
+  j.w8 = round8(cols);
+  j.planes = sizeof(T) == 4 && !codes ? 3 : 1;
+  j.vec = o.vec;
+  j.blocks = cdiv(rows * (j.w8 / 8), LT);
+  return {{room, j.planes * j.w8, j.w8}, j.planes};
+}
+template <class T>
+lrc_status prepare_operands(hipStream_t st, const OperandJobs& jobs, int count, int32_t* flag) {
+  if (count == 0) return LRC_OK;
+  int64_t grid = 0;
+  double bytes = 0;
+  for (int i = 0; i < count; ++i) {
+    const OperandJob& j = jobs.job[i];
+    grid += j.blocks;
+    bytes += double(j.rows) * double(j.cols) * ((j.exps ? 1.0 : double(sizeof(T))) + 2.0 * j.planes);
   }
-  const int64_t w8 = round8(cols), grid = cdiv(rows * (w8 / 8), LT);
-  const int planes = sizeof(T) == 4 && !codes ? 3 : 1;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-  ProfScope scope("linear_operand_kernel", st, 0.0,
-                  double(rows) * double(cols) * ((codes ? 1.0 : double(sizeof(T))) + 2.0 * planes));
-  if (codes)
-    operand_kernel<T, true><<<unsigned(grid), LT, 0, st>>>(o.p, o.ld, o.exps, o.nb, o.vec, rows, cols, w8, planes,
-                                                           room, flag);
-  else
-    operand_kernel<T, false><<<unsigned(grid), LT, 0, st>>>(o.p, o.ld, nullptr, 0, o.vec, rows, cols, w8, planes, room,
-                                                            flag);
+  ProfScope scope("linear_operand_kernel", st, 0.0, bytes);
+  operand_kernel<T><<<unsigned(grid), LT, 0, st>>>(jobs, flag);
   LRC_LAUNCHED();
-  out = {{room, planes * w8, w8}, planes};
   return LRC_OK;
 }
 
@@ -444,10 +540,19 @@ GemmSegments segments(int pa, int pb) {
   return s;
 }
 
-// Whether a product goes to the matrix-core path for large tiles.  Below this much work the
-// passes that prepare its operands cost more than they save.
+// Whether the products go to the pipelined tiles (lrc_gemm.hip) or to the ones that take any
+// operand.  Measured, both ways, forward / backward: bf16 3 x 141 x 1668 15 / 30 us against
+// 12 / 46, 1000 x 521 x 303 19 / 39 against 33 / 71, 2048 x 2048 x 1024 27 / 54 against 60 / 152:
+// pipelined ones from 2^18 products.  fp32 splits its operands first: 512^3 26 / 51 against 15 / 37,
+// 1024^3 42 / 81 against 32 / 81, 1001 x 1023 x 1021 44 / 88 against 57 / 114, 128 x 4096 x 4096
+// 77 / 127 against 50 / 127, 2048 x 2048 x 1024 80 / 159 against 86 / 224: from 2^30 and with no
+// extent so short that the splitting outweighs the products.
+template <class T>
 bool large_product(int64_t n, int64_t di, int64_t dn) {
-  return double(n) * double(di) * double(dn) >= double(1 << 24) && n <= GEMM_MAX_K;
+  const double work = double(n) * double(di) * double(dn);
+  if (n > GEMM_MAX_K) return false;
+  return sizeof(T) == 2 ? work >= double(1 << 18)
+                        : work >= double(1 << 30) && std::min({n, di, dn}) >= 192;
 }
 template <class T>
 bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two operands
@@ -456,13 +561,19 @@ bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two ope
 
 template <class T, class TO, int KA, int KB>
 lrc_status product_any(hipStream_t st, const char* name, const Operand& A, const Operand& B, int64_t M, int64_t N,
-                       int64_t K, const Epilogue& ep, const int32_t* only, double bytes) {
-  const int64_t tn = cdiv(N, GT), grid = cdiv(M, GT) * tn;
-  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+                       int64_t K, const Epilogue& ep, float* partial, const int32_t* only, double bytes) {
+  AnyPlan p = plan_any<T>(M, N, K);
+  if (only) p.splits = 1, p.k_per_split = K;
   ProfScope scope(name, st, only ? 0.0 : 2.0 * double(M) * double(N) * double(K), only ? 0.0 : bytes);
-  linear_any_kernel<T, TO, KA, KB><<<unsigned(grid), LT, 0, st>>>(A, B, M, N, K, tn, ep, only);
+  const dim3 grid(unsigned(std::min<int64_t>(p.tiles, only ? 1024 : int64_t(1) << 20)), unsigned(p.splits));
+  linear_any_kernel<T, TO, KA, KB><<<grid, LT, 0, st>>>(A, B, M, N, K, p, ep, partial, only);
   LRC_LAUNCHED();
-  return LRC_OK;
+  return p.splits > 1 ? gemm_finish<TO>(st, partial, p.splits, M, N, ep, nullptr) : LRC_OK;
+}
+template <class T>
+size_t any_room(int64_t M, int64_t N, int64_t K) {
+  const AnyPlan p = plan_any<T>(M, N, K);
+  return p.splits > 1 ? size_t(p.splits) * M * round8(N) : 0;
 }
 
 template <class T>
@@ -481,16 +592,19 @@ struct LinearRoom {
   int32_t* flag = nullptr;      // an fp32 operand holds an entry that is not finite
   float* partial = nullptr;     // split products
   float* sums = nullptr;        // db chunks
-  uint16_t *a = nullptr, *b = nullptr;   // operands
+  uint16_t *a = nullptr, *b = nullptr, *c = nullptr;   // operands
   size_t bytes = 0;
 };
 template <class T>
 LinearRoom forward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   LinearRoom r;
   Carve cv(ws);
-  if (large_product(n, di, dn) && gemm_fits<T>(di, di)) {
+  size_t part = any_room<T>(n, dn, di);
+  const bool large = large_product<T>(n, di, dn) && gemm_fits<T>(di, di);
+  if (large) part = std::max(part, gemm_bf16_workspace(n, dn, di, K_ROWS, K_ROWS) / 4);
+  r.partial = cv.take<float>(part);
+  if (large) {
     r.flag = cv.take<int32_t>(1);
-    r.partial = cv.take<float>(gemm_bf16_workspace(n, dn, di, K_ROWS, K_ROWS) / 4);
     if (sizeof(T) == 4 || di % 8 != 0) {
       r.a = cv.take<uint16_t>(operand_room<T>(n, di));
       r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
@@ -504,14 +618,17 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   LinearRoom r;
   Carve cv(ws);
   r.sums = cv.take<float>(size_t(col_plan(n).chunks) * dn);
-  if (large_product(n, di, dn) && gemm_fits<T>(di, dn)) {
+  size_t part = std::max(any_room<T>(n, di, dn), any_room<T>(dn, di, n));
+  const bool large = large_product<T>(n, di, dn) && gemm_fits<T>(di, dn);
+  if (large)
+    part = std::max({part, gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS) / 4,
+                     gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS) / 4});
+  r.partial = cv.take<float>(part);
+  if (large) {
     r.flag = cv.take<int32_t>(1);
-    r.partial = cv.take<float>(std::max(gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS),
-                                          gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS)) / 4);
     if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
-    // W for dx, then x (a checkpoint becomes one bf16 piece) for dW
-    r.b = cv.take<uint16_t>(sizeof(T) == 4 || di % 8 != 0 ? operand_room<T>(std::max(n, dn), di)
-                                                          : operand_room<T>(n, di));
+    if (sizeof(T) == 4 || di % 8 != 0) r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
+    r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x, also a checkpoint's values
   }
   r.bytes = cv.bytes();
   return r;
@@ -548,20 +665,22 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
     return linear_rows<T>(st, ox, ow, n, dn, di, ep, bytes);
   const LinearRoom room = forward_room<T>(ws, n, di, dn);
   if (room.flag == nullptr || !has_room<T>(ox, di) || !has_room<T>(ow, di) || std::max(ldx, ldw) > GEMM_MAX_LD)
-    return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, nullptr, bytes);
+    return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, room.partial, nullptr, bytes);
   const int32_t* flag = sizeof(T) == 4 ? room.flag : nullptr;
   if (flag) {
     clear_flag_kernel<<<1, 1, 0, st>>>(room.flag);
     LRC_LAUNCHED();
   }
-  Prepared a, b;
-  LRC_TRY(prepare_operand<T>(st, ox, false, n, di, room.a, room.flag, a));
-  LRC_TRY(prepare_operand<T>(st, ow, false, dn, di, room.b, room.flag, b));
+  OperandJobs jobs;
+  int count = 0;
+  const Prepared a = want_operand<T>(jobs, count, ox, n, di, room.a);
+  const Prepared b = want_operand<T>(jobs, count, ow, dn, di, room.b);
+  LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   LRC_TRY((gemm_bf16<T, K_ROWS, K_ROWS>(st, "linear_kernel", a.op, b.op, n, dn, di,
                                         segments(a.planes, b.planes), ep, room.partial, flag,
                                         2.0 * double(n) * double(dn) * double(di), bytes)));
   if (!flag) return LRC_OK;
-  return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, flag, bytes);
+  return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, room.partial, flag, bytes);
 }
 
 }  // namespace
@@ -631,9 +750,19 @@ template <class T>
 lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const LinearRoom room = backward_room<T>(ws, a.n, a.di, a.dn);
   const int64_t n = a.n, di = a.di, dn = a.dn;
-  const void* g = a.dy;
-  int64_t ldg = a.lddy;
-  if (a.act != LRC_ACT_NONE || a.db != nullptr) {
+  const bool with_dz = a.act != LRC_ACT_NONE;
+  const void* g = with_dz ? a.dz : a.dy;
+  const int64_t ldg = with_dz ? a.lddz : a.lddy;
+  const Operand og = plain<T>(g, ldg), ow = plain<T>(a.W, a.ldw);
+  const bool held = a.x == nullptr;
+  const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB),
+                                    di % 8 == 0 && (reinterpret_cast<uintptr_t>(a.xcodes) & 7) == 0}
+                          : plain<T>(a.x, a.ldx);
+  const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
+  const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD;
+  const bool fast_dw = fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD));
+  int32_t* flag = sizeof(T) == 4 && (fast_dx || fast_dw) ? room.flag : nullptr;
+  if (with_dz || a.db != nullptr) {
     const ColPlan p = col_plan(n);
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
@@ -646,49 +775,39 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
       if (a.z == nullptr && a.act != LRC_ACT_NONE) {
         const bool vec_z = dn % 8 == 0 && (reinterpret_cast<uintptr_t>(a.zcodes) & 7) == 0;
         dz_kernel<T, true><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, cdiv(dn, CKB), a.act,
-                                                dz, a.lddz, p.rows, vec, vec_z, part);
+                                                dz, a.lddz, p.rows, vec, vec_z, part, flag);
       } else {
         dz_kernel<T, false><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, nullptr, nullptr, 0, a.act, dz, a.lddz,
-                                                 p.rows, vec, rows_vec16(z, a.ldz, sizeof(T)), part);
+                                                 p.rows, vec, rows_vec16(z, a.ldz, sizeof(T)), part, flag);
       }
       LRC_LAUNCHED();
     }
     if (a.db != nullptr) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db, nullptr));
-    if (a.act != LRC_ACT_NONE) {
-      g = a.dz;
-      ldg = a.lddz;
-    }
+  } else if (flag) {
+    clear_flag_kernel<<<1, 1, 0, st>>>(flag);
+    LRC_LAUNCHED();
   }
   if (a.dx == nullptr && a.dW == nullptr) return LRC_OK;
   const double e = sizeof(T);
-  const Operand og = plain<T>(g, ldg), ow = plain<T>(a.W, a.ldw);
-  const bool held = a.x == nullptr;
-  const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB),
-                                    di % 8 == 0 && (reinterpret_cast<uintptr_t>(a.xcodes) & 7) == 0}
-                          : plain<T>(a.x, a.ldx);
-  const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
-  const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD;
-  const bool fast_dw = fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD));
-  const int32_t* flag = sizeof(T) == 4 && (fast_dx || fast_dw) ? room.flag : nullptr;
-  Prepared pg, pw;
-  if (flag) {
-    clear_flag_kernel<<<1, 1, 0, st>>>(room.flag);
-    LRC_LAUNCHED();
-  }
-  if (fast_dx || fast_dw) LRC_TRY(prepare_operand<T>(st, og, false, n, dn, room.a, room.flag, pg));
+  OperandJobs jobs;
+  int count = 0;
+  Prepared pg, pw, px;
+  if (fast_dx || fast_dw) pg = want_operand<T>(jobs, count, og, n, dn, room.a);
+  if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b);
+  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c);
+  LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   if (a.dx != nullptr) {
     Epilogue ep;
     set_out<T>(ep, a.dx, a.lddx);
     const double bytes = e * (double(n) * dn + double(dn) * di + double(n) * di);
     if (fast_dx) {
-      LRC_TRY(prepare_operand<T>(st, ow, false, dn, di, room.b, room.flag, pw));
       LRC_TRY((gemm_bf16<T, K_ROWS, K_COLS>(st, "linear_dx_kernel", pg.op, pw.op, n, di, dn,
                                             segments(pg.planes, pw.planes), ep, room.partial, flag,
                                             2.0 * double(n) * double(dn) * double(di), bytes)));
     }
     if (!fast_dx || flag)
       LRC_TRY((product_any<T, T, K_ROWS, K_COLS>(st, "linear_dx_any_kernel", og, ow, n, di, dn, ep,
-                                                 fast_dx ? flag : nullptr, bytes)));
+                                                 room.partial, fast_dx ? flag : nullptr, bytes)));
   }
   if (a.dW == nullptr) return LRC_OK;
   const double bytes = e * (double(n) * dn + double(dn) * di) + double(n) * di * (held ? 1.0 : e);
@@ -697,8 +816,6 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     Epilogue ep;
     set_out<TO>(ep, a.dW, a.lddw);
     if (fast_dw) {
-      Prepared px;
-      LRC_TRY(prepare_operand<T>(st, ox, held, n, di, room.b, room.flag, px));
       LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n,
                                              segments(pg.planes, px.planes), ep, room.partial, flag,
                                              2.0 * double(n) * double(dn) * double(di), bytes)));
@@ -706,8 +823,10 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     }
     const int32_t* only = fast_dw ? flag : nullptr;
     if (held)
-      return product_any<T, TO, K_COLS, K_CODES>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, only, bytes);
-    return product_any<T, TO, K_COLS, K_COLS>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, only, bytes);
+      return product_any<T, TO, K_COLS, K_CODES>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, room.partial, only,
+                                                    bytes);
+    return product_any<T, TO, K_COLS, K_COLS>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, room.partial, only,
+                                                    bytes);
   };
   if (a.dw_dt == LRC_F32) return go(float{});
   return go(uint16_t{});

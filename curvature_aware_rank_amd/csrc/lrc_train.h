@@ -291,6 +291,10 @@ template <class TO, int KA, int KB>
 lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperand B, int64_t M, int64_t N, int64_t K,
                      const GemmSegments& seg, const Epilogue& ep, float* partial, const int32_t* skip, double flops,
                      double bytes);
+// the splits' tiles (partial[split][M][8 ceil(N / 8)]) added in order, then the epilogue
+template <class TO>
+lrc_status gemm_finish(hipStream_t st, const float* partial, int splits, int64_t M, int64_t N, const Epilogue& ep,
+                       const int32_t* skip);
 size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB);
 
 // ---- column sums ---------------------------------------------------------------------

@@ -334,11 +334,12 @@ def test_linear_accuracy_at_long_sums(lrc, dtype, n, d_in, d_out):
     assert off(dw, dy.double().T.contiguous() @ x.double()) < 24 * U
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(520, 264, 392), (1300, 904, 1101)])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("where", ["x", "w", "dy"])
-def test_nonfinite_entries_in_a_large_product(lrc, dtype, where):
-    """Infinities and NaN at sizes that go to the large tiles: what the plain products give."""
-    n, d_in, d_out = 520, 264, 392
+def test_nonfinite_entries_in_a_large_product(lrc, dtype, where, n, d_in, d_out):
+    """Infinities and NaN at sizes that go to the large tiles (the larger one in fp32 too): what the plain products
+    give."""
     ones = lambda *s: torch.ones(*s, dtype=dtype)   # noqa: E731
     t = {"x": ones(n, d_in), "w": ones(d_out, d_in), "dy": ones(n, d_out)}
     t[where][3, 5], t[where][40, 77], t[where][41, 77] = float("inf"), float("-inf"), float("nan")

@@ -142,3 +142,23 @@ def test_definitions():
     e9 = np.zeros_like(w)
     e9[2, 7] = h
     assert abs((f(x, w + e9) - f(x, w - e9)) / (2 * h) - dw[2, 7]) < 1e-6
+
+
+@needs_lib
+def test_workspace_queries_over_the_range(lib):
+    """Every size the entry points take has a workspace size, no tokens and the largest extents among them."""
+    sizes = [1, 2, 63, 64, 65, 300, 1000, 4096, 4097, 11008, 1 << 20, 1 << 24]
+    for dt in (0, 1):
+        for n in [0, *sizes, (1 << 31) - 1]:
+            for d_in in sizes:
+                for d_out in (1, 64, 303, 4096, 1 << 24):
+                    for f in (lib.lrc_linear_workspace, lib.lrc_linear_backward_workspace):
+                        f(dt, n, d_in, d_out)
+        for n in (0, 1, 5000, (1 << 31) - 1):
+            for d in sizes:
+                lib.lrc_layer_norm_backward_workspace(n, d)
+        # a layer's scratch stays near its operands' size
+        n, d_in, d_out = 8192, 4096, 11008
+        assert lib.lrc_linear_workspace(1, n, d_in, d_out) < 1 << 20
+        assert lib.lrc_linear_backward_workspace(1, n, d_in, d_out) < 2 * n * d_in * 2 + 4 * d_out * 300
+        assert lib.lrc_linear_workspace(dt, n, d_in, 0) == lib.lrc_linear_workspace(dt, -1, d_in, d_out) == 0
