@@ -13,8 +13,8 @@ constexpr int CT = 256;
 // order over (token, block).
 template <class T>
 __global__ __launch_bounds__(CT) void pack_kernel(const T* __restrict__ x, int64_t ldx, int64_t n, int d, int64_t nb,
-                                                  bool vec_x, bool vec_c, int8_t* __restrict__ codes,
-                                                  int8_t* __restrict__ exps, int32_t* __restrict__ info) {
+                                                  int8_t* __restrict__ codes, int8_t* __restrict__ exps,
+                                                  int32_t* __restrict__ info) {
   const int64_t g = (int64_t(blockIdx.x) * CT + threadIdx.x) >> 3;   // block of 64 channels
   const int lane = threadIdx.x & 63;
   const bool live = g < n * nb;
@@ -22,16 +22,15 @@ __global__ __launch_bounds__(CT) void pack_kernel(const T* __restrict__ x, int64
   const int c = int(live ? g % nb : 0) * CKB + 8 * (lane & 7);
   const int cnt = live ? min(8, d - c) : 0;
   float v[8];
-  ld8(x + t * ldx + c, vec_x, cnt, v);
+  ld8(x + t * ldx + c, cnt, v);
   bool bad = false;
-  st8_codes(codes + t * d + c, exps + g, vec_c, cnt, v, lane, bad);
+  st8_codes(codes + t * d + c, exps + g, cnt, v, lane, bad);
   if (info != nullptr && bad) *info = LRC_ENONFINITE;
 }
 
 template <class T>
 __global__ __launch_bounds__(CT) void unpack_kernel(const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
-                                                    int64_t n, int d, int64_t nb, T* __restrict__ x, int64_t ldx,
-                                                    bool vec_x, bool vec_c) {
+                                                    int64_t n, int d, int64_t nb, T* __restrict__ x, int64_t ldx) {
   const int64_t g = (int64_t(blockIdx.x) * CT + threadIdx.x) >> 3;
   if (g >= n * nb) return;
   const int64_t t = g / nb;
@@ -39,15 +38,13 @@ __global__ __launch_bounds__(CT) void unpack_kernel(const int8_t* __restrict__ c
   const int cnt = min(8, d - c);
   if (cnt <= 0) return;
   float v[8];
-  ld8_codes(codes + t * d + c, vec_c, cnt, pow2f(exps[g]), v);
-  st8(x + t * ldx + c, vec_x, cnt, v);
+  ld8_codes(codes + t * d + c, cnt, pow2f(exps[g]), v);
+  st8(x + t * ldx + c, cnt, v);
 }
 
 bool sizes_ok(int64_t n, int64_t d, int64_t ld) {
   return n >= 0 && n < (int64_t(1) << 31) && d >= 1 && d <= (int64_t(1) << 24) && ld >= d;
 }
-
-bool codes_vec(const int8_t* codes, int64_t d) { return d % 8 == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0; }
 
 }  // namespace
 }  // namespace lrc
@@ -64,14 +61,12 @@ extern "C" lrc_status lrc_pack_activations(const void* x, lrc_dtype dt, int64_t 
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int size = dt == LRC_BF16 ? 2 : 4;
-  const bool vx = rows_vec16(x, ldx, size), vc = codes_vec(codes, d);
   ProfScope scope("pack_kernel", st, 0.0, double(n_tokens) * (double(d) * (size + 1) + double(nb)));
   if (dt == LRC_BF16)
-    pack_kernel<<<unsigned(grid), CT, 0, st>>>(static_cast<const uint16_t*>(x), ldx, n_tokens, int(d), nb, vx, vc,
-                                               codes, exps, info);
+    pack_kernel<<<unsigned(grid), CT, 0, st>>>(static_cast<const uint16_t*>(x), ldx, n_tokens, int(d), nb, codes, exps,
+                                               info);
   else
-    pack_kernel<<<unsigned(grid), CT, 0, st>>>(static_cast<const float*>(x), ldx, n_tokens, int(d), nb, vx, vc, codes,
-                                               exps, info);
+    pack_kernel<<<unsigned(grid), CT, 0, st>>>(static_cast<const float*>(x), ldx, n_tokens, int(d), nb, codes, exps, info);
   LRC_LAUNCHED();
   return LRC_OK;
 }
@@ -86,14 +81,11 @@ extern "C" lrc_status lrc_unpack_activations(const int8_t* codes, const int8_t* 
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int size = dt == LRC_BF16 ? 2 : 4;
-  const bool vx = rows_vec16(x, ldx, size), vc = codes_vec(codes, d);
   ProfScope scope("unpack_kernel", st, 0.0, double(n_tokens) * (double(d) * (size + 1) + double(nb)));
   if (dt == LRC_BF16)
-    unpack_kernel<<<unsigned(grid), CT, 0, st>>>(codes, exps, n_tokens, int(d), nb, static_cast<uint16_t*>(x), ldx, vx,
-                                                 vc);
+    unpack_kernel<<<unsigned(grid), CT, 0, st>>>(codes, exps, n_tokens, int(d), nb, static_cast<uint16_t*>(x), ldx);
   else
-    unpack_kernel<<<unsigned(grid), CT, 0, st>>>(codes, exps, n_tokens, int(d), nb, static_cast<float*>(x), ldx, vx,
-                                                 vc);
+    unpack_kernel<<<unsigned(grid), CT, 0, st>>>(codes, exps, n_tokens, int(d), nb, static_cast<float*>(x), ldx);
   LRC_LAUNCHED();
   return LRC_OK;
 }

@@ -1,4 +1,4 @@
-// bf16 matrix products on the matrix cores with a fused epilogue: the linear layer's forward,
+// bf16 (or fp16) matrix products on the matrix cores with a fused epilogue: the linear layer's forward,
 // dx and dW products.
 //
 // An output tile of BM x BN belongs to one workgroup; its waves hold blocks of 32 x 32
@@ -22,6 +22,7 @@ namespace gemm {
 
 constexpr int NXCD = 8;
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -148,7 +149,7 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
   tn = r / rows;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG>
+template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
 __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N, int64_t K,
                                           const GemmSegments& seg, const TileGrid& tg, const Epilogue& ep,
                                           float* __restrict__ partial, const int32_t* __restrict__ skip) {
@@ -234,7 +235,9 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        acc[i][j] = HALF ? __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fa[i]),
+                                                                  __builtin_bit_cast(f16x8, fb[j]), acc[i][j], 0, 0, 0)
+                         : __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
   };
   // Issue orders of the two halves of a step: the fragment reads (and the next stage's loads)
   // go out between the products, which hide them.
@@ -351,7 +354,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
       const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
       if (tg.splits > 1) {
         const int64_t np = (N + 7) & ~int64_t(7);
-        if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, true, 8, v);
+        if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, 8, v);
       } else {
         finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);
       }
@@ -368,12 +371,12 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG>
+template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_bf16_kernel(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                                     int64_t K, GemmSegments seg, TileGrid tg,
                                                                     Epilogue ep, float* __restrict__ partial,
                                                                     const int32_t* __restrict__ skip) {
-  gemm_tile<TO, KA, KB, WM, WN, FM, FN, KS, NST, SEG>(A, B, M, N, K, seg, tg, ep, partial, skip);
+  gemm_tile<TO, KA, KB, WM, WN, FM, FN, KS, NST, SEG, HALF>(A, B, M, N, K, seg, tg, ep, partial, skip);
 }
 
 // Sum of the splits' tiles in split order, then the epilogue.  One lane per eight columns, the
@@ -507,20 +510,23 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   const TileGrid& tg = p.tg;
   const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-  auto launch = [&](auto many) {
-    constexpr bool SEG = decltype(many)::value;
+  auto launch = [&](auto many, auto half) {
+    constexpr bool SEG = decltype(many)::value, HALF = decltype(half)::value;
     if (p.large)
-      gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, KL, NL, SEG><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, tg, ep,
+      gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, KL, NL, SEG, HALF><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, tg, ep,
                                                                                             partial, skip);
     else
-      gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, 64, 2, SEG><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, tg, ep,
+      gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, 64, 2, SEG, HALF><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, tg, ep,
                                                                                            partial, skip);
   };
   // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
-  if (std::is_same<TO, uint16_t>::value || seg.count == 1)
-    launch(std::false_type{});
-  else if constexpr (!std::is_same<TO, uint16_t>::value)
-    launch(std::true_type{});
+  if (seg.half) {
+    if constexpr (KA == K_COLS && KB == K_COLS) launch(std::false_type{}, std::true_type{});
+  } else if (std::is_same<TO, uint16_t>::value || seg.count == 1) {
+    launch(std::false_type{}, std::false_type{});
+  } else if constexpr (!std::is_same<TO, uint16_t>::value) {
+    launch(std::true_type{}, std::false_type{});
+  }
   LRC_LAUNCHED();
   if (tg.splits == 1) return LRC_OK;
   const int splits = tg.splits;

@@ -17,12 +17,27 @@ namespace {
 
 constexpr int LT = 256;
 
+__device__ __forceinline__ int64_t cdiv_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// eight fp32 values times 2^-e each, as fp16
+__device__ __forceinline__ void st8_half(uint16_t* p, const float (&v)[8], const int (&e)[8]) {
+  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+  f16x8 h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = _Float16(ldexpf(v[i], -e[i]));
+  *reinterpret_cast<f16x8*>(p) = h;
+}
+__device__ __forceinline__ void exps8(const int32_t* p, int cnt, int (&e)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = i < cnt ? p[i] : 0;
+}
+
 struct Operand {
   const void* p;        // elements, or int8 codes (leading dim ld)
   int64_t ld;
   const int8_t* exps;   // K_CODES: block exponents, nb per row
   int64_t nb;
-  bool vec;             // 16-byte (codes: 8-byte) pieces allowed
+  bool vec;             // rows are whole aligned 16-byte pieces
 };
 
 // ---- any size, stride and alignment: 64 x 64 tiles, four waves of 32 x 32 ---------------
@@ -45,16 +60,16 @@ __device__ __forceinline__ void operand8(const Operand& o, int64_t row, int64_t 
                                          float (&v)[8]) {
   if (KIND == K_ROWS) {
     const int64_t left = row < rows ? kk - k : 0;
-    ld8(static_cast<const T*>(o.p) + row * o.ld + k, o.vec, int(left < 0 ? 0 : left > 8 ? 8 : left), v);
+    ld8(static_cast<const T*>(o.p) + row * o.ld + k, int(left < 0 ? 0 : left > 8 ? 8 : left), v);
     return;
   }
   const int64_t left = k < kk ? rows - row : 0;
   const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
   if (KIND == K_COLS) {
-    ld8(static_cast<const T*>(o.p) + k * o.ld + row, o.vec, cnt, v);
+    ld8(static_cast<const T*>(o.p) + k * o.ld + row, cnt, v);
   } else {   // eight channels from a multiple of eight: one block
     const float step = cnt > 0 ? pow2f(o.exps[k * o.nb + (row >> 6)]) : 0.f;
-    ld8_codes(static_cast<const int8_t*>(o.p) + k * o.ld + row, o.vec, cnt, step, v);
+    ld8_codes(static_cast<const int8_t*>(o.p) + k * o.ld + row, cnt, step, v);
   }
 }
 
@@ -198,7 +213,7 @@ __global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, in
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = tile[r * EP + 8 * (lane & 7) + e];
       if (plan.splits > 1) {
-        if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, true, 8, v);
+        if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, 8, v);
       } else {
         finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);
       }
@@ -237,6 +252,26 @@ struct RowsPiece<float> {
   }
 };
 
+// 16 bytes of a row at any alignment, zeros behind the `left` elements that exist
+template <class T>
+__device__ __forceinline__ u32x4 piece(const T* p, int left) {
+  constexpr int EL = 16 / int(sizeof(T));
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (left >= EL) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (left > 0) {   // as ld_short
+    T t[EL - 1];
+#pragma unroll
+    for (int e = 0; e < EL - 1; ++e) t[e] = p[min(e, left - 1)];
+#pragma unroll
+    for (int e = 0; e < EL - 1; ++e) {
+      const uint32_t u = sizeof(T) == 4 ? __float_as_uint(float(t[e])) : uint32_t(t[e]) << (16 * (e & 1));
+      v[sizeof(T) == 4 ? e : e >> 1] |= e < left ? u : 0u;
+    }
+  }
+  return v;
+}
+
 template <class T, int G, int NW>
 __global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restrict__ x, int64_t ldx,
                                                               const T* __restrict__ W, int64_t ldw, int n, int64_t N,
@@ -258,11 +293,11 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restric
   for (; (p + U) * P::K <= K && p + U <= p1; p += U) {
     u32x4 wv[U], xv[U][G];
 #pragma unroll
-    for (int u = 0; u < U; ++u) wv[u] = *reinterpret_cast<const u32x4*>(w + (p + u) * P::K + k0);
+    for (int u = 0; u < U; ++u) wv[u] = piece<T>(w + (p + u) * P::K + k0, EL);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int g = 0; g < G; ++g) xv[u][g] = *reinterpret_cast<const u32x4*>(xr[g] + (p + u) * P::K + k0);
+      for (int g = 0; g < G; ++g) xv[u][g] = piece<T>(xr[g] + (p + u) * P::K + k0, EL);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -270,14 +305,9 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restric
   }
   for (; p < p1; ++p) {   // k past the end reads as zero on both sides
     const int k = p * P::K + k0;
-    const bool in = k < K;
-    const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
-    const u32x4 wv = in ? *reinterpret_cast<const u32x4*>(w + k) : zero;
+    const u32x4 wv = piece<T>(w + k, K - k);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const u32x4 xv = in ? *reinterpret_cast<const u32x4*>(xr[g] + k) : zero;
-      P::mma(wv, xv, acc[g]);
-    }
+    for (int g = 0; g < G; ++g) P::mma(wv, piece<T>(xr[g] + k, K - k), acc[g]);
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) *reinterpret_cast<f32x4*>(part + ((wave * G + g) * 64 + lane) * 4) = acc[g];
@@ -331,27 +361,109 @@ lrc_status linear_rows(hipStream_t st, const Operand& x, const Operand& W, int64
   return LRC_OK;
 }
 
-// ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
-// Bound by memory: dy and z read, dz written once.  A lane takes eight consecutive channels,
-// the workgroup's four waves take the chunk's tokens in turn; db's share of the chunk is the
-// waves' sums added in order.
+// ---- column exponents ------------------------------------------------------------------
+// The dW of a bf16 layer whose activation has a smooth slope takes dz in fp16, not in the bf16 of
+// the stream: three more bits, so that dW carries no more than its own rounding (with the
+// stream's bf16 its error was 1.3 to 1.55 times that), at the same matrix rate.  fp16 has little
+// range, so each channel of dz and of x is first scaled by a power of two to a largest magnitude
+// near 2^15, and dW's rows and columns are scaled back.  The channels' largest magnitudes are
+// those of dy (an activation's slope is at most 1.13) and of x; a value more than 2^29 below its
+// channel's largest loses bits, one more than 2^40 below becomes zero, far under what the
+// channel's sum keeps of it.
 struct ColPlan {
   int64_t rows, chunks;   // tokens per chunk
 };
 ColPlan col_plan(int64_t n) {
   ColPlan p;
-  p.rows = std::max<int64_t>(n <= 4096 ? 8 : 32, cdiv(n, 1024));
+  p.rows = std::max<int64_t>(n <= 1024 ? 8 : 32, cdiv(n, 1024));
   p.chunks = cdiv(n, p.rows);
   return p;
 }
 
+struct MagnitudeJob {
+  const void* p = nullptr;        // bf16 rows, or
+  const int8_t* exps = nullptr;   // the exponents of a checkpoint, ld blocks a row
+  int64_t ld = 0, cols = 0, blocks = 0;
+  uint32_t* part = nullptr;       // [chunks][cols]
+  int32_t* out = nullptr;
+};
+struct MagnitudeJobs {
+  MagnitudeJob job[2];
+};
+// largest finite magnitude (as bits) of every channel over a chunk of tokens
+__global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64_t n, int64_t rows) {
+  __shared__ uint32_t most[3][64][9];
+  const int q = int64_t(blockIdx.x) < jobs.job[0].blocks ? 0 : 1;
+  const MagnitudeJob& j = jobs.job[q];
+  const int64_t block = int64_t(blockIdx.x) - (q ? jobs.job[0].blocks : 0);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (block * 64 + lane) * 8;
+  const int64_t left = j.cols - c;
+  const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
+  const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
+  uint32_t m[8] = {};
+  if (cnt > 0) {
+#pragma unroll 4
+    for (int64_t t = t0 + wave; t < t1; t += 4) {
+      if (j.exps != nullptr) {
+        const uint32_t u = __float_as_uint(127.f * pow2f(j.exps[t * j.ld + (c >> 6)]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = max(m[e], u);
+      } else {
+        float v[8];
+        ld8(static_cast<const uint16_t*>(j.p) + t * j.ld + c, cnt, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = max(m[e], __float_as_uint(finite_mag(v[e])));
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most[wave - 1][lane][e] = m[e];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt)
+      j.part[int64_t(blockIdx.y) * j.cols + c + e] =
+          max(max(m[e], most[0][lane][e]), max(most[1][lane][e], most[2][lane][e]));
+}
+// exponent that brings a channel's largest magnitude into [2^14, 2^15); 0 for a channel of zeros
+__global__ __launch_bounds__(LT) void exponent_kernel(MagnitudeJobs jobs, int64_t chunks) {
+  __shared__ uint32_t acc[8][33];
+  const int q = int64_t(blockIdx.x) < cdiv_dev(jobs.job[0].cols, 32) ? 0 : 1;
+  const MagnitudeJob& j = jobs.job[q];
+  const int64_t block = int64_t(blockIdx.x) - (q ? cdiv_dev(jobs.job[0].cols, 32) : 0);
+  const int cx = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t c = block * 32 + cx;
+  uint32_t m = 0;
+  if (c < j.cols) {
+#pragma unroll 8
+    for (int64_t p = sl; p < chunks; p += 8) m = max(m, j.part[p * j.cols + c]);
+  }
+  acc[sl][cx] = m;
+  __syncthreads();
+  if (sl > 0 || c >= j.cols) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max(m, acc[i][cx]);
+  int e = 0;
+  const float f = frexpf(__uint_as_float(m), &e);   // in [1/2, 1)
+  j.out[c] = f > 0.f ? e - 15 : 0;
+}
+
+// ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
+// Bound by memory: dy and z read, dz written once.  A lane takes eight consecutive channels,
+// the workgroup's four waves take the chunk's tokens in turn; db's share of the chunk is the
+// waves' sums added in order.
 template <class T, bool CK>
 __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_t lddy, int64_t n, int64_t d,
                                                 const T* __restrict__ z, int64_t ldz,
                                                 const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
                                                 int64_t nb, int act, T* __restrict__ dz, int64_t lddz, int64_t rows,
-                                                bool vec, bool vec_z, float* __restrict__ partial,
-                                                int32_t* __restrict__ clear) {
+                                                float* __restrict__ partial,
+                                                int32_t* __restrict__ clear, const int32_t* __restrict__ dz_exp,
+                                                uint16_t* __restrict__ dz_half, int64_t w8) {
   __shared__ float sums[3][64][9];
   if (clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *clear = 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -361,19 +473,22 @@ __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_
   const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
   float s[8] = {};
   if (cnt > 0) {
+    int ex[8] = {};
+    if (dz_half != nullptr) exps8(dz_exp + c, cnt, ex);
 #pragma unroll 2
     for (int64_t t = t0 + wave; t < t1; t += 4) {
       float g[8];
-      ld8(dy + t * lddy + c, vec, cnt, g);
+      ld8(dy + t * lddy + c, cnt, g);
       if (act != LRC_ACT_NONE) {
         float zv[8];
         if (CK)
-          ld8_codes(codes + t * d + c, vec_z, cnt, pow2f(exps[t * nb + (c >> 6)]), zv);
+          ld8_codes(codes + t * d + c, cnt, pow2f(exps[t * nb + (c >> 6)]), zv);
         else
-          ld8(z + t * ldz + c, vec_z, cnt, zv);
+          ld8(z + t * ldz + c, cnt, zv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] *= act_slope(act, zv[e]);
-        st8(dz + t * lddz + c, vec, cnt, g);
+        st8(dz + t * lddz + c, cnt, g);
+        if (dz_half != nullptr) st8_half(dz_half + t * w8 + c, g, ex);   // zeros behind the last channel
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] += g[e];
@@ -418,7 +533,7 @@ template <class T>
 __device__ __forceinline__ void split_store(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag);
 template <>
 __device__ __forceinline__ void split_store<uint16_t>(uint16_t* o, int64_t, float (&v)[8], int32_t*) {
-  st8(o, true, 8, v);
+  st8(o, 8, v);
 }
 template <>
 __device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag) {
@@ -433,9 +548,9 @@ __device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, floa
     m[e] = round_to(r, static_cast<const uint16_t*>(nullptr));
     v[e] = r - m[e];
   }
-  st8(o, true, 8, h);
-  st8(o + w8, true, 8, m);
-  st8(o + 2 * w8, true, 8, v);
+  st8(o, 8, h);
+  st8(o + w8, 8, m);
+  st8(o + 2 * w8, 8, v);
   if (bad) *flag = 1;
 }
 // Up to three operands in one launch: a workgroup belongs to the job its index falls into.
@@ -445,8 +560,9 @@ struct OperandJob {
   uint16_t* out = nullptr;
   int64_t ld = 0, nb = 0, rows = 0, cols = 0, w8 = 0, blocks = 0;
   int planes = 1;
-  bool vec = false;
+  const int32_t* half_exp = nullptr;   // fp16 of the value times 2^-half_exp[column], not bf16
 };
+constexpr int JOB_ROWS = 4;   // rows of a thread
 struct OperandJobs {
   OperandJob job[3];
 };
@@ -456,18 +572,33 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
   int q = 0;
   while (q < 2 && block >= jobs.job[q].blocks) block -= jobs.job[q++].blocks;
   const OperandJob& j = jobs.job[q];
+  // four rows of one piece of columns
   const int64_t i = block * LT + threadIdx.x, per = j.w8 / 8;
-  if (i >= j.rows * per) return;
-  const int64_t r = i / per, c = i % per * 8;
+  const int64_t r0 = i / per * JOB_ROWS, c = i % per * 8;
+  if (r0 >= j.rows) return;
   const int cnt = int(j.cols - c > 8 ? 8 : j.cols - c);
-  float v[8];
-  uint16_t* o = j.out + r * j.planes * j.w8 + c;
-  if (j.exps != nullptr) {
-    ld8_codes(static_cast<const int8_t*>(j.p) + r * j.ld + c, j.vec, cnt, pow2f(j.exps[r * j.nb + (c >> 6)]), v);
-    split_store<uint16_t>(o, j.w8, v, flag);
-  } else {
-    ld8(static_cast<const T*>(j.p) + r * j.ld + c, j.vec, cnt, v);
-    split_store<T>(o, j.w8, v, flag);
+  int e[8] = {};
+  if (j.half_exp != nullptr) exps8(j.half_exp + c, cnt, e);
+  float v[JOB_ROWS][8];
+#pragma unroll
+  for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
+    const int64_t r = min(r0 + q4, j.rows - 1);
+    if (j.exps != nullptr)
+      ld8_codes(static_cast<const int8_t*>(j.p) + r * j.ld + c, cnt, pow2f(j.exps[r * j.nb + (c >> 6)]), v[q4]);
+    else
+      ld8(static_cast<const T*>(j.p) + r * j.ld + c, cnt, v[q4]);
+  }
+#pragma unroll
+  for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
+    const int64_t r = r0 + q4;
+    if (r >= j.rows) break;
+    uint16_t* o = j.out + r * j.planes * j.w8 + c;
+    if (j.half_exp != nullptr)
+      st8_half(o, v[q4], e);
+    else if (j.exps != nullptr)
+      split_store<uint16_t>(o, j.w8, v[q4], flag);
+    else
+      split_store<T>(o, j.w8, v[q4], flag);
   }
 }
 __global__ void clear_flag_kernel(int32_t* flag) { *flag = 0; }
@@ -487,9 +618,10 @@ struct Prepared {
 
 // Adds the operand to the jobs if it cannot be read where it lies.
 template <class T>
-Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t rows, int64_t cols, uint16_t* room) {
+Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t rows, int64_t cols, uint16_t* room,
+                      const int32_t* half_exp = nullptr) {
   const bool codes = o.exps != nullptr;
-  if (sizeof(T) == 2 && !codes && o.vec && cols % 8 == 0)
+  if (sizeof(T) == 2 && !codes && half_exp == nullptr && o.vec && cols % 8 == 0)
     return {{static_cast<const uint16_t*>(o.p), o.ld, 0}, 1};
   OperandJob& j = jobs.job[count++];
   j.p = o.p;
@@ -501,8 +633,8 @@ Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t r
   j.cols = cols;
   j.w8 = round8(cols);
   j.planes = sizeof(T) == 4 && !codes ? 3 : 1;
-  j.vec = o.vec;
-  j.blocks = cdiv(rows * (j.w8 / 8), LT);
+  j.half_exp = half_exp;
+  j.blocks = cdiv(cdiv(rows, JOB_ROWS) * (j.w8 / 8), LT);
   return {{room, j.planes * j.w8, j.w8}, j.planes};
 }
 template <class T>
@@ -559,6 +691,12 @@ bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two ope
   return std::max(round8(rows_a), round8(rows_b)) * (sizeof(T) == 4 ? 3 : 1) <= GEMM_MAX_LD;
 }
 
+// whether dW can take fp16 operands: a bf16 layer of any size the tiles' offsets reach
+template <class T>
+bool half_fits(int64_t n, int64_t di, int64_t dn) {
+  return sizeof(T) == 2 && n <= GEMM_MAX_K && gemm_fits<T>(di, dn);
+}
+
 template <class T, class TO, int KA, int KB>
 lrc_status product_any(hipStream_t st, const char* name, const Operand& A, const Operand& B, int64_t M, int64_t N,
                        int64_t K, const Epilogue& ep, float* partial, const int32_t* only, double bytes) {
@@ -584,7 +722,6 @@ template <class T>
 void set_out(Epilogue& ep, void* y, int64_t ldy) {
   ep.y = y;
   ep.ldy = ldy;
-  ep.vec_y = rows_vec16(y, ldy, sizeof(T));
 }
 
 // Workspace of the three products.
@@ -593,6 +730,9 @@ struct LinearRoom {
   float* partial = nullptr;     // split products
   float* sums = nullptr;        // db chunks
   uint16_t *a = nullptr, *b = nullptr, *c = nullptr;   // operands
+  uint16_t* dz_half = nullptr;  // fp16 dz, its channels' and x's exponents, their chunks' magnitudes
+  int32_t *dz_exp = nullptr, *x_exp = nullptr;
+  uint32_t *dz_mag = nullptr, *x_mag = nullptr;
   size_t bytes = 0;
 };
 template <class T>
@@ -623,12 +763,20 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   if (large)
     part = std::max({part, gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS) / 4,
                      gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS) / 4});
+  if (half_fits<T>(n, di, dn)) {
+    part = std::max(part, gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS) / 4);
+    r.dz_half = cv.take<uint16_t>(size_t(n) * round8(dn));
+    r.dz_exp = cv.take<int32_t>(dn);
+    r.x_exp = cv.take<int32_t>(di);
+    r.dz_mag = cv.take<uint32_t>(size_t(col_plan(n).chunks) * dn);
+    r.x_mag = cv.take<uint32_t>(size_t(col_plan(n).chunks) * di);
+  }
   r.partial = cv.take<float>(part);
+  if (large || half_fits<T>(n, di, dn)) r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x
   if (large) {
     r.flag = cv.take<int32_t>(1);
     if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
     if (sizeof(T) == 4 || di % 8 != 0) r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
-    r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x, also a checkpoint's values
   }
   r.bytes = cv.bytes();
   return r;
@@ -636,7 +784,7 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
 // whether an operand is read in place or has its room
 template <class T>
 bool has_room(const Operand& o, int64_t cols) {
-  return sizeof(T) == 4 || cols % 8 != 0 || o.vec;
+  return sizeof(T) == 4 || cols % 8 != 0 || o.vec;   // (rooms depend on sizes alone)
 }
 
 template <class T>
@@ -648,20 +796,17 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
   ep.act = act;
   ep.res = res;
   ep.ldr = ldr;
-  ep.vec_r = rows_vec16(res, ldr, sizeof(T));
   set_out<T>(ep, y, ldy);
   ep.z = z;
   ep.ldz = zcodes != nullptr ? dn : ldz;
-  ep.vec_z = rows_vec16(z, ldz, sizeof(T));
   ep.codes = zcodes;
   ep.exps = zexps;
   ep.nb = cdiv(dn, CKB);
-  ep.vec_c = dn % 8 == 0 && (reinterpret_cast<uintptr_t>(zcodes) & 7) == 0;
   ep.info = info;
   const double bytes = double(sizeof(T)) * (double(n) * di + double(dn) * di + double(n) * dn * (res ? 2 : 1));
   const Operand ox = plain<T>(x, ldx), ow = plain<T>(W, ldw);
   // the kept pre-activation's blocks of 64 channels need a tile that holds them
-  if (few_tokens(n, di, dn, sizeof(T)) && di % (16 / int(sizeof(T))) == 0 && ox.vec && ow.vec && zcodes == nullptr)
+  if (few_tokens(n, di, dn, sizeof(T)) && zcodes == nullptr)
     return linear_rows<T>(st, ox, ow, n, dn, di, ep, bytes);
   const LinearRoom room = forward_room<T>(ws, n, di, dn);
   if (room.flag == nullptr || !has_room<T>(ox, di) || !has_room<T>(ow, di) || std::max(ldx, ldw) > GEMM_MAX_LD)
@@ -755,30 +900,51 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const int64_t ldg = with_dz ? a.lddz : a.lddy;
   const Operand og = plain<T>(g, ldg), ow = plain<T>(a.W, a.ldw);
   const bool held = a.x == nullptr;
-  const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB),
-                                    di % 8 == 0 && (reinterpret_cast<uintptr_t>(a.xcodes) & 7) == 0}
+  const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB), false}
                           : plain<T>(a.x, a.ldx);
   const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
   const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD;
-  const bool fast_dw = fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD));
+  // a slope that is neither 0 nor 1 leaves bits in dz that the stream's bf16 does not hold
+  const bool half = with_dz && a.act != LRC_ACT_RELU && a.dW != nullptr && half_fits<T>(n, di, dn);
+  const bool fast_dw = half || (fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD)));
   int32_t* flag = sizeof(T) == 4 && (fast_dx || fast_dw) ? room.flag : nullptr;
+  if (half) {
+    const ColPlan p = col_plan(n);
+    MagnitudeJobs m;
+    m.job[0].p = a.dy;
+    m.job[0].ld = a.lddy;
+    m.job[0].cols = dn;
+    m.job[0].part = room.dz_mag;
+    m.job[0].out = room.dz_exp;
+    m.job[1].p = a.x;
+    m.job[1].exps = held ? a.xexps : nullptr;
+    m.job[1].ld = held ? cdiv(di, CKB) : a.ldx;
+    m.job[1].cols = di;
+    m.job[1].part = room.x_mag;
+    m.job[1].out = room.x_exp;
+    for (MagnitudeJob& j : m.job) j.blocks = cdiv(j.cols, 512);
+    ProfScope scope("magnitude_kernel", st, 0.0, double(n) * (2.0 * double(dn) + (held ? double(di) / 64 : 2.0 * di)));
+    magnitude_kernel<<<dim3(unsigned(m.job[0].blocks + m.job[1].blocks), unsigned(p.chunks)), LT, 0, st>>>(m, n, p.rows);
+    LRC_LAUNCHED();
+    exponent_kernel<<<unsigned(cdiv(dn, 32) + cdiv(di, 32)), LT, 0, st>>>(m, p.chunks);
+    LRC_LAUNCHED();
+  }
   if (with_dz || a.db != nullptr) {
     const ColPlan p = col_plan(n);
+    uint16_t* dz_half = half ? room.dz_half : nullptr;
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
       const dim3 grid(unsigned(cdiv(dn, 512)), unsigned(p.chunks));
       float* part = a.db != nullptr ? room.sums : nullptr;
       const T *dy = static_cast<const T*>(a.dy), *z = static_cast<const T*>(a.z);
       T* dz = static_cast<T*>(a.dz);
-      const bool vec = rows_vec16(dy, a.lddy, sizeof(T)) &&
-                       (a.act == LRC_ACT_NONE || rows_vec16(dz, a.lddz, sizeof(T)));
       if (a.z == nullptr && a.act != LRC_ACT_NONE) {
-        const bool vec_z = dn % 8 == 0 && (reinterpret_cast<uintptr_t>(a.zcodes) & 7) == 0;
         dz_kernel<T, true><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, cdiv(dn, CKB), a.act,
-                                                dz, a.lddz, p.rows, vec, vec_z, part, flag);
+                                                dz, a.lddz, p.rows, part, flag, room.dz_exp, dz_half, round8(dn));
       } else {
         dz_kernel<T, false><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, nullptr, nullptr, 0, a.act, dz, a.lddz,
-                                                 p.rows, vec, rows_vec16(z, a.ldz, sizeof(T)), part, flag);
+                                                 p.rows, part, flag, room.dz_exp, dz_half,
+                                                 round8(dn));
       }
       LRC_LAUNCHED();
     }
@@ -792,9 +958,9 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   OperandJobs jobs;
   int count = 0;
   Prepared pg, pw, px;
-  if (fast_dx || fast_dw) pg = want_operand<T>(jobs, count, og, n, dn, room.a);
+  if (fast_dx || (fast_dw && !half)) pg = want_operand<T>(jobs, count, og, n, dn, room.a);
   if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b);
-  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c);
+  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, half ? room.x_exp : nullptr);
   LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   if (a.dx != nullptr) {
     Epilogue ep;
@@ -816,8 +982,14 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     Epilogue ep;
     set_out<TO>(ep, a.dW, a.lddw);
     if (fast_dw) {
-      LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n,
-                                             segments(pg.planes, px.planes), ep, room.partial, flag,
+      GemmSegments seg = half ? GemmSegments{} : segments(pg.planes, px.planes);
+      if (half) {
+        seg.half = true;
+        ep.row_exp = room.dz_exp;
+        ep.col_exp = room.x_exp;
+        pg.op = {room.dz_half, round8(dn), 0};
+      }
+      LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n, seg, ep, room.partial, flag,
                                              2.0 * double(n) * double(dn) * double(di), bytes)));
       if (!flag) return LRC_OK;
     }

@@ -10,10 +10,20 @@ namespace {
 constexpr int NT = 256;
 constexpr int ROWS_PER_CHUNK = 64;   // tokens per partial of a column sum
 
+// Sum over the wave, in every lane: lane permutations inside the vector unit (neighbours, pairs,
+// mirrored eights and sixteens, then rows and halves exchanged) instead of six trips through LDS.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  auto dpp = [](float x, auto ctrl) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v += dpp(v, std::integral_constant<int, 0xb1>{});
+  v += dpp(v, std::integral_constant<int, 0x4e>{});
+  v += dpp(v, std::integral_constant<int, 0x141>{});
+  v += dpp(v, std::integral_constant<int, 0x140>{});
+  const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+  const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
 }
 // sum over the 256 threads, the same value in every one (fixed order)
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -132,85 +142,82 @@ __global__ __launch_bounds__(NT) void ln_bwd_cols_kernel(const T* __restrict__ d
 // once, the statistics are taken from the registers (values centred before they are squared),
 // and gamma, beta and the running sums of dgamma and dbeta stay in registers over all tokens of
 // the workgroup.  The next token's loads are in flight while the present one is worked on.
-//   VEC: 16-byte pieces (d a multiple of 8, rows aligned); lane l holds channels
-//        8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint block;
-//   else lane l holds channels i LANES + l, so a wave holds one block per i.
+// Lane l holds channels 8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint
+// block; pieces are 16-byte accesses at any alignment, the last one of a ragged row is short.
 constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }   // tokens of a workgroup at a time
 constexpr int row_threads(int wpr) { return 64 * wpr * row_groups(wpr); }
 
-template <class T, int WPR, int V, bool VEC>
+template <class T, int WPR, int V>
 struct RowShape {
   static constexpr int E = 8 * V, LANES = 64 * WPR, GROUPS = row_groups(WPR), THREADS = row_threads(WPR);
   static __device__ __forceinline__ int col(int i, int l) {
-    return VEC ? ((i >> 3) * LANES + l) * 8 + (i & 7) : i * LANES + l;
+    return ((i >> 3) * LANES + l) * 8 + (i & 7);
   }
 };
 
 // a token's elements as they lie in memory
-template <class T, int WPR, int V, bool VEC>
+template <class T, int WPR, int V>
 struct RawRow {
-  using S = RowShape<T, WPR, V, VEC>;
-  static constexpr int WORDS = 8 * V * int(sizeof(T)) / 16;
-  uint4 q[VEC ? WORDS : 1];
-  T s[VEC ? 1 : 8 * V];
+  using S = RowShape<T, WPR, V>;
+  static constexpr int W = 2 * int(sizeof(T));   // 32-bit words per piece
+  uint32_t q[V * W];
   __device__ __forceinline__ void load(const T* row, int d, int l, bool live) {
-    if (VEC) {
-      constexpr int W = sizeof(T) == 2 ? 1 : 2;   // 16-byte words per piece
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = (k * S::LANES + l) * 8;
-        const bool ok = live && c < d;
+    for (int k = 0; k < V; ++k) {
+      const int c = (k * S::LANES + l) * 8, left = live ? d - c : 0;
+      if (left >= 8) {
+        __builtin_memcpy(q + k * W, row + c, 4 * W);
+      } else {
 #pragma unroll
-        for (int w = 0; w < W; ++w)
-          q[W * k + w] = ok ? reinterpret_cast<const uint4*>(row + c)[w] : make_uint4(0u, 0u, 0u, 0u);
-      }
-    } else {
+        for (int w = 0; w < W; ++w) q[k * W + w] = 0u;
+        if (left > 0) {   // as ld_short
+          T t[7];
 #pragma unroll
-      for (int i = 0; i < 8 * V; ++i) {
-        const int c = i * S::LANES + l;
-        s[i] = live && c < d ? row[c] : T(0);
+          for (int e = 0; e < 7; ++e) t[e] = row[c + min(e, left - 1)];
+#pragma unroll
+          for (int e = 0; e < 7; ++e) {
+            if (sizeof(T) == 4) {
+              if (e < left) __builtin_memcpy(q + k * W + e % W, t + e, 4);
+            } else {
+              q[k * W + (e >> 1) % W] |= e < left ? uint32_t(t[e]) << (16 * (e & 1)) : 0u;
+            }
+          }
+        }
       }
     }
   }
   __device__ __forceinline__ float at(int i) const {
-    if (!VEC) return ld_elem(&s[i]);
-    const int word = sizeof(T) == 2 ? i >> 1 : i;
-    const uint4& u = q[word >> 2];
-    const uint32_t w = (word & 3) == 0 ? u.x : (word & 3) == 1 ? u.y : (word & 3) == 2 ? u.z : u.w;
-    if (sizeof(T) == 4) return __uint_as_float(w);
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    if (sizeof(T) == 4) return __uint_as_float(q[i % (V * W)]);
+    return __uint_as_float((i & 1) ? (q[i >> 1] & 0xffff0000u) : (q[i >> 1] << 16));
   }
 };
 // a token's codes and exponents
-template <int WPR, int V, bool VEC>
+template <int WPR, int V>
 struct RawCodes {
-  using S = RowShape<uint16_t, WPR, V, VEC>;
-  uint2 q[VEC ? V : 1];
-  int8_t s[VEC ? 1 : 8 * V];
-  int8_t e[VEC ? V : 8 * V];
+  using S = RowShape<uint16_t, WPR, V>;
+  uint32_t q[2 * V];
+  int8_t e[V];
   __device__ __forceinline__ void load(const int8_t* codes, const int8_t* exps, int d, int l, bool live) {
-    if (VEC) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = (k * S::LANES + l) * 8;
-        const bool ok = live && c < d;
-        q[k] = ok ? *reinterpret_cast<const uint2*>(codes + c) : make_uint2(0u, 0u);
-        e[k] = ok ? exps[c >> 6] : int8_t(0);
-      }
-    } else {
+    for (int k = 0; k < V; ++k) {
+      const int c = (k * S::LANES + l) * 8, left = live ? d - c : 0;
+      e[k] = left > 0 ? exps[c >> 6] : int8_t(0);
+      if (left >= 8) {
+        __builtin_memcpy(q + 2 * k, codes + c, 8);
+      } else {
+        q[2 * k] = q[2 * k + 1] = 0u;
+        if (left > 0) {   // as ld_short
+          uint8_t t[7];
 #pragma unroll
-      for (int i = 0; i < 8 * V; ++i) {
-        const int c = i * S::LANES + l;
-        const bool ok = live && c < d;
-        s[i] = ok ? codes[c] : int8_t(0);
-        e[i] = ok ? exps[c >> 6] : int8_t(0);
+          for (int i = 0; i < 7; ++i) t[i] = uint8_t(codes[c + min(i, left - 1)]);
+#pragma unroll
+          for (int i = 0; i < 7; ++i) q[2 * k + (i >> 2)] |= i < left ? uint32_t(t[i]) << (8 * (i & 3)) : 0u;
+        }
       }
     }
   }
   __device__ __forceinline__ float at(int i) const {
-    if (!VEC) return float(s[i]) * pow2f(e[i]);
-    const uint32_t w = (i & 4) ? q[i >> 3].y : q[i >> 3].x;
-    return float(int8_t(w >> (8 * (i & 3)))) * pow2f(e[i >> 3]);
+    return float(int8_t(q[i >> 2] >> (8 * (i & 3)))) * pow2f(e[i >> 3]);
   }
 };
 
@@ -235,28 +242,39 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int wav
   }
 }
 
-template <class T, int WPR, int V, bool VEC>
+// a lane's channels of gamma or beta, `absent` where there is none
+template <class S, int V>
+__device__ __forceinline__ void row_params(const float* p, float absent, int d, int l, float (&v)[8 * V]) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = (k * S::LANES + l) * 8;
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = absent;
+    if (p != nullptr) ld8(p + c, d - c, t);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[8 * k + e] = t[e];
+  }
+}
+
+template <class T, int WPR, int V>
 __global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
     const T* __restrict__ x, int64_t ldx, int64_t n, int d, const float* __restrict__ gamma,
     const float* __restrict__ beta, float eps, T* __restrict__ y, int64_t ldy, float* __restrict__ mean,
     float* __restrict__ rstd, int8_t* __restrict__ codes, int8_t* __restrict__ exps, int64_t nb,
     int32_t* __restrict__ info) {
-  using S = RowShape<T, WPR, V, VEC>;
+  using S = RowShape<T, WPR, V>;
   constexpr int E = S::E;
   __shared__ float red[2][WPR > 1 ? S::GROUPS * WPR : 1][1];
   const int lane = threadIdx.x & 63, group = threadIdx.x / S::LANES, l = threadIdx.x % S::LANES;
   const int wave = l >> 6;
   float ga[E], be[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = S::col(i, l);
-    ga[i] = gamma != nullptr && c < d ? gamma[c] : 1.f;
-    be[i] = beta != nullptr && c < d ? beta[c] : 0.f;
-  }
+  row_params<S, V>(gamma, 1.f, d, l, ga);
+  row_params<S, V>(beta, 0.f, d, l, be);
   const float inv_d = 1.f / float(d);
   const int64_t step = int64_t(gridDim.x) * S::GROUPS;
   int64_t t = int64_t(blockIdx.x) * S::GROUPS + group;
-  RawRow<T, WPR, V, VEC> raw;
+  RawRow<T, WPR, V> raw;
   raw.load(x + t * ldx, d, l, t < n);
   bool bad = false;
   for (int64_t t0 = int64_t(blockIdx.x) * S::GROUPS; t0 < n; t0 += step, t += step) {
@@ -270,29 +288,13 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
     row_sums<WPR, 1>(s, red[0], wave, lane, group);
     const float mu = s[0] * inv_d;
     if (codes != nullptr) {   // before v is centred
-      if (VEC) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (k * S::LANES + l) * 8;
-          float p[8];
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * S::LANES + l) * 8;
+        float p[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = v[8 * k + e];
-          st8_codes(codes + t * d + c, exps + t * nb + (c >> 6), true, t < n && c < d ? 8 : 0, p, lane, bad);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int c = S::col(i, l);
-          float m = finite_mag(v[i]);
-          bad |= !finite_f(v[i]);
-#pragma unroll
-          for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-          const int e = ckpt_exponent(m);
-          if (t < n && c < d) {
-            codes[t * d + c] = int8_t(ckpt_code(v[i], pow2f(-e)));
-            if (lane == 0) exps[t * nb + (c >> 6)] = int8_t(e);
-          }
-        }
+        for (int e = 0; e < 8; ++e) p[e] = v[8 * k + e];
+        st8_codes(codes + t * d + c, exps + t * nb + (c >> 6), t < n ? min(8, d - c) : 0, p, lane, bad);
       }
     }
     float q[1] = {0.f};
@@ -309,21 +311,13 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
       rstd[t] = rs;
     }
     T* o = y + t * ldy;
-    if (VEC) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = (k * S::LANES + l) * 8;
-        float p[8];
+    for (int k = 0; k < V; ++k) {
+      const int c = (k * S::LANES + l) * 8;
+      float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = fmaf(v[8 * k + e] * rs, ga[8 * k + e], be[8 * k + e]);
-        if (c < d) st8(o + c, true, 8, p);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = S::col(i, l);
-        if (c < d) st_elem(o + c, fmaf(v[i] * rs, ga[i], be[i]));
-      }
+      for (int e = 0; e < 8; ++e) p[e] = fmaf(v[8 * k + e] * rs, ga[8 * k + e], be[8 * k + e]);
+      if (c < d) st8(o + c, d - c, p);
     }
   }
   if (info != nullptr && bad) *info = LRC_ENONFINITE;
@@ -331,31 +325,27 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
 
 // dx of every token and the workgroup's share of dgamma and dbeta (partial[2 b], partial[2 b + 1]
 // of workgroup b; not written when NULL, and no dx when that is NULL).
-template <class T, int WPR, int V, bool VEC, bool CK>
+template <class T, int WPR, int V, bool CK>
 __global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
     const T* __restrict__ dy, int64_t lddy, int64_t n, int d, const T* __restrict__ x, int64_t ldx,
     const int8_t* __restrict__ codes, const int8_t* __restrict__ exps, int64_t nb, const float* __restrict__ mean,
     const float* __restrict__ rstd, const float* __restrict__ gamma, T* __restrict__ dx, int64_t lddx,
     float* __restrict__ partial) {
-  using S = RowShape<T, WPR, V, VEC>;
+  using S = RowShape<T, WPR, V>;
   constexpr int E = S::E;
   __shared__ float red[2][WPR > 1 ? S::GROUPS * WPR : 1][2];
   __shared__ float sums[S::GROUPS > 1 ? (S::GROUPS - 1) * 2 * E * S::LANES : 1];
   const int lane = threadIdx.x & 63, group = threadIdx.x / S::LANES, l = threadIdx.x % S::LANES;
   const int wave = l >> 6;
   float ga[E], dg[E], db[E];
+  row_params<S, V>(gamma, 1.f, d, l, ga);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = S::col(i, l);
-    ga[i] = gamma != nullptr && c < d ? gamma[c] : 1.f;
-    dg[i] = 0.f;
-    db[i] = 0.f;
-  }
+  for (int i = 0; i < E; ++i) dg[i] = db[i] = 0.f;
   const float inv_d = 1.f / float(d);
   const int64_t step = int64_t(gridDim.x) * S::GROUPS;
   int64_t t = int64_t(blockIdx.x) * S::GROUPS + group;
-  RawRow<T, WPR, V, VEC> rg, rx;
-  RawCodes<WPR, V, VEC> rc;
+  RawRow<T, WPR, V> rg, rx;
+  RawCodes<WPR, V> rc;
   float mu = 0.f, rs = 0.f;
   auto load = [&](int64_t u) {
     const bool live = u < n;
@@ -393,21 +383,13 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
     if (t >= n) continue;
     const float c1 = s[0] * inv_d, c2 = s[1] * inv_d;
     T* o = dx + t * lddx;
-    if (VEC) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = (k * S::LANES + l) * 8;
-        float p[8];
+    for (int k = 0; k < V; ++k) {
+      const int c = (k * S::LANES + l) * 8;
+      float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = r * (g[8 * k + e] - c1 - xh[8 * k + e] * c2);
-        if (c < d) st8(o + c, true, 8, p);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = S::col(i, l);
-        if (c < d) st_elem(o + c, r * (g[i] - c1 - xh[i] * c2));
-      }
+      for (int e = 0; e < 8; ++e) p[e] = r * (g[8 * k + e] - c1 - xh[8 * k + e] * c2);
+      if (c < d) st8(o + c, d - c, p);
     }
   }
   if (partial == nullptr) return;
@@ -431,11 +413,17 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
   }
   float* p = partial + int64_t(blockIdx.x) * 2 * d;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = S::col(i, l);
+  for (int k = 0; k < V; ++k) {
+    const int c = (k * S::LANES + l) * 8;
+    float a[8], b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = dg[8 * k + e];
+      b[e] = db[8 * k + e];
+    }
     if (c < d) {
-      p[c] = dg[i];
-      p[d + c] = db[i];
+      st8(p + c, d - c, a);
+      st8(p + d + c, d - c, b);
     }
   }
 }
@@ -455,11 +443,11 @@ ColPlan col_plan(int64_t n) {
 }
 
 // Workgroups of the backward kernel: each takes at least four tokens per group, so that the
-// partials stay a small part of the traffic, and 512 fill the chip (two per compute unit, each
-// with a token's loads ahead).
+// partials stay a small part of the traffic; 512 (two per compute unit, each with a token's loads
+// ahead) carry wide rows, narrow ones take as many as are resident.
 int64_t bwd_groups(int64_t n, int64_t d) {
-  const int64_t at_once = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
-  return std::max<int64_t>(1, std::min<int64_t>(512, cdiv(n, 4 * at_once)));
+  const int64_t at_once = d <= 1024 ? 4 : d <= 2048 ? 2 : 1, most = d <= 512 ? 1280 : d <= 2048 ? 768 : 512;
+  return std::max<int64_t>(1, std::min<int64_t>(most, cdiv(n, 4 * at_once)));
 }
 int64_t bwd_parts(int64_t n, int64_t d) { return d <= ROW_MAX ? bwd_groups(n, d) : col_plan(n).chunks; }
 
@@ -487,7 +475,8 @@ __global__ __launch_bounds__(NT) void reduce_partials_kernel(const float* __rest
 }
 
 // Calls f(waves per token, 8-channel pieces per lane) as compile-time constants for rows of d
-// channels; a lane holds 8 or 16 channels.
+// channels; a lane holds 8 to 32 channels (16 waves of 16 would leave 128 registers a lane, and the
+// backward kernel spills: 12192 x 11008 374 us).
 template <class F>
 lrc_status with_row_shape(int64_t d, F f) {
   using std::integral_constant;
@@ -496,10 +485,9 @@ lrc_status with_row_shape(int64_t d, F f) {
   if (d <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
   if (d <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
   if (d <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  if (d <= 12288) return f(integral_constant<int, 8>{}, integral_constant<int, 3>{});
+  return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
 }
-
-bool codes_vec(const int8_t* codes) { return (reinterpret_cast<uintptr_t>(codes) & 7) == 0; }
 
 template <class T>
 lrc_status norm_forward(hipStream_t st, const T* x, int64_t n, int64_t d, int64_t ldx, const float* gamma,
@@ -514,17 +502,12 @@ lrc_status norm_forward(hipStream_t st, const T* x, int64_t n, int64_t d, int64_
     LRC_LAUNCHED();
     return LRC_OK;
   }
-  const bool vec = d % 8 == 0 && rows_vec16(x, ldx, sizeof(T)) && rows_vec16(y, ldy, sizeof(T)) && codes_vec(codes);
   return with_row_shape(d, [&](auto w, auto v) -> lrc_status {
     constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
-    using S = RowShape<T, WPR, V, true>;
+    using S = RowShape<T, WPR, V>;
     const unsigned grid = unsigned(std::min<int64_t>(cdiv(n, S::GROUPS), 2048 / std::max(1, WPR / 4)));
-    if (vec)
-      ln_fwd_kernel<T, WPR, V, true><<<grid, S::THREADS, 0, st>>>(x, ldx, n, int(d), gamma, beta, eps, y, ldy, mean,
-                                                                  rstd, codes, exps, nb, info);
-    else
-      ln_fwd_kernel<T, WPR, V, false><<<grid, S::THREADS, 0, st>>>(x, ldx, n, int(d), gamma, beta, eps, y, ldy, mean,
-                                                                   rstd, codes, exps, nb, info);
+    ln_fwd_kernel<T, WPR, V><<<grid, S::THREADS, 0, st>>>(x, ldx, n, int(d), gamma, beta, eps, y, ldy, mean, rstd,
+                                                          codes, exps, nb, info);
     LRC_LAUNCHED();
     return LRC_OK;
   });
@@ -541,19 +524,13 @@ lrc_status norm_backward(hipStream_t st, const T* dy, int64_t n, int64_t d, int6
     ProfScope scope("ln_bwd_kernel", st, 14.0 * double(n) * double(d),
                     double(n) * double(d) * (2 * sizeof(T) + (CK ? 1 : sizeof(T))) + 8.0 * double(n) + 12.0 * d);
     if (d <= ROW_MAX) {
-      const bool vec = d % 8 == 0 && rows_vec16(dy, lddy, sizeof(T)) && (dx == nullptr || rows_vec16(dx, lddx, sizeof(T))) &&
-                       (CK ? codes_vec(codes) : rows_vec16(x, ldx, sizeof(T)));
       const unsigned grid = unsigned(bwd_groups(n, d));
       float* part = params ? partial : nullptr;
       LRC_TRY(with_row_shape(d, [&](auto w, auto v) -> lrc_status {
         constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
-        using S = RowShape<T, WPR, V, true>;
-        if (vec)
-          ln_bwd_kernel<T, WPR, V, true, CK><<<grid, S::THREADS, 0, st>>>(dy, lddy, n, int(d), x, ldx, codes, exps, nb,
-                                                                          mean, rstd, gamma, dx, lddx, part);
-        else
-          ln_bwd_kernel<T, WPR, V, false, CK><<<grid, S::THREADS, 0, st>>>(dy, lddy, n, int(d), x, ldx, codes, exps, nb,
-                                                                           mean, rstd, gamma, dx, lddx, part);
+        using S = RowShape<T, WPR, V>;
+        ln_bwd_kernel<T, WPR, V, CK><<<grid, S::THREADS, 0, st>>>(dy, lddy, n, int(d), x, ldx, codes, exps, nb, mean,
+                                                                  rstd, gamma, dx, lddx, part);
         LRC_LAUNCHED();
         return LRC_OK;
       }));

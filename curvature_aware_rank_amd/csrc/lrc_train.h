@@ -11,6 +11,9 @@ constexpr int CKB = LRC_CKPT_BLOCK;   // channels that share one checkpoint expo
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+__device__ __forceinline__ float float_of(float v) { return v; }
+__device__ __forceinline__ float float_of(uint16_t v) { return bf16_bits_to_f32(v); }
+__device__ __forceinline__ float float_of(int8_t v) { return float(v); }
 __device__ __forceinline__ float ld_elem(const float* p) { return *p; }
 __device__ __forceinline__ float ld_elem(const uint16_t* p) { return bf16_bits_to_f32(*p); }
 
@@ -29,21 +32,33 @@ __device__ __forceinline__ float round_to(float v, const uint16_t*) {
   return bf16_bits_to_f32(pack_bf16x2(v, v) & 0xffffu);
 }
 
-// eight consecutive elements; `vec`: 16-byte accesses allowed, `cnt`: elements in range
-__device__ __forceinline__ void ld8(const float* p, bool vec, int cnt, float (&v)[8]) {
-  if (vec && cnt >= 8) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+// A short piece: its loads repeat the last element that exists, so that none of them is under a
+// condition of its own and all are in flight together.
+template <class T>
+__device__ __forceinline__ void ld_short(const T* p, int cnt, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+  for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  if (cnt <= 0) return;
+  T t[7];
+#pragma unroll
+  for (int e = 0; e < 7; ++e) t[e] = p[min(e, cnt - 1)];
+#pragma unroll
+  for (int e = 0; e < 7; ++e) v[e] = e < cnt ? float_of(t[e]) : 0.f;
+}
+// Eight consecutive elements, of which `cnt` are in range.  Whole pieces travel as 16-byte
+// accesses at the element's own alignment (the memory path takes any address), so rows of any
+// pitch and start are read alike.
+__device__ __forceinline__ void ld8(const float* p, int cnt, float (&v)[8]) {
+  if (cnt >= 8) {
+    __builtin_memcpy(v, p, 32);
     return;
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? p[e] : 0.f;
+  ld_short(p, cnt, v);
 }
-__device__ __forceinline__ void ld8(const uint16_t* p, bool vec, int cnt, float (&v)[8]) {
-  if (vec && cnt >= 8) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void ld8(const uint16_t* p, int cnt, float (&v)[8]) {
+  if (cnt >= 8) {
+    uint32_t w[4];
+    __builtin_memcpy(w, p, 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       v[2 * e] = __uint_as_float(w[e] << 16);
@@ -51,25 +66,23 @@ __device__ __forceinline__ void ld8(const uint16_t* p, bool vec, int cnt, float 
     }
     return;
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? bf16_bits_to_f32(p[e]) : 0.f;
+  ld_short(p, cnt, v);
 }
-__device__ __forceinline__ void st8(float* p, bool vec, int cnt, const float (&v)[8]) {
-  if (vec && cnt >= 8) {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+__device__ __forceinline__ void st8(float* p, int cnt, const float (&v)[8]) {
+  if (cnt >= 8) {
+    __builtin_memcpy(p, v, 32);
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (e < cnt) p[e] = v[e];
 }
-__device__ __forceinline__ void st8(uint16_t* p, bool vec, int cnt, const float (&v)[8]) {
+__device__ __forceinline__ void st8(uint16_t* p, int cnt, const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-  if (vec && cnt >= 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (cnt >= 8) {
+    __builtin_memcpy(p, w, 16);
     return;
   }
 #pragma unroll
@@ -77,7 +90,7 @@ __device__ __forceinline__ void st8(uint16_t* p, bool vec, int cnt, const float 
     if (e < cnt) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
 }
 
-// rows of `ld` elements of `size` bytes starting at p can be read 16 bytes at a time
+// rows of `ld` elements of `size` bytes starting at p are whole aligned 16-byte pieces
 inline bool rows_vec16(const void* p, int64_t ld, int size) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * size) % 16 == 0;
 }
@@ -104,18 +117,17 @@ __device__ __forceinline__ int ckpt_code(float v, float inv) {
   return v == v ? int(q) : 0;
 }
 // eight codes times their block's step
-__device__ __forceinline__ void ld8_codes(const int8_t* p, bool vec, int cnt, float step, float (&v)[8]) {
-  if (vec && cnt >= 8) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ void ld8_codes(const int8_t* p, int cnt, float step, float (&v)[8]) {
+  if (cnt >= 8) {
+    uint32_t w[2];
+    __builtin_memcpy(w, p, 8);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = float(int8_t(u.x >> (8 * e))) * step;
-      v[4 + e] = float(int8_t(u.y >> (8 * e))) * step;
-    }
+    for (int e = 0; e < 8; ++e) v[e] = float(int8_t(w[e >> 2] >> (8 * (e & 3)))) * step;
     return;
   }
+  ld_short(p, cnt, v);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? float(p[e]) * step : 0.f;
+  for (int e = 0; e < 8; ++e) v[e] *= step;
 }
 // Largest of the values of the eight lanes 8 i .. 8 i + 7, in each of them (three lane
 // permutations inside the vector unit: neighbours, pairs, mirrored halves).
@@ -129,7 +141,7 @@ __device__ __forceinline__ uint32_t max_of_8(uint32_t u) {
 // Magnitudes are compared as integers, where NaN and infinities come out above every finite
 // one: a block without them, and below the exponent's upper end, needs no test per value, and
 // v * 2^-e + 1.5 * 2^23 has the code in its low byte (one rounding, ties to even).
-__device__ __forceinline__ void st8_codes(int8_t* p, int8_t* pe, bool vec, int cnt, const float (&v)[8], int lane,
+__device__ __forceinline__ void st8_codes(int8_t* p, int8_t* pe, int cnt, const float (&v)[8], int lane,
                                           bool& bad) {
   uint32_t u = 0;
 #pragma unroll
@@ -156,13 +168,14 @@ __device__ __forceinline__ void st8_codes(int8_t* p, int8_t* pe, bool vec, int c
     for (int e = 0; e < 8; ++e) q[e] = uint32_t(ckpt_code(v[e], inv));
   }
   if (cnt <= 0) return;
-  if (vec && cnt >= 8) {
+  if (cnt >= 8) {
     // the low bytes of four words in one
     auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
       const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
       return lo | hi;
     };
-    *reinterpret_cast<uint2*>(p) = make_uint2(four(q[0], q[1], q[2], q[3]), four(q[4], q[5], q[6], q[7]));
+    const uint32_t w[2] = {four(q[0], q[1], q[2], q[3]), four(q[4], q[5], q[6], q[7])};
+    __builtin_memcpy(p, w, 8);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -235,7 +248,7 @@ struct Epilogue {
   int8_t* exps = nullptr;
   int64_t nb = 0;
   int32_t* info = nullptr;
-  bool vec_y = false, vec_r = false, vec_z = false, vec_c = false;
+  const int32_t *row_exp = nullptr, *col_exp = nullptr;   // D[m][n] is 2^(row_exp[m] + col_exp[n]) times the sum
 };
 
 // the bias of eight consecutive columns, of which `cnt` exist
@@ -249,14 +262,19 @@ template <class TO>
 __device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t col, int cnt, const float (&b)[8],
                                         float (&v)[8], int lane, bool& bad) {
   float r[8];
-  if (ep.res != nullptr) ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, ep.vec_r, cnt, r);
+  if (ep.res != nullptr) ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, cnt, r);
+  if (ep.row_exp != nullptr && cnt > 0) {
+    const int re = ep.row_exp[row];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < cnt ? ldexpf(v[e], re + ep.col_exp[col + e]) : 0.f;
+  }
   if (ep.bias != nullptr) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += b[e];
   }
-  if (ep.z != nullptr && cnt > 0) st8(static_cast<TO*>(ep.z) + row * ep.ldz + col, ep.vec_z, cnt, v);
+  if (ep.z != nullptr && cnt > 0) st8(static_cast<TO*>(ep.z) + row * ep.ldz + col, cnt, v);
   if (ep.codes != nullptr)
-    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * ep.nb + (col >> 6), ep.vec_c, cnt, v, lane, bad);
+    st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * ep.nb + (col >> 6), cnt, v, lane, bad);
   if (cnt <= 0) return;
   if (ep.act != LRC_ACT_NONE) {
 #pragma unroll
@@ -266,7 +284,7 @@ __device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  st8(static_cast<TO*>(ep.y) + row * ep.ldy + col, ep.vec_y, cnt, v);
+  st8(static_cast<TO*>(ep.y) + row * ep.ldy + col, cnt, v);
 }
 
 // bf16 operands with 16-byte rows on the matrix cores (lrc_gemm.hip).
@@ -280,6 +298,7 @@ struct GemmOperand {
 struct GemmSegments {
   int count = 1;
   uint32_t pa = 0, pb = 0;
+  bool half = false;   // the operands are fp16, not bf16 (K_COLS x K_COLS, one plane)
 };
 constexpr int64_t GEMM_MAX_LD = int64_t(1) << 21;   // tile offsets stay below 2^31 bytes
 constexpr int64_t GEMM_MAX_K = int64_t(1) << 27;    // stages of all segments count in 32 bits

@@ -468,8 +468,10 @@ size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_
  * leading dim lddz) is written; with LRC_ACT_NONE dz is dy and the argument is ignored.
  * relu'(0) = 0.  dx: n_tokens x d_in (leading dim lddx); dW: d_out x d_in (leading dim
  * lddw), dtype dw_dt (LRC_F32, or `dt`); db: float[d_out]; any of the three may be NULL.
- * With dtype bf16, dx and dW are products of the rounded dz, as the stream holds it; db sums
- * the unrounded one.  Sums fp32 in an order that depends on the sizes only.
+ * With dtype bf16, dx is a product of the rounded dz, as the stream holds it; dW takes dz with
+ * three more bits where the activation is GELU or SiLU (fp16, each channel of dz and x scaled
+ * by a power of two; with RELU and NONE dz is exact in bf16), and db sums the unrounded dz.
+ * Sums fp32 in an order that depends on the sizes only.
  * n_tokens == 0 writes zeros to dW and db.  Sizes as lrc_linear.
  */
 lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,

@@ -334,6 +334,50 @@ def test_linear_accuracy_at_long_sums(lrc, dtype, n, d_in, d_out):
     assert off(dw, dy.double().T.contiguous() @ x.double()) < 24 * U
 
 
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("n,d_in,d_out", [(5, 17, 9), (300, 136, 264), (1000, 521, 303), (2500, 1032, 2056)])
+@pytest.mark.parametrize("held", [False, True])
+def test_weight_gradient_keeps_the_bits_of_dz(lrc, act, n, d_in, d_out, held):
+    """dW of a bf16 layer with a smooth activation takes dz to 11 bits: a rounding of at most 2^-11 relative (2^-12
+    half steps, uniform: 2^-12 / sqrt(3) in the 2-norm, the slope's 16 u besides), whatever the channels' scales."""
+    g = torch.Generator().manual_seed(n)
+    x, dy = stream(n, d_in, torch.bfloat16, 1), stream(n, d_out, torch.bfloat16, 2)
+    x = (x.float() * 2.0 ** torch.randint(-30, 31, (d_in,), generator=g)).bfloat16()
+    dy = (dy.float() * 2.0 ** torch.randint(-40, 41, (d_out,), generator=g)).bfloat16()
+    dy[:, 0], x[:, 1] = 0, 0
+    z = torch.randn(n, d_out, generator=g).bfloat16()
+    w = torch.zeros(d_out, d_in, dtype=torch.bfloat16, device=dev())
+    xa, xn = x.to(dev()), f64(x)
+    if held:
+        xa = lrc.lrc_pack_activations(xa)[:2]
+        xn = ref.unpack(xa[0].cpu().numpy(), xa[1].cpu().numpy())
+    _, _, dw, _ = lrc.lrc_linear_backward(dy.to(dev()), xa, w, act=act, z=z.to(dev()), dw_dtype=torch.float32)
+    dz = f64(dy) * ref.act_slope(f64(z), act)
+    want, got = dz.T @ xn, f64(dw)
+    rows = np.linalg.norm(dz, axis=0)[:, None] * np.linalg.norm(xn, axis=0)[None]   # by channel, so that each counts
+    ok = rows > 0
+    assert not got[~ok].any()
+    err = ((got - want)[ok] / rows[ok])
+    assert np.abs(err).max() < 2.0 ** -11 and math.sqrt((err ** 2).mean()) < 2.0 ** -12
+
+
+def test_weight_gradient_with_nonfinite_entries(lrc):
+    n, d = 200, 72
+    ones = lambda *s: torch.ones(*s, dtype=torch.bfloat16)   # noqa: E731
+    x, dy, z = ones(n, d), ones(n, d), ones(n, d)
+    dy[3, 5], dy[4, 6], x[7, 8], z[9, 10] = float("inf"), float("nan"), float("-inf"), float("nan")
+    args = [t.to(dev()) for t in (dy, x, ones(d, d))]
+    _, _, dw, _ = lrc.lrc_linear_backward(*args, act="silu", z=z.to(dev()))
+    dz = dy.double() * torch.from_numpy(ref.act_slope(f64(z), "silu"))
+    want = (dz.T @ x.double()).to(dev())
+    assert torch.equal(torch.isnan(dw), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(dw.double()[inf], want[inf])
+    fine = torch.isfinite(want)
+    # sums of 200 equal terms: half a bf16 step and the slope's error
+    assert ((dw.double() - want)[fine].abs() <= (2.0 ** -8 + 2.0 ** -11) * want[fine].abs()).all()
+
+
 @pytest.mark.parametrize("n,d_in,d_out", [(520, 264, 392), (1300, 904, 1101)])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("where", ["x", "w", "dy"])
