@@ -375,7 +375,8 @@ struct ColPlan {
 };
 ColPlan col_plan(int64_t n) {
   ColPlan p;
-  p.rows = std::max<int64_t>(n <= 1024 ? 8 : 32, cdiv(n, 1024));
+  // one chunk needs no second pass; more of them spread a short stream over the chip
+  p.rows = std::max<int64_t>(n > 32 && n <= 1024 ? 8 : 32, cdiv(n, 1024));
   p.chunks = cdiv(n, p.rows);
   return p;
 }
@@ -390,7 +391,14 @@ struct MagnitudeJob {
 struct MagnitudeJobs {
   MagnitudeJob job[2];
 };
-// largest finite magnitude (as bits) of every channel over a chunk of tokens
+// exponent that brings a channel's largest magnitude into [2^14, 2^15); 0 for a channel of zeros
+__device__ __forceinline__ int channel_exponent(uint32_t bits) {
+  int e = 0;
+  const float f = frexpf(__uint_as_float(bits), &e);   // in [1/2, 1)
+  return f > 0.f ? e - 15 : 0;
+}
+// largest finite magnitude (as bits) of every channel over a chunk of tokens; the exponent itself
+// where there is one chunk
 __global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64_t n, int64_t rows) {
   __shared__ uint32_t most[3][64][9];
   const int q = int64_t(blockIdx.x) < jobs.job[0].blocks ? 0 : 1;
@@ -425,11 +433,14 @@ __global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64
   if (wave > 0) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (e < cnt)
-      j.part[int64_t(blockIdx.y) * j.cols + c + e] =
-          max(max(m[e], most[0][lane][e]), max(most[1][lane][e], most[2][lane][e]));
+    if (e < cnt) {
+      const uint32_t u = max(max(m[e], most[0][lane][e]), max(most[1][lane][e], most[2][lane][e]));
+      if (gridDim.y == 1)
+        j.out[c + e] = channel_exponent(u);
+      else
+        j.part[int64_t(blockIdx.y) * j.cols + c + e] = u;
+    }
 }
-// exponent that brings a channel's largest magnitude into [2^14, 2^15); 0 for a channel of zeros
 __global__ __launch_bounds__(LT) void exponent_kernel(MagnitudeJobs jobs, int64_t chunks) {
   __shared__ uint32_t acc[8][33];
   const int q = int64_t(blockIdx.x) < cdiv_dev(jobs.job[0].cols, 32) ? 0 : 1;
@@ -447,9 +458,7 @@ __global__ __launch_bounds__(LT) void exponent_kernel(MagnitudeJobs jobs, int64_
   if (sl > 0 || c >= j.cols) return;
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = max(m, acc[i][cx]);
-  int e = 0;
-  const float f = frexpf(__uint_as_float(m), &e);   // in [1/2, 1)
-  j.out[c] = f > 0.f ? e - 15 : 0;
+  j.out[c] = channel_exponent(m);
 }
 
 // ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
@@ -926,8 +935,10 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     ProfScope scope("magnitude_kernel", st, 0.0, double(n) * (2.0 * double(dn) + (held ? double(di) / 64 : 2.0 * di)));
     magnitude_kernel<<<dim3(unsigned(m.job[0].blocks + m.job[1].blocks), unsigned(p.chunks)), LT, 0, st>>>(m, n, p.rows);
     LRC_LAUNCHED();
-    exponent_kernel<<<unsigned(cdiv(dn, 32) + cdiv(di, 32)), LT, 0, st>>>(m, p.chunks);
-    LRC_LAUNCHED();
+    if (p.chunks > 1) {
+      exponent_kernel<<<unsigned(cdiv(dn, 32) + cdiv(di, 32)), LT, 0, st>>>(m, p.chunks);
+      LRC_LAUNCHED();
+    }
   }
   if (with_dz || a.db != nullptr) {
     const ColPlan p = col_plan(n);
@@ -935,7 +946,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
       const dim3 grid(unsigned(cdiv(dn, 512)), unsigned(p.chunks));
-      float* part = a.db != nullptr ? room.sums : nullptr;
+      float* part = a.db != nullptr && p.chunks > 1 ? room.sums : a.db;   // one chunk's sums are db
       const T *dy = static_cast<const T*>(a.dy), *z = static_cast<const T*>(a.z);
       T* dz = static_cast<T*>(a.dz);
       if (a.z == nullptr && a.act != LRC_ACT_NONE) {
@@ -948,7 +959,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
       }
       LRC_LAUNCHED();
     }
-    if (a.db != nullptr) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db, nullptr));
+    if (a.db != nullptr && p.chunks > 1) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db, nullptr));
   } else if (flag) {
     clear_flag_kernel<<<1, 1, 0, st>>>(flag);
     LRC_LAUNCHED();
