@@ -1,15 +1,18 @@
 // bf16 (or fp16) matrix products on the matrix cores with a fused epilogue: the linear layer's forward,
 // dx and dW products.
 //
-// An output tile of BM x BN belongs to one workgroup; its waves hold blocks of 32 x 32
-// accumulators.  Both operands travel from memory straight into LDS (16 bytes per lane, no
-// staging registers) in stages of 32 k steps, four stage buffers, three stages in flight
-// while one is multiplied.  A buffer resource bounds each operand, so rows past the matrix and
+// An output tile of BM x BN belongs to one workgroup; its waves hold blocks of MF x MF
+// accumulators (16 x 16 x 32 or 32 x 32 x 16 matrix instructions).  Both operands travel from memory straight into LDS (16 bytes per lane, no
+// staging registers) in stages of 32 or 64 k steps, four or two stage buffers, all but one
+// in flight while one is multiplied.  A buffer resource bounds each operand, so rows past the matrix and
 // k past its end read as zeros without any masking of data.
-//   K_ROWS: a tile row's 32 k steps are 64 bytes; the 16-byte granule g of row r sits in slot
-//     g ^ ((r / 4) % 4), so the 16 rows of a fragment read cover every bank once.
-//   K_COLS: a k step's BM channels lie together; fragments come from transposing LDS reads
-//     (ds_read_b64_tr_b16), granule g of step t in slot g ^ 4 (t % 4).
+//   K_ROWS: a tile row's k steps lie together; its 16-byte granules change places by the row's
+//     number, so that the 16 rows of a fragment read cover every bank once.
+//   K_COLS: a k step's channels lie together; fragments come from transposing LDS reads
+//     (ds_read_b64_tr_b16), granules changing places by the step's number.
+// Where it stands: 8192 x 4096 x 11008 bf16 forward 680 us (1090 TFLOP/s; the vendor's library on
+// the same box 690), dx 560-585, dW 580-605; 4096^3 103 us (library 90, which holds 85 % of the
+// matrix pipes' cycles where this holds 73 %).
 // Few tiles leave compute units idle, so k may be split: every split writes its fp32 tile and
 // a second kernel adds them in split order and runs the epilogue (bit-reproducible).
 #include "lrc_train.h"
@@ -41,7 +44,7 @@ __device__ __forceinline__ void* uniform_ptr(const void* p) {
 }
 
 // One operand's stages: EDGE tile rows (channels for K_COLS), NW waves.
-template <int KIND, int EDGE, int NW, int KS>
+template <int KIND, int EDGE, int NW, int KS, int MF>
 struct Stager {
   static constexpr int LOADS = EDGE * KS * 2 / 1024 / NW;   // 1 KB loads per wave and stage
   static constexpr int ROWB = EDGE * 2;                     // K_COLS: bytes per k step
@@ -74,7 +77,7 @@ struct Stager {
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) {
         const int t = (64 / LPR) * (LOADS * wave + j) + lane / LPR;
-        const int g = (lane % LPR) ^ (4 * (t & 3));
+        const int g = (lane % LPR) ^ step_swizzle(t);
         kk[j] = 0;
         voff[j] = 8 * g < left ? unsigned(t * ld * 2) + 16 * g : OOB;
       }
@@ -109,27 +112,63 @@ struct Stager {
   // K_ROWS: rows 16 apart in a fragment read fall on every bank once
   static __device__ __forceinline__ int row_swizzle(int r) { return KS == 32 ? (r >> 2) & 3 : (r >> 1) & 7; }
 
-  // byte offset of the lane's fragment of tile rows row .. row + 31, first 16 k steps
+  // K_COLS: the four k steps a group of 16 lanes reads fall on four quarters of the banks, the
+  // groups of k steps 8 apart on halves of those
+  static __device__ __forceinline__ int step_swizzle(int t) {
+    return (4 * (t & 3)) ^ (MF == 16 ? 2 * ((t >> 3) & 1) : 0);
+  }
+
+  // A fragment is MF tile rows x KF = 512 / MF k steps, eight k of one row per lane.  Byte offset
+  // of the lane's first one for tile rows row .. row + MF - 1.
+  static constexpr int KF = 512 / MF;
   static __device__ int frag_off(int row, int lane) {
     if (KIND == K_ROWS) {
-      const int r = row + (lane & 31);
-      return r * (2 * KS) + (((lane >> 5) ^ row_swizzle(r)) << 4);
+      const int r = row + lane % MF;
+      return r * (2 * KS) + (((lane / MF) ^ row_swizzle(r)) << 4);
     }
     const int g = lane >> 4, sl = lane & 15;
-    const int ch = row + 16 * (g & 1) + 4 * (sl & 3);
-    const int tk = 8 * (g >> 1) + (sl >> 2);
-    return tk * ROWB + (((ch >> 3) ^ (4 * (tk & 3))) << 4) + (ch & 7) * 2;
+    const int ch = row + (MF == 32 ? 16 * (g & 1) : 0) + 4 * (sl & 3);
+    const int tk = 8 * (MF == 32 ? g >> 1 : g) + (sl >> 2);
+    return tk * ROWB + (((ch >> 3) ^ step_swizzle(tk)) << 4) + (ch & 7) * 2;
   }
-  // fragment of the stage's k steps [16 q, 16 q + 16)
+  // fragment of the stage's k steps [KF q, KF q + KF)
   static __device__ bf16x8 frag(const uint8_t* lds, int off, int q) {
-    if (KIND == K_ROWS) return *reinterpret_cast<const bf16x8*>(lds + (off ^ (32 * q)));
-    const uint8_t* p = lds + off + q * 16 * ROWB;
+    if (KIND == K_ROWS) return *reinterpret_cast<const bf16x8*>(lds + (off ^ (2 * KF * q)));
+    const uint8_t* p = lds + off + q * KF * ROWB;
     const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p));
     const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * ROWB));
     const short tmp[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     bf16x8 f;
     __builtin_memcpy(&f, tmp, sizeof(f));
     return f;
+  }
+};
+
+// MF x MF accumulators of one matrix instruction
+template <int MF>
+struct Block;
+template <>
+struct Block<16> {
+  typedef f32x4 acc_t;
+  static constexpr int E = 4;
+  static __device__ __forceinline__ int row(int e, int lane) { return 4 * (lane >> 4) + e; }
+  static __device__ __forceinline__ acc_t mma(bf16x8 a, bf16x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ acc_t mma_half(f16x8 a, f16x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Block<32> {
+  typedef f32x16 acc_t;
+  static constexpr int E = 16;
+  static __device__ __forceinline__ int row(int e, int lane) { return 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3); }
+  static __device__ __forceinline__ acc_t mma(bf16x8 a, bf16x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ acc_t mma_half(f16x8 a, f16x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
 };
 
@@ -149,19 +188,19 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
   tn = r / rows;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
+template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
 __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N, int64_t K,
                                           const GemmSegments& seg, const TileGrid& tg, const Epilogue& ep,
                                           float* __restrict__ partial, const int32_t* __restrict__ skip) {
-  constexpr int NW = WM * WN, BM = WM * FM * 32, BN = WN * FN * 32;
+  constexpr int NW = WM * WN, BM = WM * FM * MF, BN = WN * FN * MF;
   constexpr int AB = BM * KS * 2, STB = (BM + BN) * KS * 2;
-  using SA = Stager<KA, BM, NW, KS>;
-  using SB = Stager<KB, BN, NW, KS>;
+  using SA = Stager<KA, BM, NW, KS, MF>;
+  using SB = Stager<KB, BN, NW, KS, MF>;
   constexpr int L = SA::LOADS + SB::LOADS;      // loads of a wave per stage
   // one LDS object per stage, so that a read of one stage does not wait for the loads of others
   __shared__ __attribute__((aligned(1024))) uint8_t sb0[STB], sb1[STB], sb2[NST > 2 ? STB : 16],
       sb3[NST > 3 ? STB : 16];
-  constexpr int PART = 32 * FN * 32 * 4;        // a wave's epilogue rows
+  constexpr int PART = 32 * FN * MF * 4;        // a wave's epilogue rows
   constexpr int FIT = STB / PART;               // of them in a stage buffer
   static_assert(NST >= 2 && NST <= 4 && KS % 32 == 0 && FIT >= 1 && FIT * NST >= NW, "the epilogue rows fit the stage buffers");
 
@@ -212,16 +251,17 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
 
   int offa[FM], offb[FN];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) offa[i] = SA::frag_off((wr * FM + i) * 32, lane);
+  for (int i = 0; i < FM; ++i) offa[i] = SA::frag_off((wr * FM + i) * MF, lane);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) offb[j] = SB::frag_off((wc * FN + j) * 32, lane);
-  f32x16 acc[FM][FN];
+  for (int j = 0; j < FN; ++j) offb[j] = SB::frag_off((wc * FN + j) * MF, lane);
+  using Blk = Block<MF>;
+  typename Blk::acc_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < Blk::E; ++e) acc[i][j][e] = 0.f;
 
   bf16x8 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
   auto read_frags = [&](const uint8_t* s, int q, bf16x8* fa, bf16x8* fb) {
@@ -235,24 +275,24 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        acc[i][j] = HALF ? __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fa[i]),
-                                                                  __builtin_bit_cast(f16x8, fb[j]), acc[i][j], 0, 0, 0)
-                         : __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        acc[i][j] = HALF ? Blk::mma_half(__builtin_bit_cast(f16x8, fa[i]), __builtin_bit_cast(f16x8, fb[j]), acc[i][j])
+                         : Blk::mma(fa[i], fb[j], acc[i][j]);
   };
-  // Issue orders of the two halves of a step: the fragment reads (and the next stage's loads)
-  // go out between the products, which hide them.
-  constexpr int RD = (FM * (KA == K_ROWS ? 1 : 2) + FN * (KB == K_ROWS ? 1 : 2) + FM * FN - 1) / (FM * FN);
+  // Issue order of a step: the fragment reads (and the next stage's loads) go out between the
+  // products, which hide them.
+  constexpr int READS = FM * (KA == K_ROWS ? 1 : 2) + FN * (KB == K_ROWS ? 1 : 2), MM = FM * FN;
+  constexpr int GROUPS = MM < 8 ? 4 : 8, GRP = MM / GROUPS;   // products per group
   auto interleave_reads = [&]() {
-#define LRC_PAIR                                         \
-  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     \
-  __builtin_amdgcn_sched_group_barrier(0x100, RD, 0);
+#define LRC_PAIR                                                       \
+  __builtin_amdgcn_sched_group_barrier(0x008, GRP, 0);                 \
+  __builtin_amdgcn_sched_group_barrier(0x100, (READS + GROUPS - 1) / GROUPS, 0);
     LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR
-    if constexpr (FM * FN == 8) { LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR }
+    if constexpr (GROUPS == 8) { LRC_PAIR LRC_PAIR LRC_PAIR LRC_PAIR }
   };
   auto interleave_loads = [&]() {
-#define LRC_TRIPLE LRC_PAIR __builtin_amdgcn_sched_group_barrier(0x020, (L + FM * FN - 1) / (FM * FN), 0);
+#define LRC_TRIPLE LRC_PAIR __builtin_amdgcn_sched_group_barrier(0x020, (L + GROUPS - 1) / GROUPS, 0);
     LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE
-    if constexpr (FM * FN == 8) { LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE }
+    if constexpr (GROUPS == 8) { LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE LRC_TRIPLE }
 #undef LRC_TRIPLE
 #undef LRC_PAIR
   };
@@ -281,15 +321,19 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   }
   wait_barrier<(NST - 1) * L>();
   read_frags(sb0, 0, fa0, fb0);
-  auto step = [&](uint8_t* cur, const uint8_t* nxt, bool live) {
+  // A stage of KS / KF steps (an even number); fa0, fb0 hold its first one.  The barrier stands
+  // before the last.
+  constexpr int STEPS = KS / SA::KF;
+  static_assert(STEPS % 2 == 0 && STEPS >= 2, "the two fragment sets take turns");
+  auto stage = [&](uint8_t* cur, const uint8_t* nxt, bool live) {
     next_stage(live);
 #pragma unroll
-    for (int q = 0; q < KS / 16 - 1; q += 2) {
+    for (int q = 0; q < STEPS; q += 2) {
       read_frags(cur, q + 1, fa1, fb1);
       mma(fa0, fb0);
       interleave_reads();
       __builtin_amdgcn_sched_barrier(0);
-      if (q + 2 < KS / 16) {
+      if (q + 2 < STEPS) {
         read_frags(cur, q + 2, fa0, fb0);
         mma(fa1, fb1);
         interleave_reads();
@@ -307,49 +351,47 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   int s = 0;
   for (; s + 2 * NST - 1 < nsteps; s += NST) {
     if constexpr (NST == 2) {
-      step(sb0, sb1, true);
-      step(sb1, sb0, true);
-    } else if constexpr (NST == 3) {
-      step(sb0, sb1, true);
-      step(sb1, sb2, true);
-      step(sb2, sb0, true);
+      stage(sb0, sb1, true);
+      stage(sb1, sb0, true);
     } else {
-      step(sb0, sb1, true);
-      step(sb1, sb2, true);
-      step(sb2, sb3, true);
-      step(sb3, sb0, true);
+      static_assert(NST == 2 || NST == 4, "two or four stage buffers");
+      stage(sb0, sb1, true);
+      stage(sb1, sb2, true);
+      stage(sb2, sb3, true);
+      stage(sb3, sb0, true);
     }
   }
   // the last stages choose their buffers at run time; behind the last one only zeros are read
-  for (; s < nsteps; ++s) step(buf(s), buf(s + 1), s + NST < nsteps);
+  for (; s < nsteps; ++s) stage(buf(s), buf(s + 1), s + NST < nsteps);
   wait_barrier<0>();   // every load has landed and every read is done: the buffers are free
 
-  // Epilogue: a wave's 32 rows x (32 FN) columns pass through its own part of LDS, so that a
+  // Epilogue: a wave's 32 rows x TW columns at a time pass through its own part of LDS, so that a
   // lane holds eight consecutive columns of a row and the accesses to memory are whole pieces.
-  // Accumulator element e of lane l is row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
   float* tile = reinterpret_cast<float*>(buf(wave / FIT) + (wave % FIT) * PART);
-  constexpr int TW = FN * 32;          // tile columns
+  constexpr int TW = FN * MF;          // tile columns
   constexpr int LPR = TW / 8;          // lanes per row
+  // rows that a wave writes together fall on different banks
+  auto place = [&](int r, int c) { return r * TW + (c ^ (MF == 16 ? 16 * ((r >> 2) & 3) : (r & 4) << 3)); };
   bool bad = false;
   const int64_t col = n0 + wc * TW + 8 * (lane % LPR);   // the lane's columns
   float bias[8];
   bias8(ep, col, int(min(N - col, int64_t(8))), bias);
-  auto emit = [&](const f32x16 (&rows)[FN], int i) {
+  auto emit = [&](const typename Blk::acc_t (&upper)[FN], const typename Blk::acc_t (&lower)[FN], int i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int h = 0; h < 32 / MF; ++h)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        tile[r * TW + ((j * 32 + (lane & 31)) ^ ((r & 4) << 3))] = rows[j][e];
-      }
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < Blk::E; ++e)
+          tile[place(MF * h + Blk::row(e, lane), j * MF + lane % MF)] = h ? lower[j][e] : upper[j][e];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 2
     for (int q = 0; q < 32 * LPR / 64; ++q) {
       const int r = q * (64 / LPR) + lane / LPR, c = 8 * (lane % LPR);
-      const float* src = tile + r * TW + (c ^ ((r & 4) << 3));
+      const float* src = tile + place(r, c);
       const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      const int64_t row = m0 + (wr * FM + i) * 32 + r;
+      const int64_t row = m0 + wr * FM * MF + i * 32 + r;
       const int64_t left = row < M ? N - col : 0;
       const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
       if (tg.splits > 1) {
@@ -361,22 +403,20 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
-  static_assert(FM == 2 || FM == 4, "the accumulator rows are named, so that they stay in registers");
-  emit(acc[0], 0);
-  emit(acc[1], 1);
-  if constexpr (FM == 4) {
-    emit(acc[2], 2);
-    emit(acc[3], 3);
-  }
+  // (the accumulators' first index is a constant in each call, so that they stay in registers)
+  static_assert(FM * MF == 64, "a wave holds 64 rows");
+  constexpr int HALF_ROWS = 32 / MF;
+  emit(acc[0], acc[HALF_ROWS - 1], 0);
+  emit(acc[HALF_ROWS], acc[2 * HALF_ROWS - 1], 1);
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
 
-template <class TO, int KA, int KB, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
+template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_bf16_kernel(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                                     int64_t K, GemmSegments seg, TileGrid tg,
                                                                     Epilogue ep, float* __restrict__ partial,
                                                                     const int32_t* __restrict__ skip) {
-  gemm_tile<TO, KA, KB, WM, WN, FM, FN, KS, NST, SEG, HALF>(A, B, M, N, K, seg, tg, ep, partial, skip);
+  gemm_tile<TO, KA, KB, MF, WM, WN, FM, FN, KS, NST, SEG, HALF>(A, B, M, N, K, seg, tg, ep, partial, skip);
 }
 
 // Sum of the splits' tiles in split order, then the epilogue.  One lane per eight columns, the
@@ -421,7 +461,7 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
 
 // Tiles and splits from the sizes alone (256 compute units), so that workspace sizes are known
 // without a device and equal inputs give equal bits.  Large tiles (256 x 256, one workgroup per
-// compute unit, 1200 TFLOP/s at 4096^3) for products that fill the chip; small ones (128 x 128, two
+// compute unit, 1330 TFLOP/s at 4096^3) for products that fill the chip; small ones (128 x 128, two
 // per unit, 1060) otherwise, with k split when they are few.  Small tiles for what a last, part
 // full round of large ones holds gained nothing (8192 x 4096 x 11008, 5.4 rounds: 695 us against
 // 690): the chip is then at its power limit, and units that idle let the others run faster.  Times
@@ -431,7 +471,7 @@ struct Plan {
   TileGrid tg;
 };
 // 64 k steps of every workgroup of a round; a round's first loads and its epilogue
-constexpr double LARGE_STEP = 1.65, SMALL_STEP_FULL = 1.0, SMALL_STEP_HALF = 0.68, ROUND = 7.0, MEMORY = 4.5e6;
+constexpr double LARGE_STEP = 1.55, SMALL_STEP_FULL = 0.88, SMALL_STEP_HALF = 0.64, ROUND = 7.0, MEMORY = 4.5e6;
 
 static TileGrid tiles_of(int64_t m, int64_t n, int edge, int splits, int64_t per, int64_t steps) {
   const int64_t nm = cdiv(m, edge), nn = cdiv(n, edge);
@@ -504,7 +544,12 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   // Stages of a large tile: 64 k steps in two buffers where both operands' rows run along k (a
   // row's piece is then a whole 128-byte line: 8192 x 4096 x 11008 678 us against 712), else 32
   // in four (dx 560 against 579, dW 581 against 610).  Small tiles: 64 in two (785 against 954).
-  constexpr int KL = large_stage(KA, KB), NL = KL == 64 ? 2 : 4;
+  // The 16 x 16 x 32 matrix instruction takes less power than the 32 x 32 x 16 one, and at these
+  // sizes the chip's clock goes by its power (1.9 GHz at 4096^3): 8192 x 4096 x 4096 199 us against
+  // 215, 2048 x 4096 x 4096 on small tiles 62 against 69.  Large tiles with K_COLS operands keep the
+  // larger one: their transposing reads need more address registers, and the smaller one's two full
+  // fragment sets then spill (dx 272 against 225, dW 445 against 213).
+  constexpr int KL = large_stage(KA, KB), NL = KL == 64 ? 2 : 4, ML = KL == 64 ? 16 : 32;
   const Plan p = plan_gemm(M, N, K, seg.count, KL);
   ProfScope scope(name, st, flops, bytes);
   const TileGrid& tg = p.tg;
@@ -513,11 +558,11 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   auto launch = [&](auto many, auto half) {
     constexpr bool SEG = decltype(many)::value, HALF = decltype(half)::value;
     if (p.large)
-      gemm_bf16_kernel<TO, KA, KB, 4, 2, 2, 4, KL, NL, SEG, HALF><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, seg, tg, ep,
-                                                                                            partial, skip);
+      gemm_bf16_kernel<TO, KA, KB, ML, 4, 2, 64 / ML, 128 / ML, KL, NL, SEG, HALF><<<unsigned(grid), 512, 0, st>>>(
+          A, B, M, N, K, seg, tg, ep, partial, skip);
     else
-      gemm_bf16_kernel<TO, KA, KB, 2, 2, 2, 2, 64, 2, SEG, HALF><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, seg, tg, ep,
-                                                                                           partial, skip);
+      gemm_bf16_kernel<TO, KA, KB, 16, 2, 2, 4, 4, 64, 2, SEG, HALF><<<unsigned(grid), 256, 0, st>>>(
+          A, B, M, N, K, seg, tg, ep, partial, skip);
   };
   // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
   if (seg.half) {
