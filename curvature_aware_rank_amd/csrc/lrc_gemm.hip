@@ -471,19 +471,20 @@ struct Plan {
   TileGrid tg;
 };
 // 64 k steps of every workgroup of a round; a round's first loads and its epilogue
-constexpr double LARGE_STEP = 1.55, SMALL_STEP_FULL = 0.88, SMALL_STEP_HALF = 0.64, ROUND = 7.0, MEMORY = 4.5e6;
+constexpr double LARGE_STEP = 1.55, SMALL_STEP_FULL = 0.88, SMALL_STEP_HALF = 0.64, LARGE_ROUND = 14.0,
+                 SMALL_ROUND = 8.0, MEMORY = 4.5e6;
 
 static TileGrid tiles_of(int64_t m, int64_t n, int edge, int splits, int64_t per, int64_t steps) {
   const int64_t nm = cdiv(m, edge), nn = cdiv(n, edge);
   return {nm, nn, nm * nn, int(cdiv(nm * nn, NXCD)), splits, int(per), int(steps)};
 }
 static double large_cost(int64_t tiles, double steps64) {
-  return double(cdiv(tiles, 256)) * (steps64 * LARGE_STEP + ROUND);
+  return double(cdiv(tiles, 256)) * (steps64 * LARGE_STEP + LARGE_ROUND);
 }
 static double small_cost(int64_t groups, double steps64) {
   const int64_t full = groups / 512, rest = groups % 512;
-  double c = double(full) * (steps64 * SMALL_STEP_FULL + ROUND);
-  if (rest > 0) c += steps64 * (rest > 256 ? SMALL_STEP_FULL : SMALL_STEP_HALF) + ROUND;
+  double c = double(full) * (steps64 * SMALL_STEP_FULL + SMALL_ROUND);
+  if (rest > 0) c += steps64 * (rest > 256 ? SMALL_STEP_FULL : SMALL_STEP_HALF) + SMALL_ROUND;
   return c;
 }
 // KL: k steps per stage of a large tile

@@ -19,17 +19,18 @@ constexpr int LT = 256;
 
 __device__ __forceinline__ int64_t cdiv_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// eight fp32 values times 2^-e each, as fp16
-__device__ __forceinline__ void st8_half(uint16_t* p, const float (&v)[8], const int (&e)[8]) {
+// eight fp32 values times their channels' scales (powers of two), as fp16
+__device__ __forceinline__ void st8_half(uint16_t* p, const float (&v)[8], const float (&scale)[8]) {
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
   f16x8 h;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = _Float16(ldexpf(v[i], -e[i]));
+  for (int i = 0; i < 8; ++i) h[i] = _Float16(v[i] * scale[i]);
   *reinterpret_cast<f16x8*>(p) = h;
 }
-__device__ __forceinline__ void exps8(const int32_t* p, int cnt, int (&e)[8]) {
+// 2^-e of eight channels' exponents, of which `cnt` exist
+__device__ __forceinline__ void scales8(const int32_t* p, int cnt, float (&scale)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = i < cnt ? p[i] : 0;
+  for (int i = 0; i < 8; ++i) scale[i] = i < cnt ? pow2f(-p[i]) : 0.f;
 }
 
 struct Operand {
@@ -145,9 +146,9 @@ AnyPlan plan_any(int64_t M, int64_t N, int64_t K) {
   p.tiles_n = cdiv(N, GT);
   p.tiles = cdiv(M, GT) * p.tiles_n;
   const int64_t steps = std::max<int64_t>(1, cdiv(K, GTile<T>::K));
-  // up to two workgroups per compute unit, eight steps at least in each split (a second launch
-  // and the partial tiles cost about as much as eight steps)
-  const int64_t s = std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, p.tiles), steps / 8, 16}));
+  // up to four workgroups per compute unit (their steps' loads hide each other), eight steps at
+  // least in each split (a second launch and the partial tiles cost about as much as eight steps)
+  const int64_t s = std::max<int64_t>(1, std::min<int64_t>({1024 / std::max<int64_t>(1, p.tiles), steps / 8, 32}));
   const int64_t per = cdiv(steps, s);
   p.splits = int(cdiv(steps, per));
   p.k_per_split = per * GTile<T>::K;
@@ -323,7 +324,9 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restric
     for (int q = 0; q < NW; ++q) v += part[q * G * 256 + at];
     if (ep.bias != nullptr) v += ep.bias[col];
     if (ep.z != nullptr) st_elem(static_cast<T*>(ep.z) + t * ep.ldz + col, v);
-    v = act_value(ep.act, v);
+    float a[1] = {v};
+    act_apply(ep.act, a);
+    v = a[0];
     if (ep.res != nullptr) v += ld_elem(static_cast<const T*>(ep.res) + t * ep.ldr + col);
     st_elem(static_cast<T*>(ep.y) + t * ep.ldy + col, v);
   }
@@ -366,10 +369,8 @@ lrc_status linear_rows(hipStream_t st, const Operand& x, const Operand& W, int64
 // the stream: three more bits, so that dW carries no more than its own rounding (with the
 // stream's bf16 its error was 1.3 to 1.55 times that), at the same matrix rate.  fp16 has little
 // range, so each channel of dz and of x is first scaled by a power of two to a largest magnitude
-// near 2^15, and dW's rows and columns are scaled back.  The channels' largest magnitudes are
-// those of dy (an activation's slope is at most 1.13) and of x; a value more than 2^29 below its
-// channel's largest loses bits, one more than 2^40 below becomes zero, far under what the
-// channel's sum keeps of it.
+// near 2^15, and dW's rows and columns are scaled back.  A value more than 2^29 below its
+// channel's largest loses bits, one more than 2^40 below counts as zero.
 struct ColPlan {
   int64_t rows, chunks;   // tokens per chunk
 };
@@ -387,15 +388,20 @@ struct MagnitudeJob {
   int64_t ld = 0, cols = 0, blocks = 0;
   uint32_t* part = nullptr;       // [chunks][cols]
   int32_t* out = nullptr;
+  int act = LRC_ACT_NONE;         // p is dy, the magnitudes are those of dy act'(z):
+  const uint16_t* z = nullptr;    // z in full, or
+  const int8_t *zcodes = nullptr, *zexps = nullptr;
+  int64_t ldz = 0;
 };
 struct MagnitudeJobs {
   MagnitudeJob job[2];
 };
-// exponent that brings a channel's largest magnitude into [2^14, 2^15); 0 for a channel of zeros
+// exponent that brings a channel's largest magnitude into [2^14, 2^15); 0 for a channel of zeros,
+// and -126 at least, so that its power of two is a normal number
 __device__ __forceinline__ int channel_exponent(uint32_t bits) {
   int e = 0;
   const float f = frexpf(__uint_as_float(bits), &e);   // in [1/2, 1)
-  return f > 0.f ? e - 15 : 0;
+  return f > 0.f ? max(e - 15, -126) : 0;
 }
 // largest finite magnitude (as bits) of every channel over a chunk of tokens; the exponent itself
 // where there is one chunk
@@ -410,7 +416,8 @@ __global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64
   const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
   const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
   uint32_t m[8] = {};
-  if (cnt > 0) {
+  auto run = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
+    const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll 4
     for (int64_t t = t0 + wave; t < t1; t += 4) {
       if (j.exps != nullptr) {
@@ -419,12 +426,24 @@ __global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64
         for (int e = 0; e < 8; ++e) m[e] = max(m[e], u);
       } else {
         float v[8];
-        ld8(static_cast<const uint16_t*>(j.p) + t * j.ld + c, cnt, v);
+        ld8(static_cast<const uint16_t*>(j.p) + t * j.ld + c, len, v);
+        if (j.act != LRC_ACT_NONE) {
+          float zv[8];
+          if (j.z != nullptr)
+            ld8(j.z + t * j.ldz + c, len, zv);
+          else
+            ld8_codes(j.zcodes + t * j.cols + c, len, pow2f(j.zexps[t * j.ldz + (c >> 6)]), zv);
+          slope_apply(j.act, zv, v);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) m[e] = max(m[e], __float_as_uint(finite_mag(v[e])));
       }
     }
-  }
+  };
+  if (cnt >= 8)
+    run(std::true_type{});
+  else if (cnt > 0)
+    run(std::false_type{});
   if (wave > 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) most[wave - 1][lane][e] = m[e];
@@ -481,28 +500,32 @@ __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_
   const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
   const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
   float s[8] = {};
-  if (cnt > 0) {
-    int ex[8] = {};
-    if (dz_half != nullptr) exps8(dz_exp + c, cnt, ex);
+  float scale[8] = {};
+  if (dz_half != nullptr && cnt > 0) scales8(dz_exp + c, cnt, scale);
+  auto run = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
+    const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll 2
     for (int64_t t = t0 + wave; t < t1; t += 4) {
       float g[8];
-      ld8(dy + t * lddy + c, cnt, g);
+      ld8(dy + t * lddy + c, len, g);
       if (act != LRC_ACT_NONE) {
         float zv[8];
         if (CK)
-          ld8_codes(codes + t * d + c, cnt, pow2f(exps[t * nb + (c >> 6)]), zv);
+          ld8_codes(codes + t * d + c, len, pow2f(exps[t * nb + (c >> 6)]), zv);
         else
-          ld8(z + t * ldz + c, cnt, zv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] *= act_slope(act, zv[e]);
-        st8(dz + t * lddz + c, cnt, g);
-        if (dz_half != nullptr) st8_half(dz_half + t * w8 + c, g, ex);   // zeros behind the last channel
+          ld8(z + t * ldz + c, len, zv);
+        slope_apply(act, zv, g);
+        st8(dz + t * lddz + c, len, g);
+        if (dz_half != nullptr) st8_half(dz_half + t * w8 + c, g, scale);   // zeros behind the last channel
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] += g[e];
     }
-  }
+  };
+  if (cnt >= 8)
+    run(std::true_type{});
+  else if (cnt > 0)
+    run(std::false_type{});
   if (partial == nullptr) return;
   if (wave > 0) {
 #pragma unroll
@@ -586,24 +609,31 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
   const int64_t r0 = i / per * JOB_ROWS, c = i % per * 8;
   if (r0 >= j.rows) return;
   const int cnt = int(j.cols - c > 8 ? 8 : j.cols - c);
-  int e[8] = {};
-  if (j.half_exp != nullptr) exps8(j.half_exp + c, cnt, e);
+  float scale[8] = {};
+  if (j.half_exp != nullptr) scales8(j.half_exp + c, cnt, scale);
   float v[JOB_ROWS][8];
+  auto load = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
+    const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll
-  for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
-    const int64_t r = min(r0 + q4, j.rows - 1);
-    if (j.exps != nullptr)
-      ld8_codes(static_cast<const int8_t*>(j.p) + r * j.ld + c, cnt, pow2f(j.exps[r * j.nb + (c >> 6)]), v[q4]);
-    else
-      ld8(static_cast<const T*>(j.p) + r * j.ld + c, cnt, v[q4]);
-  }
+    for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
+      const int64_t r = min(r0 + q4, j.rows - 1);
+      if (j.exps != nullptr)
+        ld8_codes(static_cast<const int8_t*>(j.p) + r * j.ld + c, len, pow2f(j.exps[r * j.nb + (c >> 6)]), v[q4]);
+      else
+        ld8(static_cast<const T*>(j.p) + r * j.ld + c, len, v[q4]);
+    }
+  };
+  if (cnt >= 8)
+    load(std::true_type{});
+  else
+    load(std::false_type{});
 #pragma unroll
   for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
     const int64_t r = r0 + q4;
     if (r >= j.rows) break;
     uint16_t* o = j.out + r * j.planes * j.w8 + c;
     if (j.half_exp != nullptr)
-      st8_half(o, v[q4], e);
+      st8_half(o, v[q4], scale);
     else if (j.exps != nullptr)
       split_store<uint16_t>(o, j.w8, v[q4], flag);
     else
@@ -693,7 +723,7 @@ bool large_product(int64_t n, int64_t di, int64_t dn) {
   const double work = double(n) * double(di) * double(dn);
   if (n > GEMM_MAX_K) return false;
   return sizeof(T) == 2 ? work >= double(1 << 18)
-                        : work >= double(1 << 30) && std::min({n, di, dn}) >= 192;
+                        : work >= double(1 << 30) && std::min({n, di, dn}) >= 144;
 }
 template <class T>
 bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two operands
@@ -912,7 +942,10 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB), false}
                           : plain<T>(a.x, a.ldx);
   const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
-  const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD;
+  // few tokens read W once on either kind of tile: it is not laid out anew for them
+  const bool w_in_place = sizeof(T) == 2 && ow.vec && di % 8 == 0;
+  const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD &&
+                       (w_in_place || n > 64);
   // a slope that is neither 0 nor 1 leaves bits in dz that the stream's bf16 does not hold
   const bool half = with_dz && a.act != LRC_ACT_RELU && a.dW != nullptr && half_fits<T>(n, di, dn);
   const bool fast_dw = half || (fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD)));
@@ -925,6 +958,11 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     m.job[0].cols = dn;
     m.job[0].part = room.dz_mag;
     m.job[0].out = room.dz_exp;
+    m.job[0].act = a.act;
+    m.job[0].z = static_cast<const uint16_t*>(a.z);
+    m.job[0].zcodes = a.zcodes;
+    m.job[0].zexps = a.zexps;
+    m.job[0].ldz = a.z != nullptr ? a.ldz : cdiv(dn, CKB);
     m.job[1].p = a.x;
     m.job[1].exps = held ? a.xexps : nullptr;
     m.job[1].ld = held ? cdiv(di, CKB) : a.ldx;
@@ -932,7 +970,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     m.job[1].part = room.x_mag;
     m.job[1].out = room.x_exp;
     for (MagnitudeJob& j : m.job) j.blocks = cdiv(j.cols, 512);
-    ProfScope scope("magnitude_kernel", st, 0.0, double(n) * (2.0 * double(dn) + (held ? double(di) / 64 : 2.0 * di)));
+    ProfScope scope("magnitude_kernel", st, 0.0, double(n) * ((a.z ? 4.0 : 3.0) * double(dn) + (held ? double(di) / 64 : 2.0 * di)));
     magnitude_kernel<<<dim3(unsigned(m.job[0].blocks + m.job[1].blocks), unsigned(p.chunks)), LT, 0, st>>>(m, n, p.rows);
     LRC_LAUNCHED();
     if (p.chunks > 1) {

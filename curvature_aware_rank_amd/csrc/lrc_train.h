@@ -205,28 +205,48 @@ __device__ __forceinline__ float normal_tail(float x, float& e) {
 __device__ __forceinline__ float logistic(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
-__device__ __forceinline__ float act_value(int act, float z) {
-  if (act == LRC_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
-  if (act == LRC_ACT_GELU) {
-    float e;
-    const float q = normal_tail(fabsf(z), e);
-    return z * (z >= 0.f ? 1.f - q : q);
-  }
-  if (act == LRC_ACT_SILU) return z * logistic(z);
-  return z;
+__device__ __forceinline__ float relu(float z) { return z > 0.f ? z : (z == z ? 0.f : z); }
+__device__ __forceinline__ float relu_slope(float z) { return z > 0.f ? 1.f : (z == z ? 0.f : z); }
+__device__ __forceinline__ float gelu(float z) {
+  float e;
+  const float q = normal_tail(fabsf(z), e);
+  return z * (z >= 0.f ? 1.f - q : q);
 }
-__device__ __forceinline__ float act_slope(int act, float z) {
-  if (act == LRC_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
-  if (act == LRC_ACT_GELU) {
-    float e;
-    const float q = normal_tail(fabsf(z), e);
-    return fmaf(z * e, 0.39894228040143268f, z >= 0.f ? 1.f - q : q);
+__device__ __forceinline__ float gelu_slope(float z) {
+  float e;
+  const float q = normal_tail(fabsf(z), e);
+  return fmaf(z * e, 0.39894228040143268f, z >= 0.f ? 1.f - q : q);
+}
+__device__ __forceinline__ float silu_slope(float z) {
+  const float s = logistic(z);
+  return s * (1.f + z * (1.f - s));
+}
+// v = act(v), and g = g act'(z); the choice is made once for all N values
+template <int N>
+__device__ __forceinline__ void act_apply(int act, float (&v)[N]) {
+  if (act == LRC_ACT_RELU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = relu(v[e]);
+  } else if (act == LRC_ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = gelu(v[e]);
+  } else if (act == LRC_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] *= logistic(v[e]);
   }
-  if (act == LRC_ACT_SILU) {
-    const float s = logistic(z);
-    return s * (1.f + z * (1.f - s));
+}
+template <int N>
+__device__ __forceinline__ void slope_apply(int act, const float (&z)[N], float (&g)[N]) {
+  if (act == LRC_ACT_RELU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) g[e] *= relu_slope(z[e]);
+  } else if (act == LRC_ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) g[e] *= gelu_slope(z[e]);
+  } else if (act == LRC_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) g[e] *= silu_slope(z[e]);
   }
-  return 1.f;
 }
 
 // ---- products of the linear layer: D[m][n] = sum_k A(m, k) B(n, k) ----------------------
@@ -276,10 +296,7 @@ __device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t
   if (ep.codes != nullptr)
     st8_codes(ep.codes + row * ep.ldz + col, ep.exps + row * ep.nb + (col >> 6), cnt, v, lane, bad);
   if (cnt <= 0) return;
-  if (ep.act != LRC_ACT_NONE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = act_value(ep.act, v[e]);
-  }
+  act_apply(ep.act, v);
   if (ep.res != nullptr) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];

@@ -470,7 +470,8 @@ size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_
  * lddw), dtype dw_dt (LRC_F32, or `dt`); db: float[d_out]; any of the three may be NULL.
  * With dtype bf16, dx is a product of the rounded dz, as the stream holds it; dW takes dz with
  * three more bits where the activation is GELU or SiLU (fp16, each channel of dz and x scaled
- * by a power of two; with RELU and NONE dz is exact in bf16), and db sums the unrounded dz.
+ * by a power of two over the tokens; what lies 2^40 below its channel's largest counts as zero;
+ * with RELU and NONE dz is exact in bf16), and db sums the unrounded dz.
  * Sums fp32 in an order that depends on the sizes only.
  * n_tokens == 0 writes zeros to dW and db.  Sizes as lrc_linear.
  */

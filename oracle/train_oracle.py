@@ -4,7 +4,7 @@ TEST INFRASTRUCTURE ONLY: imported by the tests, never by the library's own path
 the formulas; it shares no code with the HIP kernels.
 """
 import numpy as np
-from scipy.special import erf
+from scipy.special import erfc
 
 BLOCK = 64
 
@@ -41,7 +41,7 @@ def act(z, name):
     if name == "relu":
         return np.maximum(z, 0)
     if name == "gelu":
-        return 0.5 * z * (1 + erf(z / np.sqrt(2)))
+        return 0.5 * z * erfc(-z / np.sqrt(2))
     if name == "silu":
         return z / (1 + np.exp(-z))
     return z
@@ -51,7 +51,7 @@ def act_slope(z, name):
     if name == "relu":
         return (z > 0).astype(np.float64)
     if name == "gelu":
-        return 0.5 * (1 + erf(z / np.sqrt(2))) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+        return 0.5 * erfc(-z / np.sqrt(2)) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
     if name == "silu":
         s = 1 / (1 + np.exp(-z))
         return s + z * s * (1 - s)

@@ -361,6 +361,23 @@ def test_weight_gradient_keeps_the_bits_of_dz(lrc, act, n, d_in, d_out, held):
     assert np.abs(err).max() < 2.0 ** -11 and math.sqrt((err ** 2).mean()) < 2.0 ** -12
 
 
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_weight_gradient_of_channels_that_are_shut(lrc, act):
+    """Channels whose slopes are all tiny (z near -9: 1e-17 for gelu, 1e-3 for silu) keep their gradients' bits: the
+    exponential's argument, 58 in powers of two, is off by at most 58 u twice, 5e-6 of the slope."""
+    n, d = 100, 80
+    g = torch.Generator().manual_seed(7)
+    x, dy = stream(n, d, torch.bfloat16, 1), stream(n, d, torch.bfloat16, 2, 0.01)
+    z = (torch.randn(n, d, generator=g) * 0.25 - 9 * (torch.arange(d) % 2)).bfloat16()
+    w = torch.zeros(d, d, dtype=torch.bfloat16, device=dev())
+    zk = lrc.lrc_pack_activations(z.to(dev()))[:2]
+    for za, zn in ((z.to(dev()), f64(z)), (zk, ref.unpack(zk[0].cpu().numpy(), zk[1].cpu().numpy()))):
+        _, _, dw, _ = lrc.lrc_linear_backward(dy.to(dev()), x.to(dev()), w, act=act, z=za, dw_dtype=torch.float32)
+        dz = f64(dy) * ref.act_slope(zn, act)
+        err = (f64(dw) - dz.T @ f64(x)) / (np.linalg.norm(dz, axis=0)[:, None] * np.linalg.norm(f64(x), axis=0)[None])
+        assert np.abs(err).max() < 2.0 ** -11
+
+
 def test_weight_gradient_with_nonfinite_entries(lrc):
     n, d = 200, 72
     ones = lambda *s: torch.ones(*s, dtype=torch.bfloat16)   # noqa: E731
