@@ -4,42 +4,47 @@
 // int8 codes with one power-of-two step per 64 channels of a token.
 #include "lrc_train.h"
 
+#include <algorithm>
+
 namespace lrc {
 namespace {
 
 constexpr int CT = 256;
 
 // One lane per eight channels, eight lanes per block: a wave covers eight blocks, taken in
-// order over (token, block).
+// order over (token, block).  Bound by memory.  A launch holds less than 2^32 threads, so past
+// GRID_MAX workgroups (2^29 blocks, 2^35 channels in whole blocks) they take blocks in turn.
+constexpr int64_t GRID_MAX = (int64_t(1) << 24) - 1;
+
 template <class T>
 __global__ __launch_bounds__(CT) void pack_kernel(const T* __restrict__ x, int64_t ldx, int64_t n, int d, int64_t nb,
                                                   int8_t* __restrict__ codes, int8_t* __restrict__ exps,
                                                   int32_t* __restrict__ info) {
-  const int64_t g = (int64_t(blockIdx.x) * CT + threadIdx.x) >> 3;   // block of 64 channels
   const int lane = threadIdx.x & 63;
-  const bool live = g < n * nb;
-  const int64_t t = live ? g / nb : 0;
-  const int c = int(live ? g % nb : 0) * CKB + 8 * (lane & 7);
-  const int cnt = live ? min(8, d - c) : 0;
-  float v[8];
-  ld8(x + t * ldx + c, cnt, v);
   bool bad = false;
-  st8_codes(codes + t * d + c, exps + g, cnt, v, lane, bad);
+  for (int64_t g = (int64_t(blockIdx.x) * CT + threadIdx.x) >> 3; g < n * nb; g += int64_t(gridDim.x) * (CT / 8)) {
+    const int64_t t = g / nb;
+    const int c = int(g % nb) * CKB + 8 * (lane & 7);
+    const int cnt = min(8, d - c);
+    float v[8];
+    ld8(x + t * ldx + c, cnt, v);
+    st8_codes(codes + t * d + c, exps + g, cnt, v, lane, bad);
+  }
   if (info != nullptr && bad) *info = LRC_ENONFINITE;
 }
 
 template <class T>
 __global__ __launch_bounds__(CT) void unpack_kernel(const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
                                                     int64_t n, int d, int64_t nb, T* __restrict__ x, int64_t ldx) {
-  const int64_t g = (int64_t(blockIdx.x) * CT + threadIdx.x) >> 3;
-  if (g >= n * nb) return;
-  const int64_t t = g / nb;
-  const int c = int(g % nb) * CKB + 8 * (threadIdx.x & 7);
-  const int cnt = min(8, d - c);
-  if (cnt <= 0) return;
-  float v[8];
-  ld8_codes(codes + t * d + c, cnt, pow2f(exps[g]), v);
-  st8(x + t * ldx + c, cnt, v);
+  for (int64_t g = (int64_t(blockIdx.x) * CT + threadIdx.x) >> 3; g < n * nb; g += int64_t(gridDim.x) * (CT / 8)) {
+    const int64_t t = g / nb;
+    const int c = int(g % nb) * CKB + 8 * (threadIdx.x & 7);
+    const int cnt = min(8, d - c);
+    if (cnt <= 0) continue;
+    float v[8];
+    ld8_codes(codes + t * d + c, cnt, pow2f(exps[g]), v);
+    st8(x + t * ldx + c, cnt, v);
+  }
 }
 
 bool sizes_ok(int64_t n, int64_t d, int64_t ld) {
@@ -57,8 +62,7 @@ extern "C" lrc_status lrc_pack_activations(const void* x, lrc_dtype dt, int64_t 
   if (!sizes_ok(n_tokens, d, ldx)) return LRC_EINVAL;
   if (n_tokens == 0) return LRC_OK;
   if (x == nullptr || codes == nullptr || exps == nullptr) return LRC_EINVAL;
-  const int64_t nb = cdiv(d, CKB), grid = cdiv(n_tokens * nb * 8, CT);
-  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  const int64_t nb = cdiv(d, CKB), grid = std::min(cdiv(n_tokens * nb * 8, CT), GRID_MAX);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int size = dt == LRC_BF16 ? 2 : 4;
   ProfScope scope("pack_kernel", st, 0.0, double(n_tokens) * (double(d) * (size + 1) + double(nb)));
@@ -77,8 +81,7 @@ extern "C" lrc_status lrc_unpack_activations(const int8_t* codes, const int8_t* 
   if (!sizes_ok(n_tokens, d, ldx)) return LRC_EINVAL;
   if (n_tokens == 0) return LRC_OK;
   if (x == nullptr || codes == nullptr || exps == nullptr) return LRC_EINVAL;
-  const int64_t nb = cdiv(d, CKB), grid = cdiv(n_tokens * nb * 8, CT);
-  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  const int64_t nb = cdiv(d, CKB), grid = std::min(cdiv(n_tokens * nb * 8, CT), GRID_MAX);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int size = dt == LRC_BF16 ? 2 : 4;
   ProfScope scope("unpack_kernel", st, 0.0, double(n_tokens) * (double(d) * (size + 1) + double(nb)));

@@ -397,6 +397,7 @@ size_t lrc_hybrid_ffn_workspace(int64_t n_tok, int64_t n_lr, int64_t rg, int64_t
  * info: device int32 or NULL; set to LRC_ENONFINITE when an entry is NaN or Inf, never
  * cleared.  Such an entry does not count for e; an infinity is held as +-127 * 2^e, NaN as 0.
  * Unpacking writes q * 2^e in dtype `dt` (exact in both).  n_tokens == 0 is a no-op.
+ * Here and in the four calls below an output overlaps no input except where it is said.
  */
 lrc_status lrc_pack_activations(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t ldx,
                                 int8_t* codes, int8_t* exps, int32_t* info, void* stream);
@@ -447,8 +448,11 @@ size_t lrc_layer_norm_backward_workspace(int64_t n_tokens, int64_t d);
  * The pre-activation z that the backward pass needs is kept on request: z (n_tokens x d_out,
  * dtype `dt`, leading dim ldz), or zcodes and zexps, its 8-bit checkpoint taken from the
  * fp32 z (`info` as in lrc_pack_activations); at most one of the two, NULL otherwise.
- * bf16: products exact, sums fp32.  fp32: products and sums to fp32 accuracy.  The order of
- * every sum depends on the sizes only, so equal inputs give equal bits.
+ * bf16: products exact, sums fp32.  fp32: products and sums to fp32 accuracy (an entry below
+ * 2^-110 in magnitude counts to an absolute 2^-133).  The order of every sum depends on the
+ * sizes and the alignment only, so equal inputs give equal bits.  A bf16 product of more than
+ * 64 tokens is fastest where the rows of x and W start on 16 bytes, or have a length that is
+ * no multiple of 8; others may take five times as long.
  * 1 <= d_in, d_out <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
  */
 lrc_status lrc_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out, int64_t ldx,

@@ -670,6 +670,55 @@ def test_offsets_past_32_bits(lrc):
         assert torch.equal(a, b)
 
 
+def test_more_blocks_than_a_launch_has_threads_for(lrc):
+    """2^29 + 4096 rows of one channel, eight lanes a row: the rows repeat a pattern and so do codes and values."""
+    p = stream(4096, 1, torch.bfloat16, 1).to(dev())
+    p[7], p[9] = 0.0, 300.0
+    want = lrc.lrc_pack_activations(p)
+    x = p.repeat((1 << 17) + 1, 1)
+    got = lrc.lrc_pack_activations(x)
+    for a, b in zip(got[:2], want[:2]):
+        assert (a.view(-1, 4096) == b.view(4096)).all()
+    back = lrc.lrc_unpack_activations(*got[:2])
+    assert (back.view(-1, 4096) == lrc.lrc_unpack_activations(*want[:2]).view(4096)).all()
+    x[-3] = float("inf")
+    assert int(lrc.lrc_pack_activations(x)[2].cpu()) == lrc.LRC_ENONFINITE and int(got[2].cpu()) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_large_products_of_unaligned_rows(lrc, dtype):
+    """Rows that start on no 16 bytes give the bits of rows that do (2^30 products: the operands are laid out
+    first)."""
+    n, d_in, d_out = 1030, 1024, 1032
+    x, w = stream(n, d_in, dtype, 1), stream(d_out, d_in, dtype, 2)
+    dy, z = stream(n, d_out, dtype, 3), stream(n, d_out, dtype, 4)
+    for layout in LAYOUTS[1:]:
+        xl, wl, dl, zl = (lay(t, layout) for t in (x, w, dy, z))
+        xp, wp, dp, zp = (t.to(dev()) for t in (x, w, dy, z))
+        assert torch.equal(lrc.lrc_linear(xl, wl, residual=dl)[0], lrc.lrc_linear(xp, wp, residual=dp)[0])
+        for act in ("none", "relu", "silu"):
+            got = lrc.lrc_linear_backward(dl, xl, wl, act=act, z=zl)
+            for a, b in zip(got, lrc.lrc_linear_backward(dp, xp, wp, act=act, z=zp)):
+                assert torch.equal(a, b)
+        assert lrc.lrc_linear_backward(dp[:, 8:], xp, wp[8:])[0].stride(0) == d_out
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d_in,d_out", [(5, 512, 256), (70, 100, 90), (200, 1000, 520), (1100, 1032, 1024)])
+def test_residual_in_the_output(lrc, dtype, n, d_in, d_out):
+    """The residual may be y itself: few tokens, split k, and tiles of either kind."""
+    x, w = stream(n, d_in, dtype, 1).to(dev()), stream(d_out, d_in, dtype, 2).to(dev())
+    res = stream(n, d_out, dtype, 3).to(dev())
+    want = lrc.lrc_linear(x, w, act="silu", residual=res)[0]
+    code = lrc.LRC_BF16 if dtype == torch.bfloat16 else lrc.LRC_F32
+    size = lrc.lib.lrc_linear_workspace(code, n, d_in, d_out)
+    ws = torch.empty(max(1, size), dtype=torch.uint8, device=dev())
+    st = torch.cuda.current_stream().cuda_stream
+    assert lrc.lib.lrc_linear(x.data_ptr(), code, n, d_in, d_out, d_in, w.data_ptr(), d_in, None, 3, res.data_ptr(),
+                              d_out, res.data_ptr(), d_out, None, 0, None, None, None, ws.data_ptr(), size, st) == 0
+    assert torch.equal(res, want)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_nonfinite_values_stay_in_their_rows(lrc, dtype):
     """A token with NaN or an infinity spoils its own row and the token sums, nothing else, and y of an infinite
