@@ -43,11 +43,13 @@ __device__ __forceinline__ void* uniform_ptr(const void* p) {
   return reinterpret_cast<void*>((uint64_t(hi) << 32) | lo);
 }
 
-// One operand's stages: EDGE tile rows (channels for K_COLS), NW waves.
-template <int KIND, int EDGE, int NW, int KS, int MF>
+// One operand's stages: EDGE tile rows (channels for K_COLS), NW waves, elements of ES bytes.
+template <int KIND, int EDGE, int NW, int KS, int MF, int ES>
 struct Stager {
   static constexpr int LOADS = EDGE * KS * 2 / 1024 / NW;   // 1 KB loads per wave and stage
-  static constexpr int ROWB = EDGE * 2;                     // K_COLS: bytes per k step
+  static constexpr int ROWB = EDGE * ES;                    // K_COLS: bytes per k step
+  static constexpr int KE = KS * 2 / ES;                    // k steps of a stage
+  static constexpr int GE = 16 / ES;                        // elements of a 16-byte granule
   static constexpr unsigned OOB = 0x80000000u;              // past every resource
 
   const uint16_t* base;   // first element of the tile (plane 0, k = 0)
@@ -67,34 +69,34 @@ struct Stager {
         constexpr int GPR = KS / 8;          // granules per row
         const int r = (64 / GPR) * (LOADS * wave + j) + lane / GPR;
         const int g = (lane % GPR) ^ row_swizzle(r);
-        kk[j] = 8 * g;
+        kk[j] = GE * g;
         voff[j] = r < left ? unsigned(r * ld * 2) + 16 * g : OOB;
       }
       rows_rec = int((left - 1) * ld * 2);
     } else {
-      base = o.p + row0;
-      constexpr int LPR = EDGE / 8;        // lanes (16-byte granules) per k step
+      base = o.p + row0 * (ES / 2);
+      constexpr int LPR = EDGE / GE;       // lanes (16-byte granules) per k step
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) {
         const int t = (64 / LPR) * (LOADS * wave + j) + lane / LPR;
         const int g = (lane % LPR) ^ step_swizzle(t);
         kk[j] = 0;
-        voff[j] = 8 * g < left ? unsigned(t * ld * 2) + 16 * g : OOB;
+        voff[j] = GE * g < left ? unsigned(t * ld * 2) + 16 * g : OOB;
       }
-      rows_rec = 2 * ((left + 7) & ~7);
+      rows_rec = ES * ((left + GE - 1) & ~(GE - 1));
     }
   }
 
-  // The loads of one stage: k steps [k, k + 32) of plane `pl`, of which `left` or all 32 exist.
+  // The loads of one stage: k steps [k, k + KE) of plane `pl`, of which `left` or all KE exist.
   struct Stage {
     __amdgpu_buffer_rsrc_t r;
     unsigned v[LOADS];
   };
   __device__ __forceinline__ Stage stage(int pl, int k, int left) const {
-    const int kl = max(0, min(left, KS));
+    const int kl = max(0, min(left, KE));
     // K_ROWS: rows are whole granules (zeros behind the last k where that is not one)
-    const int rec = KIND == K_ROWS ? rows_rec + 2 * ((kl + 7) & ~7) : (kl - 1) * int(ld) * 2 + rows_rec;
-    const uint16_t* p = base + pl * plane + (KIND == K_ROWS ? k : k * ld);
+    const int rec = KIND == K_ROWS ? rows_rec + ES * ((kl + GE - 1) & ~(GE - 1)) : (kl - 1) * int(ld) * 2 + rows_rec;
+    const uint16_t* p = base + pl * plane + (KIND == K_ROWS ? k * (ES / 2) : k * ld);
     Stage s;
     s.r = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(p), 0, __builtin_amdgcn_readfirstlane(kl > 0 ? rec : 0),
                                             0x00020000);
@@ -115,6 +117,7 @@ struct Stager {
   // K_COLS: the four k steps a group of 16 lanes reads fall on four quarters of the banks, the
   // groups of k steps 8 apart on halves of those
   static __device__ __forceinline__ int step_swizzle(int t) {
+    if (ES == 4) return 4 * ((t >> 2) & 3);   // the four groups read k steps 4 apart, 64 bytes of each
     return (4 * (t & 3)) ^ (MF == 16 ? 2 * ((t >> 3) & 1) : 0);
   }
 
@@ -127,6 +130,7 @@ struct Stager {
       return r * (2 * KS) + (((lane / MF) ^ row_swizzle(r)) << 4);
     }
     const int g = lane >> 4, sl = lane & 15;
+    if (ES == 4) return 4 * g * ROWB + ((((row + sl) >> 2) ^ step_swizzle(4 * g)) << 4) + 4 * (sl & 3);
     const int ch = row + (MF == 32 ? 16 * (g & 1) : 0) + 4 * (sl & 3);
     const int tk = 8 * (MF == 32 ? g >> 1 : g) + (sl >> 2);
     return tk * ROWB + (((ch >> 3) ^ step_swizzle(tk)) << 4) + (ch & 7) * 2;
@@ -134,7 +138,15 @@ struct Stager {
   // fragment of the stage's k steps [KF q, KF q + KF)
   static __device__ bf16x8 frag(const uint8_t* lds, int off, int q) {
     if (KIND == K_ROWS) return *reinterpret_cast<const bf16x8*>(lds + (off ^ (2 * KF * q)));
-    const uint8_t* p = lds + off + q * KF * ROWB;
+    const uint8_t* p = lds + off + q * (KF * 2 / ES) * ROWB;
+    if constexpr (ES == 4) {   // k steps 4 g .. 4 g + 3 of the lane's channel, as K_ROWS has them in a granule
+      const float v[4] = {*reinterpret_cast<const float*>(p), *reinterpret_cast<const float*>(p + ROWB),
+                          *reinterpret_cast<const float*>(p + 2 * ROWB),
+                          *reinterpret_cast<const float*>(p + 3 * ROWB)};
+      bf16x8 f;
+      __builtin_memcpy(&f, v, sizeof(f));
+      return f;
+    }
     const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p));
     const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * ROWB));
     const short tmp[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -157,6 +169,12 @@ struct Block<16> {
   }
   static __device__ __forceinline__ acc_t mma_half(f16x8 a, f16x8 b, acc_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  // a lane's 16 bytes are four k steps; each instruction takes one of them from every lane
+  static __device__ __forceinline__ acc_t mma_f32(f32x4 a, f32x4 b, acc_t c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
   }
 };
 template <>
@@ -188,19 +206,21 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
   tn = r / rows;
 }
 
-template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
+template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, Element EL>
 __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N, int64_t K,
                                           const GemmSegments& seg, const TileGrid& tg, const Epilogue& ep,
                                           float* __restrict__ partial, const int32_t* __restrict__ skip) {
   constexpr int NW = WM * WN, BM = WM * FM * MF, BN = WN * FN * MF;
   constexpr int AB = BM * KS * 2, STB = (BM + BN) * KS * 2;
-  using SA = Stager<KA, BM, NW, KS, MF>;
-  using SB = Stager<KB, BN, NW, KS, MF>;
+  constexpr int ES = EL == FP32 ? 4 : 2;
+  using SA = Stager<KA, BM, NW, KS, MF, ES>;
+  using SB = Stager<KB, BN, NW, KS, MF, ES>;
   constexpr int L = SA::LOADS + SB::LOADS;      // loads of a wave per stage
   // one LDS object per stage, so that a read of one stage does not wait for the loads of others
   __shared__ __attribute__((aligned(1024))) uint8_t sb0[STB], sb1[STB], sb2[NST > 2 ? STB : 16],
       sb3[NST > 3 ? STB : 16];
-  constexpr int PART = 32 * FN * MF * 4;        // a wave's epilogue rows
+  constexpr int ER = FM * MF < 32 ? FM * MF : 32;   // rows a wave finishes at a time
+  constexpr int PART = ER * FN * MF * 4;
   constexpr int FIT = STB / PART;               // of them in a stage buffer
   static_assert(NST >= 2 && NST <= 4 && KS % 32 == 0 && FIT >= 1 && FIT * NST >= NW, "the epilogue rows fit the stage buffers");
 
@@ -227,7 +247,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   const int first = split * tg.steps_per_split;
   const int nsteps = min(tg.steps_per_split, total - first);
   int sg = SEG ? first / tg.steps : 0;
-  int k = (first - sg * tg.steps) * KS;   // next stage to issue
+  int k = (first - sg * tg.steps) * SA::KE;   // next stage to issue
   const int kend = int(K);
   typename SA::Stage ga;
   typename SB::Stage gb;
@@ -237,7 +257,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     const int left = live ? kend - k : 0;
     ga = sa.stage(SEG ? int((seg.pa >> (2 * sg)) & 3) : 0, k, left);
     gb = sb.stage(SEG ? int((seg.pb >> (2 * sg)) & 3) : 0, k, left);
-    k += KS;
+    k += SA::KE;
     if (SEG) {
       const bool next = k >= kend;
       sg += next ? 1 : 0;
@@ -275,12 +295,17 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        acc[i][j] = HALF ? Blk::mma_half(__builtin_bit_cast(f16x8, fa[i]), __builtin_bit_cast(f16x8, fb[j]), acc[i][j])
-                         : Blk::mma(fa[i], fb[j], acc[i][j]);
+        if constexpr (EL == FP32)
+          acc[i][j] = Blk::mma_f32(__builtin_bit_cast(f32x4, fa[i]), __builtin_bit_cast(f32x4, fb[j]), acc[i][j]);
+        else if constexpr (EL == FP16)
+          acc[i][j] = Blk::mma_half(__builtin_bit_cast(f16x8, fa[i]), __builtin_bit_cast(f16x8, fb[j]), acc[i][j]);
+        else
+          acc[i][j] = Blk::mma(fa[i], fb[j], acc[i][j]);
   };
   // Issue order of a step: the fragment reads (and the next stage's loads) go out between the
   // products, which hide them.
-  constexpr int READS = FM * (KA == K_ROWS ? 1 : 2) + FN * (KB == K_ROWS ? 1 : 2), MM = FM * FN;
+  constexpr int COLS = EL == FP32 ? 4 : 2, READS = FM * (KA == K_ROWS ? 1 : COLS) + FN * (KB == K_ROWS ? 1 : COLS),
+                MM = FM * FN * (EL == FP32 ? 4 : 1);
   constexpr int GROUPS = MM < 8 ? 4 : 8, GRP = MM / GROUPS;   // products per group
   auto interleave_reads = [&]() {
 #define LRC_PAIR                                                       \
@@ -365,11 +390,12 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   for (; s < nsteps; ++s) stage(buf(s), buf(s + 1), s + NST < nsteps);
   wait_barrier<0>();   // every load has landed and every read is done: the buffers are free
 
-  // Epilogue: a wave's 32 rows x TW columns at a time pass through its own part of LDS, so that a
+  // Epilogue: a wave's 32 (or 16) rows x TW columns at a time pass through its own part of LDS, so that a
   // lane holds eight consecutive columns of a row and the accesses to memory are whole pieces.
   float* tile = reinterpret_cast<float*>(buf(wave / FIT) + (wave % FIT) * PART);
   constexpr int TW = FN * MF;          // tile columns
   constexpr int LPR = TW / 8;          // lanes per row
+  static_assert(TW >= 64, "a checkpoint's block belongs to one wave");
   // rows that a wave writes together fall on different banks
   auto place = [&](int r, int c) { return r * TW + (c ^ (MF == 16 ? 16 * ((r >> 2) & 3) : (r & 4) << 3)); };
   bool bad = false;
@@ -378,7 +404,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   bias8(ep, col, int(min(N - col, int64_t(8))), bias);
   auto emit = [&](const typename Blk::acc_t (&upper)[FN], const typename Blk::acc_t (&lower)[FN], int i) {
 #pragma unroll
-    for (int h = 0; h < 32 / MF; ++h)
+    for (int h = 0; h < ER / MF; ++h)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -386,7 +412,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
           tile[place(MF * h + Blk::row(e, lane), j * MF + lane % MF)] = h ? lower[j][e] : upper[j][e];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 2
-    for (int q = 0; q < 32 * LPR / 64; ++q) {
+    for (int q = 0; q < ER * LPR / 64; ++q) {
       const int r = q * (64 / LPR) + lane / LPR, c = 8 * (lane % LPR);
       const float* src = tile + place(r, c);
       const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
@@ -404,19 +430,19 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
   // (the accumulators' first index is a constant in each call, so that they stay in registers)
-  static_assert(FM * MF == 64, "a wave holds 64 rows");
-  constexpr int HALF_ROWS = 32 / MF;
+  static_assert(FM * MF == 64 || FM * MF == 16, "a wave holds 64 or 16 rows");
+  constexpr int HALF_ROWS = ER / MF;
   emit(acc[0], acc[HALF_ROWS - 1], 0);
-  emit(acc[HALF_ROWS], acc[2 * HALF_ROWS - 1], 1);
+  if constexpr (FM * MF == 64) emit(acc[HALF_ROWS], acc[2 * HALF_ROWS - 1], 1);
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
 
-template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, bool HALF>
+template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, bool SEG, Element EL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_bf16_kernel(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                                     int64_t K, GemmSegments seg, TileGrid tg,
                                                                     Epilogue ep, float* __restrict__ partial,
                                                                     const int32_t* __restrict__ skip) {
-  gemm_tile<TO, KA, KB, MF, WM, WN, FM, FN, KS, NST, SEG, HALF>(A, B, M, N, K, seg, tg, ep, partial, skip);
+  gemm_tile<TO, KA, KB, MF, WM, WN, FM, FN, KS, NST, SEG, EL>(A, B, M, N, K, seg, tg, ep, partial, skip);
 }
 
 // Sum of the splits' tiles in split order, then the epilogue.  One lane per eight columns, the
@@ -488,14 +514,14 @@ static double small_cost(int64_t groups, double steps64) {
   return c;
 }
 // KL: k steps per stage of a large tile
-static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL) {
+static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double& cost) {
   Plan best;
   const int64_t steps_l = cdiv(K, KL), steps_s = cdiv(K, 64);
   const double s64 = double(steps_s) * count;
   const double floor_us = 2.0 * double(K) * double(M + N) * (count > 1 ? 3 : 1) / MEMORY;
   best.large = true;
   best.tg = tiles_of(M, N, 256, 1, steps_l * count, steps_l);
-  double cost = std::max(floor_us, large_cost(best.tg.tiles, s64));
+  cost = std::max(floor_us, large_cost(best.tg.tiles, s64));
   const int64_t total = steps_s * count;
   for (int64_t s = 1; s <= std::min<int64_t>(32, total); ++s) {
     const int64_t per = cdiv(total, s);
@@ -510,6 +536,28 @@ static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL) {
   }
   return best;
 }
+// fp32 products: tiles of 64 x 64, four waves of 16 x 64, up to four workgroups on a unit; 32 k
+// steps take a unit F32_STEP of matrix time, F32_ALONE if nothing else runs on it
+constexpr double F32_STEP = 0.5, F32_ALONE = 0.75, F32_START = 6.0;
+static Plan plan_f32(int64_t M, int64_t N, int64_t K, double& cost) {
+  Plan best;
+  best.large = false;
+  cost = 0;
+  const int64_t steps = cdiv(K, 32);
+  for (int64_t s = 1; s <= std::min<int64_t>(32, steps); ++s) {
+    const int64_t per = cdiv(steps, s);
+    if (cdiv(steps, per) != s) continue;
+    const TileGrid tg = tiles_of(M, N, 64, int(s), per, steps);
+    const int64_t each = cdiv(tg.tiles * s, 256);
+    double c = F32_START + double(per) * (each == 1 ? F32_ALONE : double(each) * F32_STEP);
+    if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
+    if (s == 1 || c < cost) {
+      cost = c;
+      best.tg = tg;
+    }
+  }
+  return best;
+}
 static size_t plan_bytes(const Plan& p, int64_t M, int64_t N) {
   return p.tg.splits > 1 ? size_t(p.tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
 }
@@ -519,10 +567,22 @@ constexpr int large_stage(int ka, int kb) { return ka == K_ROWS && kb == K_ROWS 
 
 using namespace gemm;
 
-size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB) {
-  size_t most = 0;
-  for (int count : {1, 3, 6}) most = std::max(most, plan_bytes(plan_gemm(M, N, K, count, large_stage(KA, KB)), M, N));
+size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, bool f32) {
+  double c;
+  size_t most = f32 ? plan_bytes(plan_f32(M, N, K, c), M, N) : 0;
+  for (int count : {1, 3, 6})
+    most = std::max(most, plan_bytes(plan_gemm(M, N, K, count, large_stage(KA, KB), c), M, N));
   return most;
+}
+double gemm_f32_time(int64_t M, int64_t N, int64_t K) {
+  double c;
+  plan_f32(M, N, K, c);
+  return c;
+}
+double gemm_split_time(int64_t M, int64_t N, int64_t K, int KA, int KB) {
+  double c;
+  plan_gemm(M, N, K, 6, large_stage(KA, KB), c);
+  return c;
 }
 
 template <class TO>
@@ -551,27 +611,36 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   // larger one: their transposing reads need more address registers, and the smaller one's two full
   // fragment sets then spill (dx 272 against 225, dW 445 against 213).
   constexpr int KL = large_stage(KA, KB), NL = KL == 64 ? 2 : 4, ML = KL == 64 ? 16 : 32;
-  const Plan p = plan_gemm(M, N, K, seg.count, KL);
+  double cost;
+  const Plan p = seg.type == FP32 ? plan_f32(M, N, K, cost) : plan_gemm(M, N, K, seg.count, KL, cost);
   ProfScope scope(name, st, flops, bytes);
   const TileGrid& tg = p.tg;
   const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-  auto launch = [&](auto many, auto half) {
-    constexpr bool SEG = decltype(many)::value, HALF = decltype(half)::value;
-    if (p.large)
-      gemm_bf16_kernel<TO, KA, KB, ML, 4, 2, 64 / ML, 128 / ML, KL, NL, SEG, HALF><<<unsigned(grid), 512, 0, st>>>(
+  auto launch = [&](auto many, auto type) {
+    constexpr bool SEG = decltype(many)::value;
+    constexpr Element EL = decltype(type)::value;
+    if constexpr (EL == FP32)
+      gemm_bf16_kernel<TO, KA, KB, 16, 4, 1, 1, 4, 64, 2, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
+          A, B, M, N, K, seg, tg, ep, partial, skip);
+    else if (p.large)
+      gemm_bf16_kernel<TO, KA, KB, ML, 4, 2, 64 / ML, 128 / ML, KL, NL, SEG, EL><<<unsigned(grid), 512, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
     else
-      gemm_bf16_kernel<TO, KA, KB, 16, 2, 2, 4, 4, 64, 2, SEG, HALF><<<unsigned(grid), 256, 0, st>>>(
-          A, B, M, N, K, seg, tg, ep, partial, skip);
+      gemm_bf16_kernel<TO, KA, KB, 16, 2, 2, 4, 4, 64, 2, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
+        A, B, M, N, K, seg, tg, ep, partial, skip);
   };
+  using std::integral_constant;
   // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
-  if (seg.half) {
-    if constexpr (KA == K_COLS && KB == K_COLS) launch(std::false_type{}, std::true_type{});
+  if (seg.type == FP16) {
+    if constexpr (KA == K_COLS && KB == K_COLS) launch(std::false_type{}, integral_constant<Element, FP16>{});
+  } else if (seg.type == FP32) {
+    if constexpr (!std::is_same<TO, uint16_t>::value) launch(std::false_type{}, integral_constant<Element, FP32>{});
   } else if (std::is_same<TO, uint16_t>::value || seg.count == 1) {
-    launch(std::false_type{}, std::false_type{});
+    if constexpr (std::is_same<TO, uint16_t>::value || KA == K_COLS)
+      launch(std::false_type{}, integral_constant<Element, BF16>{});
   } else if constexpr (!std::is_same<TO, uint16_t>::value) {
-    launch(std::true_type{}, std::false_type{});
+    launch(std::true_type{}, integral_constant<Element, BF16>{});
   }
   LRC_LAUNCHED();
   if (tg.splits == 1) return LRC_OK;

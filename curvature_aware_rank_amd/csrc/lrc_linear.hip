@@ -591,7 +591,7 @@ struct OperandJob {
   const int8_t* exps = nullptr;   // codes if not NULL
   uint16_t* out = nullptr;
   int64_t ld = 0, nb = 0, rows = 0, cols = 0, w8 = 0, blocks = 0;
-  int planes = 1;
+  int planes = 1;                      // of bf16; 0: one of fp32
   const int32_t* half_exp = nullptr;   // fp16 of the value times 2^-half_exp[column], not bf16
 };
 constexpr int JOB_ROWS = 4;   // rows of a thread
@@ -632,7 +632,9 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
     const int64_t r = r0 + q4;
     if (r >= j.rows) break;
     uint16_t* o = j.out + r * j.planes * j.w8 + c;
-    if (j.half_exp != nullptr)
+    if (j.planes == 0)
+      st8(reinterpret_cast<float*>(j.out) + r * j.w8 + c, 8, v[q4]);
+    else if (j.half_exp != nullptr)
       st8_half(o, v[q4], scale);
     else if (j.exps != nullptr)
       split_store<uint16_t>(o, j.w8, v[q4], flag);
@@ -658,8 +660,9 @@ struct Prepared {
 // Adds the operand to the jobs if it cannot be read where it lies.
 template <class T>
 Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t rows, int64_t cols, uint16_t* room,
-                      const int32_t* half_exp = nullptr) {
+                      bool native, const int32_t* half_exp = nullptr) {
   const bool codes = o.exps != nullptr;
+  if (native && !codes && o.vec && cols % 4 == 0) return {{static_cast<const uint16_t*>(o.p), 2 * o.ld, 0}, 1};
   if (sizeof(T) == 2 && !codes && half_exp == nullptr && o.vec && cols % 8 == 0)
     return {{static_cast<const uint16_t*>(o.p), o.ld, 0}, 1};
   OperandJob& j = jobs.job[count++];
@@ -671,9 +674,10 @@ Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t r
   j.rows = rows;
   j.cols = cols;
   j.w8 = round8(cols);
-  j.planes = sizeof(T) == 4 && !codes ? 3 : 1;
+  j.planes = native ? 0 : sizeof(T) == 4 && !codes ? 3 : 1;
   j.half_exp = half_exp;
   j.blocks = cdiv(cdiv(rows, JOB_ROWS) * (j.w8 / 8), LT);
+  if (native) return {{room, 2 * j.w8, 0}, 1};
   return {{room, j.planes * j.w8, j.w8}, j.planes};
 }
 template <class T>
@@ -684,7 +688,7 @@ lrc_status prepare_operands(hipStream_t st, const OperandJobs& jobs, int count, 
   for (int i = 0; i < count; ++i) {
     const OperandJob& j = jobs.job[i];
     grid += j.blocks;
-    bytes += double(j.rows) * double(j.cols) * ((j.exps ? 1.0 : double(sizeof(T))) + 2.0 * j.planes);
+    bytes += double(j.rows) * double(j.cols) * ((j.exps ? 1.0 : double(sizeof(T))) + (j.planes ? 2.0 * j.planes : 4.0));
   }
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   ProfScope scope("linear_operand_kernel", st, 0.0, bytes);
@@ -722,9 +726,28 @@ template <class T>
 bool large_product(int64_t n, int64_t di, int64_t dn) {
   const double work = double(n) * double(di) * double(dn);
   if (n > GEMM_MAX_K) return false;
-  return sizeof(T) == 2 ? work >= double(1 << 18)
-                        : work >= double(1 << 30) && std::min({n, di, dn}) >= 144;
+  return work >= double(sizeof(T) == 2 ? 1 << 18 : 1 << 27);
 }
+// How the large fp32 products of a call run: on the tiles that take any operand, on pipelined fp32
+// tiles, or in three bf16 pieces, by the shortest estimate in microseconds.
+enum F32Way { ANY, NATIVE, SPLIT };
+struct F32Times {
+  double any = 0, native = 0, split = 14;   // (the split's launches before and behind its products)
+  // (the tiles that take any operand need 1.2 to 1.8 times as long, most where both run along columns)
+  void product(int64_t M, int64_t N, int64_t K, int KA, int KB) {
+    const double t = gemm_f32_time(M, N, K);
+    native += t;
+    any += t * (KA == K_COLS ? 1.7 : KB == K_COLS ? 1.35 : 1.25);
+    split += gemm_split_time(M, N, K, KA, KB);
+  }
+  void operand(const Operand& o, int64_t rows, int64_t cols) {
+    const double cells = double(rows) * double(cols);
+    split += cells * 10.0 / 4.5e6;
+    if (!(o.vec && cols % 4 == 0)) native += (native_copies++ ? 0.0 : 5.0) + cells * 8.0 / 4.5e6;
+  }
+  int native_copies = 0;
+  F32Way way() const { return any <= std::min(native, split) ? ANY : native <= split ? NATIVE : SPLIT; }
+};
 template <class T>
 bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two operands
   return std::max(round8(rows_a), round8(rows_b)) * (sizeof(T) == 4 ? 3 : 1) <= GEMM_MAX_LD;
@@ -780,7 +803,7 @@ LinearRoom forward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   Carve cv(ws);
   size_t part = any_room<T>(n, dn, di);
   const bool large = large_product<T>(n, di, dn) && gemm_fits<T>(di, di);
-  if (large) part = std::max(part, gemm_bf16_workspace(n, dn, di, K_ROWS, K_ROWS) / 4);
+  if (large) part = std::max(part, gemm_bf16_workspace(n, dn, di, K_ROWS, K_ROWS, sizeof(T) == 4) / 4);
   r.partial = cv.take<float>(part);
   if (large) {
     r.flag = cv.take<int32_t>(1);
@@ -800,10 +823,10 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   size_t part = std::max(any_room<T>(n, di, dn), any_room<T>(dn, di, n));
   const bool large = large_product<T>(n, di, dn) && gemm_fits<T>(di, dn);
   if (large)
-    part = std::max({part, gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS) / 4,
-                     gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS) / 4});
+    part = std::max({part, gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS, sizeof(T) == 4) / 4,
+                     gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS, sizeof(T) == 4) / 4});
   if (half_fits<T>(n, di, dn)) {
-    part = std::max(part, gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS) / 4);
+    part = std::max(part, gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS, false) / 4);
     r.dz_half = cv.take<uint16_t>(size_t(n) * round8(dn));
     r.dz_exp = cv.take<int32_t>(dn);
     r.x_exp = cv.take<int32_t>(di);
@@ -848,20 +871,31 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
   if (few_tokens(n, di, dn, sizeof(T)) && zcodes == nullptr)
     return linear_rows<T>(st, ox, ow, n, dn, di, ep, bytes);
   const LinearRoom room = forward_room<T>(ws, n, di, dn);
-  if (room.flag == nullptr || !has_room<T>(ox, di) || !has_room<T>(ow, di) || std::max(ldx, ldw) > GEMM_MAX_LD)
+  F32Way way = SPLIT;
+  if (sizeof(T) == 4 && room.flag != nullptr) {
+    F32Times t;
+    t.product(n, dn, di, K_ROWS, K_ROWS);
+    t.operand(ox, n, di);
+    t.operand(ow, dn, di);
+    way = t.way();
+  }
+  const bool native = way == NATIVE;
+  if (room.flag == nullptr || way == ANY || !has_room<T>(ox, di) || !has_room<T>(ow, di) ||
+      std::max(ldx, ldw) > GEMM_MAX_LD)
     return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, room.partial, nullptr, bytes);
-  const int32_t* flag = sizeof(T) == 4 ? room.flag : nullptr;
+  const int32_t* flag = sizeof(T) == 4 && !native ? room.flag : nullptr;
   if (flag) {
     clear_flag_kernel<<<1, 1, 0, st>>>(room.flag);
     LRC_LAUNCHED();
   }
   OperandJobs jobs;
   int count = 0;
-  const Prepared a = want_operand<T>(jobs, count, ox, n, di, room.a);
-  const Prepared b = want_operand<T>(jobs, count, ow, dn, di, room.b);
+  const Prepared a = want_operand<T>(jobs, count, ox, n, di, room.a, native);
+  const Prepared b = want_operand<T>(jobs, count, ow, dn, di, room.b, native);
   LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
-  LRC_TRY((gemm_bf16<T, K_ROWS, K_ROWS>(st, "linear_kernel", a.op, b.op, n, dn, di,
-                                        segments(a.planes, b.planes), ep, room.partial, flag,
+  GemmSegments seg = segments(a.planes, b.planes);
+  if (native) seg.type = FP32;
+  LRC_TRY((gemm_bf16<T, K_ROWS, K_ROWS>(st, "linear_kernel", a.op, b.op, n, dn, di, seg, ep, room.partial, flag,
                                         2.0 * double(n) * double(dn) * double(di), bytes)));
   if (!flag) return LRC_OK;
   return product_any<T, T, K_ROWS, K_ROWS>(st, "linear_any_kernel", ox, ow, n, dn, di, ep, room.partial, flag, bytes);
@@ -944,12 +978,22 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
   // few tokens read W once on either kind of tile: it is not laid out anew for them
   const bool w_in_place = sizeof(T) == 2 && ow.vec && di % 8 == 0;
-  const bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD &&
+  bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD &&
                        (w_in_place || n > 64);
   // a slope that is neither 0 nor 1 leaves bits in dz that the stream's bf16 does not hold
   const bool half = with_dz && a.act != LRC_ACT_RELU && a.dW != nullptr && half_fits<T>(n, di, dn);
-  const bool fast_dw = half || (fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD)));
-  int32_t* flag = sizeof(T) == 4 && (fast_dx || fast_dw) ? room.flag : nullptr;
+  bool fast_dw = half || (fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD)));
+  F32Way way = SPLIT;
+  if (sizeof(T) == 4 && (fast_dx || fast_dw)) {
+    F32Times t;
+    t.operand(og, n, dn);
+    if (fast_dx) t.product(n, di, dn, K_ROWS, K_COLS), t.operand(ow, dn, di);
+    if (fast_dw) t.product(dn, di, n, K_COLS, K_COLS), t.operand(ox, n, di);
+    way = t.way();
+    if (way == ANY) fast_dx = fast_dw = false;
+  }
+  const bool native = way == NATIVE;
+  int32_t* flag = sizeof(T) == 4 && !native && (fast_dx || fast_dw) ? room.flag : nullptr;
   if (half) {
     const ColPlan p = col_plan(n);
     MagnitudeJobs m;
@@ -1007,17 +1051,18 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   OperandJobs jobs;
   int count = 0;
   Prepared pg, pw, px;
-  if (fast_dx || (fast_dw && !half)) pg = want_operand<T>(jobs, count, og, n, dn, room.a);
-  if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b);
-  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, half ? room.x_exp : nullptr);
+  if (fast_dx || (fast_dw && !half)) pg = want_operand<T>(jobs, count, og, n, dn, room.a, native);
+  if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b, native);
+  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, native, half ? room.x_exp : nullptr);
   LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   if (a.dx != nullptr) {
     Epilogue ep;
     set_out<T>(ep, a.dx, a.lddx);
     const double bytes = e * (double(n) * dn + double(dn) * di + double(n) * di);
     if (fast_dx) {
-      LRC_TRY((gemm_bf16<T, K_ROWS, K_COLS>(st, "linear_dx_kernel", pg.op, pw.op, n, di, dn,
-                                            segments(pg.planes, pw.planes), ep, room.partial, flag,
+      GemmSegments seg = segments(pg.planes, pw.planes);
+      if (native) seg.type = FP32;
+      LRC_TRY((gemm_bf16<T, K_ROWS, K_COLS>(st, "linear_dx_kernel", pg.op, pw.op, n, di, dn, seg, ep, room.partial, flag,
                                             2.0 * double(n) * double(dn) * double(di), bytes)));
     }
     if (!fast_dx || flag)
@@ -1033,10 +1078,12 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     if (fast_dw) {
       GemmSegments seg = half ? GemmSegments{} : segments(pg.planes, px.planes);
       if (half) {
-        seg.half = true;
+        seg.type = FP16;
         ep.row_exp = room.dz_exp;
         ep.col_exp = room.x_exp;
         pg.op = {room.dz_half, round8(dn), 0};
+      } else if (native) {
+        seg.type = FP32;
       }
       LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n, seg, ep, room.partial, flag,
                                              2.0 * double(n) * double(dn) * double(di), bytes)));

@@ -312,10 +312,15 @@ struct GemmOperand {
 };
 // The reduction may run over several pairs of planes, one after the other: segment s
 // multiplies plane (pa >> 2 s) & 3 of A with plane (pb >> 2 s) & 3 of B.
+//
+// What the operands' elements are (fp16: K_COLS x K_COLS only; fp16 and fp32: one plane).  fp32
+// operands are addressed in 16-bit halves as the others are: ld and plane count halves, rows are
+// whole pieces of four.
+enum Element { BF16, FP16, FP32 };
 struct GemmSegments {
   int count = 1;
   uint32_t pa = 0, pb = 0;
-  bool half = false;   // the operands are fp16, not bf16 (K_COLS x K_COLS, one plane)
+  Element type = BF16;
 };
 constexpr int64_t GEMM_MAX_LD = int64_t(1) << 21;   // tile offsets stay below 2^31 bytes
 constexpr int64_t GEMM_MAX_K = int64_t(1) << 27;    // stages of all segments count in 32 bits
@@ -331,7 +336,10 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
 template <class TO>
 lrc_status gemm_finish(hipStream_t st, const float* partial, int splits, int64_t M, int64_t N, const Epilogue& ep,
                        const int32_t* skip);
-size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB);
+size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, bool f32);
+// estimates in microseconds of an fp32 product, on fp32 operands and on ones split in three
+double gemm_f32_time(int64_t M, int64_t N, int64_t K);
+double gemm_split_time(int64_t M, int64_t N, int64_t K, int KA, int KB);
 
 // ---- column sums ---------------------------------------------------------------------
 // out0[c] (c < split) and out1[c - split] (c >= split) = sum over p < parts of

@@ -413,6 +413,51 @@ def test_nonfinite_entries_in_a_large_product(lrc, dtype, where, n, d_in, d_out)
     assert same(dx, dy.double() @ w.double()) and same(dw, dy.double().T.contiguous() @ x.double())
 
 
+F32_SHAPES = [(700, 516, 1300), (701, 517, 1301), (513, 2047, 900), (130, 4100, 1000), (900, 100, 3500), (67, 3001, 777),
+              (3000, 260, 514), (2048, 2048, 1024), (6912, 1080, 1984), (6913, 1075, 1981)]
+
+
+@pytest.mark.parametrize("n,d_in,d_out", F32_SHAPES)
+def test_fp32_products_of_every_kind_exact(lrc, n, d_in, d_out):
+    """Small integers, whose products and sums are exact: sizes on either side of every choice between the kernels
+    of an fp32 product, whole pieces and ragged rows, split k and not."""
+    g = torch.Generator().manual_seed(n)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).float().to(dev())   # noqa: E731
+    x, w, dy, z, res = ints(n, d_in), ints(d_out, d_in), ints(n, d_out), ints(n, d_out), ints(n, d_out)
+    b = ints(d_out)
+    want = x.double() @ w.double().T + b.double()
+    y, kept, _ = lrc.lrc_linear(x, w, b, act="relu", residual=res, save="z")
+    assert torch.equal(kept.double(), want) and torch.equal(y.double(), want.clamp(min=0) + res.double())
+    y, kept, info = lrc.lrc_linear(x, w, b, save="checkpoint")
+    assert torch.equal(y.double(), want) and int(info.cpu()) == 0
+    for a, c in zip(kept, lrc.lrc_pack_activations(want.float())[:2]):
+        assert torch.equal(a, c)
+    dz = dy.double() * (z.double() > 0)
+    for held in (False, True):
+        xa, za = (lrc.lrc_pack_activations(x)[:2], lrc.lrc_pack_activations(z)[:2]) if held else (x, z)
+        got = lrc.lrc_linear_backward(dy, xa, w, act="relu", z=za)
+        assert torch.equal(got[0].double(), dz) and torch.equal(got[1].double(), dz @ w.double())
+        assert torch.equal(got[2].double(), dz.T.contiguous() @ x.double())
+        for only in ("need_dx", "need_dw"):
+            some = lrc.lrc_linear_backward(dy, xa, w, act="relu", z=za, **{only: False})
+            k = 2 if only == "need_dx" else 1
+            assert torch.equal(some[k], got[k])
+
+
+@pytest.mark.parametrize("n,d_in,d_out", F32_SHAPES)
+@pytest.mark.parametrize("where", ["x", "w", "dy"])
+def test_fp32_products_of_every_kind_with_nonfinite_entries(lrc, n, d_in, d_out, where):
+    """What the plain products give, on every kernel of an fp32 product."""
+    t = {"x": torch.ones(n, d_in), "w": torch.ones(d_out, d_in), "dy": torch.ones(n, d_out)}
+    t[where][3, 5], t[where][40, -1], t[where][-1, -2] = float("inf"), float("-inf"), float("nan")
+    x, w, dy = (t[k].to(dev()) for k in ("x", "w", "dy"))
+    same = lambda p, q: torch.equal(torch.nan_to_num(p.double(), 9e9, 8e8, 7e7),   # noqa: E731
+                                    torch.nan_to_num(q.float().double(), 9e9, 8e8, 7e7))
+    assert same(lrc.lrc_linear(x, w)[0], x.double() @ w.double().T)
+    _, dx, dw, _ = lrc.lrc_linear_backward(dy, x, w)
+    assert same(dx, dy.double() @ w.double()) and same(dw, dy.double().T.contiguous() @ x.double())
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n,d_in,d_out", LINEAR_SHAPES)
 @pytest.mark.parametrize("held", [False, True])
