@@ -550,7 +550,7 @@ static Plan plan_f32(int64_t M, int64_t N, int64_t K, double& cost) {
     const TileGrid tg = tiles_of(M, N, 64, int(s), per, steps);
     const int64_t each = cdiv(tg.tiles * s, 256);
     double c = F32_START + double(per) * (each == 1 ? F32_ALONE : double(each) * F32_STEP);
-    if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
+    if (s > 1) c += 6.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
     if (s == 1 || c < cost) {
       cost = c;
       best.tg = tg;

@@ -374,10 +374,13 @@ lrc_status linear_rows(hipStream_t st, const Operand& x, const Operand& W, int64
 struct ColPlan {
   int64_t rows, chunks;   // tokens per chunk
 };
-ColPlan col_plan(int64_t n) {
+// Chunks of 8 to 32 tokens, enough of them to spread a short or narrow stream over the chip (dz of
+// 3588 x 22: 32 tokens a chunk 21 us, 8 tokens 8 us); up to 32 tokens are one chunk of sixteen waves
+// (25 x 866: 12 us against 20 on four), whose sums need no second pass.
+ColPlan col_plan(int64_t n, int64_t d) {
   ColPlan p;
-  // one chunk needs no second pass; more of them spread a short stream over the chip
-  p.rows = std::max<int64_t>(n > 32 && n <= 1024 ? 8 : 32, cdiv(n, 1024));
+  const int64_t spread = (n * cdiv(d, 512) / 1024 + 3) & ~int64_t(3);
+  p.rows = n <= 32 ? 32 : std::max(std::min<int64_t>(32, std::max<int64_t>(8, spread)), cdiv(n, 1024));
   p.chunks = cdiv(n, p.rows);
   return p;
 }
@@ -405,8 +408,9 @@ __device__ __forceinline__ int channel_exponent(uint32_t bits) {
 }
 // largest finite magnitude (as bits) of every channel over a chunk of tokens; the exponent itself
 // where there is one chunk
-__global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64_t n, int64_t rows) {
-  __shared__ uint32_t most[3][64][9];
+template <int NW>
+__global__ __launch_bounds__(64 * NW) void magnitude_kernel(MagnitudeJobs jobs, int64_t n, int64_t rows) {
+  __shared__ uint32_t most[NW - 1][64][9];
   const int q = int64_t(blockIdx.x) < jobs.job[0].blocks ? 0 : 1;
   const MagnitudeJob& j = jobs.job[q];
   const int64_t block = int64_t(blockIdx.x) - (q ? jobs.job[0].blocks : 0);
@@ -419,7 +423,7 @@ __global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64
   auto run = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
     const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll 4
-    for (int64_t t = t0 + wave; t < t1; t += 4) {
+    for (int64_t t = t0 + wave; t < t1; t += NW) {
       if (j.exps != nullptr) {
         const uint32_t u = __float_as_uint(127.f * pow2f(j.exps[t * j.ld + (c >> 6)]));
 #pragma unroll
@@ -453,7 +457,9 @@ __global__ __launch_bounds__(LT) void magnitude_kernel(MagnitudeJobs jobs, int64
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (e < cnt) {
-      const uint32_t u = max(max(m[e], most[0][lane][e]), max(most[1][lane][e], most[2][lane][e]));
+      uint32_t u = m[e];
+#pragma unroll
+      for (int w = 0; w < NW - 1; ++w) u = max(u, most[w][lane][e]);
       if (gridDim.y == 1)
         j.out[c + e] = channel_exponent(u);
       else
@@ -481,18 +487,20 @@ __global__ __launch_bounds__(LT) void exponent_kernel(MagnitudeJobs jobs, int64_
 }
 
 // ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
-// Bound by memory: dy and z read, dz written once.  A lane takes eight consecutive channels,
-// the workgroup's four waves take the chunk's tokens in turn; db's share of the chunk is the
+// Bound by memory: dy and z read, dz written once, and once more in fp16 for dW (8192 x 11008 from
+// codes 150 us, 4.2 TB/s; the magnitudes before it 87 us, 3.1 TB/s, about even with their slopes'
+// arithmetic).  A lane takes eight consecutive channels,
+// the workgroup's waves take the chunk's tokens in turn; db's share of the chunk is the
 // waves' sums added in order.
-template <class T, bool CK>
-__global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_t lddy, int64_t n, int64_t d,
+template <class T, bool CK, int NW>
+__global__ __launch_bounds__(64 * NW) void dz_kernel(const T* __restrict__ dy, int64_t lddy, int64_t n, int64_t d,
                                                 const T* __restrict__ z, int64_t ldz,
                                                 const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
                                                 int64_t nb, int act, T* __restrict__ dz, int64_t lddz, int64_t rows,
                                                 float* __restrict__ partial,
                                                 int32_t* __restrict__ clear, const int32_t* __restrict__ dz_exp,
                                                 uint16_t* __restrict__ dz_half, int64_t w8) {
-  __shared__ float sums[3][64][9];
+  __shared__ float sums[NW - 1][64][9];
   if (clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *clear = 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t(blockIdx.x) * 64 + lane) * 8;
@@ -505,7 +513,7 @@ __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_
   auto run = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
     const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll 2
-    for (int64_t t = t0 + wave; t < t1; t += 4) {
+    for (int64_t t = t0 + wave; t < t1; t += NW) {
       float g[8];
       ld8(dy + t * lddy + c, len, g);
       if (act != LRC_ACT_NONE) {
@@ -535,7 +543,8 @@ __global__ __launch_bounds__(LT) void dz_kernel(const T* __restrict__ dy, int64_
   if (wave > 0) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    s[e] = ((s[e] + sums[0][lane][e]) + sums[1][lane][e]) + sums[2][lane][e];
+#pragma unroll
+    for (int w = 0; w < NW - 1; ++w) s[e] += sums[w][lane][e];
     if (e < cnt) partial[int64_t(blockIdx.y) * d + c + e] = s[e];
   }
 }
@@ -557,7 +566,8 @@ bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
 // An operand the bf16 product cannot read where it lies is first written to the workspace as
 // rows of `planes` pieces of w8 = 8 ceil(cols / 8) bf16 (zeros behind the columns):
 //   bf16 whose rows are not whole 16-byte pieces, and checkpoints (exact in bf16): one piece;
-//   fp32: three pieces with x = h + m + l exactly (8 + 8 + 8 significant bits).  A product of
+//   fp32 on fp32 tiles: one piece of fp32, where its rows are not whole 16-byte pieces;
+//   fp32 otherwise: three pieces with x = h + m + l exactly (8 + 8 + 8 significant bits).  A product of
 //   two such operands is h h + h m + m h + h l + m m + l h, the terms left out are below
 //   2^-24 of it: six bf16 products give fp32 accuracy at more than the fp32 matrix rate.  An
 //   entry that is not finite raises `flag`; the product is then done on fp32 tiles instead.
@@ -715,35 +725,39 @@ GemmSegments segments(int pa, int pb) {
   return s;
 }
 
-// Whether the products go to the pipelined tiles (lrc_gemm.hip) or to the ones that take any
-// operand.  Measured, both ways, forward / backward: bf16 3 x 141 x 1668 15 / 30 us against
-// 12 / 46, 1000 x 521 x 303 19 / 39 against 33 / 71, 2048 x 2048 x 1024 27 / 54 against 60 / 152:
-// pipelined ones from 2^18 products.  fp32 splits its operands first: 512^3 26 / 51 against 15 / 37,
-// 1024^3 42 / 81 against 32 / 81, 1001 x 1023 x 1021 44 / 88 against 57 / 114, 128 x 4096 x 4096
-// 77 / 127 against 50 / 127, 2048 x 2048 x 1024 80 / 159 against 86 / 224: from 2^30 and with no
-// extent so short that the splitting outweighs the products.
+// Whether the products may go to the pipelined tiles (lrc_gemm.hip) or all to the ones that take
+// any operand.  bf16, both ways, forward / backward in us: 3 x 141 x 1668 15 / 30 on the pipelined
+// against 12 / 46, 1000 x 521 x 303 19 / 39 against 33 / 71, 2048 x 2048 x 1024 27 / 54 against 60 /
+// 152: pipelined from 2^18 multiplications.  fp32 from 2^24, where F32Times chooses.
 template <class T>
 bool large_product(int64_t n, int64_t di, int64_t dn) {
   const double work = double(n) * double(di) * double(dn);
   if (n > GEMM_MAX_K) return false;
-  return work >= double(sizeof(T) == 2 ? 1 << 18 : 1 << 27);
+  return work >= double(sizeof(T) == 2 ? 1 << 18 : 1 << 24);
 }
-// How the large fp32 products of a call run: on the tiles that take any operand, on pipelined fp32
-// tiles, or in three bf16 pieces, by the shortest estimate in microseconds.
+// How the large fp32 products of a call run: on the tiles that take any operand (ANY), on pipelined
+// fp32 tiles (NATIVE), or in three bf16 pieces (SPLIT), by the shortest estimate in microseconds.
+// Measured forward, all three: 301 x 1928 x 768 22 / 19 / 39, 1024^3 33 / 23 / 42, 123 x 7725 x 1049
+// (rows laid out anew) 36 / 50 / 70, 2048 x 2048 x 1024 93 / 68 / 83, 6913 x 1075 x 1981 299 / 257 /
+// 191, 7547 x 3581 x 640 365 / 334 / 269.
 enum F32Way { ANY, NATIVE, SPLIT };
 struct F32Times {
   double any = 0, native = 0, split = 14;   // (the split's launches before and behind its products)
-  // (the tiles that take any operand need 1.2 to 1.8 times as long, most where both run along columns)
   void product(int64_t M, int64_t N, int64_t K, int KA, int KB) {
-    const double t = gemm_f32_time(M, N, K);
-    native += t;
-    any += t * (KA == K_COLS ? 1.7 : KB == K_COLS ? 1.35 : 1.25);
+    // 32 k steps of a 64 x 64 tile: 1.3 us alone on a compute unit (the latency of its loads), less
+    // by far with others there, more where operands run along columns
+    const AnyPlan p = plan_any<float>(M, N, K);
+    const double each = double(cdiv(p.tiles * p.splits, 256)), step = KA == K_COLS ? 0.9 : KB == K_COLS ? 0.72 : 0.65;
+    any += 6.0 + double(cdiv(p.k_per_split, 32)) * std::max(1.3, each * step);
+    if (p.splits > 1) any += 6.0 + 8.0 * p.splits * double(M) * double(N) / 4.5e6;
+    native += gemm_f32_time(M, N, K);
     split += gemm_split_time(M, N, K, KA, KB);
   }
-  void operand(const Operand& o, int64_t rows, int64_t cols) {
+  // (by the sizes alone, so that rows of another alignment give the same bits)
+  void operand(int64_t rows, int64_t cols) {
     const double cells = double(rows) * double(cols);
     split += cells * 10.0 / 4.5e6;
-    if (!(o.vec && cols % 4 == 0)) native += (native_copies++ ? 0.0 : 5.0) + cells * 8.0 / 4.5e6;
+    if (cols % 4 != 0) native += (native_copies++ ? 0.0 : 5.0) + cells * 8.0 / 4.5e6;
   }
   int native_copies = 0;
   F32Way way() const { return any <= std::min(native, split) ? ANY : native <= split ? NATIVE : SPLIT; }
@@ -819,7 +833,7 @@ template <class T>
 LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   LinearRoom r;
   Carve cv(ws);
-  r.sums = cv.take<float>(size_t(col_plan(n).chunks) * dn);
+  r.sums = cv.take<float>(size_t(col_plan(n, dn).chunks) * dn);
   size_t part = std::max(any_room<T>(n, di, dn), any_room<T>(dn, di, n));
   const bool large = large_product<T>(n, di, dn) && gemm_fits<T>(di, dn);
   if (large)
@@ -830,8 +844,8 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
     r.dz_half = cv.take<uint16_t>(size_t(n) * round8(dn));
     r.dz_exp = cv.take<int32_t>(dn);
     r.x_exp = cv.take<int32_t>(di);
-    r.dz_mag = cv.take<uint32_t>(size_t(col_plan(n).chunks) * dn);
-    r.x_mag = cv.take<uint32_t>(size_t(col_plan(n).chunks) * di);
+    r.dz_mag = cv.take<uint32_t>(size_t(col_plan(n, std::max(di, dn)).chunks) * dn);
+    r.x_mag = cv.take<uint32_t>(size_t(col_plan(n, std::max(di, dn)).chunks) * di);
   }
   r.partial = cv.take<float>(part);
   if (large || half_fits<T>(n, di, dn)) r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x
@@ -875,8 +889,8 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
   if (sizeof(T) == 4 && room.flag != nullptr) {
     F32Times t;
     t.product(n, dn, di, K_ROWS, K_ROWS);
-    t.operand(ox, n, di);
-    t.operand(ow, dn, di);
+    t.operand(n, di);
+    t.operand(dn, di);
     way = t.way();
   }
   const bool native = way == NATIVE;
@@ -976,8 +990,8 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB), false}
                           : plain<T>(a.x, a.ldx);
   const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
-  // few tokens read W once on either kind of tile: it is not laid out anew for them
-  const bool w_in_place = sizeof(T) == 2 && ow.vec && di % 8 == 0;
+  // few tokens read W once on either kind of tile: a large one is not laid out anew for them
+  const bool w_in_place = sizeof(T) == 2 && ((ow.vec && di % 8 == 0) || di * dn <= (int64_t(1) << 21));
   bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD &&
                        (w_in_place || n > 64);
   // a slope that is neither 0 nor 1 leaves bits in dz that the stream's bf16 does not hold
@@ -986,16 +1000,16 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   F32Way way = SPLIT;
   if (sizeof(T) == 4 && (fast_dx || fast_dw)) {
     F32Times t;
-    t.operand(og, n, dn);
-    if (fast_dx) t.product(n, di, dn, K_ROWS, K_COLS), t.operand(ow, dn, di);
-    if (fast_dw) t.product(dn, di, n, K_COLS, K_COLS), t.operand(ox, n, di);
+    t.operand(n, dn);
+    if (fast_dx) t.product(n, di, dn, K_ROWS, K_COLS), t.operand(dn, di);
+    if (fast_dw) t.product(dn, di, n, K_COLS, K_COLS), t.operand(n, di);
     way = t.way();
     if (way == ANY) fast_dx = fast_dw = false;
   }
   const bool native = way == NATIVE;
   int32_t* flag = sizeof(T) == 4 && !native && (fast_dx || fast_dw) ? room.flag : nullptr;
   if (half) {
-    const ColPlan p = col_plan(n);
+    const ColPlan p = col_plan(n, std::max(di, dn));
     MagnitudeJobs m;
     m.job[0].p = a.dy;
     m.job[0].ld = a.lddy;
@@ -1015,7 +1029,11 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     m.job[1].out = room.x_exp;
     for (MagnitudeJob& j : m.job) j.blocks = cdiv(j.cols, 512);
     ProfScope scope("magnitude_kernel", st, 0.0, double(n) * ((a.z ? 4.0 : 3.0) * double(dn) + (held ? double(di) / 64 : 2.0 * di)));
-    magnitude_kernel<<<dim3(unsigned(m.job[0].blocks + m.job[1].blocks), unsigned(p.chunks)), LT, 0, st>>>(m, n, p.rows);
+    const dim3 grid(unsigned(m.job[0].blocks + m.job[1].blocks), unsigned(p.chunks));
+    if (p.chunks == 1)
+      magnitude_kernel<16><<<grid, 1024, 0, st>>>(m, n, p.rows);
+    else
+      magnitude_kernel<4><<<grid, 256, 0, st>>>(m, n, p.rows);
     LRC_LAUNCHED();
     if (p.chunks > 1) {
       exponent_kernel<<<unsigned(cdiv(dn, 32) + cdiv(di, 32)), LT, 0, st>>>(m, p.chunks);
@@ -1023,7 +1041,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     }
   }
   if (with_dz || a.db != nullptr) {
-    const ColPlan p = col_plan(n);
+    const ColPlan p = col_plan(n, dn);
     uint16_t* dz_half = half ? room.dz_half : nullptr;
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
@@ -1031,14 +1049,23 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
       float* part = a.db != nullptr && p.chunks > 1 ? room.sums : a.db;   // one chunk's sums are db
       const T *dy = static_cast<const T*>(a.dy), *z = static_cast<const T*>(a.z);
       T* dz = static_cast<T*>(a.dz);
-      if (a.z == nullptr && a.act != LRC_ACT_NONE) {
-        dz_kernel<T, true><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, cdiv(dn, CKB), a.act,
-                                                dz, a.lddz, p.rows, part, flag, room.dz_exp, dz_half, round8(dn));
-      } else {
-        dz_kernel<T, false><<<grid, LT, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, nullptr, nullptr, 0, a.act, dz, a.lddz,
-                                                 p.rows, part, flag, room.dz_exp, dz_half,
-                                                 round8(dn));
-      }
+      const bool codes = a.z == nullptr && a.act != LRC_ACT_NONE;
+      const int64_t nb = cdiv(dn, CKB), w8 = round8(dn);
+      auto go = [&](auto held_z, auto waves) {
+        constexpr bool CK = decltype(held_z)::value;
+        constexpr int NW = decltype(waves)::value;
+        dz_kernel<T, CK, NW><<<grid, 64 * NW, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, nb, a.act, dz,
+                                                       a.lddz, p.rows, part, flag, room.dz_exp, dz_half, w8);
+      };
+      using std::integral_constant;
+      if (codes && p.chunks == 1)
+        go(std::true_type{}, integral_constant<int, 16>{});
+      else if (codes)
+        go(std::true_type{}, integral_constant<int, 4>{});
+      else if (p.chunks == 1)
+        go(std::false_type{}, integral_constant<int, 16>{});
+      else
+        go(std::false_type{}, integral_constant<int, 4>{});
       LRC_LAUNCHED();
     }
     if (a.db != nullptr && p.chunks > 1) LRC_TRY(reduce_partials(st, room.sums, p.chunks, dn, dn, a.db, nullptr));
