@@ -332,12 +332,15 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restric
   }
 }
 
-// Up to 16 tokens always; up to 64 where x, which every 16 channels read again, is small beside
-// a launch: bf16 weights up to 2^24 entries (4096 x 4096: 24 tokens 13 us against 22 on tiles
-// with split k, 64 tokens 23 against 22; 11008 x 4096: 24 tokens 36 against 25).  fp32 weights
-// would be split into three pieces first: always (4096 x 11008, 64 tokens: 124 us against 191).
+// Up to 8 tokens always.  Up to 64 where x, which every 16 channels read again, is small beside a
+// launch (bf16 rows / tiles with split k, us: 4096 x 4096 at 32 tokens 13.7 / 15.9, at 48 18.6 / 16.3;
+// 8192 x 1024 at 16 16.5 / 17.5, at 24 21 / 17; fp32 4096 x 4096 at 16 23 / 27, at 32 31 / 29) and W,
+// in bf16, too (4096 x 11008 at 16 30 / 26); and where tiles would first lay W out anew (whole rows
+// of no whole pieces: as much again as reading it twice).
 bool few_tokens(int64_t n, int64_t di, int64_t dn, size_t size) {
-  return n <= 16 || (n <= 64 && (size == 4 || di * dn <= (int64_t(1) << 24)));
+  if (n <= 8 || n > 64) return n <= 8;
+  if (di % int64_t(16 / size) != 0) return true;
+  return size == 2 ? n * di <= (int64_t(1) << 17) && di * dn <= (int64_t(1) << 24) : n * di <= (int64_t(1) << 16);
 }
 
 template <class T>
@@ -990,8 +993,9 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const Operand ox = held ? Operand{a.xcodes, di, a.xexps, cdiv(di, CKB), false}
                           : plain<T>(a.x, a.ldx);
   const bool fast_g = room.flag != nullptr && has_room<T>(og, dn) && ldg <= GEMM_MAX_LD;
-  // few tokens read W once on either kind of tile: a large one is not laid out anew for them
-  const bool w_in_place = sizeof(T) == 2 && ((ow.vec && di % 8 == 0) || di * dn <= (int64_t(1) << 21));
+  // few tokens read W once on either kind of tile: a large one is not laid out anew for them (in fp32
+  // the estimates count that)
+  const bool w_in_place = sizeof(T) == 4 || ((ow.vec && di % 8 == 0) || di * dn <= (int64_t(1) << 21));
   bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD &&
                        (w_in_place || n > 64);
   // a slope that is neither 0 nor 1 leaves bits in dz that the stream's bf16 does not hold

@@ -444,6 +444,24 @@ def test_fp32_products_of_every_kind_exact(lrc, n, d_in, d_out):
             assert torch.equal(some[k], got[k])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [8, 9, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("d_in,d_out", [(4096, 520), (4100, 1000), (8192, 640), (2047, 333), (1024, 4096), (5000, 1)])
+def test_few_tokens_exact(lrc, dtype, n, d_in, d_out):
+    """On either side of the choices between streaming the weight and tiles with split k; entries of one keep the
+    sums below 2^24."""
+    g = torch.Generator().manual_seed(n)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g).to(dtype).to(dev())   # noqa: E731
+    x, w, dy, res = ints(n, d_in), ints(d_out, d_in), ints(n, d_out), ints(n, d_out)
+    want = x.double() @ w.double().T
+    y, z, _ = lrc.lrc_linear(x, w, act="relu", residual=res, save="z")
+    assert torch.equal(z, want.to(dtype)) and torch.equal(y, (want.clamp_min(0) + res.double()).to(dtype))
+    _, dx, dw, db = lrc.lrc_linear_backward(dy, x, w)
+    assert torch.equal(dx, (dy.double() @ w.double()).to(dtype))
+    assert torch.equal(dw, (dy.double().T.contiguous() @ x.double()).to(dtype))
+    assert torch.equal(db.double(), dy.double().sum(0))
+
+
 @pytest.mark.parametrize("n,d_in,d_out", F32_SHAPES)
 @pytest.mark.parametrize("where", ["x", "w", "dy"])
 def test_fp32_products_of_every_kind_with_nonfinite_entries(lrc, n, d_in, d_out, where):
