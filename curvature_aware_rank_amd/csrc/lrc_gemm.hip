@@ -1,18 +1,24 @@
-// bf16 (or fp16) matrix products on the matrix cores with a fused epilogue: the linear layer's forward,
-// dx and dW products.
+// Matrix products on the matrix cores with a fused epilogue: the linear layer's forward, dx and dW
+// products of bf16, fp16 or fp32 operands, sums in fp32.
 //
 // An output tile of BM x BN belongs to one workgroup; its waves hold blocks of MF x MF
-// accumulators (16 x 16 x 32 or 32 x 32 x 16 matrix instructions).  Both operands travel from memory straight into LDS (16 bytes per lane, no
-// staging registers) in stages of 32 or 64 k steps, four or two stage buffers, all but one
-// in flight while one is multiplied.  A buffer resource bounds each operand, so rows past the matrix and
-// k past its end read as zeros without any masking of data.
+// accumulators (16 x 16 x 32, 32 x 32 x 16 or, in fp32, 16 x 16 x 4 matrix instructions).  Both
+// operands travel from memory straight into LDS (16 bytes per lane, no staging registers) in stages
+// of 64 or 128 bytes of a row, four or two stage buffers, all but one in flight while one is
+// multiplied.  A buffer resource bounds each operand, so rows past the matrix and k past its end
+// read as zeros without any masking of data.
 //   K_ROWS: a tile row's k steps lie together; its 16-byte granules change places by the row's
 //     number, so that the 16 rows of a fragment read cover every bank once.
 //   K_COLS: a k step's channels lie together; fragments come from transposing LDS reads
-//     (ds_read_b64_tr_b16), granules changing places by the step's number.
-// Where it stands: 8192 x 4096 x 11008 bf16 forward 680 us (1090 TFLOP/s; the vendor's library on
-// the same box 690), dx 560-585, dW 580-605; 4096^3 103 us (library 90, which holds 85 % of the
-// matrix pipes' cycles where this holds 73 %).
+//     (ds_read_b64_tr_b16), in fp32 from four reads of 4 bytes, granules changing places by the
+//     step's number.
+// What bounds it: large bf16 products the chip's power, which sets its clock (1.6 to 1.9 GHz), then
+// the matrix pipes (73 % of their cycles at 4096^3): 8192 x 4096 x 11008 forward 680 us in a
+// row of its own calls (1090 TFLOP/s; the vendor's library on the same box 690), 730 between other
+// kernels; dx 585-640, dW in bf16 605, in fp16 650-700; 4096^3 103 us (library 90).  fp32 split in
+// three: 8192 x 1024 x 4096 315-345 us (200 TFLOP/s of fp32 products, fp32 instructions reach 140).
+// fp32 tiles: 2048 x 2048 x 1024 68 us (126 TFLOP/s; library 65).  24 tokens x 11008 x 4096: 22 us,
+// 4.1 TB/s of weight, and 5 for the splits' sums.
 // Few tiles leave compute units idle, so k may be split: every split writes its fp32 tile and
 // a second kernel adds them in split order and runs the epilogue (bit-reproducible).
 #include "lrc_train.h"
@@ -326,10 +332,11 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     return q == 0 ? sb0 : q == 1 ? sb1 : q == 2 ? sb2 : sb3;
   };
 
-  // Schedule, stage s in buffer s % NST.  Iteration s: read the second half of stage s, multiply
-  // its first half, then a barrier that leaves the loads of the stages behind s + 1 (L each per
-  // wave) in flight: stage s + 1 is then in LDS and nobody reads stage s any more, so its buffer
-  // takes stage s + NST; read the first half of stage s + 1, multiply the second half of stage s.
+  // Schedule, stage s in buffer s % NST, in STEPS steps of one fragment each.  Iteration s: read the
+  // fragments of a step while the step before it is multiplied, up to the last of stage s; then a
+  // barrier that leaves the loads of the stages behind s + 1 (L each per wave) in flight: stage
+  // s + 1 is then in LDS and nobody reads stage s any more, so its buffer takes stage s + NST; read
+  // the first step of stage s + 1, multiply the last of stage s.
   // Stages past the end are issued with empty resources (zeros, never multiplied), so that the
   // count of loads in flight stays the same to the end.
   next_stage(nsteps > 0);
@@ -346,8 +353,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   }
   wait_barrier<(NST - 1) * L>();
   read_frags(sb0, 0, fa0, fb0);
-  // A stage of KS / KF steps (an even number); fa0, fb0 hold its first one.  The barrier stands
-  // before the last.
+  // a stage of KS / KF steps (an even number); fa0, fb0 hold its first one
   constexpr int STEPS = KS / SA::KF;
   static_assert(STEPS % 2 == 0 && STEPS >= 2, "the two fragment sets take turns");
   auto stage = [&](uint8_t* cur, const uint8_t* nxt, bool live) {
@@ -536,8 +542,10 @@ static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double
   }
   return best;
 }
-// fp32 products: tiles of 64 x 64, four waves of 16 x 64, up to four workgroups on a unit; 32 k
-// steps take a unit F32_STEP of matrix time, F32_ALONE if nothing else runs on it
+// fp32 products: tiles of 64 x 64, four waves of 16 x 64, up to five workgroups on a unit (tiles of
+// 128 x 128, two on a unit, leave more units idle at these sizes: 2048 x 2048 x 1024 76 us against
+// 68, 246 x 6316 x 2096 108 against 67).  32 k steps take a unit F32_STEP of matrix time, F32_ALONE
+// if nothing else runs on it.
 constexpr double F32_STEP = 0.5, F32_ALONE = 0.75, F32_START = 6.0;
 static Plan plan_f32(int64_t M, int64_t N, int64_t K, double& cost) {
   Plan best;

