@@ -4,7 +4,7 @@
 // An output tile of BM x BN belongs to one workgroup; its waves hold blocks of MF x MF
 // accumulators (16 x 16 x 32, 32 x 32 x 16 or, in fp32, 16 x 16 x 4 matrix instructions).  Both
 // operands travel from memory straight into LDS (16 bytes per lane, no staging registers) in stages
-// of 64 or 128 bytes of a row, four or two stage buffers, all but one in flight while one is
+// of 64 or 128 bytes of a row, two or four stage buffers, all but one in flight while one is
 // multiplied.  A buffer resource bounds each operand, so rows past the matrix and k past its end
 // read as zeros without any masking of data.
 //   K_ROWS: a tile row's k steps lie together; its 16-byte granules change places by the row's
@@ -17,8 +17,8 @@
 // row of its own calls (1090 TFLOP/s; the vendor's library on the same box 690), 730 between other
 // kernels; dx 585-640, dW in bf16 605, in fp16 650-700; 4096^3 103 us (library 90).  fp32 split in
 // three: 8192 x 1024 x 4096 315-345 us (200 TFLOP/s of fp32 products, fp32 instructions reach 140).
-// fp32 tiles: 2048 x 2048 x 1024 68 us (126 TFLOP/s; library 65).  24 tokens x 11008 x 4096: 22 us,
-// 4.1 TB/s of weight, and 5 for the splits' sums.
+// fp32 tiles: 2048 x 2048 x 1024 68 us (126 TFLOP/s; library 65).  24 tokens x 11008 x 4096: 23 us
+// with the splits' sums, 3.9 TB/s of weight.
 // Few tiles leave compute units idle, so k may be split: every split writes its fp32 tile and
 // a second kernel adds them in split order and runs the epilogue (bit-reproducible).
 #include "lrc_train.h"
@@ -56,6 +56,7 @@ struct Stager {
   static constexpr int ROWB = EDGE * ES;                    // K_COLS: bytes per k step
   static constexpr int KE = KS * 2 / ES;                    // k steps of a stage
   static constexpr int GE = 16 / ES;                        // elements of a 16-byte granule
+  static_assert(EDGE >= 128 || (EDGE == 64 && MF == 16), "the granules of a k step hold their swizzle");
   static constexpr unsigned OOB = 0x80000000u;              // past every resource
 
   const uint16_t* base;   // first element of the tile (plane 0, k = 0)
@@ -124,6 +125,7 @@ struct Stager {
   // groups of k steps 8 apart on halves of those
   static __device__ __forceinline__ int step_swizzle(int t) {
     if (ES == 4) return 4 * ((t >> 2) & 3);   // the four groups read k steps 4 apart, 64 bytes of each
+    if (EDGE == 64) return (4 * ((t >> 1) & 1)) ^ (2 * ((t >> 3) & 1));   // a k step is half the banks
     return (4 * (t & 3)) ^ (MF == 16 ? 2 * ((t >> 3) & 1) : 0);
   }
 
@@ -492,19 +494,24 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
 }
 
 // Tiles and splits from the sizes alone (256 compute units), so that workspace sizes are known
-// without a device and equal inputs give equal bits.  Large tiles (256 x 256, one workgroup per
-// compute unit, 1330 TFLOP/s at 4096^3) for products that fill the chip; small ones (128 x 128, two
-// per unit, 1060) otherwise, with k split when they are few.  Small tiles for what a last, part
+// without a device and equal inputs give equal bits.  LARGE tiles (256 x 256, one workgroup per
+// compute unit, 1330 TFLOP/s at 4096^3) for products that fill the chip; SMALL ones (128 x 128, two
+// per unit, 1060) and TINY ones (64 x 64, four stages ahead) otherwise, with k split when they are
+// few.  Tiny ones need twice the loads but wait less for each: 1000 x 1024 x 1024 forward / dx / dW
+// 7.9 / 9.0 / 9.2 us against 13.5 / 15.5 / 16.8 on small ones, 64 x 4096 x 11008 18 / 25 / 42 against
+// 26 / 26 / 43; 4096 x 1024 x 1024 stays on large ones (17).  Small tiles for what a last, part
 // full round of large ones holds gained nothing (8192 x 4096 x 11008, 5.4 rounds: 695 us against
 // 690): the chip is then at its power limit, and units that idle let the others run faster.  Times
-// below in microseconds, taken at 256 x 4096 x 4096 to 8192 x 4096 x 11008.
+// below in microseconds, taken at 100 x 64 x 64 to 8192 x 4096 x 11008.
+enum Tile { LARGE, SMALL, TINY };
 struct Plan {
-  bool large;
+  Tile tile;
   TileGrid tg;
 };
 // 64 k steps of every workgroup of a round; a round's first loads and its epilogue
 constexpr double LARGE_STEP = 1.55, SMALL_STEP_FULL = 0.88, SMALL_STEP_HALF = 0.64, LARGE_ROUND = 14.0,
-                 SMALL_ROUND = 8.0, MEMORY = 4.5e6;
+                 SMALL_ROUND = 8.0, TINY_STEP_FULL = 0.38, TINY_STEP_HALF = 0.25, TINY_ROUND = 4.0,
+                 MEMORY = 4.5e6;
 
 static TileGrid tiles_of(int64_t m, int64_t n, int edge, int splits, int64_t per, int64_t steps) {
   const int64_t nm = cdiv(m, edge), nn = cdiv(n, edge);
@@ -513,10 +520,11 @@ static TileGrid tiles_of(int64_t m, int64_t n, int edge, int splits, int64_t per
 static double large_cost(int64_t tiles, double steps64) {
   return double(cdiv(tiles, 256)) * (steps64 * LARGE_STEP + LARGE_ROUND);
 }
-static double small_cost(int64_t groups, double steps64) {
+// small and tiny tiles: two workgroups on a unit, or one
+static double round_cost(int64_t groups, double steps64, double step_full, double step_half, double round) {
   const int64_t full = groups / 512, rest = groups % 512;
-  double c = double(full) * (steps64 * SMALL_STEP_FULL + SMALL_ROUND);
-  if (rest > 0) c += steps64 * (rest > 256 ? SMALL_STEP_FULL : SMALL_STEP_HALF) + SMALL_ROUND;
+  double c = double(full) * (steps64 * step_full + round);
+  if (rest > 0) c += steps64 * (rest > 256 ? step_full : step_half) + round;
   return c;
 }
 // KL: k steps per stage of a large tile
@@ -525,7 +533,7 @@ static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double
   const int64_t steps_l = cdiv(K, KL), steps_s = cdiv(K, 64);
   const double s64 = double(steps_s) * count;
   const double floor_us = 2.0 * double(K) * double(M + N) * (count > 1 ? 3 : 1) / MEMORY;
-  best.large = true;
+  best.tile = LARGE;
   best.tg = tiles_of(M, N, 256, 1, steps_l * count, steps_l);
   cost = std::max(floor_us, large_cost(best.tg.tiles, s64));
   const int64_t total = steps_s * count;
@@ -533,11 +541,22 @@ static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double
     const int64_t per = cdiv(total, s);
     if (cdiv(total, per) != s) continue;
     const TileGrid tg = tiles_of(M, N, 128, int(s), per, steps_s);
-    double c = std::max(floor_us, small_cost(tg.tiles * s, double(per)));
+    double c = std::max(floor_us, round_cost(tg.tiles * s, double(per), SMALL_STEP_FULL, SMALL_STEP_HALF, SMALL_ROUND));
     if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
     if (c < cost) {
       cost = c;
-      best = {false, tg};
+      best = {SMALL, tg};
+    }
+  }
+  for (int64_t s = 1; count == 1 && s <= std::min<int64_t>(32, total); ++s) {
+    const int64_t per = cdiv(total, s);
+    if (cdiv(total, per) != s) continue;
+    const TileGrid tg = tiles_of(M, N, 64, int(s), per, steps_s);
+    double c = std::max(floor_us, round_cost(tg.tiles * s, double(per), TINY_STEP_FULL, TINY_STEP_HALF, TINY_ROUND));
+    if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
+    if (c < cost) {
+      cost = c;
+      best = {TINY, tg};
     }
   }
   return best;
@@ -549,7 +568,7 @@ static Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double
 constexpr double F32_STEP = 0.5, F32_ALONE = 0.75, F32_START = 6.0;
 static Plan plan_f32(int64_t M, int64_t N, int64_t K, double& cost) {
   Plan best;
-  best.large = false;
+  best.tile = TINY;
   cost = 0;
   const int64_t steps = cdiv(K, 32);
   for (int64_t s = 1; s <= std::min<int64_t>(32, steps); ++s) {
@@ -631,12 +650,15 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
     if constexpr (EL == FP32)
       gemm_bf16_kernel<TO, KA, KB, 16, 4, 1, 1, 4, 64, 2, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
-    else if (p.large)
+    else if (p.tile == LARGE)
       gemm_bf16_kernel<TO, KA, KB, ML, 4, 2, 64 / ML, 128 / ML, KL, NL, SEG, EL><<<unsigned(grid), 512, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
-    else
+    else if (p.tile == SMALL)
       gemm_bf16_kernel<TO, KA, KB, 16, 2, 2, 4, 4, 64, 2, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
-        A, B, M, N, K, seg, tg, ep, partial, skip);
+          A, B, M, N, K, seg, tg, ep, partial, skip);
+    else if constexpr (!SEG)
+      gemm_bf16_kernel<TO, KA, KB, 16, 4, 1, 1, 4, 64, 4, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
+          A, B, M, N, K, seg, tg, ep, partial, skip);
   };
   using std::integral_constant;
   // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
