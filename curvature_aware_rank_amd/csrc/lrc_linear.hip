@@ -334,14 +334,15 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_kernel(const T* __restric
 }
 
 // Up to 8 tokens always.  Up to 64 where x, which every 16 channels read again, is small beside a
-// launch (bf16 rows / tiles with split k, us: 4096 x 4096 at 32 tokens 13.7 / 15.9, at 48 18.6 / 16.3;
-// 8192 x 1024 at 16 16.5 / 17.5, at 24 21 / 17; fp32 4096 x 4096 at 16 23 / 27, at 32 31 / 29) and W,
-// in bf16, too (4096 x 11008 at 16 30 / 26); and where tiles would first lay W out anew (whole rows
-// of no whole pieces: as much again as reading it twice).
+// launch (bf16 rows / tiles with split k, us: 4096 x 4096 at 16 tokens 10.0 / 13.4, at 32 13.8 / 13.0;
+// 2048 x 2048 at 48 10.5 / 11.0, at 64 12.0 / 11.8; 8192 x 1024 at 8 13.9 / 14.3, at 24 21 / 12; fp32
+// 4096 x 4096 at 16 23 / 27, at 32 31 / 29) and W, in bf16, too (4096 x 11008 at 16 29 / 24); and
+// where tiles would first lay W out anew (whole rows of no whole pieces: as much again as reading
+// it twice).
 bool few_tokens(int64_t n, int64_t di, int64_t dn, size_t size) {
   if (n <= 8 || n > 64) return n <= 8;
   if (di % int64_t(16 / size) != 0) return true;
-  return size == 2 ? n * di <= (int64_t(1) << 17) && di * dn <= (int64_t(1) << 24) : n * di <= (int64_t(1) << 16);
+  return size == 2 ? n * di <= (int64_t(3) << 15) && di * dn <= (int64_t(1) << 24) : n * di <= (int64_t(1) << 16);
 }
 
 template <class T>
