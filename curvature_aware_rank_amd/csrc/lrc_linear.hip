@@ -731,13 +731,16 @@ GemmSegments segments(int pa, int pb) {
 }
 
 // Whether the products may go to the pipelined tiles (lrc_gemm.hip) or all to the ones that take
-// any operand.  bf16, both ways, forward / backward in us: 3 x 141 x 1668 15 / 30 on the pipelined
-// against 12 / 46, 1000 x 521 x 303 19 / 39 against 33 / 71, 2048 x 2048 x 1024 27 / 54 against 60 /
-// 152: pipelined from 2^18 multiplications.  fp32 from 2^24, where F32Times chooses.
+// any operand.  bf16, forward / dx / dW in us, pipelined against any: in place 65 x 16 x 16 3.9 / 5.3 /
+// 4.3 against 4.5 / 5.0 / 6.6, 1000 x 16 x 16 4 / 4 / 8 against 5 / 5 / 20, 2048 x 2048 x 1024 18 / 18
+// / 19 against 68 / 66 / 89; laid out first 1000 x 17 x 17 8 / 8 / 12 against 6 / 6 / 27, 300 x 65 x 65
+// 9 / 9 / 10 against 6 / 7 / 15, 1000 x 521 x 303 12 / 12 / 14 against 14 / 14 / 28: whole pieces
+// always, others from 2^18 multiplications.  fp32 from 2^24, where F32Times chooses.
 template <class T>
 bool large_product(int64_t n, int64_t di, int64_t dn) {
   const double work = double(n) * double(di) * double(dn);
   if (n > GEMM_MAX_K) return false;
+  if (sizeof(T) == 2 && di % 8 == 0 && dn % 8 == 0) return true;
   return work >= double(sizeof(T) == 2 ? 1 << 18 : 1 << 24);
 }
 // How the large fp32 products of a call run: on the tiles that take any operand (ANY), on pipelined
