@@ -575,7 +575,10 @@ bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
 //   fp32 otherwise: three pieces with x = h + m + l exactly (8 + 8 + 8 significant bits).  A product of
 //   two such operands is h h + h m + m h + h l + m m + l h, the terms left out are below
 //   2^-24 of it: six bf16 products give fp32 accuracy at more than the fp32 matrix rate.  An
-//   entry that is not finite raises `flag`; the product is then done on fp32 tiles instead.
+//   infinity would meet one of the other sign from the lower pieces.  So an entry that is not finite
+//   or passes SPLIT_MAX raises `flag`, and the product is done on fp32 tiles instead; without one no
+//   sum of up to GEMM_MAX_K terms passes 2^127.
+constexpr float SPLIT_MAX = 0x1p50f;
 template <class T>
 __device__ __forceinline__ void split_store(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag);
 template <>
@@ -588,9 +591,8 @@ __device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, floa
   bool bad = false;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    bad |= !finite_f(v[e]);
+    bad |= !(fabsf(v[e]) <= SPLIT_MAX);
     h[e] = round_to(v[e], static_cast<const uint16_t*>(nullptr));
-    if (!finite_f(h[e])) h[e] = __uint_as_float(__float_as_uint(v[e]) & 0xffff0000u);   // rounded past the largest
     const float r = v[e] - h[e];
     m[e] = round_to(r, static_cast<const uint16_t*>(nullptr));
     v[e] = r - m[e];
@@ -651,9 +653,15 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
       st8(reinterpret_cast<float*>(j.out) + r * j.w8 + c, 8, v[q4]);
     else if (j.half_exp != nullptr)
       st8_half(o, v[q4], scale);
-    else if (j.exps != nullptr)
+    else if (j.exps != nullptr) {
       split_store<uint16_t>(o, j.w8, v[q4], flag);
-    else
+      if (sizeof(T) == 4) {   // one exact piece, which meets three
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bad |= fabsf(v[q4][e]) > SPLIT_MAX;
+        if (bad) *flag = 1;
+      }
+    } else
       split_store<T>(o, j.w8, v[q4], flag);
   }
 }
@@ -810,7 +818,7 @@ void set_out(Epilogue& ep, void* y, int64_t ldy) {
 
 // Workspace of the three products.
 struct LinearRoom {
-  int32_t* flag = nullptr;      // an fp32 operand holds an entry that is not finite
+  int32_t* flag = nullptr;      // an fp32 operand holds an entry that must not be split
   float* partial = nullptr;     // split products
   float* sums = nullptr;        // db chunks
   uint16_t *a = nullptr, *b = nullptr, *c = nullptr;   // operands

@@ -450,7 +450,9 @@ size_t lrc_layer_norm_backward_workspace(int64_t n_tokens, int64_t d);
  * fp32 z (`info` as in lrc_pack_activations); at most one of the two, NULL otherwise.
  * bf16: products exact, sums fp32.  fp32: products and sums to fp32 accuracy (an entry below
  * 2^-110 in magnitude counts to an absolute 2^-133).  The order of every sum depends on the
- * sizes and the alignment only, so equal inputs give equal bits.  A bf16 product of more than
+ * sizes, the alignment and the leading dims, and in a large fp32 product on whether an entry of x
+ * or W passes 2^50 or is not finite (a single one moves the whole product to another kernel, as
+ * accurate but slower), so equal inputs give equal bits.  A bf16 product of more than
  * 64 tokens is fastest where the rows of x and W start on 16 bytes, or have a length that is
  * no multiple of 8; others may take five times as long.
  * 1 <= d_in, d_out <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.

@@ -51,3 +51,54 @@ def test_fp32_gradients_alone_have_the_bits_of_the_joint_call(lrc, n, d_in, d_ou
             for name, p, q in zip(("dz", "dx", "dw", "db"), some, joint):
                 assert (p is None) == (f"need_{name}" in need)
                 assert p is None or torch.equal(p, q), (act, need, name)
+
+
+# ----------------------------------------------------------------------------- the ends of the range
+F32_WAYS = [(100, 300, 520), (700, 516, 1300), (6912, 1080, 1984)]   # any operand, fp32 tiles, three bf16 pieces
+
+
+def three_products(lrc, a, b, m, n, k):
+    """A B^T of A (m, k) and B (n, k) as y of the forward, dx and dW of the backward pass (sizes as given in each)."""
+    y = lrc.lrc_linear(a, b)[0]
+    dx = lrc.lrc_linear_backward(a, torch.zeros(m, n, dtype=a.dtype, device=dev()), b.t().contiguous())[1]
+    w = torch.zeros(m, n, dtype=a.dtype, device=dev())
+    dw = lrc.lrc_linear_backward(a.t().contiguous(), b.t().contiguous(), w)[2]
+    return {"y": y, "dx": dx, "dW": dw}
+
+
+@pytest.mark.parametrize("m,k,n", F32_WAYS)
+def test_finite_fp32_entries_whose_product_overflows(lrc, m, k, n):
+    """Finite entries near the largest number: an overflow is the infinity that the product's sign says, whatever
+    pieces an entry is split in, and every other row is as accurate as before."""
+    a, b = normal(1, m, k), normal(2, n, k)
+    for i in range(16):   # mantissas whose lower bf16 pieces have either sign
+        a[5 + i, 7] = (-1) ** (i // 8) * 2.0 ** 126 * (1 + i % 8 * 2.0 ** -9 + 2.0 ** -18)
+    b[:, 7] = 2.0 ** 12
+    b[3, 7] = -2.0 ** 12
+    want = a.double() @ b.double().T
+    bound = (k + 8) * 2 * U * (a.double().abs() @ b.double().abs().T)
+    over = want.float().isinf()
+    assert over[5:21].all() and int(over.sum()) == 16 * n
+    for name, got in three_products(lrc, a, b, m, n, k).items():
+        assert torch.equal(got[over], want.float()[over]), name
+        assert ((got.double() - want).abs() <= bound)[~over].all(), name
+
+
+def test_finite_fp32_entries_whose_product_with_a_checkpoint_overflows(lrc):
+    """As above with x in 8 bits, whose values are one exact piece."""
+    n, d_in, d_out = 6912, 1080, 1984
+    x, dy = normal(1, n, d_in), normal(2, n, d_out)
+    x[7] = 2.0 ** 120 * torch.where(torch.arange(d_in, device=dev()) % 3 == 0, -1.0, 1.0)
+    dy[7] = 2.0 ** -100
+    for i in range(16):
+        dy[7, 5 + i] = (-1) ** (i // 8) * 2.0 ** 18 * (1 + i % 8 * 2.0 ** -9 + 2.0 ** -18)
+    codes, exps, _ = lrc.lrc_pack_activations(x)
+    held = lrc.lrc_unpack_activations(codes, exps, torch.float32)
+    assert torch.equal(held[7], x[7])
+    dw = lrc.lrc_linear_backward(dy, (codes, exps), torch.zeros(d_out, d_in, device=dev()))[2]
+    want = dy.double().T.contiguous() @ held.double()
+    over = want.float().isinf()
+    assert over[5:21].all() and int(over.sum()) == 16 * d_in
+    assert torch.equal(dw[over], want.float()[over])
+    bound = (n + 8) * 2 * U * (dy.double().abs().T.contiguous() @ held.double().abs())
+    assert ((dw.double() - want).abs() <= bound)[~over].all()
