@@ -506,7 +506,7 @@ __global__ __launch_bounds__(64 * NW) void dz_kernel(const T* __restrict__ dy, i
                                                 int32_t* __restrict__ clear, const int32_t* __restrict__ dz_exp,
                                                 uint16_t* __restrict__ dz_half, int64_t w8) {
   __shared__ float sums[NW - 1][64][9];
-  if (clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *clear = 0;
+  if (clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) clear[0] = clear[1] = 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t(blockIdx.x) * 64 + lane) * 8;
   const int64_t left = d - c;
@@ -580,15 +580,14 @@ bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
 //   sum of up to GEMM_MAX_K terms passes 2^127.
 constexpr float SPLIT_MAX = 0x1p50f;
 template <class T>
-__device__ __forceinline__ void split_store(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag);
+__device__ __forceinline__ void split_store(uint16_t* o, int64_t w8, float (&v)[8], bool& bad);
 template <>
-__device__ __forceinline__ void split_store<uint16_t>(uint16_t* o, int64_t, float (&v)[8], int32_t*) {
+__device__ __forceinline__ void split_store<uint16_t>(uint16_t* o, int64_t, float (&v)[8], bool&) {
   st8(o, 8, v);
 }
 template <>
-__device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, float (&v)[8], int32_t* flag) {
+__device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, float (&v)[8], bool& bad) {
   float h[8], m[8];
-  bool bad = false;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     bad |= !(fabsf(v[e]) <= SPLIT_MAX);
@@ -600,7 +599,6 @@ __device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, floa
   st8(o, 8, h);
   st8(o + w8, 8, m);
   st8(o + 2 * w8, 8, v);
-  if (bad) *flag = 1;
 }
 // Up to three operands in one launch: a workgroup belongs to the job its index falls into.
 struct OperandJob {
@@ -609,6 +607,7 @@ struct OperandJob {
   uint16_t* out = nullptr;
   int64_t ld = 0, nb = 0, rows = 0, cols = 0, w8 = 0, blocks = 0;
   int planes = 1;                      // of bf16; 0: one of fp32
+  unsigned raises = 0;                 // the products that read it, bit i the one that flag[i] moves
   const int32_t* half_exp = nullptr;   // fp16 of the value times 2^-half_exp[column], not bf16
 };
 constexpr int JOB_ROWS = 4;   // rows of a thread
@@ -629,6 +628,7 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
   float scale[8] = {};
   if (j.half_exp != nullptr) scales8(j.half_exp + c, cnt, scale);
   float v[JOB_ROWS][8];
+  bool bad = false;
   auto load = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
     const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll
@@ -654,18 +654,21 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
     else if (j.half_exp != nullptr)
       st8_half(o, v[q4], scale);
     else if (j.exps != nullptr) {
-      split_store<uint16_t>(o, j.w8, v[q4], flag);
+      split_store<uint16_t>(o, j.w8, v[q4], bad);
       if (sizeof(T) == 4) {   // one exact piece, which meets three
-        bool bad = false;
 #pragma unroll
         for (int e = 0; e < 8; ++e) bad |= fabsf(v[q4][e]) > SPLIT_MAX;
-        if (bad) *flag = 1;
       }
-    } else
-      split_store<T>(o, j.w8, v[q4], flag);
+    } else {
+      split_store<T>(o, j.w8, v[q4], bad);
+    }
+  }
+  if (sizeof(T) == 4 && bad) {
+    if (j.raises & 1) flag[0] = 1;
+    if (j.raises & 2) flag[1] = 1;
   }
 }
-__global__ void clear_flag_kernel(int32_t* flag) { *flag = 0; }
+__global__ void clear_flag_kernel(int32_t* flag) { flag[0] = flag[1] = 0; }
 
 int64_t round8(int64_t v) { return (v + 7) & ~int64_t(7); }
 
@@ -683,7 +686,7 @@ struct Prepared {
 // Adds the operand to the jobs if it cannot be read where it lies.
 template <class T>
 Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t rows, int64_t cols, uint16_t* room,
-                      bool native, const int32_t* half_exp = nullptr) {
+                      bool native, unsigned raises, const int32_t* half_exp = nullptr) {
   const bool codes = o.exps != nullptr;
   if (native && !codes && o.vec && cols % 4 == 0) return {{static_cast<const uint16_t*>(o.p), 2 * o.ld, 0}, 1};
   if (sizeof(T) == 2 && !codes && half_exp == nullptr && o.vec && cols % 8 == 0)
@@ -699,6 +702,7 @@ Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t r
   j.w8 = round8(cols);
   j.planes = native ? 0 : sizeof(T) == 4 && !codes ? 3 : 1;
   j.half_exp = half_exp;
+  j.raises = raises;
   j.blocks = cdiv(cdiv(rows, JOB_ROWS) * (j.w8 / 8), LT);
   if (native) return {{room, 2 * j.w8, 0}, 1};
   return {{room, j.planes * j.w8, j.w8}, j.planes};
@@ -818,7 +822,7 @@ void set_out(Epilogue& ep, void* y, int64_t ldy) {
 
 // Workspace of the three products.
 struct LinearRoom {
-  int32_t* flag = nullptr;      // an fp32 operand holds an entry that must not be split
+  int32_t* flag = nullptr;      // an fp32 operand of y or dx, or of dW, holds an entry that must not be split
   float* partial = nullptr;     // split products
   float* sums = nullptr;        // db chunks
   uint16_t *a = nullptr, *b = nullptr, *c = nullptr;   // operands
@@ -836,7 +840,7 @@ LinearRoom forward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   if (large) part = std::max(part, gemm_bf16_workspace(n, dn, di, K_ROWS, K_ROWS, sizeof(T) == 4) / 4);
   r.partial = cv.take<float>(part);
   if (large) {
-    r.flag = cv.take<int32_t>(1);
+    r.flag = cv.take<int32_t>(2);
     if (sizeof(T) == 4 || di % 8 != 0) {
       r.a = cv.take<uint16_t>(operand_room<T>(n, di));
       r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
@@ -866,7 +870,7 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   r.partial = cv.take<float>(part);
   if (large || half_fits<T>(n, di, dn)) r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x
   if (large) {
-    r.flag = cv.take<int32_t>(1);
+    r.flag = cv.take<int32_t>(2);
     if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
     if (sizeof(T) == 4 || di % 8 != 0) r.b = cv.take<uint16_t>(operand_room<T>(dn, di));
   }
@@ -920,8 +924,8 @@ lrc_status linear_forward(hipStream_t st, const void* x, int64_t n, int64_t di, 
   }
   OperandJobs jobs;
   int count = 0;
-  const Prepared a = want_operand<T>(jobs, count, ox, n, di, room.a, native);
-  const Prepared b = want_operand<T>(jobs, count, ow, dn, di, room.b, native);
+  const Prepared a = want_operand<T>(jobs, count, ox, n, di, room.a, native, 1);
+  const Prepared b = want_operand<T>(jobs, count, ow, dn, di, room.b, native, 1);
   LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   GemmSegments seg = segments(a.planes, b.planes);
   if (native) seg.type = FP32;
@@ -1098,9 +1102,9 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   OperandJobs jobs;
   int count = 0;
   Prepared pg, pw, px;
-  if (fast_dx || (fast_dw && !half)) pg = want_operand<T>(jobs, count, og, n, dn, room.a, native);
-  if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b, native);
-  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, native, half ? room.x_exp : nullptr);
+  if (fast_dx || (fast_dw && !half)) pg = want_operand<T>(jobs, count, og, n, dn, room.a, native, 3);
+  if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b, native, 1);
+  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, native, 2, half ? room.x_exp : nullptr);
   LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   if (a.dx != nullptr) {
     Epilogue ep;
@@ -1120,6 +1124,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   const double bytes = e * (double(n) * dn + double(dn) * di) + double(n) * di * (held ? 1.0 : e);
   auto go = [&](auto tag) -> lrc_status {
     using TO = decltype(tag);
+    const int32_t* moved = flag ? flag + 1 : nullptr;
     Epilogue ep;
     set_out<TO>(ep, a.dW, a.lddw);
     if (fast_dw) {
@@ -1132,11 +1137,11 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
       } else if (native) {
         seg.type = FP32;
       }
-      LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n, seg, ep, room.partial, flag,
+      LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n, seg, ep, room.partial, moved,
                                              2.0 * double(n) * double(dn) * double(di), bytes)));
-      if (!flag) return LRC_OK;
+      if (!moved) return LRC_OK;
     }
-    const int32_t* only = fast_dw ? flag : nullptr;
+    const int32_t* only = fast_dw ? moved : nullptr;
     if (held)
       return product_any<T, TO, K_COLS, K_CODES>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, room.partial, only,
                                                     bytes);

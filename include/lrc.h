@@ -478,8 +478,9 @@ size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_
  * three more bits where the activation is GELU or SiLU (fp16, each channel of dz and x scaled
  * by a power of two over the tokens; what lies 2^40 below its channel's largest counts as zero;
  * with RELU and NONE dz is exact in bf16), and db sums the unrounded dz.
- * Sums fp32 in an order that depends on the sizes, the alignment and leading dims, not on which
- * outputs are asked for: a gradient alone has the bits of the joint call.
+ * Sums fp32 in an order that depends on what lrc_linear's depends on (of dx entries of dz and W
+ * count, of dW those of dz and x), not on which outputs are asked for: a gradient alone has the
+ * bits of the joint call.
  * n_tokens == 0 writes zeros to dW and db.  Sizes as lrc_linear.
  */
 lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,

@@ -102,3 +102,21 @@ def test_finite_fp32_entries_whose_product_with_a_checkpoint_overflows(lrc):
     assert torch.equal(dw[over], want.float()[over])
     bound = (n + 8) * 2 * U * (dy.double().abs().T.contiguous() @ held.double().abs())
     assert ((dw.double() - want).abs() <= bound)[~over].all()
+
+
+def test_an_infinity_moves_only_the_product_it_is_in(lrc):
+    """An infinity in x does not change dx, nor one in W dW, at sizes that split fp32 entries: each has the bits of
+    the call that asks for it alone."""
+    n, d_in, d_out = 6912, 1080, 1984
+    x, dy, w = normal(1, n, d_in), normal(2, n, d_out), normal(3, d_out, d_in)
+    clean = lrc.lrc_linear_backward(dy, x, w)
+    for where in ("x", "w"):
+        t = {"x": x.clone(), "w": w.clone()}
+        t[where][5, 7] = float("inf")
+        joint = lrc.lrc_linear_backward(dy, t["x"], t["w"])
+        kept = 1 if where == "x" else 2
+        assert torch.equal(joint[kept], clean[kept]), where
+        alone = lrc.lrc_linear_backward(dy, t["x"], t["w"], **{"need_dw" if where == "x" else "need_dx": False})
+        assert torch.equal(alone[kept], clean[kept]), where
+        other = joint[3 - kept]      # dW has an infinite column, dx one
+        assert not other[:, 7].isfinite().any() and other[:, :7].isfinite().all() and other[:, 8:].isfinite().all()
