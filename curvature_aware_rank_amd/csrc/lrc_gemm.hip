@@ -1,5 +1,5 @@
 // Matrix products on the matrix cores with a fused epilogue: the linear layer's forward, dx and dW
-// products of bf16, fp16 or fp32 operands, sums in fp32.
+// products of bf16 or fp32 operands, sums in fp32.
 //
 // An output tile of BM x BN belongs to one workgroup; its waves hold blocks of MF x MF
 // accumulators (16 x 16 x 32, 32 x 32 x 16 or, in fp32, 16 x 16 x 4 matrix instructions).  Both
@@ -15,7 +15,7 @@
 // What bounds it: large bf16 products the chip's power, which sets its clock (1.6 to 1.9 GHz), then
 // the matrix pipes (73 % of their cycles at 4096^3): 8192 x 4096 x 11008 forward 680 us in a
 // row of its own calls (1090 TFLOP/s; the vendor's library on the same box 690), 730 between other
-// kernels; dx 585-640, dW in bf16 605, in fp16 650-700; 4096^3 103 us (library 90).  fp32 split in
+// kernels; dx 590-640, dW 590-650 (twice where dz has two pieces); 4096^3 103 us (library 90).  fp32 split in
 // three: 8192 x 1024 x 4096 315-345 us (200 TFLOP/s of fp32 products, fp32 instructions reach 140).
 // fp32 tiles: 2048 x 2048 x 1024 68 us (126 TFLOP/s; library 65).  24 tokens x 11008 x 4096: 23 us
 // with the splits' sums, 3.9 TB/s of weight.
@@ -31,7 +31,6 @@ namespace gemm {
 
 constexpr int NXCD = 8;
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -175,9 +174,6 @@ struct Block<16> {
   static __device__ __forceinline__ acc_t mma(bf16x8 a, bf16x8 b, acc_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ acc_t mma_half(f16x8 a, f16x8 b, acc_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-  }
   // a lane's 16 bytes are four k steps; each instruction takes one of them from every lane
   static __device__ __forceinline__ acc_t mma_f32(f32x4 a, f32x4 b, acc_t c) {
 #pragma unroll
@@ -192,9 +188,6 @@ struct Block<32> {
   static __device__ __forceinline__ int row(int e, int lane) { return 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3); }
   static __device__ __forceinline__ acc_t mma(bf16x8 a, bf16x8 b, acc_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ acc_t mma_half(f16x8 a, f16x8 b, acc_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
 };
 
@@ -305,8 +298,6 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
       for (int j = 0; j < FN; ++j)
         if constexpr (EL == FP32)
           acc[i][j] = Blk::mma_f32(__builtin_bit_cast(f32x4, fa[i]), __builtin_bit_cast(f32x4, fb[j]), acc[i][j]);
-        else if constexpr (EL == FP16)
-          acc[i][j] = Blk::mma_half(__builtin_bit_cast(f16x8, fa[i]), __builtin_bit_cast(f16x8, fb[j]), acc[i][j]);
         else
           acc[i][j] = Blk::mma(fa[i], fb[j], acc[i][j]);
   };
@@ -662,9 +653,7 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   };
   using std::integral_constant;
   // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
-  if (seg.type == FP16) {
-    if constexpr (KA == K_COLS && KB == K_COLS) launch(std::false_type{}, integral_constant<Element, FP16>{});
-  } else if (seg.type == FP32) {
+  if (seg.type == FP32) {
     if constexpr (!std::is_same<TO, uint16_t>::value) launch(std::false_type{}, integral_constant<Element, FP32>{});
   } else if (std::is_same<TO, uint16_t>::value || seg.count == 1) {
     if constexpr (std::is_same<TO, uint16_t>::value || KA == K_COLS)

@@ -19,20 +19,6 @@ constexpr int LT = 256;
 
 __device__ __forceinline__ int64_t cdiv_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// eight fp32 values times their channels' scales (powers of two), as fp16
-__device__ __forceinline__ void st8_half(uint16_t* p, const float (&v)[8], const float (&scale)[8]) {
-  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-  f16x8 h;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = _Float16(v[i] * scale[i]);
-  *reinterpret_cast<f16x8*>(p) = h;
-}
-// 2^-e of eight channels' exponents, of which `cnt` exist
-__device__ __forceinline__ void scales8(const int32_t* p, int cnt, float (&scale)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) scale[i] = i < cnt ? pow2f(-p[i]) : 0.f;
-}
-
 struct Operand {
   const void* p;        // elements, or int8 codes (leading dim ld)
   int64_t ld;
@@ -369,13 +355,7 @@ lrc_status linear_rows(hipStream_t st, const Operand& x, const Operand& W, int64
   return LRC_OK;
 }
 
-// ---- column exponents ------------------------------------------------------------------
-// The dW of a bf16 layer whose activation has a smooth slope takes dz in fp16, not in the bf16 of
-// the stream: three more bits, so that dW carries no more than its own rounding (with the
-// stream's bf16 its error was 1.3 to 1.55 times that), at the same matrix rate.  fp16 has little
-// range, so each channel of dz and of x is first scaled by a power of two to a largest magnitude
-// near 2^15, and dW's rows and columns are scaled back.  A value more than 2^29 below its
-// channel's largest loses bits, one more than 2^40 below counts as zero.
+// ---- chunks of tokens ---------------------------------------------------------------------
 struct ColPlan {
   int64_t rows, chunks;   // tokens per chunk
 };
@@ -390,121 +370,24 @@ ColPlan col_plan(int64_t n, int64_t d) {
   return p;
 }
 
-struct MagnitudeJob {
-  const void* p = nullptr;        // bf16 rows, or
-  const int8_t* exps = nullptr;   // the exponents of a checkpoint, ld blocks a row
-  int64_t ld = 0, cols = 0, blocks = 0;
-  uint32_t* part = nullptr;       // [chunks][cols]
-  int32_t* out = nullptr;
-  int act = LRC_ACT_NONE;         // p is dy, the magnitudes are those of dy act'(z):
-  const uint16_t* z = nullptr;    // z in full, or
-  const int8_t *zcodes = nullptr, *zexps = nullptr;
-  int64_t ldz = 0;
-};
-struct MagnitudeJobs {
-  MagnitudeJob job[2];
-};
-// exponent that brings a channel's largest magnitude into [2^14, 2^15); 0 for a channel of zeros,
-// and -126 at least, so that its power of two is a normal number
-__device__ __forceinline__ int channel_exponent(uint32_t bits) {
-  int e = 0;
-  const float f = frexpf(__uint_as_float(bits), &e);   // in [1/2, 1)
-  return f > 0.f ? max(e - 15, -126) : 0;
-}
-// largest finite magnitude (as bits) of every channel over a chunk of tokens; the exponent itself
-// where there is one chunk
-template <int NW>
-__global__ __launch_bounds__(64 * NW) void magnitude_kernel(MagnitudeJobs jobs, int64_t n, int64_t rows) {
-  __shared__ uint32_t most[NW - 1][64][9];
-  const int q = int64_t(blockIdx.x) < jobs.job[0].blocks ? 0 : 1;
-  const MagnitudeJob& j = jobs.job[q];
-  const int64_t block = int64_t(blockIdx.x) - (q ? jobs.job[0].blocks : 0);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (block * 64 + lane) * 8;
-  const int64_t left = j.cols - c;
-  const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
-  const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
-  uint32_t m[8] = {};
-  auto run = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
-    const int len = decltype(whole)::value ? 8 : cnt;
-#pragma unroll 4
-    for (int64_t t = t0 + wave; t < t1; t += NW) {
-      if (j.exps != nullptr) {
-        const uint32_t u = __float_as_uint(127.f * pow2f(j.exps[t * j.ld + (c >> 6)]));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = max(m[e], u);
-      } else {
-        float v[8];
-        ld8(static_cast<const uint16_t*>(j.p) + t * j.ld + c, len, v);
-        if (j.act != LRC_ACT_NONE) {
-          float zv[8];
-          if (j.z != nullptr)
-            ld8(j.z + t * j.ldz + c, len, zv);
-          else
-            ld8_codes(j.zcodes + t * j.cols + c, len, pow2f(j.zexps[t * j.ldz + (c >> 6)]), zv);
-          slope_apply(j.act, zv, v);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = max(m[e], __float_as_uint(finite_mag(v[e])));
-      }
-    }
-  };
-  if (cnt >= 8)
-    run(std::true_type{});
-  else if (cnt > 0)
-    run(std::false_type{});
-  if (wave > 0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) most[wave - 1][lane][e] = m[e];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < cnt) {
-      uint32_t u = m[e];
-#pragma unroll
-      for (int w = 0; w < NW - 1; ++w) u = max(u, most[w][lane][e]);
-      if (gridDim.y == 1)
-        j.out[c + e] = channel_exponent(u);
-      else
-        j.part[int64_t(blockIdx.y) * j.cols + c + e] = u;
-    }
-}
-__global__ __launch_bounds__(LT) void exponent_kernel(MagnitudeJobs jobs, int64_t chunks) {
-  __shared__ uint32_t acc[8][33];
-  const int q = int64_t(blockIdx.x) < cdiv_dev(jobs.job[0].cols, 32) ? 0 : 1;
-  const MagnitudeJob& j = jobs.job[q];
-  const int64_t block = int64_t(blockIdx.x) - (q ? cdiv_dev(jobs.job[0].cols, 32) : 0);
-  const int cx = threadIdx.x & 31, sl = threadIdx.x >> 5;
-  const int64_t c = block * 32 + cx;
-  uint32_t m = 0;
-  if (c < j.cols) {
-#pragma unroll 8
-    for (int64_t p = sl; p < chunks; p += 8) m = max(m, j.part[p * j.cols + c]);
-  }
-  acc[sl][cx] = m;
-  __syncthreads();
-  if (sl > 0 || c >= j.cols) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max(m, acc[i][cx]);
-  j.out[c] = channel_exponent(m);
-}
-
 // ---- dz = dy act'(z), and the chunk sums of db ------------------------------------------
-// Bound by memory: dy and z read, dz written once, and once more in fp16 for dW (8192 x 11008 from
-// codes 150 us, 4.2 TB/s; the magnitudes before it 87 us, 3.1 TB/s, about even with their slopes'
-// arithmetic).  A lane takes eight consecutive channels,
-// the workgroup's waves take the chunk's tokens in turn; db's share of the chunk is the
-// waves' sums added in order.
+// Bound by memory: dy and z read, dz written, and its lower piece (8192 x 11008 from codes 139 us,
+// 4.5 TB/s).  A lane takes eight consecutive channels, the workgroup's waves take the chunk's tokens
+// in turn; db's share of the chunk is the waves' sums added in order.
+//
+// The dW of a bf16 layer whose activation has a smooth slope takes dz in two bf16 pieces, the stream
+// and `low`, what the stream's rounding left out (rows of w8): 16 bits, so that dW carries no more
+// than its own rounding (with the stream alone its error was 1.3 to 1.55 times that), for a second
+// product (650 us at 8192 x 4096 x 11008).  Both pieces have the range of fp32, so a token that counts
+// for nothing may hold any finite value on the side that meets zeros.
 template <class T, bool CK, int NW>
 __global__ __launch_bounds__(64 * NW) void dz_kernel(const T* __restrict__ dy, int64_t lddy, int64_t n, int64_t d,
                                                 const T* __restrict__ z, int64_t ldz,
                                                 const int8_t* __restrict__ codes, const int8_t* __restrict__ exps,
                                                 int64_t nb, int act, T* __restrict__ dz, int64_t lddz, int64_t rows,
                                                 float* __restrict__ partial,
-                                                int32_t* __restrict__ clear, const int32_t* __restrict__ dz_exp,
-                                                uint16_t* __restrict__ dz_half, int64_t w8) {
+                                                int32_t* __restrict__ clear, uint16_t* __restrict__ low,
+                                                int64_t w8) {
   __shared__ float sums[NW - 1][64][9];
   if (clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) clear[0] = clear[1] = 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -513,8 +396,6 @@ __global__ __launch_bounds__(64 * NW) void dz_kernel(const T* __restrict__ dy, i
   const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
   const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
   float s[8] = {};
-  float scale[8] = {};
-  if (dz_half != nullptr && cnt > 0) scales8(dz_exp + c, cnt, scale);
   auto run = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
     const int len = decltype(whole)::value ? 8 : cnt;
 #pragma unroll 2
@@ -529,7 +410,15 @@ __global__ __launch_bounds__(64 * NW) void dz_kernel(const T* __restrict__ dy, i
           ld8(z + t * ldz + c, len, zv);
         slope_apply(act, zv, g);
         st8(dz + t * lddz + c, len, g);
-        if (dz_half != nullptr) st8_half(dz_half + t * w8 + c, g, scale);   // zeros behind the last channel
+        if (low != nullptr) {   // zeros behind the last channel, and where the stream is not finite
+          float r[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float h = round_to(g[e], static_cast<const uint16_t*>(nullptr));
+            r[e] = finite_f(h) ? g[e] - h : 0.f;
+          }
+          st8(low + t * w8 + c, 8, r);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] += g[e];
@@ -608,7 +497,6 @@ struct OperandJob {
   int64_t ld = 0, nb = 0, rows = 0, cols = 0, w8 = 0, blocks = 0;
   int planes = 1;                      // of bf16; 0: one of fp32
   unsigned raises = 0;                 // the products that read it, bit i the one that flag[i] moves
-  const int32_t* half_exp = nullptr;   // fp16 of the value times 2^-half_exp[column], not bf16
 };
 constexpr int JOB_ROWS = 4;   // rows of a thread
 struct OperandJobs {
@@ -625,8 +513,6 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
   const int64_t r0 = i / per * JOB_ROWS, c = i % per * 8;
   if (r0 >= j.rows) return;
   const int cnt = int(j.cols - c > 8 ? 8 : j.cols - c);
-  float scale[8] = {};
-  if (j.half_exp != nullptr) scales8(j.half_exp + c, cnt, scale);
   float v[JOB_ROWS][8];
   bool bad = false;
   auto load = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
@@ -651,8 +537,6 @@ __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* 
     uint16_t* o = j.out + r * j.planes * j.w8 + c;
     if (j.planes == 0)
       st8(reinterpret_cast<float*>(j.out) + r * j.w8 + c, 8, v[q4]);
-    else if (j.half_exp != nullptr)
-      st8_half(o, v[q4], scale);
     else if (j.exps != nullptr) {
       split_store<uint16_t>(o, j.w8, v[q4], bad);
       if (sizeof(T) == 4) {   // one exact piece, which meets three
@@ -686,10 +570,10 @@ struct Prepared {
 // Adds the operand to the jobs if it cannot be read where it lies.
 template <class T>
 Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t rows, int64_t cols, uint16_t* room,
-                      bool native, unsigned raises, const int32_t* half_exp = nullptr) {
-  const bool codes = o.exps != nullptr;
-  if (native && !codes && o.vec && cols % 4 == 0) return {{static_cast<const uint16_t*>(o.p), 2 * o.ld, 0}, 1};
-  if (sizeof(T) == 2 && !codes && half_exp == nullptr && o.vec && cols % 8 == 0)
+                      bool native, unsigned raises) {
+  const bool codes = o.exps != nullptr, there = !codes && o.vec && o.ld <= GEMM_MAX_LD;
+  if (native && there && cols % 4 == 0) return {{static_cast<const uint16_t*>(o.p), 2 * o.ld, 0}, 1};
+  if (sizeof(T) == 2 && there && cols % 8 == 0)
     return {{static_cast<const uint16_t*>(o.p), o.ld, 0}, 1};
   OperandJob& j = jobs.job[count++];
   j.p = o.p;
@@ -701,7 +585,6 @@ Prepared want_operand(OperandJobs& jobs, int& count, const Operand& o, int64_t r
   j.cols = cols;
   j.w8 = round8(cols);
   j.planes = native ? 0 : sizeof(T) == 4 && !codes ? 3 : 1;
-  j.half_exp = half_exp;
   j.raises = raises;
   j.blocks = cdiv(cdiv(rows, JOB_ROWS) * (j.w8 / 8), LT);
   if (native) return {{room, 2 * j.w8, 0}, 1};
@@ -787,12 +670,6 @@ bool gemm_fits(int64_t rows_a, int64_t rows_b) {   // row lengths of the two ope
   return std::max(round8(rows_a), round8(rows_b)) * (sizeof(T) == 4 ? 3 : 1) <= GEMM_MAX_LD;
 }
 
-// whether dW can take fp16 operands: a bf16 layer of any size the tiles' offsets reach
-template <class T>
-bool half_fits(int64_t n, int64_t di, int64_t dn) {
-  return sizeof(T) == 2 && n <= GEMM_MAX_K && gemm_fits<T>(di, dn);
-}
-
 template <class T, class TO, int KA, int KB>
 lrc_status product_any(hipStream_t st, const char* name, const Operand& A, const Operand& B, int64_t M, int64_t N,
                        int64_t K, const Epilogue& ep, float* partial, const int32_t* only, double bytes) {
@@ -826,9 +703,7 @@ struct LinearRoom {
   float* partial = nullptr;     // split products
   float* sums = nullptr;        // db chunks
   uint16_t *a = nullptr, *b = nullptr, *c = nullptr;   // operands
-  uint16_t* dz_half = nullptr;  // fp16 dz, its channels' and x's exponents, their chunks' magnitudes
-  int32_t *dz_exp = nullptr, *x_exp = nullptr;
-  uint32_t *dz_mag = nullptr, *x_mag = nullptr;
+  uint16_t* low = nullptr;      // lower piece of a bf16 dz
   size_t bytes = 0;
 };
 template <class T>
@@ -859,16 +734,9 @@ LinearRoom backward_room(void* ws, int64_t n, int64_t di, int64_t dn) {
   if (large)
     part = std::max({part, gemm_bf16_workspace(n, di, dn, K_ROWS, K_COLS, sizeof(T) == 4) / 4,
                      gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS, sizeof(T) == 4) / 4});
-  if (half_fits<T>(n, di, dn)) {
-    part = std::max(part, gemm_bf16_workspace(dn, di, n, K_COLS, K_COLS, false) / 4);
-    r.dz_half = cv.take<uint16_t>(size_t(n) * round8(dn));
-    r.dz_exp = cv.take<int32_t>(dn);
-    r.x_exp = cv.take<int32_t>(di);
-    r.dz_mag = cv.take<uint32_t>(size_t(col_plan(n, std::max(di, dn)).chunks) * dn);
-    r.x_mag = cv.take<uint32_t>(size_t(col_plan(n, std::max(di, dn)).chunks) * di);
-  }
+  if (sizeof(T) == 2) r.low = cv.take<uint16_t>(operand_room<T>(n, dn));
   r.partial = cv.take<float>(part);
-  if (large || half_fits<T>(n, di, dn)) r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x
+  if (large) r.c = cv.take<uint16_t>(operand_room<T>(n, di));   // x
   if (large) {
     r.flag = cv.take<int32_t>(2);
     if (sizeof(T) == 4 || dn % 8 != 0) r.a = cv.take<uint16_t>(operand_room<T>(n, dn));
@@ -1016,8 +884,8 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   bool fast_dx = fast_g && a.dx != nullptr && has_room<T>(ow, di) && a.ldw <= GEMM_MAX_LD &&
                        (w_in_place || n > 64);
   // a slope that is neither 0 nor 1 leaves bits in dz that the stream's bf16 does not hold
-  const bool half = with_dz && a.act != LRC_ACT_RELU && a.dW != nullptr && half_fits<T>(n, di, dn);
-  bool fast_dw = half || (fast_g && a.dW != nullptr && (held || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD)));
+  const bool low = sizeof(T) == 2 && with_dz && a.act != LRC_ACT_RELU && a.dW != nullptr;
+  bool fast_dw = fast_g && a.dW != nullptr && (held || low || (has_room<T>(ox, di) && a.ldx <= GEMM_MAX_LD));
   F32Way way = SPLIT;
   if (sizeof(T) == 4 && (fast_dx || fast_dw)) {
     // one way for both products, whether both are wanted or not: a gradient's bits do not depend on
@@ -1032,41 +900,8 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   }
   const bool native = way == NATIVE;
   int32_t* flag = sizeof(T) == 4 && !native && (fast_dx || fast_dw) ? room.flag : nullptr;
-  if (half) {
-    const ColPlan p = col_plan(n, std::max(di, dn));
-    MagnitudeJobs m;
-    m.job[0].p = a.dy;
-    m.job[0].ld = a.lddy;
-    m.job[0].cols = dn;
-    m.job[0].part = room.dz_mag;
-    m.job[0].out = room.dz_exp;
-    m.job[0].act = a.act;
-    m.job[0].z = static_cast<const uint16_t*>(a.z);
-    m.job[0].zcodes = a.zcodes;
-    m.job[0].zexps = a.zexps;
-    m.job[0].ldz = a.z != nullptr ? a.ldz : cdiv(dn, CKB);
-    m.job[1].p = a.x;
-    m.job[1].exps = held ? a.xexps : nullptr;
-    m.job[1].ld = held ? cdiv(di, CKB) : a.ldx;
-    m.job[1].cols = di;
-    m.job[1].part = room.x_mag;
-    m.job[1].out = room.x_exp;
-    for (MagnitudeJob& j : m.job) j.blocks = cdiv(j.cols, 512);
-    ProfScope scope("magnitude_kernel", st, 0.0, double(n) * ((a.z ? 4.0 : 3.0) * double(dn) + (held ? double(di) / 64 : 2.0 * di)));
-    const dim3 grid(unsigned(m.job[0].blocks + m.job[1].blocks), unsigned(p.chunks));
-    if (p.chunks == 1)
-      magnitude_kernel<16><<<grid, 1024, 0, st>>>(m, n, p.rows);
-    else
-      magnitude_kernel<4><<<grid, 256, 0, st>>>(m, n, p.rows);
-    LRC_LAUNCHED();
-    if (p.chunks > 1) {
-      exponent_kernel<<<unsigned(cdiv(dn, 32) + cdiv(di, 32)), LT, 0, st>>>(m, p.chunks);
-      LRC_LAUNCHED();
-    }
-  }
   if (with_dz || a.db != nullptr) {
     const ColPlan p = col_plan(n, dn);
-    uint16_t* dz_half = half ? room.dz_half : nullptr;
     {
       ProfScope scope("dz_kernel", st, 0.0, double(n) * dn * sizeof(T) * (a.act != LRC_ACT_NONE ? 3 : 1));
       const dim3 grid(unsigned(cdiv(dn, 512)), unsigned(p.chunks));
@@ -1079,7 +914,7 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
         constexpr bool CK = decltype(held_z)::value;
         constexpr int NW = decltype(waves)::value;
         dz_kernel<T, CK, NW><<<grid, 64 * NW, 0, st>>>(dy, a.lddy, n, dn, z, a.ldz, a.zcodes, a.zexps, nb, a.act, dz,
-                                                       a.lddz, p.rows, part, flag, room.dz_exp, dz_half, w8);
+                                                       a.lddz, p.rows, part, flag, low ? room.low : nullptr, w8);
       };
       using std::integral_constant;
       if (codes && p.chunks == 1)
@@ -1102,9 +937,9 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   OperandJobs jobs;
   int count = 0;
   Prepared pg, pw, px;
-  if (fast_dx || (fast_dw && !half)) pg = want_operand<T>(jobs, count, og, n, dn, room.a, native, 3);
+  if (fast_dx || fast_dw) pg = want_operand<T>(jobs, count, og, n, dn, room.a, native, 3);
   if (fast_dx) pw = want_operand<T>(jobs, count, ow, dn, di, room.b, native, 1);
-  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, native, 2, half ? room.x_exp : nullptr);
+  if (fast_dw) px = want_operand<T>(jobs, count, ox, n, di, room.c, native, 2);
   LRC_TRY(prepare_operands<T>(st, jobs, count, room.flag));
   if (a.dx != nullptr) {
     Epilogue ep;
@@ -1127,26 +962,37 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
     const int32_t* moved = flag ? flag + 1 : nullptr;
     Epilogue ep;
     set_out<TO>(ep, a.dW, a.lddw);
+    auto any = [&](const Operand& g8, const Epilogue& e8, const int32_t* only) -> lrc_status {
+      if (held)
+        return product_any<T, TO, K_COLS, K_CODES>(st, "linear_dw_any_kernel", g8, ox, dn, di, n, e8, room.partial, only,
+                                                   bytes);
+      return product_any<T, TO, K_COLS, K_COLS>(st, "linear_dw_any_kernel", g8, ox, dn, di, n, e8, room.partial, only,
+                                                bytes);
+    };
+    auto fast = [&](const GemmOperand& g8, const GemmSegments& seg, const Epilogue& e8) -> lrc_status {
+      return gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", g8, px.op, dn, di, n, seg, e8, room.partial, moved,
+                                           2.0 * double(n) * double(dn) * double(di), bytes);
+    };
+    // dW = low^T x first, then dz^T x on top of it.  Where the first is not finite, an entry of x is
+    // not, or the second overflows by itself: its infinity or NaN is the result.
+    if (low) {
+      const int64_t w8 = round8(dn);
+      Epilogue first = ep;
+      first.finite = true;
+      if (fast_dw)
+        LRC_TRY(fast({room.low, w8, 0}, GemmSegments{}, first));
+      else
+        LRC_TRY(any(plain<T>(room.low, w8), first, nullptr));
+      ep.res = a.dW;
+      ep.ldr = a.lddw;
+    }
     if (fast_dw) {
-      GemmSegments seg = half ? GemmSegments{} : segments(pg.planes, px.planes);
-      if (half) {
-        seg.type = FP16;
-        ep.row_exp = room.dz_exp;
-        ep.col_exp = room.x_exp;
-        pg.op = {room.dz_half, round8(dn), 0};
-      } else if (native) {
-        seg.type = FP32;
-      }
-      LRC_TRY((gemm_bf16<TO, K_COLS, K_COLS>(st, "linear_dw_kernel", pg.op, px.op, dn, di, n, seg, ep, room.partial, moved,
-                                             2.0 * double(n) * double(dn) * double(di), bytes)));
+      GemmSegments seg = segments(pg.planes, px.planes);
+      if (native) seg.type = FP32;
+      LRC_TRY(fast(pg.op, seg, ep));
       if (!moved) return LRC_OK;
     }
-    const int32_t* only = fast_dw ? moved : nullptr;
-    if (held)
-      return product_any<T, TO, K_COLS, K_CODES>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, room.partial, only,
-                                                    bytes);
-    return product_any<T, TO, K_COLS, K_COLS>(st, "linear_dw_any_kernel", og, ox, dn, di, n, ep, room.partial, only,
-                                                    bytes);
+    return any(og, ep, fast_dw ? moved : nullptr);
   };
   if (a.dw_dt == LRC_F32) return go(float{});
   return go(uint16_t{});

@@ -268,7 +268,7 @@ struct Epilogue {
   int8_t* exps = nullptr;
   int64_t nb = 0;
   int32_t* info = nullptr;
-  const int32_t *row_exp = nullptr, *col_exp = nullptr;   // D[m][n] is 2^(row_exp[m] + col_exp[n]) times the sum
+  bool finite = false;   // a sum that is not finite counts as zero
 };
 
 // the bias of eight consecutive columns, of which `cnt` exist
@@ -283,10 +283,9 @@ __device__ __forceinline__ void finish8(const Epilogue& ep, int64_t row, int64_t
                                         float (&v)[8], int lane, bool& bad) {
   float r[8];
   if (ep.res != nullptr) ld8(static_cast<const TO*>(ep.res) + row * ep.ldr + col, cnt, r);
-  if (ep.row_exp != nullptr && cnt > 0) {
-    const int re = ep.row_exp[row];
+  if (ep.finite) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < cnt ? ldexpf(v[e], re + ep.col_exp[col + e]) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = finite_f(v[e]) ? v[e] : 0.f;
   }
   if (ep.bias != nullptr) {
 #pragma unroll
@@ -313,10 +312,9 @@ struct GemmOperand {
 // The reduction may run over several pairs of planes, one after the other: segment s
 // multiplies plane (pa >> 2 s) & 3 of A with plane (pb >> 2 s) & 3 of B.
 //
-// What the operands' elements are (fp16: K_COLS x K_COLS only; fp16 and fp32: one plane).  fp32
-// operands are addressed in 16-bit halves as the others are: ld and plane count halves, rows are
-// whole pieces of four.
-enum Element { BF16, FP16, FP32 };
+// What the operands' elements are (fp32: one plane).  fp32 operands are addressed in 16-bit halves as
+// the others are: ld and plane count halves, rows are whole pieces of four.
+enum Element { BF16, FP32 };
 struct GemmSegments {
   int count = 1;
   uint32_t pa = 0, pb = 0;

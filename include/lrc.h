@@ -474,10 +474,10 @@ size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_
  * leading dim lddz) is written; with LRC_ACT_NONE dz is dy and the argument is ignored.
  * relu'(0) = 0.  dx: n_tokens x d_in (leading dim lddx); dW: d_out x d_in (leading dim
  * lddw), dtype dw_dt (LRC_F32, or `dt`); db: float[d_out]; any of the three may be NULL.
- * With dtype bf16, dx is a product of the rounded dz, as the stream holds it; dW takes dz with
- * three more bits where the activation is GELU or SiLU (fp16, each channel of dz and x scaled
- * by a power of two over the tokens; what lies 2^40 below its channel's largest counts as zero;
- * with RELU and NONE dz is exact in bf16), and db sums the unrounded dz.
+ * With dtype bf16, dx is a product of the rounded dz, as the stream holds it; dW takes dz to 16
+ * bits where the activation is GELU or SiLU (the stream and what its rounding left out, two
+ * products; with RELU and NONE dz is exact in bf16), and db sums the unrounded dz.  Tokens that
+ * count for nothing may hold any finite value on the side that meets zeros.
  * Sums fp32 in an order that depends on what lrc_linear's depends on (of dx entries of dz and W
  * count, of dW those of dz and x), not on which outputs are asked for: a gradient alone has the
  * bits of the joint call.

@@ -120,3 +120,49 @@ def test_an_infinity_moves_only_the_product_it_is_in(lrc):
         assert torch.equal(alone[kept], clean[kept]), where
         other = joint[3 - kept]      # dW has an infinite column, dx one
         assert not other[:, 7].isfinite().any() and other[:, :7].isfinite().all() and other[:, 8:].isfinite().all()
+
+
+# ----------------------------------------------------------------------------- entries that meet only zeros
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("n,d_in,d_out", [(5, 17, 9), (300, 136, 264), (1000, 521, 303), (2500, 1032, 2056)])
+@pytest.mark.parametrize("held", [False, True])
+def test_weight_gradient_with_values_in_masked_tokens(lrc, act, n, d_in, d_out, held):
+    """Tokens that count for nothing hold large values on one side and zeros on the other: the type's lowest value in
+    x where dy is zero, 1e30 in dy where x is zero, and 1e30 in single entries that meet a zero channel of x.  dW is
+    as accurate as without them: to 2^-11 of its terms' magnitudes, element by element."""
+    x, dy, z = normal(1, n, d_in).bfloat16(), normal(2, n, d_out).bfloat16(), normal(3, n, d_out).bfloat16()
+    dy[1], x[1] = 0, BF16_LOWEST
+    x[3], dy[3] = 0, 1e30
+    if n > 100:
+        dy[70::64], x[70::64] = 0, -BF16_LOWEST
+        x[101::64], dy[101::64] = 0, -1e30
+        x[:-20, 5:9], dy[:-20, 3] = 0, 1e30     # channels of x that only the last tokens feed
+    w = torch.zeros(d_out, d_in, dtype=torch.bfloat16, device=dev())
+    xa, xn = x, f64(x)
+    if held:
+        xa = lrc.lrc_pack_activations(x)[:2]
+        xn = ref.unpack(xa[0].cpu().numpy(), xa[1].cpu().numpy())
+    _, _, dw, _ = lrc.lrc_linear_backward(dy, xa, w, act=act, z=z, dw_dtype=torch.float32)
+    dz = f64(dy) * ref.act_slope(f64(z), act)
+    terms, got = np.abs(dz).T @ np.abs(xn), f64(dw)
+    beyond = terms > 1e60      # 1e30 meets the lowest value: 3e68, which no fp32 number is near
+    assert not beyond[:3].any() and not beyond[4:].any() and not np.isfinite(got[beyond]).any()
+    assert (np.abs(got - dz.T @ xn) <= 2.0 ** -11 * terms)[~beyond].all()
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_weight_gradient_with_an_infinite_activation(lrc, act):
+    """An infinity or NaN in x gives its channel of dW what arithmetic gives, whatever the sign of dz's lower bits, and
+    leaves the other channels' bits as they are."""
+    n, d_in, d_out = 700, 264, 392
+    x, dy, z = normal(1, n, d_in).bfloat16(), normal(2, n, d_out).bfloat16(), normal(3, n, d_out).bfloat16()
+    w = torch.zeros(d_out, d_in, dtype=torch.bfloat16, device=dev())
+    clean = lrc.lrc_linear_backward(dy, x, w, act=act, z=z)[2]
+    bad = x.clone()
+    bad[6, 40], bad[9, 41], bad[12, 42] = float("inf"), float("-inf"), float("nan")
+    dw = lrc.lrc_linear_backward(dy, bad, w, act=act, z=z)[2]
+    dz = torch.from_numpy(f64(dy) * ref.act_slope(f64(z), act)).to(dev())
+    want = dz.T.contiguous()[:, [6, 9, 12]].sign() * torch.tensor([math.inf, -math.inf, math.nan], device=dev())
+    assert torch.equal(torch.nan_to_num(dw[:, 40:43].double(), 9e9, 8e8, 7e7), torch.nan_to_num(want, 9e9, 8e8, 7e7))
+    keep = [c for c in range(d_in) if not 40 <= c < 43]
+    assert torch.equal(dw[:, keep], clean[:, keep])
