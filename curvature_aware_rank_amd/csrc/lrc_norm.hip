@@ -34,6 +34,12 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// The mean from the sum of x_j / 2 d, which no finite token overflows; it ends at the largest number.
+__device__ __forceinline__ float mean_of(float half) {
+  const float m = 2.f * half;
+  return finite_f(half) ? fminf(fmaxf(m, -3.402823466e38f), 3.402823466e38f) : m;
+}
+
 // ---- any width: one workgroup per token, three passes over the row --------------------
 template <class T>
 __global__ __launch_bounds__(NT) void ln_fwd_rows_kernel(const T* __restrict__ x, int64_t ldx, int d,
@@ -47,8 +53,9 @@ __global__ __launch_bounds__(NT) void ln_fwd_rows_kernel(const T* __restrict__ x
   const int64_t t = blockIdx.x;
   const T* row = x + t * ldx;
   float s = 0.f;
-  for (int j = threadIdx.x; j < d; j += NT) s += ld_elem(row + j);
-  const float mu = block_sum(s, red) / float(d);
+  const float half = 0.5f / float(d);
+  for (int j = threadIdx.x; j < d; j += NT) s = fmaf(ld_elem(row + j), half, s);
+  const float mu = mean_of(block_sum(s, red));
   float q = 0.f;
   for (int j = threadIdx.x; j < d; j += NT) {
     const float c = ld_elem(row + j) - mu;
@@ -287,9 +294,9 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
     raw.load(x + (t + step) * ldx, d, l, t + step < n);
     float s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < E; ++i) s[0] += v[i];
+    for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], 0.5f * inv_d, s[0]);
     row_sums<WPR, 1>(s, red[0], wave, lane, group);
-    const float mu = s[0] * inv_d;
+    const float mu = mean_of(s[0]);
     if (codes != nullptr) {   // before v is centred
 #pragma unroll
       for (int k = 0; k < V; ++k) {

@@ -412,7 +412,9 @@ lrc_status lrc_unpack_activations(const int8_t* codes, const int8_t* exps, int64
  * NULL for 1 and 0.  eps >= 0.  mean, rstd: float[n_tokens] (written; lrc_layer_norm_backward
  * takes them).  codes, exps: both given or both NULL; when given they receive the checkpoint
  * of x, the same bits as lrc_pack_activations of x, and `info` is used as there (NULL for
- * no check).  Statistics are fp32 over values centred first (two passes over registers).
+ * no check).  Statistics are fp32 over values centred first (two passes over registers).  A token
+ * of finite values has a finite mean; where the square of its spread passes the range of fp32,
+ * rstd is 0 and y is beta.
  * 1 <= d <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
  */
 lrc_status lrc_layer_norm(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t ldx,

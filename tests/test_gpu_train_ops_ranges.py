@@ -166,3 +166,31 @@ def test_weight_gradient_with_an_infinite_activation(lrc, act):
     assert torch.equal(torch.nan_to_num(dw[:, 40:43].double(), 9e9, 8e8, 7e7), torch.nan_to_num(want, 9e9, 8e8, 7e7))
     keep = [c for c in range(d_in) if not 40 <= c < 43]
     assert torch.equal(dw[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [2, 65, 512, 1000, 2048, 4096, 11008, 16384, 20000])
+def test_layer_norm_of_tokens_of_the_lowest_value(lrc, dtype, d):
+    """Tokens that a mask filled with the type's lowest (or largest) value: their mean is that value, not an infinity,
+    y is beta, the checkpoint is that of the tokens, and in the backward pass a dy of zeros there leaves the gradients'
+    sums as they are without those tokens."""
+    n = 12
+    x, dy = normal(1, n, d).to(dtype), normal(2, n, d).to(dtype)
+    gamma, beta = 1 + 0.1 * normal(3, d), normal(4, d)
+    low = float(torch.finfo(dtype).min)
+    x[3], x[7] = low, -low
+    dy[3], dy[7] = 0, 0
+    y, mean, rstd, kept, info = lrc.lrc_layer_norm(x, gamma, beta, checkpoint=True)
+    assert torch.equal(y[[3, 7]], beta.to(dtype).expand(2, d)) and int(info.cpu()) == 0
+    # a sum of d terms over per-thread runs and a tree (at most d / 64 + 24 deep), and 1 / d to half a step
+    off = (mean[[3, 7]].double() - torch.tensor([low, -low], device=dev(), dtype=torch.float64)).abs() / -low
+    assert (off <= (d / 64 + 26) * U).all() and rstd.isfinite().all()
+    dx, dgamma, dbeta = lrc.lrc_layer_norm_backward(dy, x, mean, rstd, gamma)
+    assert not dx[[3, 7]].any()
+    xh = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    rows = [t for t in range(n) if t not in (3, 7)]
+    want, terms = (dy.double() * xh)[rows].sum(0), (dy.double() * xh).abs()[rows].sum(0)
+    # the sum, and xh's two roundings around the centred value
+    slack = ((x.double().abs() + mean.double().abs()[:, None]) * rstd.double()[:, None] * dy.double().abs())[rows].sum(0)
+    assert ((dgamma.double() - want).abs() <= (n + 8) * U * terms + 2 * U * slack).all()
+    assert ((dbeta.double() - dy.double().sum(0)).abs() <= (n + 8) * U * dy.double().abs().sum(0)).all()
