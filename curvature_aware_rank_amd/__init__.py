@@ -571,7 +571,7 @@ def _pieces(t, ld, work):
     bytes keeps the product off the direct loads; from 2^30 multiplications on a copy costs less
     (2048 x 4096 x 4096 373 us against 74 with the copy, 65 x 4096 x 4096 35 against 22; below, 256
     x 1024 x 1024 17 against 22)."""
-    if (t is None or t.dtype != torch.bfloat16 or work < 1 << 30 or t.shape[0] <= 64 or t.shape[1] % 8
+    if (t is None or t.dtype != torch.bfloat16 or work < 1 << 30 or t.shape[1] % 8
             or (t.data_ptr() % 16 == 0 and ld % 8 == 0)):
         return t, ld
     return t.clone(memory_format=torch.contiguous_format), t.shape[1]

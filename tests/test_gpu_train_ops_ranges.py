@@ -194,3 +194,17 @@ def test_layer_norm_of_tokens_of_the_lowest_value(lrc, dtype, d):
     slack = ((x.double().abs() + mean.double().abs()[:, None]) * rstd.double()[:, None] * dy.double().abs())[rows].sum(0)
     assert ((dgamma.double() - want).abs() <= (n + 8) * U * terms + 2 * U * slack).all()
     assert ((dbeta.double() - dy.double().sum(0)).abs() <= (n + 8) * U * dy.double().abs().sum(0)).all()
+
+
+# ----------------------------------------------------------------------------- alignment
+@pytest.mark.parametrize("n,d_in,d_out", [(4200, 4096, 64), (4200, 64, 4096), (16400, 2048, 40)])
+def test_large_products_of_a_narrow_unaligned_weight(lrc, n, d_in, d_out):
+    """W of at most 64 rows, or columns, that start on no 16 bytes (a slice of a larger factor): the bits of an
+    aligned W."""
+    x, dy = normal(1, n, d_in).bfloat16(), normal(2, n, d_out).bfloat16()
+    w = normal(3, d_out, d_in).bfloat16()
+    far = torch.zeros(d_out, d_in + 8, dtype=torch.bfloat16, device=dev())[:, 3:3 + d_in]
+    far.copy_(w)
+    assert far.data_ptr() % 16 and torch.equal(lrc.lrc_linear(x, far, save="z")[1], lrc.lrc_linear(x, w, save="z")[1])
+    for a, b in zip(lrc.lrc_linear_backward(dy, x, far), lrc.lrc_linear_backward(dy, x, w)):
+        assert torch.equal(a, b)
