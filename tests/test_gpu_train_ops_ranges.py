@@ -208,3 +208,71 @@ def test_large_products_of_a_narrow_unaligned_weight(lrc, n, d_in, d_out):
     assert far.data_ptr() % 16 and torch.equal(lrc.lrc_linear(x, far, save="z")[1], lrc.lrc_linear(x, w, save="z")[1])
     for a, b in zip(lrc.lrc_linear_backward(dy, x, far), lrc.lrc_linear_backward(dy, x, w)):
         assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------- borders
+def test_pack_at_the_borders_of_the_exponent(lrc):
+    """Blocks whose largest magnitude lies one step below, at and one step above 127 * 2^e, over the whole range of e
+    (the highest ones, and those from 127 * 2^114 on, among them), with ties below them: bit-exact."""
+    rows = []
+    for e in [-126, -125, -1, 0, 1, 60, 113, 114, 115, 119, 120, 121]:
+        top = np.float32(127.0) * np.float32(2.0) ** e
+        for big in (np.nextafter(top, np.float32(0)), top, np.nextafter(top, np.float32(np.inf))):
+            rows.append([big, -big, top * 0.5, top * np.float32(2.5 / 127), -top * np.float32(63.5 / 127), 0.0])
+    x = torch.from_numpy(np.array(rows, np.float32))
+    codes, exps, info = lrc.lrc_pack_activations(x.to(dev()))
+    qc, qe = ref.pack(x.double().numpy())
+    assert np.array_equal(codes.cpu().numpy(), qc) and np.array_equal(exps.cpu().numpy(), qe)
+    assert int(info.cpu()) == 0
+
+
+def relative_tail(x, name):
+    """Bound of act(x) in fp32 relative to itself.  The exponential's argument goes through two roundings and a rounded
+    constant, 3 u of itself for GELU (x^2 / 2) and 2 u for SiLU (x), which is the relative error of the exponential;
+    the fit's error (5e-7) and ten more roundings, of two steps each where an instruction is good to one step."""
+    return (1.5 * x * x if name == "gelu" else 2 * np.abs(x)) * U + 5e-7 + 20 * U
+
+
+@pytest.mark.parametrize("name,low", [("gelu", -12.0), ("silu", -80.0)])
+def test_activations_of_negative_tails(lrc, name, low):
+    """act(z) of z down to where it is 1e-32: accurate relative to itself, not to z."""
+    x = torch.linspace(low, 0, 20001, dtype=torch.float32)[:, None]
+    y = lrc.lrc_linear(x.to(dev()), torch.ones(1, 1, device=dev()), act=name)[0]
+    want = ref.act(f64(x), name)
+    assert (np.abs(f64(y) - want) <= relative_tail(f64(x), name) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_operands_past_2_to_31_elements(lrc, dtype):
+    """More than 2^31 elements in x and dx, on the pipelined tiles: small integers, exact in any order."""
+    n, d_in, d_out = 524416, 4104, 72
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g, device=dev(), dtype=torch.int8).to(dtype)   # noqa: E731
+    x, w, dy = ints(n, d_in), ints(d_out, d_in), ints(n, d_out)
+    assert x.numel() > 1 << 31
+    y = lrc.lrc_linear(x, w)[0]
+    _, dx, dw, _ = lrc.lrc_linear_backward(dy, x, w, dw_dtype=torch.float32)
+    total = torch.zeros(d_out, d_in, dtype=torch.float64, device=dev())
+    for a in range(0, n, 65536):
+        xs, ds = x[a:a + 65536].double(), dy[a:a + 65536].double()
+        assert torch.equal(y[a:a + 65536], (xs @ w.double().T).to(dtype)), a
+        assert torch.equal(dx[a:a + 65536], (ds @ w.double()).to(dtype)), a
+        total += ds.T.contiguous() @ xs
+    assert torch.equal(dw.double(), total)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,d_in,d_out", [(24, 11008, 4096), (1000, 1024, 1024), (4096, 4096, 4104), (3900, 1100, 2500)])
+def test_equal_inputs_give_equal_bits_on_every_tile(lrc, dtype, n, d_in, d_out):
+    """Calls again and again on the same inputs, at sizes of one and several rounds of tiles and of split k."""
+    x, dy, z = normal(1, n, d_in).to(dtype), normal(2, n, d_out).to(dtype), normal(3, n, d_out).to(dtype)
+    w = normal(4, d_out, d_in, scale=1 / math.sqrt(d_in)).to(dtype)
+
+    def call():
+        y, (codes, exps), _ = lrc.lrc_linear(x, w, act="gelu", residual=dy, save="checkpoint")
+        return (y, codes, exps, *lrc.lrc_linear_backward(dy, x, w, act="silu", z=z))
+
+    first = call()
+    for _ in range(6):
+        for a, b in zip(call(), first):
+            assert torch.equal(a, b)
