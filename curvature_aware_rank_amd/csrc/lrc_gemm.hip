@@ -650,17 +650,23 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
     else if constexpr (!SEG)
       gemm_bf16_kernel<TO, KA, KB, 16, 4, 1, 1, 4, 64, 4, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
+    else
+      return false;
+    return true;
   };
   using std::integral_constant;
-  // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more
+  // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more.  What no
+  // caller asks for has no kernel, and is refused.
+  constexpr bool BITS = std::is_same<TO, uint16_t>::value;
+  bool launched = false;
   if (seg.type == FP32) {
-    if constexpr (!std::is_same<TO, uint16_t>::value) launch(std::false_type{}, integral_constant<Element, FP32>{});
-  } else if (std::is_same<TO, uint16_t>::value || seg.count == 1) {
-    if constexpr (std::is_same<TO, uint16_t>::value || KA == K_COLS)
-      launch(std::false_type{}, integral_constant<Element, BF16>{});
-  } else if constexpr (!std::is_same<TO, uint16_t>::value) {
-    launch(std::true_type{}, integral_constant<Element, BF16>{});
+    if constexpr (!BITS) launched = launch(std::false_type{}, integral_constant<Element, FP32>{});
+  } else if (seg.count == 1) {
+    if constexpr (BITS || KA == K_COLS) launched = launch(std::false_type{}, integral_constant<Element, BF16>{});
+  } else if constexpr (!BITS) {
+    launched = launch(std::true_type{}, integral_constant<Element, BF16>{});
   }
+  if (!launched) return LRC_EINVAL;
   LRC_LAUNCHED();
   if (tg.splits == 1) return LRC_OK;
   const int splits = tg.splits;

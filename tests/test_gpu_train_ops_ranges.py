@@ -276,3 +276,34 @@ def test_equal_inputs_give_equal_bits_on_every_tile(lrc, dtype, n, d_in, d_out):
     for _ in range(6):
         for a, b in zip(call(), first):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("n,d_in,d_out", [(37, 72, 104), (300, 264, 520), (300, 265, 521)])
+def test_weight_gradient_beside_a_dz_of_any_pitch(lrc, act, n, d_in, d_out):
+    """Through the C interface: dz rows of an odd pitch and start, dW with a gap behind its rows.  dW is as accurate as
+    with rows of whole pieces, and what lies between the rows is left as it was."""
+    x, dy, z = normal(1, n, d_in).bfloat16(), normal(2, n, d_out).bfloat16(), normal(3, n, d_out).bfloat16()
+    w = normal(4, d_out, d_in).bfloat16()
+    lddz, lddw = d_out + 3, d_in + 5
+    dz = torch.full((n * lddz + 1,), 7.0, dtype=torch.bfloat16, device=dev())
+    dw = torch.full((d_out, lddw), 7.0, device=dev())
+    dx = torch.empty(n, d_in, dtype=torch.bfloat16, device=dev())
+    size = lrc.lib.lrc_linear_backward_workspace(lrc.LRC_BF16, n, d_in, d_out)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev())
+    assert lrc.lib.lrc_linear_backward(
+        dy.data_ptr(), lrc.LRC_BF16, n, d_in, d_out, d_out, w.data_ptr(), d_in, x.data_ptr(), d_in, None, None,
+        {"gelu": 2, "silu": 3}[act], z.data_ptr(), d_out, None, None, dz.data_ptr() + 2, lddz, dx.data_ptr(), d_in,
+        dw.data_ptr(), lrc.LRC_F32, lddw, None, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream) == 0
+    got = dz[1:].view(n, lddz)
+    assert (got[:, d_out:] == 7).all() and (dz[0] == 7) and (dw[:, d_in:] == 7).all()
+    want = lrc.lrc_linear_backward(dy, x, w, act=act, z=z, dw_dtype=torch.float32)
+    assert torch.equal(got[:, :d_out], want[0])
+    dzn = f64(dy) * ref.act_slope(f64(z), act)
+    terms = np.abs(dzn).T @ np.abs(f64(x))
+    for t in (dw[:, :d_in], want[2]):
+        assert (np.abs(f64(t) - dzn.T @ f64(x)) <= 2.0 ** -11 * terms).all()
+    # a product of the stream: dz to half a bf16 step, the sum in fp32, dx to half a step
+    mags = np.abs(dzn) @ np.abs(f64(w))
+    for t in (dx, want[1]):
+        assert (np.abs(f64(t) - dzn @ f64(w)) <= 1.01 * (2.0 ** -8 * mags + 2.0 ** -8 * np.abs(dzn @ f64(w)))).all()
