@@ -12,13 +12,14 @@
 //   K_COLS: a k step's channels lie together; fragments come from transposing LDS reads
 //     (ds_read_b64_tr_b16), in fp32 from four reads of 4 bytes, granules changing places by the
 //     step's number.
-// What bounds it: large bf16 products the chip's power, which sets its clock (1.6 to 1.9 GHz), then
-// the matrix pipes (73 % of their cycles at 4096^3): 8192 x 4096 x 11008 forward 680 us in a
+// What bounds it: the matrix pipes, busy 64 % of the cycles of dx at 8192 x 4096 x 11008 (at 1.8 GHz) and
+// 63 % of dW's (1.9), and what leaves them idle: 47 % forward (2.1 GHz), where the sixth round of tiles
+// is 38 % full and nothing hides the epilogue.  8192 x 4096 x 11008 forward 680 us in a
 // row of its own calls (1090 TFLOP/s; the vendor's library on the same box 690), 730 between other
 // kernels; dx 590-640, dW 590-650 (twice where dz has two pieces); 4096^3 103 us (library 90).  fp32 split in
 // three: 8192 x 1024 x 4096 315-345 us (200 TFLOP/s of fp32 products, fp32 instructions reach 140).
-// fp32 tiles: 2048 x 2048 x 1024 68 us (126 TFLOP/s; library 65).  24 tokens x 11008 x 4096: 23 us
-// with the splits' sums, 3.9 TB/s of weight.
+// fp32 tiles: 2048 x 2048 x 1024 68 us (126 TFLOP/s; library 65).  24 tokens x 11008 x 4096: 21 us
+// and 4 for the splits' sums, 4.3 TB/s of weight.
 // Few tiles leave compute units idle, so k may be split: every split writes its fp32 tile and
 // a second kernel adds them in split order and runs the epilogue (bit-reproducible).
 #include "lrc_train.h"
@@ -492,8 +493,7 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
 // 7.9 / 9.0 / 9.2 us against 13.5 / 15.5 / 16.8 on small ones, 64 x 4096 x 11008 18 / 25 / 42 against
 // 26 / 26 / 43; 4096 x 1024 x 1024 stays on large ones (17).  Small tiles for what a last, part
 // full round of large ones holds gained nothing (8192 x 4096 x 11008, 5.4 rounds: 695 us against
-// 690): the chip is then at its power limit, and units that idle let the others run faster.  Times
-// below in microseconds, taken at 100 x 64 x 64 to 8192 x 4096 x 11008.
+// 690).  Times below in microseconds, taken at 100 x 64 x 64 to 8192 x 4096 x 11008.
 enum Tile { LARGE, SMALL, TINY };
 struct Plan {
   Tile tile;
@@ -623,11 +623,10 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   // Stages of a large tile: 64 k steps in two buffers where both operands' rows run along k (a
   // row's piece is then a whole 128-byte line: 8192 x 4096 x 11008 678 us against 712), else 32
   // in four (dx 560 against 579, dW 581 against 610).  Small tiles: 64 in two (785 against 954).
-  // The 16 x 16 x 32 matrix instruction takes less power than the 32 x 32 x 16 one, and at these
-  // sizes the chip's clock goes by its power (1.9 GHz at 4096^3): 8192 x 4096 x 4096 199 us against
-  // 215, 2048 x 4096 x 4096 on small tiles 62 against 69.  Large tiles with K_COLS operands keep the
-  // larger one: their transposing reads need more address registers, and the smaller one's two full
-  // fragment sets then spill (dx 272 against 225, dW 445 against 213).
+  // The 16 x 16 x 32 matrix instruction is the faster one (8192 x 4096 x 4096 199 us against 215 with
+  // 32 x 32 x 16, 2048 x 4096 x 4096 on small tiles 62 against 69).  Large tiles with K_COLS operands
+  // keep the larger one: their transposing reads need more address registers, and the smaller one's
+  // two full fragment sets then spill (dx 272 against 225, dW 445 against 213).
   constexpr int KL = large_stage(KA, KB), NL = KL == 64 ? 2 : 4, ML = KL == 64 ? 16 : 32;
   double cost;
   const Plan p = seg.type == FP32 ? plan_f32(M, N, K, cost) : plan_gemm(M, N, K, seg.count, KL, cost);

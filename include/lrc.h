@@ -484,6 +484,9 @@ size_t lrc_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_
  * count, of dW those of dz and x), not on which outputs are asked for: a gradient alone has the
  * bits of the joint call.
  * n_tokens == 0 writes zeros to dW and db.  Sizes as lrc_linear.
+ * The workspace holds what the products cannot read where it lies: x of a checkpoint in full (fp32:
+ * three bf16 pieces of x, dz and W in large products), and in bf16 the bits dz has beyond the
+ * stream (8192 x 4096 x 11008: bf16 259 MB, fp32 1024).
  */
 lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,
                                int64_t lddy, const void* W, int64_t ldw, const void* x, int64_t ldx,
