@@ -94,6 +94,15 @@ __device__ __forceinline__ float input_at(const T* x, int64_t ldx, const int8_t*
   return ld_elem(x + t * ldx + j);
 }
 
+// xh of the backward pass.  A held value may lie a step away from the token's: where a mask filled the
+// token with the lowest value, centred and divided by a spread of zero it passes the largest number,
+// and must not turn the token's dy of zeros into NaN.
+template <bool CK>
+__device__ __forceinline__ float normalised(float x, float mu, float r) {
+  const float t = (x - mu) * r;
+  return CK && fabsf(t) == __builtin_inff() ? copysignf(3.402823466e38f, t) : t;
+}
+
 template <class T, bool CK>
 __global__ __launch_bounds__(NT) void ln_bwd_rows_kernel(const T* __restrict__ dy, int64_t lddy, int d,
                                                          const T* __restrict__ x, int64_t ldx,
@@ -108,14 +117,14 @@ __global__ __launch_bounds__(NT) void ln_bwd_rows_kernel(const T* __restrict__ d
   const float mu = mean[t], rs = rstd[t];
   float s1 = 0.f, s2 = 0.f;
   for (int j = threadIdx.x; j < d; j += NT) {
-    const float xh = (input_at<T, CK>(x, ldx, codes, exps, nb, t, j, d) - mu) * rs;
+    const float xh = normalised<CK>(input_at<T, CK>(x, ldx, codes, exps, nb, t, j, d), mu, rs);
     const float g = ld_elem(dy + t * lddy + j) * (gamma ? gamma[j] : 1.f);
     s1 += g;
     s2 = fmaf(g, xh, s2);
   }
   const float c1 = block_sum(s1, red) / float(d), c2 = block_sum(s2, red) / float(d);
   for (int j = threadIdx.x; j < d; j += NT) {
-    const float xh = (input_at<T, CK>(x, ldx, codes, exps, nb, t, j, d) - mu) * rs;
+    const float xh = normalised<CK>(input_at<T, CK>(x, ldx, codes, exps, nb, t, j, d), mu, rs);
     const float g = ld_elem(dy + t * lddy + j) * (gamma ? gamma[j] : 1.f);
     st_elem(dx + t * lddx + j, rs * (g - c1 - xh * c2));
   }
@@ -135,7 +144,7 @@ __global__ __launch_bounds__(NT) void ln_bwd_cols_kernel(const T* __restrict__ d
   const int64_t t0 = int64_t(blockIdx.y) * rows, t1 = min(n, t0 + rows);
   float a = 0.f, b = 0.f;
   for (int64_t t = t0; t < t1; ++t) {
-    const float xh = (input_at<T, CK>(x, ldx, codes, exps, nb, t, j, d) - mean[t]) * rstd[t];
+    const float xh = normalised<CK>(input_at<T, CK>(x, ldx, codes, exps, nb, t, j, d), mean[t], rstd[t]);
     const float g = ld_elem(dy + t * lddy + j);
     a = fmaf(g, xh, a);
     b += g;
@@ -377,6 +386,12 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
       g[i] = rg.at(i);
       const float xv = CK ? rc.at(i) : rx.at(i);
       xh[i] = S::col(i, l) < d ? (xv - mu) * r : 0.f;
+    }
+    // as `normalised`; a wave's lanes share the token, and only a spread far below the mean gets there
+    // (a test of every value took 145 us against 139 at 32768 x 4096)
+    if (CK && __builtin_amdgcn_readfirstlane(fabsf(mu) * r > 0x1p120f)) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) xh[i] = normalised<CK>(xh[i], 0.f, 1.f);
     }
     load(t + step);
     float s[2] = {0.f, 0.f};

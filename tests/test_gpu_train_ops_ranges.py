@@ -307,3 +307,38 @@ def test_weight_gradient_beside_a_dz_of_any_pitch(lrc, act, n, d_in, d_out):
     mags = np.abs(dzn) @ np.abs(f64(w))
     for t in (dx, want[1]):
         assert (np.abs(f64(t) - dzn @ f64(w)) <= 1.01 * (2.0 ** -8 * mags + 2.0 ** -8 * np.abs(dzn @ f64(w)))).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,h", [(96, 160), (512, 264), (4096, 96), (20000, 40)])
+@pytest.mark.parametrize("held", [False, True])
+def test_step_with_tokens_of_the_lowest_value(lrc, dtype, d, h, held):
+    """norm -> linear (GELU) and back where a mask filled tokens of x with the lowest value: the norm sends them to beta
+    as it does zeros, dy is zero there, and every output is that of a step whose masked tokens hold zeros."""
+    n = 75
+    x, dy = normal(1, n, d).to(dtype), normal(2, n, h, scale=0.01).to(dtype)
+    w, b = normal(3, h, d, scale=1 / math.sqrt(d)).to(dtype), normal(4, h)
+    gamma, beta = 1 + 0.1 * normal(5, d), normal(6, d)
+    masked = torch.arange(n, device=dev()) % 9 == 4
+    dy[masked] = 0
+    got = []
+    for fill in (torch.finfo(dtype).min, 0.0):
+        x[masked] = fill
+        a, mean, rstd, xk, _ = lrc.lrc_layer_norm(x, gamma, beta, checkpoint=True)
+        y, zk, _ = lrc.lrc_linear(a, w, b, act="gelu", save="checkpoint" if held else "z")
+        dz, da, dw, db = lrc.lrc_linear_backward(dy, lrc.lrc_pack_activations(a)[:2] if held else a, w, act="gelu", z=zk)
+        dx, dgamma, dbeta = lrc.lrc_layer_norm_backward(da, xk if held else x, mean, rstd, gamma)
+        got.append({"a": a, "y": y, "dz": dz, "da": da, "dw": dw, "db": db, "dgamma": dgamma, "dbeta": dbeta, "dx": dx})
+    for k, t in got[0].items():
+        assert torch.isfinite(t).all() and torch.equal(t, got[1][k]), k
+
+
+def test_fp32_rows_beside_a_row_that_is_not_finite(lrc):
+    """A token with a NaN at a size that splits fp32 entries: the other tokens as accurate as without it."""
+    n, d_in, d_out = 6912, 1080, 1984
+    x, w = normal(1, n, d_in), normal(2, d_out, d_in)
+    x[5, 7] = float("nan")
+    y = lrc.lrc_linear(x, w)[0]
+    rows = [t for t in range(n) if t != 5]
+    bound = (d_in + 8) * 2 * U * (x[rows].double().abs() @ w.double().abs().T)
+    assert y[5].isnan().all() and ((y[rows].double() - x[rows].double() @ w.double().T).abs() <= bound).all()
