@@ -161,7 +161,7 @@ __global__ __launch_bounds__(NT) void ln_bwd_cols_kernel(const T* __restrict__ d
 // Lane l holds channels 8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint
 // block; pieces are 16-byte accesses at any alignment, the last one of a ragged row is short.
 // Bound by memory: forward with its checkpoint 65536 x 4096 bf16 250 us (1.35 GB, 5.4 TB/s), backward
-// from a checkpoint 32768 x 4096 bf16 140 us (0.67 GB, 4.8 TB/s), the partials' sum 5 us more; one
+// from a checkpoint 32768 x 4096 bf16 117 us (0.67 GB, 5.7 TB/s), the partials' sum 5 us more; one
 // token of 4096 3 us, a launch.
 constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }   // tokens of a workgroup at a time
 constexpr int row_threads(int wpr) { return 64 * wpr * row_groups(wpr); }
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
       xh[i] = S::col(i, l) < d ? (xv - mu) * r : 0.f;
     }
     // as `normalised`; a wave's lanes share the token, and only a spread far below the mean gets there
-    // (a test of every value took 145 us against 139 at 32768 x 4096)
+    // (a test of every value took 145 us against 122 at 32768 x 4096)
     if (CK && __builtin_amdgcn_readfirstlane(fabsf(mu) * r > 0x1p120f)) {
 #pragma unroll
       for (int i = 0; i < E; ++i) xh[i] = normalised<CK>(xh[i], 0.f, 1.f);
