@@ -27,7 +27,9 @@ __all__ = [
     "library_path", "lrc_accumulate_cov", "lrc_whiten_decompose", "lrc_score_components", "lrc_allocate_ranks",
     "lrc_rank_scores", "lrc_rotate_quantize", "lrc_quantize_rows", "lrc_lowrank_ffn", "lrc_ffn_select_channels",
     "lrc_hybrid_ffn", "LRC_CKPT_BLOCK", "lrc_pack_activations", "lrc_unpack_activations", "lrc_layer_norm",
-    "lrc_layer_norm_backward", "lrc_linear", "lrc_linear_backward",
+    "lrc_layer_norm_backward", "lrc_linear", "lrc_linear_backward", "lrc_gated_linear",
+    "lrc_gated_linear_backward", "lrc_quantize_tokens", "lrc_int8_linear", "lrc_int8_gated_linear",
+    "lrc_block_norm", "lrc_block_norm_backward",
     "lrc_status_string", "lrc_profile_start", "lrc_profile_stop", "lrc_profile_kernels",
 ]
 
@@ -40,6 +42,7 @@ LRC_RANKSCORE_UNIRANK = 0x1
 LRC_RANKSCORE_SWIFT = 0x2
 LRC_CKPT_BLOCK = 64                     # channels that share one checkpoint exponent
 _ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+_NORMS = {"layer": 0, "rms": 1}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "liblrc.so")
@@ -88,6 +91,27 @@ _SIGS = {
     "lrc_linear_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64,
                                    _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _sz, _vp]),
     "lrc_linear_backward_workspace": (_sz, [_i32, _i64, _i64, _i64]),
+    "lrc_gated_linear": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i64,
+                                _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "lrc_gated_linear_workspace": (_sz, [_i32, _i64, _i64, _i64]),
+    "lrc_gated_linear_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i32,
+                                         _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i32,
+                                         _i64, _vp, _sz, _vp]),
+    "lrc_gated_linear_backward_workspace": (_sz, [_i32, _i64, _i64, _i64]),
+    "lrc_quantize_tokens": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "lrc_int8_linear": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64,
+                               _vp, _i64, _vp, _vp, _sz, _vp]),
+    "lrc_int8_linear_workspace": (_sz, [_i64, _i64, _i64]),
+    "lrc_int8_gated_linear": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp,
+                                     _i32, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "lrc_int8_gated_linear_workspace": (_sz, [_i64, _i64, _i64]),
+    "lrc_block_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _i32, ctypes.c_float, _i32, _vp, _vp, _vp,
+                              ctypes.c_float, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
+                              _vp]),
+    "lrc_block_norm_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                       _i32, _i32, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                                       _vp, _vp, _vp, _vp, _sz, _vp]),
+    "lrc_block_norm_backward_workspace": (_sz, [_i64, _i64]),
     "lrc_status_string": (ctypes.c_char_p, [_i32]),
     "lrc_last_hip_error": (_i32, []),
     "lrc_profile_start": (_i32, []),
@@ -771,6 +795,297 @@ def lrc_linear_backward(dy: torch.Tensor, x, W: torch.Tensor, act: str = "none",
          _ptr(xt), ldx, _ptr(xcodes), _ptr(xexps), code, _ptr(zt), ldz, _ptr(zcodes), _ptr(zexps), _ptr(dz),
          max(d_out, 1), _ptr(dx), max(d_in, 1), _ptr(dW), dw_dt, max(d_in, 1), _ptr(db), _ptr(ws), ws.numel())
     return dz if code else dy, dx, dW, db
+
+
+def _in_pieces(t, ld):
+    """(tensor, leading dim) of an operand the products read where it lies: rows that could be whole 16-byte
+    pieces are, at a pitch below 2^22 bytes; a tensor laid out otherwise is copied."""
+    size = t.element_size()
+    if t.shape[1] * size % 16 or (t.data_ptr() % 16 == 0 and ld * size % 16 == 0 and ld * size <= 1 << 22):
+        return t, ld
+    return t.clone(memory_format=torch.contiguous_format), t.shape[1]
+
+
+def _pair_of_weights(Wg, Wu, d_ff, d_in, dtype, device, read):
+    """(Wg, Wu, leading dim) of two weights of one shape and, where the products read them, one pitch."""
+    Wg, ldw = _rows(Wg, "Wg", d_ff, d_in, dtype, device)
+    Wu, ldu = _rows(Wu, "Wu", Wg.shape[0], Wg.shape[1], dtype, Wg.device)
+    if read and dtype == torch.bfloat16:
+        (Wg, ldw), (Wu, ldu) = _in_pieces(Wg, ldw), _in_pieces(Wu, ldu)
+    if ldw != ldu:
+        Wg, Wu, ldw = Wg.contiguous(), Wu.contiguous(), max(Wg.shape[1], 1)
+    return Wg, Wu, ldw
+
+
+def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", save: str = "none",
+                     info=None):
+    """h = act(x Wg^T) * (x Wu^T), the gate and up projection of a gated feed-forward block.  x: (n_tokens, d_in), Wg,
+    Wu: (d_ff, d_in), all bf16 or all fp32; act: none, relu, gelu (exact) or silu.  save keeps g = x Wg^T and
+    u = x Wu^T for the backward pass: "z" in full, "checkpoint" in 8 bits, "none" not at all.
+
+    Returns (h, saved, info): saved is (g, u), ((codes, exps), (codes, exps)) or None; info (int32 (1,), sticky
+    LRC_ENONFINITE) is None unless given or save is "checkpoint"."""
+    x, ldx = _rows(x, "x")
+    dt, dev = _dtype_code(x), x.device
+    n, d_in = x.shape
+    Wg, Wu, ldw = _pair_of_weights(Wg, Wu, None, d_in, x.dtype, dev, True)
+    d_ff = Wg.shape[0]
+    if x.dtype == torch.bfloat16:
+        x, ldx = _in_pieces(x, ldx)
+    code = _act_code(act)
+    h = torch.empty(n, d_ff, dtype=x.dtype, device=dev)
+    g = u = None
+    kept = (None, None), (None, None)
+    if save == "z":
+        g, u = (torch.empty(n, d_ff, dtype=x.dtype, device=dev) for _ in range(2))
+    elif save == "checkpoint":
+        kept = _new_checkpoint(n, d_ff, dev), _new_checkpoint(n, d_ff, dev)
+    elif save != "none":
+        raise ValueError("save is none, z or checkpoint")
+    if save == "checkpoint" or info is not None:
+        info = _info(info, dev)
+    ws = _workspace(lib.lrc_gated_linear_workspace(dt, n, d_in, d_ff), dev)
+    _run("lrc_gated_linear", dev, lib.lrc_gated_linear, _ptr(x), dt, n, d_in, d_ff, ldx, _ptr(Wg), _ptr(Wu), ldw, code,
+         _ptr(h), max(d_ff, 1), _ptr(g), _ptr(u), max(d_ff, 1), _ptr(kept[0][0]), _ptr(kept[0][1]), _ptr(kept[1][0]),
+         _ptr(kept[1][1]), _ptr(info), _ptr(ws), ws.numel())
+    return h, (g, u) if save == "z" else kept if save == "checkpoint" else None, info
+
+
+def lrc_gated_linear_backward(dh: torch.Tensor, x, Wg: torch.Tensor, Wu: torch.Tensor, g, u, act: str = "silu",
+                              need_dx: bool = True, need_dw: bool = True, dw_dtype=None):
+    """Gradients of lrc_gated_linear.  dh: (n_tokens, d_ff); x: the input (n_tokens, d_in) like dh, or its (codes, exps)
+    checkpoint (may be None without need_dw); Wg, Wu: (d_ff, d_in); g, u: as kept, both in full or both as (codes, exps).
+
+    Returns (dg, du, dx, dWg, dWu): dg = dh * u * act'(g) and du = dh * act(g), the output-gradient streams of the two
+    projections, dx (n_tokens, d_in), dWg and dWu (d_ff, d_in) in dw_dtype (default dh's; torch.float32 allowed); None
+    where not needed."""
+    dh, lddh = _rows(dh, "dh")
+    dt, dev = _dtype_code(dh), dh.device
+    n, d_ff = dh.shape
+    Wg, Wu, ldw = _pair_of_weights(Wg, Wu, d_ff, None, dh.dtype, dev, need_dx)
+    d_in = Wg.shape[1]
+    code = _act_code(act)
+    if need_dw and x is None:
+        raise ValueError("dWg and dWu need x or its checkpoint")
+    if g is None or u is None:
+        raise ValueError("the gradients need g and u or their checkpoints")
+    xt, ldx, xcodes, xexps = _kept(x if need_dw else None, "x", n, d_in, dh.dtype, dev)
+    gt, ldz, gcodes, gexps = _kept(g, "g", n, d_ff, dh.dtype, dev)
+    ut, ldu, ucodes, uexps = _kept(u, "u", n, d_ff, dh.dtype, dev)
+    if (gt is None) != (ut is None):
+        raise ValueError("g and u are both tensors or both (codes, exps) pairs")
+    if ldz != ldu:
+        gt, ut, ldz = gt.contiguous(), ut.contiguous(), max(d_ff, 1)
+    if xt is not None and xt.dtype == torch.bfloat16:
+        xt, ldx = _in_pieces(xt, ldx)
+    dw_dtype = dw_dtype or dh.dtype
+    if dw_dtype not in (dh.dtype, torch.float32):
+        raise ValueError("dw_dtype is dh's dtype or torch.float32")
+    dg, du = (torch.empty(n, d_ff, dtype=dh.dtype, device=dev) for _ in range(2))
+    dx = torch.empty(n, d_in, dtype=dh.dtype, device=dev) if need_dx else None
+    dWg, dWu = ((torch.empty(d_ff, d_in, dtype=dw_dtype, device=dev) if need_dw else None) for _ in range(2))
+    dw_dt = LRC_F32 if dw_dtype == torch.float32 else LRC_BF16
+    ws = _workspace(lib.lrc_gated_linear_backward_workspace(dt, n, d_in, d_ff), dev)
+    _run("lrc_gated_linear_backward", dev, lib.lrc_gated_linear_backward, _ptr(dh), dt, n, d_in, d_ff, lddh, _ptr(Wg),
+         _ptr(Wu), ldw, _ptr(xt), ldx, _ptr(xcodes), _ptr(xexps), code, _ptr(gt), _ptr(ut), ldz, _ptr(gcodes),
+         _ptr(gexps), _ptr(ucodes), _ptr(uexps), _ptr(dg), _ptr(du), _ptr(dx), max(d_in, 1), _ptr(dWg), _ptr(dWu),
+         dw_dt, max(d_in, 1), _ptr(ws), ws.numel())
+    return dg, du, dx, dWg, dWu
+
+
+def lrc_quantize_tokens(x: torch.Tensor, info=None):
+    """Symmetric int8 codes of token rows (the quantiser of LRC_COV_QUANT_INT8_TOKEN).  x: (n_tokens, d) bf16 or fp32.
+
+    Returns (codes int8 (n_tokens, d), scale fp32 (n_tokens,), info int32 (1,)): the values held are
+    codes * scale[:, None].  info (sticky, optional) receives LRC_ENONFINITE when an entry is NaN or Inf."""
+    x, ldx = _rows(x, "x")
+    dt, dev = _dtype_code(x), x.device
+    n, d = x.shape
+    codes = torch.empty(n, d, dtype=torch.int8, device=dev)
+    scale = torch.empty(n, dtype=torch.float32, device=dev)
+    info = _info(info, dev)
+    _run("lrc_quantize_tokens", dev, lib.lrc_quantize_tokens, _ptr(x), dt, n, d, ldx, _ptr(codes), max(d, 1),
+         _ptr(scale), _ptr(info))
+    return codes, scale, info
+
+
+def _int8_tokens(x, dtype):
+    """(x, leading dim, codes, their leading dim, scale, n, d_in, result's dtype, device) of tokens given in full, or
+    as a (codes, scale) pair."""
+    if not isinstance(x, (tuple, list)):
+        x, ldx = _rows(x, "x")
+        _dtype_code(x)
+        if dtype not in (None, x.dtype):
+            raise ValueError("dtype is that of x; it is chosen where x is a (codes, scale) pair")
+        return x, ldx, None, 0, None, *x.shape, x.dtype, x.device
+    if len(x) != 2:
+        raise ValueError("x must be a tensor or a (codes, scale) pair")
+    codes, ldc = _rows(x[0], "x codes", None, None, torch.int8)
+    n, d_in = codes.shape
+    scale = _vector(x[1], "x scale", n, codes.device)
+    if scale is None:
+        raise ValueError("x codes need their scale")
+    codes, ldc = _in_pieces(codes, ldc)
+    return None, max(d_in, 1), codes, ldc, scale, n, d_in, dtype or torch.bfloat16, codes.device
+
+
+def _int8_weight(W, name, d_out, d_in, device):
+    if not isinstance(W, (tuple, list)) or len(W) != 2:
+        raise ValueError(f"{name} must be a (codes, scale) pair")
+    codes, ld = _rows(W[0], f"{name} codes", d_out, d_in, torch.int8, device)
+    scale = _vector(W[1], f"{name} scale", codes.shape[0], device)
+    if scale is None:
+        raise ValueError(f"{name} codes need their scale")
+    codes, ld = _in_pieces(codes, ld)
+    return codes, ld, scale
+
+
+def lrc_int8_linear(x, W, bias=None, act: str = "none", residual=None, dtype=None, info=None):
+    """y = act(x W^T + bias) + residual in 8-bit integers.  x: (n_tokens, d_in) bf16 or fp32, quantised within the call,
+    or the (codes, scale) pair of lrc_quantize_tokens or lrc_block_norm; W: the (codes (d_out, d_in) int8, scale
+    (d_out,)) pair of lrc_quantize_rows; bias: (d_out,) fp32; residual: (n_tokens, d_out) like y; act: none, relu, gelu
+    or silu.  y has x's dtype; for a pair `dtype` (bf16 unless given).
+
+    Returns (y, info): info (int32 (1,), sticky LRC_ENONFINITE of x) is None unless given."""
+    x, ldx, xc, ldxc, xs, n, d_in, dtype, dev = _int8_tokens(x, dtype)
+    wq, ldw, wscale = _int8_weight(W, "W", None, d_in, dev)
+    d_out = wq.shape[0]
+    code = _act_code(act)
+    bias = _vector(bias, "bias", d_out, dev)
+    ldr = d_out
+    if residual is not None:
+        residual, ldr = _rows(residual, "residual", n, d_out, dtype, dev)
+    if info is not None:
+        info = _info(info, dev)
+    y = torch.empty(n, d_out, dtype=dtype, device=dev)
+    ws = _workspace(lib.lrc_int8_linear_workspace(n, d_in, d_out), dev)
+    _run("lrc_int8_linear", dev, lib.lrc_int8_linear, _ptr(x), _dtype_code(y), n, d_in, d_out, ldx, _ptr(xc), ldxc,
+         _ptr(xs), _ptr(wq), ldw, _ptr(wscale), _ptr(bias), code, _ptr(residual), ldr, _ptr(y), max(d_out, 1),
+         _ptr(info), _ptr(ws), ws.numel())
+    return y, info
+
+
+def lrc_int8_gated_linear(x, Wg, Wu, act: str = "silu", dtype=None, info=None):
+    """h = act(x Wg^T) * (x Wu^T) in 8-bit integers: lrc_gated_linear's forward with x, dtype and info as in
+    lrc_int8_linear and Wg, Wu the (codes (d_ff, d_in) int8, scale (d_ff,)) pairs of lrc_quantize_rows.
+
+    Returns (h, info)."""
+    x, ldx, xc, ldxc, xs, n, d_in, dtype, dev = _int8_tokens(x, dtype)
+    gq, ldg, gscale = _int8_weight(Wg, "Wg", None, d_in, dev)
+    d_ff = gq.shape[0]
+    uq, ldu, uscale = _int8_weight(Wu, "Wu", d_ff, d_in, dev)
+    code = _act_code(act)
+    if info is not None:
+        info = _info(info, dev)
+    h = torch.empty(n, d_ff, dtype=dtype, device=dev)
+    ws = _workspace(lib.lrc_int8_gated_linear_workspace(n, d_in, d_ff), dev)
+    _run("lrc_int8_gated_linear", dev, lib.lrc_int8_gated_linear, _ptr(x), _dtype_code(h), n, d_in, d_ff, ldx, _ptr(xc),
+         ldxc, _ptr(xs), _ptr(gq), ldg, _ptr(gscale), _ptr(uq), ldu, _ptr(uscale), code, _ptr(h), max(d_ff, 1),
+         _ptr(info), _ptr(ws), ws.numel())
+    return h, info
+
+
+def _norm_code(kind):
+    if kind not in _NORMS:
+        raise ValueError(f"kind is one of {', '.join(_NORMS)}")
+    return _NORMS[kind]
+
+
+def _norm_params(pair, name, d, device, rms):
+    """(gamma, beta) of a norm, each None or a vector; no pair is (None, None)."""
+    if pair is None:
+        return None, None
+    if len(pair) != 2:
+        raise ValueError(f"{name} is a (gamma, beta) pair")
+    if rms and pair[1] is not None:
+        raise ValueError(f"an RMS norm takes no beta ({name})")
+    return _vector(pair[0], f"{name} gamma", d, device), _vector(pair[1], f"{name} beta", d, device)
+
+
+def lrc_block_norm(b: torch.Tensor, residual=None, kind: str = "rms", eps: float = 1e-5, post=None, gate=None,
+                   scale: float = 1.0, pre=None, need_s: bool = True, need_h: bool = True, quantize: bool = False,
+                   info=None):
+    """What lies between two blocks: p = norm(b) (where `post`, a (gamma, beta) pair, is given; else b),
+    s = residual + scale * gate * p, h = norm(s) with `pre`, a (gamma, beta) pair (None: 1 and 0).  kind: "rms" (takes
+    no beta) or "layer".  b, residual: (n_tokens, d) bf16 or fp32 (residual None: zero); gate, gammas, betas: (d,) fp32
+    or None.  With `quantize` h is returned as int8 codes for lrc_int8_linear instead.
+
+    Returns (s, h, stats, quantized, info): s and h like b (None where not needed, h None with quantize), stats
+    (mean_b, rstd_b, mean_s, rstd_s) for the backward pass (None where there is none), quantized (codes, scale) or
+    None; info (sticky LRC_ENONFINITE of the codes) is None unless given or with quantize."""
+    b, ldb = _rows(b, "b")
+    dt, dev = _dtype_code(b), b.device
+    n, d = b.shape
+    code = _norm_code(kind)
+    rms = kind == "rms"
+    ldr = max(d, 1)
+    if residual is not None:
+        residual, ldr = _rows(residual, "residual", n, d, b.dtype, dev)
+    pg, pb = _norm_params(post, "post", d, dev, rms)
+    ga, be = _norm_params(pre, "pre", d, dev, rms)
+    gate = _vector(gate, "gate", d, dev)
+    need_h = need_h and not quantize
+    if not (need_s or need_h or quantize):
+        raise ValueError("at least one of s, h and the codes is needed")
+    row = lambda want: torch.empty(n, dtype=torch.float32, device=dev) if want else None   # noqa: E731
+    normed = need_h or quantize
+    stats = (row(post is not None and not rms), row(post is not None), row(normed and not rms), row(normed))
+    s = torch.empty(n, d, dtype=b.dtype, device=dev) if need_s else None
+    h = torch.empty(n, d, dtype=b.dtype, device=dev) if need_h else None
+    quantized = (torch.empty(n, d, dtype=torch.int8, device=dev), row(True)) if quantize else None
+    if quantize or info is not None:
+        info = _info(info, dev)
+    q, qs = quantized or (None, None)
+    _run("lrc_block_norm", dev, lib.lrc_block_norm, _ptr(b), dt, n, d, ldb, _ptr(residual), ldr, code, float(eps),
+         int(post is not None), _ptr(pg), _ptr(pb), _ptr(gate), float(scale), _ptr(ga), _ptr(be), _ptr(s), max(d, 1),
+         _ptr(h), max(d, 1), *(_ptr(v) for v in stats), _ptr(q), max(d, 1), _ptr(qs), _ptr(info))
+    return s, h, stats, quantized, info
+
+
+def lrc_block_norm_backward(dh, ds, s, b, stats, kind: str = "rms", post=None, gate=None, scale: float = 1.0, pre=None,
+                            need_dresidual: bool = True, need_db: bool = True, need_dparams: bool = True):
+    """Gradients of lrc_block_norm.  dh, ds: gradients of h and s, (n_tokens, d), one of them may be None; s, b: as in the
+    forward pass (s may be None without dh); stats, kind, post, gate, scale, pre: those of the forward pass.
+
+    Returns (dresidual, db, dgamma, dbeta, dpost_gamma, dpost_beta, dgate): the first two like dh, the others fp32 (d,);
+    None where not needed or where the forward pass had no such parameter (a gamma or beta that was None included)."""
+    if dh is None and ds is None:
+        raise ValueError("dh or ds is needed")
+    lead, lead_ld = _rows(ds if dh is None else dh, "ds" if dh is None else "dh")
+    dt, dev = _dtype_code(lead), lead.device
+    n, d = lead.shape
+    code = _norm_code(kind)
+    rms = kind == "rms"
+    full = lambda t, name: (None, max(d, 1)) if t is None else _rows(t, name, n, d, lead.dtype, dev)   # noqa: E731
+    dh, lddh = (lead, lead_ld) if dh is not None else (None, max(d, 1))
+    ds, ldds = full(ds, "ds")
+    if dh is not None and s is None:
+        raise ValueError("the gradient of h needs s")
+    s, lds = full(s if dh is not None else None, "s")
+    pg, pb = _norm_params(post, "post", d, dev, rms)
+    ga, be = _norm_params(pre, "pre", d, dev, rms)
+    gate = _vector(gate, "gate", d, dev)
+    if len(stats) != 4:
+        raise ValueError("stats is (mean_b, rstd_b, mean_s, rstd_s)")
+    names = ("mean_b", "rstd_b", "mean_s", "rstd_s")
+    used = (post is not None and not rms, post is not None, dh is not None and not rms, dh is not None)
+    stats = [_vector(v, nm, n, dev) if use else None for v, nm, use in zip(stats, names, used)]
+    if any(use and v is None for v, use in zip(stats, used)):
+        raise ValueError("the statistics of the forward pass are needed")
+    if b is None and (gate is not None and need_dparams or post is not None):
+        raise ValueError("the gradients need b")
+    b, ldb = full(b, "b")
+    new = lambda want: torch.empty(n, d, dtype=lead.dtype, device=dev) if want else None   # noqa: E731
+    vec = lambda want: torch.empty(d, dtype=torch.float32, device=dev) if want and need_dparams else None   # noqa: E731
+    dr, db = new(need_dresidual), new(need_db)
+    grads = (vec(ga is not None and dh is not None), vec(be is not None and dh is not None), vec(pg is not None),
+             vec(pb is not None), vec(gate is not None))
+    ws = _workspace(lib.lrc_block_norm_backward_workspace(n, d), dev)
+    _run("lrc_block_norm_backward", dev, lib.lrc_block_norm_backward, _ptr(dh), dt, n, d, lddh, _ptr(ds), ldds, _ptr(s),
+         lds, _ptr(b), ldb, *(_ptr(v) for v in stats), code, int(post is not None), _ptr(pg), _ptr(pb), _ptr(gate),
+         float(scale), _ptr(ga), _ptr(dr), max(d, 1), _ptr(db), max(d, 1), *(_ptr(v) for v in grads), _ptr(ws),
+         ws.numel())
+    return dr, db, *grads
 
 
 def lrc_profile_start() -> None:

@@ -864,6 +864,7 @@ struct BackArgs {
   int dw_dt;
   int64_t lddw;
   float* db;
+  bool add;   // dx is added to what it holds
 };
 
 template <class T>
@@ -944,6 +945,10 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   if (a.dx != nullptr) {
     Epilogue ep;
     set_out<T>(ep, a.dx, a.lddx);
+    if (a.add) {
+      ep.res = a.dx;
+      ep.ldr = a.lddx;
+    }
     const double bytes = e * (double(n) * dn + double(dn) * di + double(n) * di);
     if (fast_dx) {
       GemmSegments seg = segments(pg.planes, pw.planes);
@@ -998,6 +1003,38 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
   return go(uint16_t{});
 }
 }  // namespace
+
+lrc_status lay_out_bf16(hipStream_t st, const LayOut* jobs, int count) {
+  OperandJobs q;
+  for (int i = 0; i < count; ++i) {
+    OperandJob& j = q.job[i];
+    j.p = jobs[i].p;
+    j.exps = jobs[i].exps;
+    j.out = jobs[i].out;
+    j.ld = jobs[i].ld;
+    j.nb = cdiv(jobs[i].cols, CKB);
+    j.rows = jobs[i].rows;
+    j.cols = jobs[i].cols;
+    j.w8 = round8(j.cols);
+    j.blocks = cdiv(cdiv(j.rows, JOB_ROWS) * (j.w8 / 8), LT);
+  }
+  return prepare_operands<uint16_t>(st, q, count, nullptr);
+}
+
+lrc_status linear_grads_f32(hipStream_t st, int64_t n, int64_t di, int64_t dn, const float* dz, int64_t lddz,
+                            const float* W, int64_t ldw, const float* x, int64_t ldx, const int8_t* xcodes,
+                            const int8_t* xexps, float* dx, int64_t lddx, bool add, float* dW, int64_t lddw, void* ws) {
+  const BackArgs a = {n,       di, dn,      dz,      lddz, W,    ldw, x,    ldx, xcodes,  xexps, LRC_ACT_NONE,
+                      nullptr, 0,  nullptr, nullptr, nullptr, 0, dx,  lddx, dW,  LRC_F32, lddw,  nullptr, add};
+  return linear_back<float>(st, a, ws);
+}
+
+lrc_status zero_rows(hipStream_t st, void* p, int64_t rows, int64_t cols, int64_t ld, int size) {
+  const int64_t half = size / 2, grid = std::min<int64_t>(cdiv(rows * cols * half, LT), 16384);
+  zero_rows_kernel<<<unsigned(grid), LT, 0, st>>>(static_cast<uint16_t*>(p), rows, cols * half, ld * half);
+  LRC_LAUNCHED();
+  return LRC_OK;
+}
 }  // namespace lrc
 
 extern "C" lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out,
@@ -1022,16 +1059,11 @@ extern "C" lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t 
   if (ws_bytes < need || (need > 0 && ws == nullptr)) return LRC_EWORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (n_tokens == 0) {   // sums over nothing
-    if (dW != nullptr) {
-      const int64_t half = dw_dt == LRC_F32 ? 2 : 1;
-      const int64_t grid = std::min<int64_t>(cdiv(d_out * d_in * half, LT), 16384);
-      zero_rows_kernel<<<unsigned(grid), LT, 0, st>>>(static_cast<uint16_t*>(dW), d_out, d_in * half, lddw * half);
-      LRC_LAUNCHED();
-    }
+    if (dW != nullptr) LRC_TRY(zero_rows(st, dW, d_out, d_in, lddw, dw_dt == LRC_F32 ? 4 : 2));
     if (db != nullptr) LRC_TRY(reduce_partials(st, nullptr, 0, d_out, d_out, db, nullptr));
     return LRC_OK;
   }
   const BackArgs a = {n_tokens, d_in, d_out, dy,  lddy,  W,     ldw, x,    ldx, xcodes, xexps, act,
-                      z,        ldz,  zcodes, zexps, dz, lddz, dx,  lddx, dW,  int(dw_dt), lddw, db};
+                      z,        ldz,  zcodes, zexps, dz, lddz, dx,  lddx, dW,  int(dw_dt), lddw, db, false};
   return dt == LRC_BF16 ? linear_back<uint16_t>(st, a, ws) : linear_back<float>(st, a, ws);
 }

@@ -1,5 +1,5 @@
 // Layer norm of token rows: forward (with the input's 8-bit checkpoint) and backward.
-#include "lrc_train.h"
+#include "lrc_rows.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -10,21 +10,6 @@ namespace {
 constexpr int NT = 256;
 constexpr int ROWS_PER_CHUNK = 64;   // tokens per partial of a column sum
 
-// Sum over the wave, in every lane: lane permutations inside the vector unit (neighbours, pairs,
-// mirrored eights and sixteens, then rows and halves exchanged) instead of six trips through LDS.
-__device__ __forceinline__ float wave_sum(float v) {
-  auto dpp = [](float x, auto ctrl) {
-    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
-  };
-  v += dpp(v, std::integral_constant<int, 0xb1>{});
-  v += dpp(v, std::integral_constant<int, 0x4e>{});
-  v += dpp(v, std::integral_constant<int, 0x141>{});
-  v += dpp(v, std::integral_constant<int, 0x140>{});
-  const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
-  const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
-}
 // sum over the 256 threads, the same value in every one (fixed order)
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = wave_sum(v);
@@ -32,12 +17,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   return (red[0] + red[1]) + (red[2] + red[3]);
-}
-
-// The mean from the sum of x_j / 2 d, which no finite token overflows; it ends at the largest number.
-__device__ __forceinline__ float mean_of(float half) {
-  const float m = 2.f * half;
-  return finite_f(half) ? fminf(fmaxf(m, -3.402823466e38f), 3.402823466e38f) : m;
 }
 
 // ---- any width: one workgroup per token, three passes over the row --------------------
@@ -163,119 +142,6 @@ __global__ __launch_bounds__(NT) void ln_bwd_cols_kernel(const T* __restrict__ d
 // Bound by memory: forward with its checkpoint 65536 x 4096 bf16 250 us (1.35 GB, 5.4 TB/s), backward
 // from a checkpoint 32768 x 4096 bf16 117 us (0.67 GB, 5.7 TB/s), the partials' sum 5 us more; one
 // token of 4096 3 us, a launch.
-constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }   // tokens of a workgroup at a time
-constexpr int row_threads(int wpr) { return 64 * wpr * row_groups(wpr); }
-
-template <class T, int WPR, int V>
-struct RowShape {
-  static constexpr int E = 8 * V, LANES = 64 * WPR, GROUPS = row_groups(WPR), THREADS = row_threads(WPR);
-  static __device__ __forceinline__ int col(int i, int l) {
-    return ((i >> 3) * LANES + l) * 8 + (i & 7);
-  }
-};
-
-// a token's elements as they lie in memory
-template <class T, int WPR, int V>
-struct RawRow {
-  using S = RowShape<T, WPR, V>;
-  static constexpr int W = 2 * int(sizeof(T));   // 32-bit words per piece
-  uint32_t q[V * W];
-  __device__ __forceinline__ void load(const T* row, int d, int l, bool live) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = (k * S::LANES + l) * 8, left = live ? d - c : 0;
-      if (left >= 8) {
-        __builtin_memcpy(q + k * W, row + c, 4 * W);
-      } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) q[k * W + w] = 0u;
-        if (left > 0) {   // as ld_short
-          T t[7];
-#pragma unroll
-          for (int e = 0; e < 7; ++e) t[e] = row[c + min(e, left - 1)];
-#pragma unroll
-          for (int e = 0; e < 7; ++e) {
-            if (sizeof(T) == 4) {
-              if (e < left) __builtin_memcpy(q + k * W + e % W, t + e, 4);
-            } else {
-              q[k * W + (e >> 1) % W] |= e < left ? uint32_t(t[e]) << (16 * (e & 1)) : 0u;
-            }
-          }
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if (sizeof(T) == 4) return __uint_as_float(q[i % (V * W)]);
-    return __uint_as_float((i & 1) ? (q[i >> 1] & 0xffff0000u) : (q[i >> 1] << 16));
-  }
-};
-// a token's codes and exponents
-template <int WPR, int V>
-struct RawCodes {
-  using S = RowShape<uint16_t, WPR, V>;
-  uint32_t q[2 * V];
-  int8_t e[V];
-  __device__ __forceinline__ void load(const int8_t* codes, const int8_t* exps, int d, int l, bool live) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = (k * S::LANES + l) * 8, left = live ? d - c : 0;
-      e[k] = left > 0 ? exps[c >> 6] : int8_t(0);
-      if (left >= 8) {
-        __builtin_memcpy(q + 2 * k, codes + c, 8);
-      } else {
-        q[2 * k] = q[2 * k + 1] = 0u;
-        if (left > 0) {   // as ld_short
-          uint8_t t[7];
-#pragma unroll
-          for (int i = 0; i < 7; ++i) t[i] = uint8_t(codes[c + min(i, left - 1)]);
-#pragma unroll
-          for (int i = 0; i < 7; ++i) q[2 * k + (i >> 2)] |= i < left ? uint32_t(t[i]) << (8 * (i & 3)) : 0u;
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    return float(int8_t(q[i >> 2] >> (8 * (i & 3)))) * pow2f(e[i >> 3]);
-  }
-};
-
-// Sums of the token's WPR waves, the same in all its lanes; one barrier when waves share a
-// token (`red`: a slot per wave, not reused before the barrier after the next one).
-template <int WPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int wave_in_row, int lane, int group) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
-  if (WPR == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) red[group * WPR + wave_in_row][k] = v[k];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) s += red[group * WPR + w][k];
-    v[k] = s;
-  }
-}
-
-// a lane's channels of gamma or beta, `absent` where there is none
-template <class S, int V>
-__device__ __forceinline__ void row_params(const float* p, float absent, int d, int l, float (&v)[8 * V]) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int c = (k * S::LANES + l) * 8;
-    float t[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = absent;
-    if (p != nullptr) ld8(p + c, d - c, t);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[8 * k + e] = t[e];
-  }
-}
-
 template <class T, int WPR, int V>
 __global__ __launch_bounds__(row_threads(WPR)) void ln_fwd_kernel(
     const T* __restrict__ x, int64_t ldx, int64_t n, int d, const float* __restrict__ gamma,
@@ -453,7 +319,6 @@ __global__ __launch_bounds__(row_threads(WPR)) void ln_bwd_kernel(
   }
 }
 
-constexpr int ROW_MAX = 16384;        // widest row held in registers
 constexpr int MAX_PARTS = 1024;       // partials of dgamma and dbeta
 
 // chunks of tokens of a column sum of wider rows
@@ -497,21 +362,6 @@ __global__ __launch_bounds__(NT) void reduce_partials_kernel(const float* __rest
     float* out = c < split ? out0 : out1;
     if (out != nullptr) out[c < split ? c : c - split] = v;
   }
-}
-
-// Calls f(waves per token, 8-channel pieces per lane) as compile-time constants for rows of d
-// channels; a lane holds 8 to 32 channels (16 waves of 16 would leave 128 registers a lane, and the
-// backward kernel spills: 12192 x 11008 374 us).
-template <class F>
-lrc_status with_row_shape(int64_t d, F f) {
-  using std::integral_constant;
-  if (d <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (d <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (d <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-  if (d <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (d <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  if (d <= 12288) return f(integral_constant<int, 8>{}, integral_constant<int, 3>{});
-  return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
 }
 
 template <class T>

@@ -1,0 +1,277 @@
+// Products of a token block with weights whose rows run along k, beside those of lrc_gemm.hip: 8-bit
+// integers, and two weights that share x (g = x Wg^T, u = x Wu^T, h = act(g) u).
+#pragma once
+
+#include "lrc_gemm_tile.h"
+
+namespace lrc {
+namespace gemm {
+
+template <class TO, int WM, int WN, int FM, int FN, int NST, Element EL, bool PAIR>
+__global__ __launch_bounds__(64 * WM * WN, 2) void rows_product_kernel(GemmOperand A, GemmOperand B, int64_t M,
+                                                                       int64_t N, int64_t K, TileGrid tg, Epilogue ep,
+                                                                       Companion co, float* __restrict__ partial) {
+  gemm_tile<TO, K_ROWS, K_ROWS, 16, WM, WN, FM, FN, 64, NST, false, EL, PAIR>(A, B, M, N, K, GemmSegments{}, tg, ep,
+                                                                              partial, nullptr, co);
+}
+
+// Sum of the splits' tiles in split order (integers: exact in any), then the epilogue.  One lane per
+// eight channels, the eight lanes of a 64-channel block together.
+template <class TO, Element EL, bool PAIR>
+__global__ __launch_bounds__(256) void rows_finish_kernel(const float* __restrict__ partial, int splits, int64_t M,
+                                                          int64_t N, int64_t np, int64_t blocks, Epilogue ep,
+                                                          Companion co) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 3;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = i / blocks, col = i % blocks * CKB + 8 * (lane & 7);
+  const int64_t left = row < M ? N - col : 0;
+  const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
+  constexpr int W = PAIR ? 2 : 1;
+  using V4 = std::conditional_t<EL == INT8, i32x4, f32x4>;
+  V4 acc[W][2] = {};
+  if (cnt > 0) {
+    const float* p = partial + row * W * np + col;
+    const int64_t plane = M * W * np;
+    for (int s0 = 0; s0 < splits; s0 += 4) {   // four splits' loads in flight, added in order
+      V4 t[4][W][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const V4* q = reinterpret_cast<const V4*>(p + min(s0 + u, splits - 1) * plane + w * np);
+          t[u][w][0] = q[0];
+          t[u][w][1] = q[1];
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (s0 + u < splits) {
+            acc[w][0] += t[u][w][0];
+            acc[w][1] += t[u][w][1];
+          }
+    }
+  }
+  float v[W][8];
+#pragma unroll
+  for (int w = 0; w < W; ++w) __builtin_memcpy(v[w], acc[w], 32);
+  if constexpr (EL == INT8) {
+    const float s = cnt > 0 ? co.row_scale[row] : 0.f;
+    float sc[8];
+    col8(co.col_scale + col, cnt, sc);
+    scale8(s, sc, v[0]);
+    if constexpr (PAIR) {
+      col8(co.col_scale2 + col, cnt, sc);
+      scale8(s, sc, v[1]);
+    }
+  }
+  bool bad = false;
+  if constexpr (PAIR) {
+    finish_pair8<TO>(ep, co, row, col, cnt, v[0], v[1], lane, bad);
+  } else {
+    float bias[8];
+    bias8(ep, col, cnt, bias);
+    finish8<TO>(ep, row, col, cnt, bias, v[0], lane, bad);
+  }
+  if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
+}
+
+// K: k steps in 16-bit halves
+inline Plan plan_rows(int64_t M, int64_t N, int64_t K, bool pair) {
+  double cost;
+  return plan_gemm(M, pair ? 2 * N : N, K, 1, 64, cost);
+}
+// bytes of the tiles in the workspace; those of a pair's checkpoint pass through it unless tiles are large
+inline size_t rows_workspace(int64_t M, int64_t N, int64_t K, bool pair) {
+  const Plan p = plan_rows(M, N, K, pair);
+  if (!pair) return plan_bytes(p, M, N);
+  return p.tg.splits > 1 || p.tile != LARGE ? 2 * size_t(p.tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
+}
+
+template <class TO, Element EL, bool PAIR>
+lrc_status rows_product(hipStream_t st, const char* name, GemmOperand A, GemmOperand B, int64_t M, int64_t N,
+                        int64_t K, const Epilogue& ep, const Companion& co, float* partial, double flops,
+                        double bytes) {
+  Plan p = plan_rows(M, N, K, PAIR);
+  TileGrid& tg = p.tg;
+  tg.hold = PAIR && ep.codes != nullptr && p.tile != LARGE;
+  const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
+  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  ProfScope scope(name, st, flops, bytes);
+  if (p.tile == LARGE)
+    rows_product_kernel<TO, 4, 2, 4, 8, 2, EL, PAIR><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+  else if (p.tile == SMALL)
+    rows_product_kernel<TO, 2, 2, 4, 4, 2, EL, PAIR><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+  else
+    rows_product_kernel<TO, 4, 1, 1, 4, 4, EL, PAIR><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+  LRC_LAUNCHED();
+  if (tg.splits == 1 && !tg.hold) return LRC_OK;
+  const int64_t np = (N + 7) & ~int64_t(7), blocks = cdiv(N, CKB), threads = M * blocks * 8;
+  if (cdiv(threads, 256) >= (int64_t(1) << 31)) return LRC_EINVAL;
+  rows_finish_kernel<TO, EL, PAIR><<<unsigned(cdiv(threads, 256)), 256, 0, st>>>(partial, tg.splits, M, N, np, blocks,
+                                                                                 ep, co);
+  LRC_LAUNCHED();
+  return LRC_OK;
+}
+
+// ---- few tokens: the weights streamed once ------------------------------------------------
+// A wave holds 16 channels (of each weight) x 16 G tokens and takes a share of k; its weight fragments
+// come straight from memory (a lane reads 16 bytes of one weight row, the four lanes of a row 64 bytes),
+// x from the caches.  The waves' sums are added in order in LDS, then the epilogue.  PIECE: k steps of 64
+// bytes of a row.
+template <Element EL>
+struct RowPiece;
+template <>
+struct RowPiece<BF16> {
+  using T = uint16_t;
+  using Acc = f32x4;
+  static constexpr int K = 32;
+  static __device__ __forceinline__ Acc mma(const u32x4& w, const u32x4& x, Acc c) {
+    return Block<16>::mma(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), c);
+  }
+};
+template <>
+struct RowPiece<INT8> {
+  using T = uint8_t;
+  using Acc = i32x4;
+  static constexpr int K = 64;
+  static __device__ __forceinline__ Acc mma(const u32x4& w, const u32x4& x, Acc c) {
+    return Block<16>::mma_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), c);
+  }
+};
+
+// 16 bytes of a row at any alignment, zeros behind the `left` elements that exist
+template <class T>
+__device__ __forceinline__ u32x4 row_piece(const T* p, int left) {
+  constexpr int EL = 16 / int(sizeof(T)), BITS = 8 * int(sizeof(T)), PER = 4 / int(sizeof(T));
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (left >= EL) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (left > 0) {   // as ld_short
+    T t[EL - 1];
+#pragma unroll
+    for (int e = 0; e < EL - 1; ++e) t[e] = p[min(e, left - 1)];
+#pragma unroll
+    for (int e = 0; e < EL - 1; ++e) v[e / PER] |= e < left ? uint32_t(t[e]) << (BITS * (e % PER)) : 0u;
+  }
+  return v;
+}
+
+template <class TO, Element EL, int W, int G, int NW>
+__global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPiece<EL>::T* __restrict__ x, int64_t ldx,
+                                                           const typename RowPiece<EL>::T* __restrict__ W0, int64_t ld0,
+                                                           const typename RowPiece<EL>::T* __restrict__ W1, int64_t ld1,
+                                                           int n, int64_t N, int K, Epilogue ep, Companion co) {
+  using P = RowPiece<EL>;
+  using T = typename P::T;
+  constexpr int U = 4, E = 16 / int(sizeof(T));   // pieces in flight, elements of a lane's 16 bytes
+  __shared__ __attribute__((aligned(16))) typename P::Acc part[NW * W * G * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  // rows past the end repeat the last one, their results are not written
+  const int64_t ch = min(n0 + (lane & 15), N - 1);
+  const T* w[W];
+  w[0] = W0 + ch * ld0;
+  if constexpr (W == 2) w[1] = W1 + ch * ld1;
+  const T* xr[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) xr[g] = x + int64_t(min(16 * g + (lane & 15), n - 1)) * ldx;
+  const int pieces = (K + P::K - 1) / P::K, per = (pieces + NW - 1) / NW;
+  const int p0 = wave * per, p1 = min(pieces, p0 + per), k0 = E * (lane >> 4);
+  typename P::Acc acc[W][G] = {};
+  int p = p0;
+  for (; (p + U) * P::K <= K && p + U <= p1; p += U) {
+    u32x4 wv[U][W], xv[U][G];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < W; ++j) wv[u][j] = row_piece<T>(w[j] + (p + u) * P::K + k0, E);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int g = 0; g < G; ++g) xv[u][g] = row_piece<T>(xr[g] + (p + u) * P::K + k0, E);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j][g] = P::mma(wv[u][j], xv[u][g], acc[j][g]);
+  }
+  for (; p < p1; ++p) {   // k past the end reads as zero on both sides
+    const int k = p * P::K + k0;
+    u32x4 wv[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) wv[j] = row_piece<T>(w[j] + k, K - k);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const u32x4 xv = row_piece<T>(xr[g] + k, K - k);
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j][g] = P::mma(wv[j], xv, acc[j][g]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+#pragma unroll
+    for (int g = 0; g < G; ++g) part[((wave * W + j) * G + g) * 64 + lane] = acc[j][g];
+  __syncthreads();
+  // accumulator element e of lane l: channel 4 (l / 16) + e, token l % 16
+  using S = std::conditional_t<EL == INT8, int, float>;
+  const S* sums = reinterpret_cast<const S*>(part);
+  for (int i = threadIdx.x; i < G * 256; i += 64 * NW) {
+    const int t = i >> 4, c = i & 15;
+    const int64_t col = n0 + c;
+    if (t >= n || col >= N) continue;
+    const int at = (t >> 4) * 256 + ((c >> 2) * 16 + (t & 15)) * 4 + (c & 3);
+    float v[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      S s = 0;
+#pragma unroll
+      for (int q = 0; q < NW; ++q) s += sums[(q * W + j) * G * 256 + at];
+      v[j] = EL == INT8 ? float(s) * (j ? co.col_scale2 : co.col_scale)[col] * co.row_scale[t] : float(s);
+    }
+    if constexpr (W == 1) {
+      if (ep.bias != nullptr) v[0] += ep.bias[col];
+    }
+    if (W == 2 && ep.z != nullptr) {
+      st_elem(static_cast<TO*>(ep.z) + t * ep.ldz + col, v[0]);
+      st_elem(static_cast<TO*>(co.z) + t * ep.ldz + col, v[W - 1]);
+    }
+    float a[1] = {v[0]};
+    act_apply(ep.act, a);
+    if (W == 2) a[0] *= v[W - 1];
+    if (ep.res != nullptr) a[0] += ld_elem(static_cast<const TO*>(ep.res) + t * ep.ldr + col);
+    st_elem(static_cast<TO*>(ep.y) + t * ep.ldy + col, a[0]);
+  }
+}
+
+// n <= 64
+template <class TO, Element EL, int W>
+lrc_status few_rows(hipStream_t st, const char* name, const void* x, int64_t ldx, const void* W0, int64_t ld0,
+                    const void* W1, int64_t ld1, int64_t n, int64_t N, int64_t K, const Epilogue& ep,
+                    const Companion& co, double flops, double bytes) {
+  using T = typename RowPiece<EL>::T;
+  ProfScope scope(name, st, flops, bytes);
+  const unsigned grid = unsigned(cdiv(N, 16));
+  auto go = [&](auto groups, auto waves) {
+    constexpr int G = decltype(groups)::value, NW = decltype(waves)::value;
+    few_rows_kernel<TO, EL, W, G, NW><<<grid, 64 * NW, 0, st>>>(static_cast<const T*>(x), ldx, static_cast<const T*>(W0),
+                                                                ld0, static_cast<const T*>(W1), ld1, int(n), N, int(K),
+                                                                ep, co);
+  };
+  using std::integral_constant;
+  // few channels: more waves share the k of each
+  if (n > 32)
+    go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+  else if (n > 16)
+    go(integral_constant<int, 2>{}, integral_constant<int, 8>{});
+  else if (grid <= 256)
+    go(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+  else
+    go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  LRC_LAUNCHED();
+  return LRC_OK;
+}
+
+}  // namespace gemm
+}  // namespace lrc

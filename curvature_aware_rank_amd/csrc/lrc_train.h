@@ -313,9 +313,9 @@ struct GemmOperand {
 // The reduction may run over several pairs of planes, one after the other: segment s
 // multiplies plane (pa >> 2 s) & 3 of A with plane (pb >> 2 s) & 3 of B.
 //
-// What the operands' elements are (fp32: one plane).  fp32 operands are addressed in 16-bit halves as
-// the others are: ld and plane count halves, rows are whole pieces of four.
-enum Element { BF16, FP32 };
+// What the operands' elements are (fp32 and int8: one plane).  Those operands are addressed in 16-bit
+// halves as the others are: ld and plane count halves, rows are whole pieces of 16 bytes.
+enum Element { BF16, FP32, INT8 };
 struct GemmSegments {
   int count = 1;
   uint32_t pa = 0, pb = 0;
@@ -336,9 +336,29 @@ template <class TO>
 lrc_status gemm_finish(hipStream_t st, const float* partial, int splits, int64_t M, int64_t N, const Epilogue& ep,
                        const int32_t* skip);
 size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, bool f32);
+// the same for products of `count` segments alone
+size_t gemm_segments_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, int count);
 // estimates in microseconds of an fp32 product, on fp32 operands and on ones split in three
 double gemm_f32_time(int64_t M, int64_t N, int64_t K);
 double gemm_split_time(int64_t M, int64_t N, int64_t K, int KA, int KB);
+
+// ---- shared by the gated block (lrc_linear.hip) ------------------------------------------------
+// Up to three bf16 operands, or checkpoints (exps), written as rows of 8 ceil(cols / 8) bf16 with zeros
+// behind the columns.
+struct LayOut {
+  const void* p;
+  const int8_t* exps;
+  int64_t ld, rows, cols;
+  uint16_t* out;
+};
+lrc_status lay_out_bf16(hipStream_t st, const LayOut* jobs, int count);
+// dx (+)= dz W and dW = dz^T x of an fp32 layer, as lrc_linear_backward without an activation computes
+// them, in its workspace.  x or its checkpoint (xcodes, xexps).
+lrc_status linear_grads_f32(hipStream_t st, int64_t n, int64_t di, int64_t dn, const float* dz, int64_t lddz,
+                            const float* W, int64_t ldw, const float* x, int64_t ldx, const int8_t* xcodes,
+                            const int8_t* xexps, float* dx, int64_t lddx, bool add, float* dW, int64_t lddw, void* ws);
+// rows x cols elements of `size` bytes (2 or 4), leading dim ld, set to zero
+lrc_status zero_rows(hipStream_t st, void* p, int64_t rows, int64_t cols, int64_t ld, int size);
 
 // ---- column sums ---------------------------------------------------------------------
 // out0[c] (c < split) and out1[c - split] (c >= split) = sum over p < parts of

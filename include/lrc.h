@@ -59,6 +59,9 @@ typedef enum { LRC_F32 = 0, LRC_BF16 = 1 } lrc_dtype;
 /* activation of lrc_linear: z, max(z, 0), z Phi(z) (the exact GELU), z / (1 + exp(-z)) */
 typedef enum { LRC_ACT_NONE = 0, LRC_ACT_RELU = 1, LRC_ACT_GELU = 2, LRC_ACT_SILU = 3 } lrc_act;
 
+/* norm of lrc_block_norm: centred and divided by the spread, or divided by the root mean square */
+typedef enum { LRC_NORM_LAYER = 0, LRC_NORM_RMS = 1 } lrc_norm;
+
 #define LRC_CKPT_BLOCK 64              /* channels that share one checkpoint exponent */
 
 /* lrc_accumulate_cov flags */
@@ -495,6 +498,140 @@ lrc_status lrc_linear_backward(const void* dy, lrc_dtype dt, int64_t n_tokens, i
                                int64_t lddx, void* dW, lrc_dtype dw_dt, int64_t lddw, float* db, void* ws,
                                size_t ws_bytes, void* stream);
 size_t lrc_linear_backward_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out);
+
+/*
+ * lrc_gated_linear -- gate and up projection of a gated feed-forward block in one product.
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u
+ * x: n_tokens x d_in (leading dim ldx), Wg and Wu: d_ff x d_in (leading dim ldw, of both), h:
+ * n_tokens x d_ff (leading dim ldh), all dtype `dt`.  The down projection is lrc_linear of h.
+ * What the backward pass needs is kept on request: g and u (n_tokens x d_ff, dtype `dt`, leading dim
+ * ldz), or their 8-bit checkpoints gcodes, gexps and ucodes, uexps, taken from the fp32 values (`info`
+ * as in lrc_pack_activations); both pointers or all four, NULL otherwise.
+ * Sums fp32 (fp32 operands: as lrc_linear); h is formed from the fp32 g and u and rounded once.
+ * bf16: where d_in is a multiple of 8, x, Wg and Wu start on 16 bytes and have leading dims that are
+ * multiples of 8, at most 2^21 (else LRC_EINVAL); other d_in are laid out in the workspace.
+ * 1 <= d_in, d_ff <= 2^20, 0 <= n_tokens < 2^27; n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_gated_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_ff, int64_t ldx,
+                            const void* Wg, const void* Wu, int64_t ldw, lrc_act act, void* h, int64_t ldh, void* g,
+                            void* u, int64_t ldz, int8_t* gcodes, int8_t* gexps, int8_t* ucodes, int8_t* uexps,
+                            int32_t* info, void* ws, size_t ws_bytes, void* stream);
+size_t lrc_gated_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_ff);
+
+/*
+ * lrc_gated_linear_backward -- gradients of lrc_gated_linear from kept g and u.
+ *   dg = dh * u * act'(g),  du = dh * act(g),
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+ * dg and du are the output-gradient streams B of the two projections.  dh: n_tokens x d_ff (leading
+ * dim lddh).  g and u (leading dim ldz) or, with both NULL, the four checkpoint arrays.  x (leading dim
+ * ldx) or, with x NULL, its checkpoint (for dWg and dWu only).  Outputs: dg, du (n_tokens x d_ff, dtype
+ * `dt`, packed), dx (leading dim lddx), dWg, dWu (d_ff x d_in, dtype dw_dt, LRC_F32 or `dt`, leading dim
+ * lddw); dx, dWg, dWu may be NULL.  relu'(0) = 0.
+ * bf16: dx is a product of the rounded streams, both projections in one fp32 sum; dWg and dWu take dg
+ * and du to 16 bits (the stream and what its rounding left out, in one sum; where an entry of x is not
+ * finite the stream alone counts).
+ * fp32: dx is the sum of two products.  bf16 alignment: as lrc_gated_linear for x, Wg and Wu, and dg and
+ * du start on 16 bytes where d_ff is a multiple of 8.  Equal inputs give equal bits; a gradient asked for
+ * alone has the bits of the joint call.  n_tokens == 0 writes zeros to dWg and dWu.
+ */
+lrc_status lrc_gated_linear_backward(const void* dh, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_ff,
+                                     int64_t lddh, const void* Wg, const void* Wu, int64_t ldw, const void* x,
+                                     int64_t ldx, const int8_t* xcodes, const int8_t* xexps, lrc_act act,
+                                     const void* g, const void* u, int64_t ldz, const int8_t* gcodes,
+                                     const int8_t* gexps, const int8_t* ucodes, const int8_t* uexps, void* dg,
+                                     void* du, void* dx, int64_t lddx, void* dWg, void* dWu, lrc_dtype dw_dt,
+                                     int64_t lddw, void* ws, size_t ws_bytes, void* stream);
+size_t lrc_gated_linear_backward_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_ff);
+
+/*
+ * lrc_quantize_tokens -- the symmetric int8 quantiser of LASER Methodology 1 (QAW) on token rows.
+ *   scale = fl32(max|x| / 127),  q = clamp(round_half_even(fl32(x / scale)), -127, 127)
+ * per token (the codes lrc_accumulate_cov's QAW flag forms; lrc_quantize_rows is the same for fp32
+ * rows).  x: n_tokens x d, dtype `dt`, leading dim ldx.  q: n_tokens x d int8, leading dim ldq.  scale:
+ * float[n_tokens].  A token of zeros has scale 0 and codes 0.
+ * info: device int32 or NULL; set to LRC_ENONFINITE when an entry is NaN or Inf, never cleared.  Such an
+ * entry does not count for the scale; an infinity is held as +-127, NaN as 0.
+ * 1 <= d <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_quantize_tokens(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t ldx, int8_t* q,
+                               int64_t ldq, float* scale, int32_t* info, void* stream);
+
+/*
+ * lrc_int8_linear -- linear layer in 8-bit integers: what a layer calibrated with QAW runs as.
+ *   z = (sum_k q_tk p_nk) * wscale_n * xscale_t + bias_n,  y = act(z) + residual
+ * W: codes p (d_out x d_in int8, leading dim ldw) and wscale (float[d_out]), as lrc_quantize_rows writes
+ * them.  The tokens are x (n_tokens x d_in, dtype `dt`, leading dim ldx), quantised within the call as
+ * lrc_quantize_tokens does (`info` as there), or, with x NULL, their codes and scales (leading dim ldxc).
+ * residual and y: n_tokens x d_out, dtype `dt` (leading dims ldr, ldy); residual may be NULL, and may be
+ * y itself; bias: float[d_out] or NULL.
+ * The integer sum is exact, so equal inputs give equal bits at any split of it.  Codes may take all 256
+ * values.  With more than 16 tokens and d_in a multiple of 16, given codes (of W and of the tokens) start
+ * on 16 bytes and have leading dims that are multiples of 16, at most 2^22 (else LRC_EINVAL); other d_in
+ * are laid out in the workspace.
+ * 1 <= d_in < 2^17, 1 <= d_out <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_int8_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out, int64_t ldx,
+                           const int8_t* xcodes, int64_t ldxc, const float* xscale, const int8_t* W, int64_t ldw,
+                           const float* wscale, const float* bias, lrc_act act, const void* residual, int64_t ldr,
+                           void* y, int64_t ldy, int32_t* info, void* ws, size_t ws_bytes, void* stream);
+size_t lrc_int8_linear_workspace(int64_t n_tokens, int64_t d_in, int64_t d_out);
+
+/*
+ * lrc_int8_gated_linear -- lrc_gated_linear in 8-bit integers (forward only).
+ *   g, u = the two integer products with their scales,  h = act(g) * u
+ * Wg, Wu: d_ff x d_in int8 (leading dims ldwg, ldwu) with gscale, uscale (float[d_ff]); everything else
+ * as lrc_int8_linear.  h: n_tokens x d_ff, dtype `dt`, leading dim ldh.
+ */
+lrc_status lrc_int8_gated_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_ff,
+                                 int64_t ldx, const int8_t* xcodes, int64_t ldxc, const float* xscale,
+                                 const int8_t* Wg, int64_t ldwg, const float* gscale, const int8_t* Wu, int64_t ldwu,
+                                 const float* uscale, lrc_act act, void* h, int64_t ldh, int32_t* info, void* ws,
+                                 size_t ws_bytes, void* stream);
+size_t lrc_int8_gated_linear_workspace(int64_t n_tokens, int64_t d_in, int64_t d_ff);
+
+/*
+ * lrc_block_norm -- what lies between two blocks of a residual network, in one pass.
+ *   p = norm(b) * post_gamma + post_beta  (post != 0; else p = b)
+ *   s = residual + scale * gate * p,   h = norm(s) * gamma + beta
+ * norm is layer norm ((x - mean) * rstd, LRC_NORM_LAYER) or RMS norm (x * rstd without a mean,
+ * LRC_NORM_RMS, which takes no beta), rstd = 1 / sqrt(mean square of the centred values + eps), eps >= 0.
+ * b: the block's output, residual: the stream, NULL for zero; both n_tokens x d, dtype `dt` (leading dims
+ * ldb, ldr).  gate: float[d] or NULL for 1.  post_gamma, post_beta, gamma, beta: float[d] or NULL for 1 and
+ * 0.  Outputs, any of which may be NULL: s (leading dim lds; may be residual or b itself), h (leading dim
+ * ldh), the statistics of b (where post) and of s that lrc_block_norm_backward takes (float[n_tokens]; RMS
+ * has no means; those of s come with h or q), and q and qscale (both or neither; leading dim ldq): h as
+ * lrc_quantize_tokens holds it, the same bits, for lrc_int8_linear (`info` as there).  At least one of s, h
+ * and q.  Sums fp32; h is formed from the fp32 s.  Where a mean square passes the range of fp32, rstd is 0.
+ * 1 <= d <= 16384, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
+ */
+lrc_status lrc_block_norm(const void* b, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t ldb, const void* residual,
+                          int64_t ldr, lrc_norm kind, float eps, int post, const float* post_gamma,
+                          const float* post_beta, const float* gate, float scale, const float* gamma,
+                          const float* beta, void* s, int64_t lds, void* h, int64_t ldh, float* mean_b, float* rstd_b,
+                          float* mean_s, float* rstd_s, int8_t* q, int64_t ldq, float* qscale, int32_t* info,
+                          void* stream);
+
+/*
+ * lrc_block_norm_backward -- gradients of lrc_block_norm.
+ *   t = ds + (dh * gamma taken back through the norm of s)      total gradient of s
+ *   dresidual = t,  db = scale * gate * t (post: * post_gamma, taken back through the norm of b)
+ *   dgamma = sum dh s^, dbeta = sum dh, dpost_gamma = sum scale gate t b^, dpost_beta = sum scale gate t,
+ *   dgate = sum scale t p      (sums over tokens, ^: normalised with the given statistics)
+ * dh or ds may be NULL (zero), not both; without dh there are no dgamma and dbeta.  s and its statistics are
+ * needed with dh; b and, where post, its statistics for db through a post-norm, dpost_* and dgate.  s, b,
+ * mean_*, rstd_* as lrc_block_norm took and wrote them (s in dtype `dt`).  Any output may be NULL; dresidual
+ * may be ds itself.  The token sums run over fixed chunks in a fixed order (equal inputs give equal bits).
+ * n_tokens == 0 writes zeros to the parameters' gradients.  Sizes as lrc_block_norm.
+ */
+lrc_status lrc_block_norm_backward(const void* dh, lrc_dtype dt, int64_t n_tokens, int64_t d, int64_t lddh,
+                                   const void* ds, int64_t ldds, const void* s, int64_t lds, const void* b,
+                                   int64_t ldb, const float* mean_b, const float* rstd_b, const float* mean_s,
+                                   const float* rstd_s, lrc_norm kind, int post, const float* post_gamma,
+                                   const float* post_beta, const float* gate, float scale, const float* gamma,
+                                   void* dresidual, int64_t lddr, void* db, int64_t lddb, float* dgamma,
+                                   float* dbeta, float* dpost_gamma, float* dpost_beta, float* dgate, void* ws,
+                                   size_t ws_bytes, void* stream);
+size_t lrc_block_norm_backward_workspace(int64_t n_tokens, int64_t d);
 
 /*
  * Measurement support (benchmarks and profilers; not needed for results).
