@@ -1012,7 +1012,7 @@ def lrc_block_norm(b: torch.Tensor, residual=None, kind: str = "rms", eps: float
 
     Returns (s, h, stats, quantized, info): s and h like b (None where not needed, h None with quantize), stats
     (mean_b, rstd_b, mean_s, rstd_s) for the backward pass (None where there is none), quantized (codes, scale) or
-    None; info (sticky LRC_ENONFINITE of the codes) is None unless given or with quantize."""
+    None; info (int32 (1,), sticky LRC_ENONFINITE of the codes) is None unless given."""
     b, ldb = _rows(b, "b")
     dt, dev = _dtype_code(b), b.device
     n, d = b.shape
@@ -1033,7 +1033,7 @@ def lrc_block_norm(b: torch.Tensor, residual=None, kind: str = "rms", eps: float
     s = torch.empty(n, d, dtype=b.dtype, device=dev) if need_s else None
     h = torch.empty(n, d, dtype=b.dtype, device=dev) if need_h else None
     quantized = (torch.empty(n, d, dtype=torch.int8, device=dev), row(True)) if quantize else None
-    if quantize or info is not None:
+    if info is not None:
         info = _info(info, dev)
     q, qs = quantized or (None, None)
     _run("lrc_block_norm", dev, lib.lrc_block_norm, _ptr(b), dt, n, d, ldb, _ptr(residual), ldr, code, float(eps),

@@ -194,16 +194,18 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_kernel(NormForwar
 #pragma unroll
     for (int k = 0; k < V; ++k) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[k][e] = S::col(8 * k + e, l) < d ? round_to(v[8 * k + e], static_cast<const T*>(nullptr)) : 0.f;
+      for (int e = 0; e < 8; ++e)
+        p[k][e] = S::col(8 * k + e, l) < d ? round_to(v[8 * k + e], static_cast<const T*>(nullptr)) : 0.f;
       m = mag8(p[k], m, bad);
     }
     const float qs = token_step(reduce.largest(m, red, wave, lane, group));
     if (!live) continue;
     if (l == 0) a.qscale[t] = qs;
+    const float inv = token_inverse(qs);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c = (k * S::LANES + l) * 8;
-      if (c < d) st8_token_codes(a.q + t * a.ldq + c, d - c, p[k], qs);
+      if (c < d) st8_token_codes(a.q + t * a.ldq + c, d - c, p[k], qs, inv, bad);
     }
   }
   if (a.info != nullptr && bad) *a.info = LRC_ENONFINITE;

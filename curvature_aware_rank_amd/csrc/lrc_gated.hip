@@ -10,6 +10,7 @@
 // rounding).  Sums fp32 throughout.
 // fp32: the products are those of the linear layer (fp32 instructions, or six of bf16 pieces), the gate an
 // elementwise pass: the products take 10 to 100 times as long.
+#include "lrc_operand.h"
 #include "lrc_pair.h"
 
 namespace lrc {
@@ -18,7 +19,6 @@ namespace {
 constexpr int ET = 256;
 constexpr int64_t WIDE = int64_t(1) << 20;       // channels (a tile's offsets hold their rows)
 constexpr int64_t FEW = 8;                       // tokens up to which the weights are streamed
-int64_t round8(int64_t v) { return (v + 7) & ~int64_t(7); }
 
 bool sizes_ok(int64_t n, int64_t i, int64_t f) {
   return n >= 0 && n < GEMM_MAX_K && i >= 1 && i <= WIDE && f >= 1 && f <= WIDE;
@@ -97,8 +97,13 @@ __device__ __forceinline__ void put_grad(T* o, uint16_t* copy, uint16_t* low, in
     st8(low + at8, 8, r);
   }
 }
+// The workgroups behind `blocks` lay out the products' other operands, so that those cost no launch of their own.
 template <class T, bool CK>
-__global__ __launch_bounds__(ET) void gated_dz_kernel(GatePass<T> p) {
+__global__ __launch_bounds__(ET) void gated_dz_kernel(GatePass<T> p, int64_t blocks, OperandJobs jobs) {
+  if (blockIdx.x >= blocks) {
+    if constexpr (std::is_same<T, uint16_t>::value) lay_operand<T>(jobs, blockIdx.x - blocks, nullptr);
+    return;
+  }
   const int64_t i = int64_t(blockIdx.x) * ET + threadIdx.x, per = p.w8 / 8;
   const int64_t t = i / per, c = i % per * 8;
   if (t >= p.n) return;
@@ -164,15 +169,15 @@ lrc_status gated_bf16(hipStream_t st, GatedArgs& a, void* ws) {
   const double flops = 4.0 * double(a.n) * double(a.df) * double(a.di);
   const double bytes = 2.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df);
   if (a.n <= FEW && a.ep.codes == nullptr)
-    return gemm::few_rows<uint16_t, BF16, 2>(st, "gated_rows_kernel", a.x, a.ldx, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
+    return gemm::few_rows<uint16_t, BF16, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
                                              a.di, a.ep, a.co, flops, bytes);
   const GatedRoom room = forward_room(ws, LRC_BF16, a.n, a.di, a.df);
   GemmOperand x = {static_cast<const uint16_t*>(a.x), a.ldx, 0}, g = {static_cast<const uint16_t*>(a.Wg), a.ldw, 0},
               u = {static_cast<const uint16_t*>(a.Wu), a.ldw, 0};
   if (a.di % 8 != 0) {
-    const LayOut jobs[3] = {{a.x, nullptr, a.ldx, a.n, a.di, room.x},
-                            {a.Wg, nullptr, a.ldw, a.df, a.di, room.wg},
-                            {a.Wu, nullptr, a.ldw, a.df, a.di, room.wu}};
+    const OperandJobs jobs = {{bf16_job(a.x, nullptr, a.ldx, a.n, a.di, room.x),
+                               bf16_job(a.Wg, nullptr, a.ldw, a.df, a.di, room.wg),
+                               bf16_job(a.Wu, nullptr, a.ldw, a.df, a.di, room.wu)}};
     LRC_TRY(lay_out_bf16(st, jobs, 3));
     const int64_t w8 = round8(a.di);
     x = {room.x, w8, 0};
@@ -220,7 +225,7 @@ GatedRoom backward_room(void* ws, int dt, int64_t n, int64_t di, int64_t df) {
     r.x = cv.take<uint16_t>(size_t(n) * i8);
     if (di % 8 != 0) r.wg = cv.take<uint16_t>(size_t(2) * df * i8);
     r.partial = cv.take<float>(std::max(gemm_segments_workspace(n, di, df, K_ROWS, K_COLS, 2),
-                                        gemm_segments_workspace(df, di, n, K_COLS, K_COLS, 2)) / 4);
+                                        gemm_weight_pair_workspace(df, di, n)) / 4);
   }
   r.bytes = cv.bytes();
   return r;
@@ -247,7 +252,7 @@ struct GatedBack {
 };
 
 template <class T>
-lrc_status gate_backward(hipStream_t st, const GatedBack& a, const GatedRoom& room, bool low) {
+lrc_status gate_backward(hipStream_t st, const GatedBack& a, const GatedRoom& room, bool low, const OperandJobs& jobs) {
   GatePass<T> p = {};
   p.dh = static_cast<const T*>(a.dh);
   p.g = static_cast<const T*>(a.g);
@@ -274,21 +279,22 @@ lrc_status gate_backward(hipStream_t st, const GatedBack& a, const GatedRoom& ro
     p.lg = room.low;
     p.lu = room.low + plane;
   }
-  const int64_t grid = cdiv(a.n * (p.w8 / 8), ET);
+  const int64_t blocks = cdiv(a.n * (p.w8 / 8), ET);
+  const int64_t grid = blocks + jobs.job[0].blocks + jobs.job[1].blocks + jobs.job[2].blocks;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   const double e = sizeof(T), kept = a.g == nullptr ? 1 : e;
   ProfScope scope("gated_dz_kernel", st, 0.0, double(a.n) * double(a.df) * (3 * e + 2 * kept + (low ? 4 : 0)));
   if (a.g == nullptr)
-    gated_dz_kernel<T, true><<<unsigned(grid), ET, 0, st>>>(p);
+    gated_dz_kernel<T, true><<<unsigned(grid), ET, 0, st>>>(p, blocks, jobs);
   else
-    gated_dz_kernel<T, false><<<unsigned(grid), ET, 0, st>>>(p);
+    gated_dz_kernel<T, false><<<unsigned(grid), ET, 0, st>>>(p, blocks, jobs);
   LRC_LAUNCHED();
   return LRC_OK;
 }
 
 lrc_status gated_back_f32(hipStream_t st, const GatedBack& a, void* ws) {
   const GatedRoom room = backward_room(ws, LRC_F32, a.n, a.di, a.df);
-  LRC_TRY(gate_backward<float>(st, a, room, false));
+  LRC_TRY(gate_backward<float>(st, a, room, false, OperandJobs{}));
   auto grads = [&](const void* dz, const void* W, void* dW, bool add) -> lrc_status {
     if (a.dx == nullptr && dW == nullptr) return LRC_OK;
     return linear_grads_f32(st, a.n, a.di, a.df, static_cast<const float*>(dz), a.df, static_cast<const float*>(W),
@@ -306,8 +312,7 @@ int64_t apart(const uint16_t* from, const uint16_t* to) {
 
 lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
   const GatedRoom room = backward_room(ws, LRC_BF16, a.n, a.di, a.df);
-  const bool dw = a.dWg != nullptr || a.dWu != nullptr, held = a.x == nullptr;
-  LRC_TRY(gate_backward<uint16_t>(st, a, room, dw));
+  const bool dw = a.dWg != nullptr, held = a.x == nullptr;
   const int64_t f8 = round8(a.df), i8 = round8(a.di), plane = a.n * f8;
   const uint16_t *dg = static_cast<const uint16_t*>(a.dg), *du = static_cast<const uint16_t*>(a.du);
   if (room.dz != nullptr) {
@@ -317,23 +322,22 @@ lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
   const uint16_t *wg = static_cast<const uint16_t*>(a.Wg), *wu = static_cast<const uint16_t*>(a.Wu);
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
   int64_t ldw = a.ldw, ldx = a.ldx;
-  LayOut jobs[3];
-  int count = 0;
+  OperandJobs jobs;
+  if (dw && (held || a.di % 8 != 0)) {
+    jobs.job[0] = bf16_job(held ? static_cast<const void*>(a.xcodes) : a.x, held ? a.xexps : nullptr,
+                           held ? a.di : a.ldx, a.n, a.di, room.x);
+    x = room.x;
+    ldx = i8;
+  }
   if (a.dx != nullptr && room.wg != nullptr) {
     uint16_t* second = room.wg + a.df * i8;
-    jobs[count++] = {a.Wg, nullptr, a.ldw, a.df, a.di, room.wg};
-    jobs[count++] = {a.Wu, nullptr, a.ldw, a.df, a.di, second};
+    jobs.job[1] = bf16_job(a.Wg, nullptr, a.ldw, a.df, a.di, room.wg);
+    jobs.job[2] = bf16_job(a.Wu, nullptr, a.ldw, a.df, a.di, second);
     wg = room.wg;
     wu = second;
     ldw = i8;
   }
-  if (dw && (held || a.di % 8 != 0)) {
-    jobs[count++] = {held ? static_cast<const void*>(a.xcodes) : a.x, held ? a.xexps : nullptr, held ? a.di : a.ldx,
-                     a.n, a.di, room.x};
-    x = room.x;
-    ldx = i8;
-  }
-  LRC_TRY(lay_out_bf16(st, jobs, count));
+  LRC_TRY(gate_backward<uint16_t>(st, a, room, dw, jobs));
   const double product = 2.0 * double(a.n) * double(a.df) * double(a.di);
   if (a.dx != nullptr) {
     Epilogue ep;
@@ -347,24 +351,18 @@ lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
                                                  nullptr, 2 * product,
                                                  2.0 * (2.0 * double(a.n) * a.df + 2.0 * double(a.df) * a.di + double(a.n) * a.di))));
   }
-  auto weight = [&](const uint16_t* dz, const uint16_t* low, void* dW) -> lrc_status {
-    if (dW == nullptr) return LRC_OK;
-    Epilogue ep;
-    ep.y = dW;
-    ep.ldy = a.lddw;
-    GemmSegments seg;
-    seg.count = 2;
-    seg.pa = 1u;   // the left-out piece first
-    const GemmOperand A = {dz, f8, apart(dz, low)}, B = {x, ldx, 0};
-    const double bytes = 2.0 * (double(a.n) * a.df * 2 + double(a.n) * a.di + double(a.df) * a.di);
-    if (a.dw_dt == LRC_F32)
-      return gemm_bf16<float, K_COLS, K_COLS>(st, "gated_dw_kernel", A, B, a.df, a.di, a.n, seg, ep, room.partial,
-                                              nullptr, 2 * product, bytes);
-    return gemm_bf16<uint16_t, K_COLS, K_COLS>(st, "gated_dw_kernel", A, B, a.df, a.di, a.n, seg, ep, room.partial,
-                                               nullptr, 2 * product, bytes);
+  if (!dw) return LRC_OK;
+  Epilogue ep;
+  ep.y = a.dWg;
+  ep.y2 = a.dWu;
+  ep.ldy = a.lddw;
+  const GemmOperand A1 = {dg, f8, apart(dg, room.low)}, A2 = {du, f8, apart(du, room.low + plane)}, B = {x, ldx, 0};
+  const double bytes = 2.0 * (4.0 * double(a.n) * a.df + double(a.n) * a.di + 2.0 * double(a.df) * a.di);
+  auto go = [&](auto tag) {
+    return gemm_weight_pair<decltype(tag)>(st, "gated_dw_kernel", A1, A2, B, a.df, a.di, a.n, ep, room.partial,
+                                           4 * product, bytes);
   };
-  LRC_TRY(weight(dg, room.low, a.dWg));
-  return weight(du, room.low + plane, a.dWu);
+  return a.dw_dt == LRC_F32 ? go(float{}) : go(uint16_t{});
 }
 
 bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
@@ -428,10 +426,11 @@ extern "C" lrc_status lrc_gated_linear_backward(const void* dh, lrc_dtype dt, in
                                                 const int8_t* ucodes, const int8_t* uexps, void* dg, void* du,
                                                 void* dx, int64_t lddx, void* dWg, void* dWu, lrc_dtype dw_dt,
                                                 int64_t lddw, void* ws, size_t ws_bytes, void* stream) {
-  const bool dw = dWg != nullptr || dWu != nullptr;
+  const bool dw = dWg != nullptr;
   if ((dt != LRC_F32 && dt != LRC_BF16) || !act_ok(act)) return LRC_EDTYPE;
   if (dw && dw_dt != LRC_F32 && dw_dt != dt) return LRC_EDTYPE;
-  if (!sizes_ok(n_tokens, d_in, d_ff) || lddh < d_ff || (g != nullptr && ldz < d_ff)) return LRC_EINVAL;
+  if (!sizes_ok(n_tokens, d_in, d_ff) || lddh < d_ff || (g != nullptr && ldz < d_ff) || (dWu != nullptr) != dw)
+    return LRC_EINVAL;
   if ((dx != nullptr && (lddx < d_in || ldw < d_in)) || (dw && (lddw < d_in || (x != nullptr && ldx < d_in))))
     return LRC_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);

@@ -34,6 +34,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_bf16_kernel(GemmOperand 
                                                                     const int32_t* __restrict__ skip) {
   gemm_tile<TO, KA, KB, MF, WM, WN, FM, FN, KS, NST, SEG, EL>(A, B, M, N, K, seg, tg, ep, partial, skip);
 }
+template <class TO, int MF, int WM, int WN, int FM, int FN, int KS, int NST>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_weight_pair_kernel(GemmOperand A1, GemmOperand A2, GemmOperand B,
+                                                                           int64_t M, int64_t N, int64_t K,
+                                                                           GemmSegments seg, TileGrid tg, Epilogue ep,
+                                                                           float* __restrict__ partial) {
+  Companion co;
+  co.B = A2;
+  gemm_tile<TO, K_COLS, K_COLS, MF, WM, WN, FM, FN, KS, NST, 2, BF16>(A1, B, M, N, K, seg, tg, ep, partial, nullptr, co);
+}
 
 // Sum of the splits' tiles in split order, then the epilogue.  One lane per eight columns, the
 // eight lanes of a 64-column block together.
@@ -44,7 +53,8 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
   if (skip != nullptr && *skip != 0) return;
   const int64_t g = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 3;
   const int lane = threadIdx.x & 63;
-  const int64_t row = g / blocks, col = g % blocks * CKB + 8 * (lane & 7);
+  int64_t row = g / blocks;
+  const int64_t col = g % blocks * CKB + 8 * (lane & 7);
   const int64_t left = row < M ? N - col : 0;
   const int cnt = int(left < 0 ? 0 : left > 8 ? 8 : left);
   float v[8] = {};
@@ -71,6 +81,10 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const float* __restric
   bool bad = false;
   float bias[8];
   bias8(ep, col, cnt, bias);
+  if (ep.y2 != nullptr && 2 * row >= M) {   // the second of two products
+    row -= M / 2;
+    ep.y = ep.y2;
+  }
   finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);
   if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
 }
@@ -145,7 +159,7 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
     else if (p.tile == SMALL)
       gemm_bf16_kernel<TO, KA, KB, 16, 2, 2, 4, 4, 64, 2, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
-    else if constexpr (SEG == 0 || SEG == 2 || BITS)
+    else if constexpr (SEG == 0 || BITS)
       gemm_bf16_kernel<TO, KA, KB, 16, 4, 1, 1, 4, 64, 4, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
     else
@@ -161,9 +175,8 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   } else if (seg.count == 1) {
     if constexpr (BITS || KA == K_COLS) launched = launch(integral_constant<int, 0>{}, integral_constant<Element, BF16>{});
   } else if (seg.count == 2) {
-    constexpr int WAY = KA == K_COLS ? 2 : 1;
-    if constexpr (KB == K_COLS && (BITS || WAY == 2))
-      launched = launch(integral_constant<int, WAY>{}, integral_constant<Element, BF16>{});
+    if constexpr (BITS && KA == K_ROWS && KB == K_COLS)
+      launched = launch(integral_constant<int, 1>{}, integral_constant<Element, BF16>{});
   } else if constexpr (!BITS) {
     launched = launch(integral_constant<int, 1>{}, integral_constant<Element, BF16>{});
   }
@@ -173,6 +186,47 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   const int splits = tg.splits;
   return gemm_finish<TO>(st, partial, splits, M, N, ep, skip);
 }
+
+// Tiles and splits as for one product of twice the rows, each product's own edge apart.
+static Plan plan_weight_pair(int64_t M, int64_t N, int64_t K) {
+  double cost;
+  Plan p = plan_gemm(2 * M, N, K, 2, 32, cost);
+  TileGrid& tg = p.tg;
+  const int edge = p.tile == LARGE ? 256 : p.tile == SMALL ? 128 : 64;
+  tg.nm = cdiv(M, edge);
+  tg.half = tg.nm * tg.nn;
+  tg.tiles = 2 * tg.half;
+  tg.per_xcd = int(cdiv(tg.tiles, NXCD));
+  return p;
+}
+size_t gemm_weight_pair_workspace(int64_t M, int64_t N, int64_t K) {
+  return plan_bytes(plan_weight_pair(M, N, K), 2 * M, N);
+}
+template <class TO>
+lrc_status gemm_weight_pair(hipStream_t st, const char* name, GemmOperand A1, GemmOperand A2, GemmOperand B, int64_t M,
+                            int64_t N, int64_t K, const Epilogue& ep, float* partial, double flops, double bytes) {
+  const Plan p = plan_weight_pair(M, N, K);
+  const TileGrid& tg = p.tg;
+  const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
+  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  GemmSegments seg;
+  seg.count = 2;
+  seg.pa = 1u;
+  ProfScope scope(name, st, flops, bytes);
+  const unsigned g = unsigned(grid);
+  if (p.tile == LARGE)
+    gemm_weight_pair_kernel<TO, 32, 4, 2, 2, 4, 32, 4><<<g, 512, 0, st>>>(A1, A2, B, M, N, K, seg, tg, ep, partial);
+  else if (p.tile == SMALL)
+    gemm_weight_pair_kernel<TO, 16, 2, 2, 4, 4, 64, 2><<<g, 256, 0, st>>>(A1, A2, B, M, N, K, seg, tg, ep, partial);
+  else
+    gemm_weight_pair_kernel<TO, 16, 4, 1, 1, 4, 64, 4><<<g, 256, 0, st>>>(A1, A2, B, M, N, K, seg, tg, ep, partial);
+  LRC_LAUNCHED();
+  return tg.splits == 1 ? LRC_OK : gemm_finish<TO>(st, partial, tg.splits, 2 * M, N, ep, nullptr);
+}
+template lrc_status gemm_weight_pair<float>(hipStream_t, const char*, GemmOperand, GemmOperand, GemmOperand, int64_t,
+                                            int64_t, int64_t, const Epilogue&, float*, double, double);
+template lrc_status gemm_weight_pair<uint16_t>(hipStream_t, const char*, GemmOperand, GemmOperand, GemmOperand, int64_t,
+                                               int64_t, int64_t, const Epilogue&, float*, double, double);
 
 #define LRC_GEMM(TO, KA, KB)                                                                                   \
   template lrc_status gemm_bf16<TO, KA, KB>(hipStream_t, const char*, GemmOperand, GemmOperand, int64_t, int64_t, \

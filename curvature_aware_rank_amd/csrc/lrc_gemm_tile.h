@@ -190,12 +190,13 @@ struct TileGrid {
   int per_xcd, splits;
   int steps_per_split;   // stages of one split
   int steps;             // stages of one segment
+  int64_t half = 0;      // of two products in one launch: tiles of each
   bool hold = false;     // the tiles go to the workspace also where k is not split
 };
 
 // What a product of 8-bit integers, or of two weights that share x, has besides.
 struct Companion {
-  GemmOperand B;                  // the second weight (u = x B^T)
+  GemmOperand B = {};             // the second weight (u = x B^T)
   void* z = nullptr;              // u, kept as the epilogue keeps z, which is g
   int8_t* codes = nullptr;
   int8_t* exps = nullptr;
@@ -243,7 +244,8 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
 }
 
 // EL = INT8: the operands are addressed in 16-bit halves, K counts those; sums are exact int32.
-// SEG: 0, one segment; 1, several; 2, two, and a sum of the first that is not finite counts as zero.
+// SEG: 0, one segment; 1, several; 2, two, and a sum of the first that is not finite counts as zero, of two products in
+// one launch (the second one's A is co.B, its y ep.y2).
 // PAIR: the tile holds BN / 2 channels of each of two weights; a wave's first FN MF / 2 columns are the
 // first one's, the others the same channels of the second.
 template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, int SEG, Element EL,
@@ -273,8 +275,9 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   const int split = local / tg.per_xcd;
   const int64_t ti = int64_t(b % NXCD) * tg.per_xcd + local % tg.per_xcd;
   if (ti >= tg.tiles) return;
+  const bool other = SEG == 2 && ti >= tg.half;   // of two products, the second
   int64_t tm, tn;
-  tile_at(ti, tg.nm, tg.nn, tm, tn);
+  tile_at(other ? ti - tg.half : ti, tg.nm, tg.nn, tm, tn);
   const int64_t m0 = tm * BM, n0 = tn * (PAIR ? BN / 2 : BN);
 
   const int lane = threadIdx.x & 63;
@@ -282,7 +285,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   const int wr = wave / WN, wc = wave % WN;
   SA sa;
   SB sb;
-  sa.init(A, m0, M, wave, lane);
+  sa.init(other ? co.B : A, m0, M, wave, lane);
   if constexpr (PAIR)
     sb.init(SB::second(wave) ? co.B : B, n0, N, wave, lane);
   else
@@ -518,8 +521,10 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
           finish_pair8<TO>(ep, co, row, col, cnt, v, u, lane, bad);
         }
       } else if (tg.splits > 1) {
-        const int64_t np = (N + 7) & ~int64_t(7);
-        if (cnt > 0) st8(partial + (int64_t(split) * M + row) * np + col, 8, v);
+        const int64_t np = (N + 7) & ~int64_t(7), at = SEG == 2 ? (2 * split + other) * M + row : int64_t(split) * M + row;
+        if (cnt > 0) st8(partial + at * np + col, 8, v);
+      } else if constexpr (SEG == 2) {
+        if (cnt > 0) st8(static_cast<TO*>(other ? ep.y2 : ep.y) + row * ep.ldy + col, cnt, v);
       } else {
         if constexpr (EL == INT8) scale8(row < M ? co.row_scale[row] : 0.f, sc, v);
         finish8<TO>(ep, row, col, cnt, bias, v, lane, bad);

@@ -4,7 +4,6 @@
 //   z = s_t w_n sum_k q_tk p_nk:  the integer sum is exact (below 2^31 for fewer than 2^17 input channels),
 // and scales, bias, activation, residual or the gate's product are applied to it in the epilogue.
 #include "lrc_pair.h"
-#include "lrc_rows.h"
 
 namespace lrc {
 namespace {
@@ -42,10 +41,11 @@ __global__ __launch_bounds__(row_threads(WPR)) void quantize_tokens_kernel(const
     const float s = token_step(row_max<WPR>(m, red[slot], l >> 6, lane, group));
     if (t >= n) continue;
     if (l == 0) scale[t] = s;
+    const float inv = token_inverse(s);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c = (k * S::LANES + l) * 8;
-      if (c < dq) st8_token_codes(q + t * ldq + c, dq - c, v[k], s);
+      if (c < dq) st8_token_codes(q + t * ldq + c, dq - c, v[k], s, inv, bad);
     }
   }
   if (info != nullptr && bad) *info = LRC_ENONFINITE;
@@ -64,10 +64,11 @@ __global__ __launch_bounds__(QT) void quantize_wide_kernel(const T* __restrict__
     m = mag8(v, m, bad);
   }
   const float s = token_step(row_max<4>(m, red, threadIdx.x >> 6, threadIdx.x & 63, 0));
+  const float inv = token_inverse(s);
   if (threadIdx.x == 0) scale[t] = s;
   for (int c = 8 * threadIdx.x; c < dq; c += 8 * QT) {
     ld8(x + t * ldx + c, d - c, v);
-    st8_token_codes(q + t * ldq + c, dq - c, v, s);
+    st8_token_codes(q + t * ldq + c, dq - c, v, s, inv, bad);
   }
   if (info != nullptr && bad) *info = LRC_ENONFINITE;
 }
@@ -173,18 +174,23 @@ lrc_status int8_product(hipStream_t st, const Int8Args& a, void* ws, int32_t* in
   co.row_scale = a.xs;
   co.col_scale = a.ws[0];
   co.col_scale2 = a.ws[1];
+  constexpr int W = PAIR ? 2 : 1;
+  const double flops = 2.0 * W * double(a.n) * double(a.dn) * double(a.di);
+  const double bytes = double(a.n) * a.di + W * double(a.dn) * a.di + double(sizeof(T)) * double(a.n) * a.dn;
+  auto few = [&](const void* x, int64_t ld, bool own) {
+    Epilogue ep = a.ep;
+    ep.info = own ? info : nullptr;
+    return gemm::few_rows<T, INT8, W>(st, "int8_rows_kernel", x, ld, own, a.w[0], a.ldw[0], a.w[1], a.ldw[1], a.n,
+                                      a.dn, a.di, ep, co, flops, bytes);
+  };
+  if (a.x != nullptr && gemm::own_tokens(a.n, a.di)) return few(a.x, a.ldx, true);
   if (a.x != nullptr) {
     LRC_TRY(quantize(st, static_cast<const T*>(a.x), a.n, a.di, a.ldx, room.x, k, k, room.scale, info));
     xq = room.x;
     ldx = k;
     co.row_scale = room.scale;
   }
-  constexpr int W = PAIR ? 2 : 1;
-  const double flops = 2.0 * W * double(a.n) * double(a.dn) * double(a.di);
-  const double bytes = double(a.n) * a.di + W * double(a.dn) * a.di + double(sizeof(T)) * double(a.n) * a.dn;
-  if (a.n <= FEW)
-    return gemm::few_rows<T, INT8, W>(st, "int8_rows_kernel", xq, ldx, a.w[0], a.ldw[0], a.w[1], a.ldw[1], a.n, a.dn,
-                                      a.di, a.ep, co, flops, bytes);
+  if (a.n <= FEW) return few(xq, ldx, false);
   const int8_t* w[2] = {a.w[0], a.w[1]};
   int64_t ldw[2] = {a.ldw[0], a.ldw[1]};
   if (a.di % 16 != 0) {   // rows of no whole pieces are laid out anew

@@ -7,7 +7,7 @@
 //   dW       m = output channel, n = input channel, k = token;   A, B = columns of dz and x
 // An operand is therefore a row-major matrix whose rows run along k (K_ROWS) or whose rows
 // are the k steps (K_COLS), or a checkpoint of the latter kind (K_CODES).
-#include "lrc_train.h"
+#include "lrc_operand.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -15,7 +15,6 @@
 namespace lrc {
 namespace {
 
-constexpr int LT = 256;
 
 __device__ __forceinline__ int64_t cdiv_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -467,94 +466,11 @@ bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
 //   infinity would meet one of the other sign from the lower pieces.  So an entry that is not finite
 //   or passes SPLIT_MAX raises `flag`, and the product is done on fp32 tiles instead; without one no
 //   sum of up to GEMM_MAX_K terms passes 2^127.
-constexpr float SPLIT_MAX = 0x1p50f;
-template <class T>
-__device__ __forceinline__ void split_store(uint16_t* o, int64_t w8, float (&v)[8], bool& bad);
-template <>
-__device__ __forceinline__ void split_store<uint16_t>(uint16_t* o, int64_t, float (&v)[8], bool&) {
-  st8(o, 8, v);
-}
-template <>
-__device__ __forceinline__ void split_store<float>(uint16_t* o, int64_t w8, float (&v)[8], bool& bad) {
-  float h[8], m[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    bad |= !(fabsf(v[e]) <= SPLIT_MAX);
-    h[e] = round_to(v[e], static_cast<const uint16_t*>(nullptr));
-    const float r = v[e] - h[e];
-    m[e] = round_to(r, static_cast<const uint16_t*>(nullptr));
-    v[e] = r - m[e];
-  }
-  st8(o, 8, h);
-  st8(o + w8, 8, m);
-  st8(o + 2 * w8, 8, v);
-}
-// Up to three operands in one launch: a workgroup belongs to the job its index falls into.
-struct OperandJob {
-  const void* p = nullptr;
-  const int8_t* exps = nullptr;   // codes if not NULL
-  uint16_t* out = nullptr;
-  int64_t ld = 0, nb = 0, rows = 0, cols = 0, w8 = 0, blocks = 0;
-  int planes = 1;                      // of bf16; 0: one of fp32
-  unsigned raises = 0;                 // the products that read it, bit i the one that flag[i] moves
-};
-constexpr int JOB_ROWS = 4;   // rows of a thread
-struct OperandJobs {
-  OperandJob job[3];
-};
 template <class T>
 __global__ __launch_bounds__(LT) void operand_kernel(OperandJobs jobs, int32_t* __restrict__ flag) {
-  int64_t block = blockIdx.x;
-  int q = 0;
-  while (q < 2 && block >= jobs.job[q].blocks) block -= jobs.job[q++].blocks;
-  const OperandJob& j = jobs.job[q];
-  // four rows of one piece of columns
-  const int64_t i = block * LT + threadIdx.x, per = j.w8 / 8;
-  const int64_t r0 = i / per * JOB_ROWS, c = i % per * 8;
-  if (r0 >= j.rows) return;
-  const int cnt = int(j.cols - c > 8 ? 8 : j.cols - c);
-  float v[JOB_ROWS][8];
-  bool bad = false;
-  auto load = [&](auto whole) {   // whole pieces: no branches between the loads, which overlap
-    const int len = decltype(whole)::value ? 8 : cnt;
-#pragma unroll
-    for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
-      const int64_t r = min(r0 + q4, j.rows - 1);
-      if (j.exps != nullptr)
-        ld8_codes(static_cast<const int8_t*>(j.p) + r * j.ld + c, len, pow2f(j.exps[r * j.nb + (c >> 6)]), v[q4]);
-      else
-        ld8(static_cast<const T*>(j.p) + r * j.ld + c, len, v[q4]);
-    }
-  };
-  if (cnt >= 8)
-    load(std::true_type{});
-  else
-    load(std::false_type{});
-#pragma unroll
-  for (int q4 = 0; q4 < JOB_ROWS; ++q4) {
-    const int64_t r = r0 + q4;
-    if (r >= j.rows) break;
-    uint16_t* o = j.out + r * j.planes * j.w8 + c;
-    if (j.planes == 0)
-      st8(reinterpret_cast<float*>(j.out) + r * j.w8 + c, 8, v[q4]);
-    else if (j.exps != nullptr) {
-      split_store<uint16_t>(o, j.w8, v[q4], bad);
-      if (sizeof(T) == 4) {   // one exact piece, which meets three
-#pragma unroll
-        for (int e = 0; e < 8; ++e) bad |= fabsf(v[q4][e]) > SPLIT_MAX;
-      }
-    } else {
-      split_store<T>(o, j.w8, v[q4], bad);
-    }
-  }
-  if (sizeof(T) == 4 && bad) {
-    if (j.raises & 1) flag[0] = 1;
-    if (j.raises & 2) flag[1] = 1;
-  }
+  lay_operand<T>(jobs, blockIdx.x, flag);
 }
 __global__ void clear_flag_kernel(int32_t* flag) { flag[0] = flag[1] = 0; }
-
-int64_t round8(int64_t v) { return (v + 7) & ~int64_t(7); }
 
 // Room in the workspace for one such operand, in bf16.
 template <class T>
@@ -1004,21 +920,8 @@ lrc_status linear_back(hipStream_t st, const BackArgs& a, void* ws) {
 }
 }  // namespace
 
-lrc_status lay_out_bf16(hipStream_t st, const LayOut* jobs, int count) {
-  OperandJobs q;
-  for (int i = 0; i < count; ++i) {
-    OperandJob& j = q.job[i];
-    j.p = jobs[i].p;
-    j.exps = jobs[i].exps;
-    j.out = jobs[i].out;
-    j.ld = jobs[i].ld;
-    j.nb = cdiv(jobs[i].cols, CKB);
-    j.rows = jobs[i].rows;
-    j.cols = jobs[i].cols;
-    j.w8 = round8(j.cols);
-    j.blocks = cdiv(cdiv(j.rows, JOB_ROWS) * (j.w8 / 8), LT);
-  }
-  return prepare_operands<uint16_t>(st, q, count, nullptr);
+lrc_status lay_out_bf16(hipStream_t st, const OperandJobs& jobs, int count) {
+  return prepare_operands<uint16_t>(st, jobs, count, nullptr);
 }
 
 lrc_status linear_grads_f32(hipStream_t st, int64_t n, int64_t di, int64_t dn, const float* dz, int64_t lddz,

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "lrc_gemm_tile.h"
+#include "lrc_rows.h"
 
 namespace lrc {
 namespace gemm {
@@ -157,8 +158,41 @@ __device__ __forceinline__ u32x4 row_piece(const T* p, int left) {
   return v;
 }
 
-template <class TO, Element EL, int W, int G, int NW>
-__global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPiece<EL>::T* __restrict__ x, int64_t ldx,
+// OWN (integers, at most OWN_TOKENS): x is the tokens themselves, in the type of y, and every workgroup quantises them
+// into LDS while its first weights are on the way: a launch less (one token 4096 -> 11008: @@).
+constexpr int OWN_TOKENS = 4, OWN_ROOM = 16384, OWN_PIECES = 2;
+template <int NW>
+constexpr int own_width() { return OWN_PIECES * 8 * 64 * NW; }   // channels the threads hold
+
+template <class TO, int NW>
+__device__ __forceinline__ void quantize_own(const TO* x, int64_t ldx, int n, int K, int pitch, int8_t* xq, float* xs,
+                                             uint32_t (*red)[NW], bool& bad) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int t = 0; t < n; ++t) {
+    float v[OWN_PIECES][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < OWN_PIECES; ++i) ld8(x + t * ldx + 8 * (threadIdx.x + 64 * NW * i), K - 8 * int(threadIdx.x + 64 * NW * i), v[i]);
+#pragma unroll
+    for (int i = 0; i < OWN_PIECES; ++i) m = mag8(v[i], m, bad);
+    m = wave_max(m);
+    if (lane == 0) red[t & 1][wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = max(m, red[t & 1][w]);
+    const float s = token_step(m), inv = token_inverse(s);
+    if (threadIdx.x == 0) xs[t] = s;
+#pragma unroll
+    for (int i = 0; i < OWN_PIECES; ++i) {
+      const int c = 8 * (threadIdx.x + 64 * NW * i);
+      if (c < pitch) st8_token_codes(xq + t * pitch + c, 8, v[i], s, inv, bad);
+    }
+  }
+  __syncthreads();
+}
+
+template <class TO, Element EL, int W, int G, int NW, bool OWN>
+__global__ __launch_bounds__(64 * NW) void few_rows_kernel(const void* __restrict__ x, int64_t ldx,
                                                            const typename RowPiece<EL>::T* __restrict__ W0, int64_t ld0,
                                                            const typename RowPiece<EL>::T* __restrict__ W1, int64_t ld1,
                                                            int n, int64_t N, int K, Epilogue ep, Companion co) {
@@ -166,6 +200,9 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPie
   using T = typename P::T;
   constexpr int U = 4, E = 16 / int(sizeof(T));   // pieces in flight, elements of a lane's 16 bytes
   __shared__ __attribute__((aligned(16))) typename P::Acc part[NW * W * G * 64];
+  __shared__ __attribute__((aligned(16))) int8_t xq[OWN ? OWN_ROOM : 16];
+  __shared__ float xs[OWN ? OWN_TOKENS : 1];
+  __shared__ uint32_t red[2][NW];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t n0 = int64_t(blockIdx.x) * 16;
   // rows past the end repeat the last one, their results are not written
@@ -173,19 +210,35 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPie
   const T* w[W];
   w[0] = W0 + ch * ld0;
   if constexpr (W == 2) w[1] = W1 + ch * ld1;
-  const T* xr[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) xr[g] = x + int64_t(min(16 * g + (lane & 15), n - 1)) * ldx;
   const int pieces = (K + P::K - 1) / P::K, per = (pieces + NW - 1) / NW;
   const int p0 = wave * per, p1 = min(pieces, p0 + per), k0 = E * (lane >> 4);
-  typename P::Acc acc[W][G] = {};
-  int p = p0;
-  for (; (p + U) * P::K <= K && p + U <= p1; p += U) {
-    u32x4 wv[U][W], xv[U][G];
+  auto whole = [&](int p) { return (p + U) * P::K <= K && p + U <= p1; };
+  u32x4 wv[U][W];
+  auto load = [&](int p, u32x4 (&to)[U][W]) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < W; ++j) wv[u][j] = row_piece<T>(w[j] + (p + u) * P::K + k0, E);
+      for (int j = 0; j < W; ++j) to[u][j] = row_piece<T>(w[j] + (p + u) * P::K + k0, E);
+  };
+  if (whole(p0)) load(p0, wv);
+  const int pitch = (K + 63) & ~63;
+  if constexpr (OWN) {
+    bool bad = false;
+    quantize_own<TO, NW>(static_cast<const TO*>(x), ldx, n, K, pitch, xq, xs, red, bad);
+    if (ep.info != nullptr && bad) *ep.info = LRC_ENONFINITE;
+  }
+  const T* xr[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int t = min(16 * g + (lane & 15), n - 1);
+    xr[g] = OWN ? reinterpret_cast<const T*>(xq) + t * pitch : static_cast<const T*>(x) + t * ldx;
+  }
+  typename P::Acc acc[W][G] = {};
+  int p = p0;
+  for (; whole(p); p += U) {   // the next pieces of the weights are loaded before these are used
+    u32x4 next[U][W], xv[U][G];
+    const bool more = whole(p + U);
+    if (more) load(p + U, next);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -196,17 +249,23 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPie
       for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[j][g] = P::mma(wv[u][j], xv[u][g], acc[j][g]);
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < W; ++j) wv[u][j] = next[u][j];
+    }
   }
   for (; p < p1; ++p) {   // k past the end reads as zero on both sides
     const int k = p * P::K + k0;
-    u32x4 wv[W];
+    u32x4 wt[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) wv[j] = row_piece<T>(w[j] + k, K - k);
+    for (int j = 0; j < W; ++j) wt[j] = row_piece<T>(w[j] + k, K - k);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const u32x4 xv = row_piece<T>(xr[g] + k, K - k);
+      const u32x4 xv = row_piece<T>(xr[g] + k, OWN ? E : K - k);
 #pragma unroll
-      for (int j = 0; j < W; ++j) acc[j][g] = P::mma(wv[j], xv, acc[j][g]);
+      for (int j = 0; j < W; ++j) acc[j][g] = P::mma(wt[j], xv, acc[j][g]);
     }
   }
 #pragma unroll
@@ -228,7 +287,7 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPie
       S s = 0;
 #pragma unroll
       for (int q = 0; q < NW; ++q) s += sums[(q * W + j) * G * 256 + at];
-      v[j] = EL == INT8 ? float(s) * (j ? co.col_scale2 : co.col_scale)[col] * co.row_scale[t] : float(s);
+      v[j] = EL == INT8 ? float(s) * (j ? co.col_scale2 : co.col_scale)[col] * (OWN ? xs[t] : co.row_scale[t]) : float(s);
     }
     if constexpr (W == 1) {
       if (ep.bias != nullptr) v[0] += ep.bias[col];
@@ -245,30 +304,43 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const typename RowPie
   }
 }
 
-// n <= 64
+// whether the few tokens are quantised by the product itself
+inline bool own_tokens(int64_t n, int64_t K) {
+  return n <= OWN_TOKENS && n * ((K + 63) & ~int64_t(63)) <= OWN_ROOM && K <= own_width<8>();
+}
+
+// n <= 64; own: x is the tokens themselves (own_tokens)
 template <class TO, Element EL, int W>
-lrc_status few_rows(hipStream_t st, const char* name, const void* x, int64_t ldx, const void* W0, int64_t ld0,
+lrc_status few_rows(hipStream_t st, const char* name, const void* x, int64_t ldx, bool own, const void* W0, int64_t ld0,
                     const void* W1, int64_t ld1, int64_t n, int64_t N, int64_t K, const Epilogue& ep,
                     const Companion& co, double flops, double bytes) {
   using T = typename RowPiece<EL>::T;
   ProfScope scope(name, st, flops, bytes);
   const unsigned grid = unsigned(cdiv(N, 16));
-  auto go = [&](auto groups, auto waves) {
+  auto go = [&](auto groups, auto waves, auto quantise) {
     constexpr int G = decltype(groups)::value, NW = decltype(waves)::value;
-    few_rows_kernel<TO, EL, W, G, NW><<<grid, 64 * NW, 0, st>>>(static_cast<const T*>(x), ldx, static_cast<const T*>(W0),
-                                                                ld0, static_cast<const T*>(W1), ld1, int(n), N, int(K),
-                                                                ep, co);
+    few_rows_kernel<TO, EL, W, G, NW, decltype(quantise)::value><<<grid, 64 * NW, 0, st>>>(
+        x, ldx, static_cast<const T*>(W0), ld0, static_cast<const T*>(W1), ld1, int(n), N, int(K), ep, co);
   };
+  using std::false_type;
   using std::integral_constant;
   // few channels: more waves share the k of each
-  if (n > 32)
-    go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
-  else if (n > 16)
-    go(integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  else if (grid <= 256)
-    go(integral_constant<int, 1>{}, integral_constant<int, 16>{});
-  else
-    go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  if (own) {
+    if constexpr (EL == INT8) {
+      if (grid <= 256)
+        go(integral_constant<int, 1>{}, integral_constant<int, 16>{}, std::true_type{});
+      else
+        go(integral_constant<int, 1>{}, integral_constant<int, 8>{}, std::true_type{});
+    }
+  } else if (n > 32) {
+    go(integral_constant<int, 4>{}, integral_constant<int, 8>{}, false_type{});
+  } else if (n > 16) {
+    go(integral_constant<int, 2>{}, integral_constant<int, 8>{}, false_type{});
+  } else if (grid <= 256) {
+    go(integral_constant<int, 1>{}, integral_constant<int, 16>{}, false_type{});
+  } else {
+    go(integral_constant<int, 1>{}, integral_constant<int, 8>{}, false_type{});
+  }
   LRC_LAUNCHED();
   return LRC_OK;
 }

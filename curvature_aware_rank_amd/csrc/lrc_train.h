@@ -270,6 +270,7 @@ struct Epilogue {
   int64_t nb = 0;
   int32_t* info = nullptr;
   bool finite = false;   // a sum that is not finite counts as zero
+  void* y2 = nullptr;    // of two products in one launch: the second one's y
 };
 
 // the bias of eight consecutive columns, of which `cnt` exist
@@ -336,22 +337,23 @@ template <class TO>
 lrc_status gemm_finish(hipStream_t st, const float* partial, int splits, int64_t M, int64_t N, const Epilogue& ep,
                        const int32_t* skip);
 size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, bool f32);
-// the same for products of `count` segments alone
+// The weight gradients of a gated block, both in one launch: ep.y = A1^T B and ep.y2 = A2^T B (M x N each; columns of
+// all operands), every sum over two segments, plane 1 of A (what rounding left out) and then plane 0; a sum of the
+// first that is not finite counts as zero.
+template <class TO>
+lrc_status gemm_weight_pair(hipStream_t st, const char* name, GemmOperand A1, GemmOperand A2, GemmOperand B, int64_t M,
+                            int64_t N, int64_t K, const Epilogue& ep, float* partial, double flops, double bytes);
+size_t gemm_weight_pair_workspace(int64_t M, int64_t N, int64_t K);
+// workspace of a product of `count` segments
 size_t gemm_segments_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, int count);
 // estimates in microseconds of an fp32 product, on fp32 operands and on ones split in three
 double gemm_f32_time(int64_t M, int64_t N, int64_t K);
 double gemm_split_time(int64_t M, int64_t N, int64_t K, int KA, int KB);
 
 // ---- shared by the gated block (lrc_linear.hip) ------------------------------------------------
-// Up to three bf16 operands, or checkpoints (exps), written as rows of 8 ceil(cols / 8) bf16 with zeros
-// behind the columns.
-struct LayOut {
-  const void* p;
-  const int8_t* exps;
-  int64_t ld, rows, cols;
-  uint16_t* out;
-};
-lrc_status lay_out_bf16(hipStream_t st, const LayOut* jobs, int count);
+// up to three bf16 operands, or checkpoints, laid out (lrc_operand.h)
+struct OperandJobs;
+lrc_status lay_out_bf16(hipStream_t st, const OperandJobs& jobs, int count);
 // dx (+)= dz W and dW = dz^T x of an fp32 layer, as lrc_linear_backward without an activation computes
 // them, in its workspace.  x or its checkpoint (xcodes, xexps).
 lrc_status linear_grads_f32(hipStream_t st, int64_t n, int64_t di, int64_t dn, const float* dz, int64_t lddz,

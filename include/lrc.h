@@ -526,7 +526,7 @@ size_t lrc_gated_linear_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, 
  * dim lddh).  g and u (leading dim ldz) or, with both NULL, the four checkpoint arrays.  x (leading dim
  * ldx) or, with x NULL, its checkpoint (for dWg and dWu only).  Outputs: dg, du (n_tokens x d_ff, dtype
  * `dt`, packed), dx (leading dim lddx), dWg, dWu (d_ff x d_in, dtype dw_dt, LRC_F32 or `dt`, leading dim
- * lddw); dx, dWg, dWu may be NULL.  relu'(0) = 0.
+ * lddw); dx may be NULL, and dWg and dWu together.  relu'(0) = 0.
  * bf16: dx is a product of the rounded streams, both projections in one fp32 sum; dWg and dWu take dg
  * and du to 16 bits (the stream and what its rounding left out, in one sum; where an entry of x is not
  * finite the stream alone counts).

@@ -60,6 +60,10 @@ def lay8(t, layout):
     return t.to(dev())
 
 
+def flag():
+    return torch.zeros(1, dtype=torch.int32, device=dev())
+
+
 def on(*ts):
     return [None if t is None else t.to(dev()) for t in ts]
 
@@ -498,7 +502,7 @@ def test_block_norm(lrc, dtype, n, d, kind):
             # codes: those of the written h
             out = lrc.lrc_block_norm(lay(b, layout), lay(res, layout) if use_res else None, kind=kind, eps=eps, post=po,
                                      gate=gate.to(dev()) if use_gate else None, scale=scale,
-                                     pre=tuple(on(*pre)) if i != 2 else None, need_s=False, quantize=True)
+                                     pre=tuple(on(*pre)) if i != 2 else None, need_s=False, quantize=True, info=flag())
             wq, wqs, _ = lrc.lrc_quantize_tokens(h)
             assert out[0] is None and out[1] is None and torch.equal(out[3][0], wq) and torch.equal(out[3][1], wqs)
             assert int(out[4].cpu()) == 0 and torch.equal(out[2][3], stats[3])
@@ -663,7 +667,7 @@ def test_block_norm_extremes(lrc, kind):
         keep = [t for t in range(n) if t not in (3, 4, 5, 6, 7)]
         assert torch.equal(h[keep], clean[keep]) and not h[3].any() and not h[4].any() and not h[7].any()
         assert torch.isnan(h[5]).all() and torch.isnan(h[6]).any()
-        out = lrc.lrc_block_norm(y.to(dev()), kind=kind, quantize=True)
+        out = lrc.lrc_block_norm(y.to(dev()), kind=kind, quantize=True, info=flag())
         assert int(out[4].cpu()) == lrc.LRC_ENONFINITE
         wq, ws, _ = lrc.lrc_quantize_tokens(h)
         assert torch.equal(out[3][0], wq) and torch.equal(out[3][1], ws)
@@ -726,7 +730,7 @@ def test_block_in_8_bits(lrc):
     gamma = (1 + 0.1 * torch.randn(d, generator=r)).to(dev())
     for n in (1, 8, 40, 300):
         b, res = stream(n, d, torch.bfloat16, 2).to(dev()), stream(n, d, torch.bfloat16, 3).to(dev())
-        s, _, _, q, info = lrc.lrc_block_norm(b, res, pre=(gamma, None), quantize=True)
+        s, _, _, q, info = lrc.lrc_block_norm(b, res, pre=(gamma, None), quantize=True, info=flag())
         a, _ = lrc.lrc_int8_gated_linear(q, wg, wu)
         y, _ = lrc.lrc_int8_linear(a, wd, residual=s, info=info)
         assert int(info.cpu()) == 0
