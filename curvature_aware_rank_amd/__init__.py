@@ -1008,11 +1008,11 @@ def lrc_block_norm(b: torch.Tensor, residual=None, kind: str = "rms", eps: float
     """What lies between two blocks: p = norm(b) (where `post`, a (gamma, beta) pair, is given; else b),
     s = residual + scale * gate * p, h = norm(s) with `pre`, a (gamma, beta) pair (None: 1 and 0).  kind: "rms" (takes
     no beta) or "layer".  b, residual: (n_tokens, d) bf16 or fp32 (residual None: zero); gate, gammas, betas: (d,) fp32
-    or None.  With `quantize` h is returned as int8 codes for lrc_int8_linear instead.
+    or None.  With `quantize` (forward only) h is returned as int8 codes for lrc_int8_linear instead.
 
     Returns (s, h, stats, quantized, info): s and h like b (None where not needed, h None with quantize), stats
-    (mean_b, rstd_b, mean_s, rstd_s) for the backward pass (None where there is none), quantized (codes, scale) or
-    None; info (int32 (1,), sticky LRC_ENONFINITE of the codes) is None unless given."""
+    (mean_b, rstd_b, mean_s, rstd_s) for the backward pass (each None where there is none; None with quantize),
+    quantized (codes, scale) or None; info (int32 (1,), sticky LRC_ENONFINITE of the codes) is None unless given."""
     b, ldb = _rows(b, "b")
     dt, dev = _dtype_code(b), b.device
     n, d = b.shape
@@ -1027,19 +1027,25 @@ def lrc_block_norm(b: torch.Tensor, residual=None, kind: str = "rms", eps: float
     need_h = need_h and not quantize
     if not (need_s or need_h or quantize):
         raise ValueError("at least one of s, h and the codes is needed")
-    row = lambda want: torch.empty(n, dtype=torch.float32, device=dev) if want else None   # noqa: E731
-    normed = need_h or quantize
-    stats = (row(post is not None and not rms), row(post is not None), row(normed and not rms), row(normed))
-    s = torch.empty(n, d, dtype=b.dtype, device=dev) if need_s else None
-    h = torch.empty(n, d, dtype=b.dtype, device=dev) if need_h else None
-    quantized = (torch.empty(n, d, dtype=torch.int8, device=dev), row(True)) if quantize else None
+    row = lambda: torch.empty(n, dtype=torch.float32, device=dev)   # noqa: E731
+    mean_b = rstd_b = mean_s = rstd_s = q = qs = h = s = None
+    if quantize:
+        q, qs = torch.empty(n, d, dtype=torch.int8, device=dev), row()
+    else:
+        if post is not None:
+            mean_b, rstd_b = None if rms else row(), row()
+        if need_h:
+            mean_s, rstd_s = None if rms else row(), row()
+            h = torch.empty(n, d, dtype=b.dtype, device=dev)
+    if need_s:
+        s = torch.empty(n, d, dtype=b.dtype, device=dev)
     if info is not None:
         info = _info(info, dev)
-    q, qs = quantized or (None, None)
     _run("lrc_block_norm", dev, lib.lrc_block_norm, _ptr(b), dt, n, d, ldb, _ptr(residual), ldr, code, float(eps),
          int(post is not None), _ptr(pg), _ptr(pb), _ptr(gate), float(scale), _ptr(ga), _ptr(be), _ptr(s), max(d, 1),
-         _ptr(h), max(d, 1), *(_ptr(v) for v in stats), _ptr(q), max(d, 1), _ptr(qs), _ptr(info))
-    return s, h, stats, quantized, info
+         _ptr(h), max(d, 1), _ptr(mean_b), _ptr(rstd_b), _ptr(mean_s), _ptr(rstd_s), _ptr(q), max(d, 1), _ptr(qs),
+         _ptr(info))
+    return s, h, None if quantize else (mean_b, rstd_b, mean_s, rstd_s), (q, qs) if quantize else None, info
 
 
 def lrc_block_norm_backward(dh, ds, s, b, stats, kind: str = "rms", post=None, gate=None, scale: float = 1.0, pre=None,

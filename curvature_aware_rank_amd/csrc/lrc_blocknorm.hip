@@ -431,8 +431,9 @@ lrc_status with_norm(int64_t d, int kind, bool post, F f) {
 
 template <class T>
 lrc_status forward(hipStream_t st, const NormForward& a, int kind, bool post) {
-  const double cells = double(a.n) * double(a.d), streams = 1 + (a.res != nullptr) + (a.s != nullptr) + (a.h != nullptr);
-  ProfScope scope("block_norm_kernel", st, 16.0 * cells, cells * (streams * sizeof(T) + (a.q != nullptr)));
+  const double cells = double(a.n) * double(a.d);
+  const int streams = 1 + (a.res != nullptr) + (a.s != nullptr) + (a.h != nullptr);
+  ProfScope scope("block_norm_kernel", st, 16.0 * cells, cells * double(streams * sizeof(T) + (a.q != nullptr)));
   return with_norm(a.d, kind, post, [&](auto w, auto v, auto layer, auto after) -> lrc_status {
     constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
     using S = RowShape<T, WPR, V>;
@@ -476,8 +477,8 @@ extern "C" lrc_status lrc_block_norm(const void* b, lrc_dtype dt, int64_t n_toke
   if (kind == LRC_NORM_RMS && beta != nullptr) return LRC_EINVAL;
   if (n_tokens == 0) return LRC_OK;
   if (b == nullptr || (s == nullptr && h == nullptr && q == nullptr)) return LRC_EINVAL;
-  const NormForward a = {b,     residual, n_tokens, ldb, ldr, int(d), post_gamma, post_beta, gate,   gamma,  beta, scale,
-                         eps,   s,        h,        lds, ldh, mean_b, rstd_b,     mean_s,    rstd_s, q,      ldq,  qscale,
+  const NormForward a = {b,   residual, n_tokens, ldb, ldr, int(d), post_gamma, post_beta, gate,   gamma, beta, scale,
+                         eps, s,        h,        lds, ldh, mean_b, rstd_b,     mean_s,    rstd_s, q,     ldq,  qscale,
                          info};
   hipStream_t st = static_cast<hipStream_t>(stream);
   return dt == LRC_BF16 ? forward<uint16_t>(st, a, kind, post != 0) : forward<float>(st, a, kind, post != 0);
@@ -501,7 +502,8 @@ extern "C" lrc_status lrc_block_norm_backward(const void* dh, lrc_dtype dt, int6
                                               size_t ws_bytes, void* stream) {
   const bool layer = kind == LRC_NORM_LAYER;
   if ((dt != LRC_F32 && dt != LRC_BF16) || !kind_ok(kind)) return LRC_EDTYPE;
-  if (!sizes_ok(n_tokens, d) || (dh != nullptr && (lddh < d || lds < d)) || (ds != nullptr && ldds < d)) return LRC_EINVAL;
+  if (!sizes_ok(n_tokens, d) || (dh != nullptr && (lddh < d || lds < d)) || (ds != nullptr && ldds < d))
+    return LRC_EINVAL;
   if ((b != nullptr && ldb < d) || (dresidual != nullptr && lddr < d) || (db != nullptr && lddb < d)) return LRC_EINVAL;
   if (!post && (post_gamma != nullptr || post_beta != nullptr || dpost_gamma != nullptr || dpost_beta != nullptr))
     return LRC_EINVAL;
@@ -520,7 +522,8 @@ extern "C" lrc_status lrc_block_norm_backward(const void* dh, lrc_dtype dt, int6
   }
   if (dh == nullptr && (ds == nullptr || dgamma != nullptr || dbeta != nullptr)) return LRC_EINVAL;
   if (dh != nullptr && (s == nullptr || rstd_s == nullptr || (layer && mean_s == nullptr))) return LRC_EINVAL;
-  const bool after = post != 0 && (db != nullptr || dpost_gamma != nullptr || dpost_beta != nullptr || dgate != nullptr);
+  const bool after = post != 0 && (db != nullptr || dpost_gamma != nullptr || dpost_beta != nullptr ||
+                                   dgate != nullptr);
   if (after && (rstd_b == nullptr || (layer && mean_b == nullptr))) return LRC_EINVAL;
   if (b == nullptr && (after || dgate != nullptr)) return LRC_EINVAL;
   const size_t need = lrc_block_norm_backward_workspace(n_tokens, d);

@@ -18,7 +18,6 @@ namespace {
 
 constexpr int ET = 256;
 constexpr int64_t WIDE = int64_t(1) << 20;       // channels (a tile's offsets hold their rows)
-constexpr int64_t FEW = 8;                       // tokens up to which the weights are streamed
 
 bool sizes_ok(int64_t n, int64_t i, int64_t f) {
   return n >= 0 && n < GEMM_MAX_K && i >= 1 && i <= WIDE && f >= 1 && f <= WIDE;
@@ -168,7 +167,7 @@ struct GatedArgs {
 lrc_status gated_bf16(hipStream_t st, GatedArgs& a, void* ws) {
   const double flops = 4.0 * double(a.n) * double(a.df) * double(a.di);
   const double bytes = 2.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df);
-  if (a.n <= FEW && a.ep.codes == nullptr)
+  if (gemm::stream_bf16_pair(a.n, a.df, a.di) && a.ep.codes == nullptr)
     return gemm::few_rows<uint16_t, BF16, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
                                              a.di, a.ep, a.co, flops, bytes);
   const GatedRoom room = forward_room(ws, LRC_BF16, a.n, a.di, a.df);
@@ -252,7 +251,8 @@ struct GatedBack {
 };
 
 template <class T>
-lrc_status gate_backward(hipStream_t st, const GatedBack& a, const GatedRoom& room, bool low, const OperandJobs& jobs) {
+lrc_status gate_backward(hipStream_t st, const GatedBack& a, const GatedRoom& room, bool low,
+                         const OperandJobs& jobs) {
   GatePass<T> p = {};
   p.dh = static_cast<const T*>(a.dh);
   p.g = static_cast<const T*>(a.g);

@@ -51,7 +51,9 @@ struct Stager {
 
   static constexpr int WAVE_ROWS = LOADS * 512 / KS;   // K_ROWS: tile rows a wave loads
   static_assert(HW == 0 || (KIND == K_ROWS && HW % WAVE_ROWS == 0), "a wave's rows belong to one of the two operands");
-  static __device__ __forceinline__ bool second(int wave) { return HW > 0 && (wave * WAVE_ROWS / (HW > 0 ? HW : 1)) % 2 == 1; }
+  static __device__ __forceinline__ bool second(int wave) {
+    return HW > 0 && (wave * WAVE_ROWS / (HW > 0 ? HW : 1)) % 2 == 1;
+  }
 
   __device__ void init(const GemmOperand& o, int64_t row0, int64_t rows, int wave, int lane) {
     ld = o.ld;
@@ -521,7 +523,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
           finish_pair8<TO>(ep, co, row, col, cnt, v, u, lane, bad);
         }
       } else if (tg.splits > 1) {
-        const int64_t np = (N + 7) & ~int64_t(7), at = SEG == 2 ? (2 * split + other) * M + row : int64_t(split) * M + row;
+        const int64_t np = (N + 7) & ~int64_t(7), at = int64_t(SEG == 2 ? 2 * split + other : split) * M + row;
         if (cnt > 0) st8(partial + at * np + col, 8, v);
       } else if constexpr (SEG == 2) {
         if (cnt > 0) st8(static_cast<TO*>(other ? ep.y2 : ep.y) + row * ep.ldy + col, cnt, v);

@@ -119,7 +119,6 @@ __global__ __launch_bounds__(QT) void pitch_kernel(PitchJob a, PitchJob b, Pitch
 
 constexpr int64_t KMAX = int64_t(1) << 17;    // input channels stay below: |sum| < 2^31 for codes of any value
 constexpr int64_t NMAX = int64_t(1) << 24;
-constexpr int64_t FEW = 16;                   // tokens up to which the weights are streamed
 int64_t round16(int64_t v) { return (v + 15) & ~int64_t(15); }
 
 bool sizes_ok(int64_t n, int64_t i, int64_t o) {
@@ -137,7 +136,7 @@ Int8Room int8_room(void* ws, int64_t n, int64_t di, int64_t dn, bool pair) {
   const int64_t k = round16(di);
   r.x = cv.take<int8_t>(size_t(n) * k);
   r.scale = cv.take<float>(size_t(n));
-  if (n > FEW) {
+  if (!gemm::stream_int8(n, dn, di, pair)) {
     if (di % 16 != 0) {
       r.w0 = cv.take<int8_t>(size_t(dn) * k);
       if (pair) r.w1 = cv.take<int8_t>(size_t(dn) * k);
@@ -183,14 +182,15 @@ lrc_status int8_product(hipStream_t st, const Int8Args& a, void* ws, int32_t* in
     return gemm::few_rows<T, INT8, W>(st, "int8_rows_kernel", x, ld, own, a.w[0], a.ldw[0], a.w[1], a.ldw[1], a.n,
                                       a.dn, a.di, ep, co, flops, bytes);
   };
-  if (a.x != nullptr && gemm::own_tokens(a.n, a.di)) return few(a.x, a.ldx, true);
+  const bool rows = gemm::stream_int8(a.n, a.dn, a.di, PAIR);
+  if (rows && a.x != nullptr && gemm::own_tokens(a.n, a.dn, a.di)) return few(a.x, a.ldx, true);
   if (a.x != nullptr) {
     LRC_TRY(quantize(st, static_cast<const T*>(a.x), a.n, a.di, a.ldx, room.x, k, k, room.scale, info));
     xq = room.x;
     ldx = k;
     co.row_scale = room.scale;
   }
-  if (a.n <= FEW) return few(xq, ldx, false);
+  if (rows) return few(xq, ldx, false);
   const int8_t* w[2] = {a.w[0], a.w[1]};
   int64_t ldw[2] = {a.ldw[0], a.ldw[1]};
   if (a.di % 16 != 0) {   // rows of no whole pieces are laid out anew
@@ -233,7 +233,7 @@ lrc_status check(const A& a, int dt, int act, int weights, size_t need, void* ws
   if ((a.x == nullptr && a.xq == nullptr) || a.ep.y == nullptr) return LRC_EINVAL;
   for (int i = 0; i < weights; ++i)
     if (a.w[i] == nullptr || a.ws[i] == nullptr) return LRC_EINVAL;
-  if (a.n > FEW && a.di % 16 == 0) {   // the tiles read these where they lie
+  if (a.di % 16 == 0) {   // the tiles read these where they lie
     if (a.xq != nullptr && !in_place(a.xq, a.ldxq)) return LRC_EINVAL;
     for (int i = 0; i < weights; ++i)
       if (!in_place(a.w[i], a.ldw[i])) return LRC_EINVAL;

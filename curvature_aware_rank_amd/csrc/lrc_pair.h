@@ -33,10 +33,11 @@ __global__ __launch_bounds__(256) void rows_finish_kernel(const float* __restric
   if (cnt > 0) {
     const float* p = partial + row * W * np + col;
     const int64_t plane = M * W * np;
-    for (int s0 = 0; s0 < splits; s0 += 4) {   // four splits' loads in flight, added in order
-      V4 t[4][W][2];
+    constexpr int U = 8 / W;
+    for (int s0 = 0; s0 < splits; s0 += U) {   // eight loads of 32 bytes in flight, added in order
+      V4 t[U][W][2];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const V4* q = reinterpret_cast<const V4*>(p + min(s0 + u, splits - 1) * plane + w * np);
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(256) void rows_finish_kernel(const float* __restric
           t[u][w][1] = q[1];
         }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int w = 0; w < W; ++w)
           if (s0 + u < splits) {
@@ -99,12 +100,13 @@ lrc_status rows_product(hipStream_t st, const char* name, GemmOperand A, GemmOpe
   const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   ProfScope scope(name, st, flops, bytes);
+  const unsigned g = unsigned(grid);
   if (p.tile == LARGE)
-    rows_product_kernel<TO, 4, 2, 4, 8, 2, EL, PAIR><<<unsigned(grid), 512, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+    rows_product_kernel<TO, 4, 2, 4, 8, 2, EL, PAIR><<<g, 512, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
   else if (p.tile == SMALL)
-    rows_product_kernel<TO, 2, 2, 4, 4, 2, EL, PAIR><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+    rows_product_kernel<TO, 2, 2, 4, 4, 2, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
   else
-    rows_product_kernel<TO, 4, 1, 1, 4, 4, EL, PAIR><<<unsigned(grid), 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+    rows_product_kernel<TO, 4, 1, 1, 4, 4, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
   LRC_LAUNCHED();
   if (tg.splits == 1 && !tg.hold) return LRC_OK;
   const int64_t np = (N + 7) & ~int64_t(7), blocks = cdiv(N, CKB), threads = M * blocks * 8;
@@ -160,45 +162,39 @@ __device__ __forceinline__ u32x4 row_piece(const T* p, int left) {
 
 // OWN (integers, at most OWN_TOKENS): x is the tokens themselves, in the type of y, and every workgroup quantises them
 // into LDS while its first weights are on the way: a launch less (one token 4096 -> 11008: @@).
-constexpr int OWN_TOKENS = 4, OWN_ROOM = 16384, OWN_PIECES = 2;
-template <int NW>
-constexpr int own_width() { return OWN_PIECES * 8 * 64 * NW; }   // channels the threads hold
+constexpr int OWN_TOKENS = 4, OWN_ROOM = 16384;
 
 template <class TO, int NW>
 __device__ __forceinline__ void quantize_own(const TO* x, int64_t ldx, int n, int K, int pitch, int8_t* xq, float* xs,
                                              uint32_t (*red)[NW], bool& bad) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int t = 0; t < n; ++t) {
-    float v[OWN_PIECES][8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < OWN_PIECES; ++i) ld8(x + t * ldx + 8 * (threadIdx.x + 64 * NW * i), K - 8 * int(threadIdx.x + 64 * NW * i), v[i]);
-#pragma unroll
-    for (int i = 0; i < OWN_PIECES; ++i) m = mag8(v[i], m, bad);
-    m = wave_max(m);
+    const int c = 8 * threadIdx.x;   // K <= 512 NW
+    float v[8];
+    ld8(x + t * ldx + c, K - c, v);
+    uint32_t m = wave_max(mag8(v, 0, bad));
     if (lane == 0) red[t & 1][wave] = m;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NW; ++w) m = max(m, red[t & 1][w]);
-    const float s = token_step(m), inv = token_inverse(s);
+    const float s = token_step(m);
     if (threadIdx.x == 0) xs[t] = s;
-#pragma unroll
-    for (int i = 0; i < OWN_PIECES; ++i) {
-      const int c = 8 * (threadIdx.x + 64 * NW * i);
-      if (c < pitch) st8_token_codes(xq + t * pitch + c, 8, v[i], s, inv, bad);
-    }
+    if (c < pitch) st8_token_codes(xq + t * pitch + c, 8, v, s, token_inverse(s), bad);
   }
   __syncthreads();
 }
 
+// (Six waves on a SIMD where a wave has 16 tokens: three workgroups on a unit, 688 of them in one go rather than two.)
 template <class TO, Element EL, int W, int G, int NW, bool OWN>
-__global__ __launch_bounds__(64 * NW) void few_rows_kernel(const void* __restrict__ x, int64_t ldx,
+__global__ __launch_bounds__(64 * NW, G == 1 ? 6 : 1) void few_rows_kernel(const void* __restrict__ x, int64_t ldx,
                                                            const typename RowPiece<EL>::T* __restrict__ W0, int64_t ld0,
                                                            const typename RowPiece<EL>::T* __restrict__ W1, int64_t ld1,
                                                            int n, int64_t N, int K, Epilogue ep, Companion co) {
   using P = RowPiece<EL>;
   using T = typename P::T;
-  constexpr int U = 4, E = 16 / int(sizeof(T));   // pieces in flight, elements of a lane's 16 bytes
+  // pieces in flight (of both weights; registers for more would leave a compute unit too few waves), elements of a
+  // lane's 16 bytes
+  constexpr int U = 4 / W, E = 16 / int(sizeof(T));
   __shared__ __attribute__((aligned(16))) typename P::Acc part[NW * W * G * 64];
   __shared__ __attribute__((aligned(16))) int8_t xq[OWN ? OWN_ROOM : 16];
   __shared__ float xs[OWN ? OWN_TOKENS : 1];
@@ -287,7 +283,8 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const void* __restric
       S s = 0;
 #pragma unroll
       for (int q = 0; q < NW; ++q) s += sums[(q * W + j) * G * 256 + at];
-      v[j] = EL == INT8 ? float(s) * (j ? co.col_scale2 : co.col_scale)[col] * (OWN ? xs[t] : co.row_scale[t]) : float(s);
+      v[j] = float(s);
+      if (EL == INT8) v[j] = v[j] * (j ? co.col_scale2 : co.col_scale)[col] * (OWN ? xs[t] : co.row_scale[t]);
     }
     if constexpr (W == 1) {
       if (ep.bias != nullptr) v[0] += ep.bias[col];
@@ -304,9 +301,29 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const void* __restric
   }
 }
 
+// waves of a workgroup of up to 16 tokens: with few channels more waves share the k of each
+inline int few_waves(int64_t N) { return cdiv(N, 16) <= 256 ? 16 : 8; }
 // whether the few tokens are quantised by the product itself
-inline bool own_tokens(int64_t n, int64_t K) {
-  return n <= OWN_TOKENS && n * ((K + 63) & ~int64_t(63)) <= OWN_ROOM && K <= own_width<8>();
+inline bool own_tokens(int64_t n, int64_t N, int64_t K) {
+  return n <= OWN_TOKENS && n * ((K + 63) & ~int64_t(63)) <= OWN_ROOM && K <= 512 * few_waves(N);
+}
+
+// Whether up to 64 tokens stream the weights.  Every 16 channels read x again (from the caches, about 9.5 TB/s), tiles
+// read it once but where k is split end in a second launch of 4 to 5 us.  Integers, rows / tiles in us: 4096 -> 11008
+// 10.8 / 11.3 at 4 tokens, 11.7 / 11.2 at 8, 19 / 11.7 at 32; split, 11008 -> 4096 15.9 / 16.5 at 24, 17.7 / 16.6 at 32,
+// 4096 -> 4096 11.7 / 12.6 at 64; two weights 4096 -> 4096 9.9 / 10.1 at 32, 11.6 / 10.4 at 33.  Rows of no whole
+// pieces, which tiles would first lay out anew, always do.
+inline bool stream_int8(int64_t n, int64_t N, int64_t K, bool pair) {
+  if (n > 64 || K % 16 != 0) return n <= 64;
+  if (pair && n > 32) return false;
+  const double x = double(cdiv(N, 16)) * double(n) * double(K);
+  return x <= (plan_rows(n, N, K / 2, pair).tg.splits > 1 ? 75e6 : pair ? 16e6 : 24e6);
+}
+// bf16, two weights: 4096 -> 11008 32.0 / 30.6 at 8 tokens, 11008 -> 4096 32.2 / 35.5 at 8, 36.9 / 35.8 at 17,
+// 1024 -> 4096 6.8 / 6.8 at 32.
+inline bool stream_bf16_pair(int64_t n, int64_t N, int64_t K) {
+  if (n > 64 || K % 8 != 0) return n <= 64;
+  return n <= 8 || (n <= 32 && N * K <= (int64_t(1) << 22));
 }
 
 // n <= 64; own: x is the tokens themselves (own_tokens)
@@ -324,10 +341,9 @@ lrc_status few_rows(hipStream_t st, const char* name, const void* x, int64_t ldx
   };
   using std::false_type;
   using std::integral_constant;
-  // few channels: more waves share the k of each
   if (own) {
     if constexpr (EL == INT8) {
-      if (grid <= 256)
+      if (few_waves(N) == 16)
         go(integral_constant<int, 1>{}, integral_constant<int, 16>{}, std::true_type{});
       else
         go(integral_constant<int, 1>{}, integral_constant<int, 8>{}, std::true_type{});
@@ -336,7 +352,7 @@ lrc_status few_rows(hipStream_t st, const char* name, const void* x, int64_t ldx
     go(integral_constant<int, 4>{}, integral_constant<int, 8>{}, false_type{});
   } else if (n > 16) {
     go(integral_constant<int, 2>{}, integral_constant<int, 8>{}, false_type{});
-  } else if (grid <= 256) {
+  } else if (few_waves(N) == 16) {
     go(integral_constant<int, 1>{}, integral_constant<int, 16>{}, false_type{});
   } else {
     go(integral_constant<int, 1>{}, integral_constant<int, 8>{}, false_type{});

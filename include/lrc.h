@@ -565,9 +565,9 @@ lrc_status lrc_quantize_tokens(const void* x, lrc_dtype dt, int64_t n_tokens, in
  * residual and y: n_tokens x d_out, dtype `dt` (leading dims ldr, ldy); residual may be NULL, and may be
  * y itself; bias: float[d_out] or NULL.
  * The integer sum is exact, so equal inputs give equal bits at any split of it.  Codes may take all 256
- * values.  With more than 16 tokens and d_in a multiple of 16, given codes (of W and of the tokens) start
- * on 16 bytes and have leading dims that are multiples of 16, at most 2^22 (else LRC_EINVAL); other d_in
- * are laid out in the workspace.
+ * values.  Where d_in is a multiple of 16, given codes (of W and of the tokens) start on 16 bytes and have
+ * leading dims that are multiples of 16, at most 2^22 (else LRC_EINVAL); other d_in are laid out in the
+ * workspace.
  * 1 <= d_in < 2^17, 1 <= d_out <= 2^24, 0 <= n_tokens < 2^31; n_tokens == 0 is a no-op.
  */
 lrc_status lrc_int8_linear(const void* x, lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_out, int64_t ldx,

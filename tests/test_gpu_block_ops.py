@@ -505,7 +505,7 @@ def test_block_norm(lrc, dtype, n, d, kind):
                                      pre=tuple(on(*pre)) if i != 2 else None, need_s=False, quantize=True, info=flag())
             wq, wqs, _ = lrc.lrc_quantize_tokens(h)
             assert out[0] is None and out[1] is None and torch.equal(out[3][0], wq) and torch.equal(out[3][1], wqs)
-            assert int(out[4].cpu()) == 0 and torch.equal(out[2][3], stats[3])
+            assert int(out[4].cpu()) == 0 and out[2] is None
 
 
 def through(v, e_v, xh, e_xh, r, kind):
