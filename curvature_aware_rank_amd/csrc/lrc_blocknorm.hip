@@ -38,14 +38,14 @@ struct NormForward {
 // inside the next call lies between reading a slot and writing it again.
 template <int WPR, int GROUPS>
 struct RowReduce {
-  static constexpr int SLOTS = WPR > 1 ? GROUPS * WPR : 1;
+  static constexpr int SLOTS = WPR > 1 ? GROUPS * WPR : 1, LANES = row_lanes(WPR) < 64 ? row_lanes(WPR) : 64;
   int slot = 0;
   template <int N>
   __device__ __forceinline__ void sums(float (&v)[N], float (*red)[SLOTS][2], int wave, int lane, int group) {
     static_assert(N <= 2, "two values to a slot");
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
-    if (WPR == 1) return;
+    for (int k = 0; k < N; ++k) v[k] = lanes_sum<LANES>(v[k]);
+    if (WPR <= 1) return;
     if (lane == 0) {
 #pragma unroll
       for (int k = 0; k < N; ++k) red[slot][group * WPR + wave][k] = v[k];
@@ -66,8 +66,8 @@ struct RowReduce {
     return v[0];
   }
   __device__ __forceinline__ uint32_t largest(uint32_t v, float (*red)[SLOTS][2], int wave, int lane, int group) {
-    v = wave_max(v);
-    if (WPR == 1) return v;
+    v = lanes_max<LANES>(v);
+    if (WPR <= 1) return v;
     if (lane == 0) red[slot][group * WPR + wave][0] = __uint_as_float(v);
     __syncthreads();
 #pragma unroll
@@ -110,7 +110,8 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_kernel(NormForwar
     rb.load(b + u * a.ldb, d, l, u < a.n);
     rr.load(res + u * a.ldr, d, l, u < a.n && res != nullptr);
   };
-  load(t);
+  constexpr bool AHEAD = V * sizeof(T) < 16;   // the widest fp32 rows leave no registers for the next token
+  if (AHEAD) load(t);
   R reduce;
   bool bad = false;
   // centres (LAYER) and returns 1 / spread; what lies behind the last channel stays zero
@@ -133,12 +134,13 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_kernel(NormForwar
   for (int64_t t0 = int64_t(blockIdx.x) * S::GROUPS; t0 < a.n; t0 += step, t += step) {
     const bool live = t < a.n;
     float v[E], r[E];
+    if (!AHEAD) load(t);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       v[i] = rb.at(i);
       r[i] = rr.at(i);
     }
-    load(t + step);
+    if (AHEAD) load(t + step);
     float mu;
     if constexpr (POST) {
       const float rs = standardise(v, mu);
@@ -219,7 +221,7 @@ struct NormBackward {
   float scale;
   void *dres, *db;
   int64_t lddr, lddb;
-  float* partial;   // [workgroup][4][d] (LAYER) or [workgroup][2][d]: A, (B,) C, (D)
+  float* partial;   // [workgroup][4][d] (LAYER) or [workgroup][2][d]: A, C(, B, D)
 };
 
 // a row of the backward pass of a norm: g = dy gamma -> r (g - mean(g) - x^ mean(g x^))
@@ -228,23 +230,55 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
   using S = RowShape<T, WPR, V>;
   using R = RowReduce<WPR, S::GROUPS>;
   constexpr int E = S::E, NS = LAYER ? 4 : 2;
+  // rows past 8192 channels: A and C are kept in LDS (a lane's own places, 16 bytes a time), B and D in registers,
+  // and tokens are not loaded ahead where that spills (6100 x 11008 rms 412 us with all sums in registers: @@)
+  constexpr bool WIDE = V > 2, AHEAD = !WIDE || (V * sizeof(T) <= 6 && !LAYER);
+  constexpr int NR = WIDE ? NS / 2 : NS;   // sums in registers
+  __shared__ __attribute__((aligned(16))) f32x4 wide[WIDE ? 2 * 2 * V * S::LANES : 1];
   __shared__ float red[2][R::SLOTS][2];
   __shared__ float share[S::GROUPS > 1 ? (S::GROUPS - 1) * NS * E * S::LANES : 1];
   const int lane = threadIdx.x & 63, group = threadIdx.x / S::LANES, l = threadIdx.x % S::LANES;
   const int wave = l >> 6, d = a.d;
   const T *dh = static_cast<const T*>(a.dh), *ds = static_cast<const T*>(a.ds), *s = static_cast<const T*>(a.s),
           *b = static_cast<const T*>(a.b);
-  float ga[E], gs[E], pg[POST ? E : 1];
-  row_params<S, V>(a.gamma, 1.f, d, l, ga);
+  float ga[E], gs[E];   // gamma; scale * gate, and * post_gamma
   row_params<S, V>(a.gate, 1.f, d, l, gs);
+  if constexpr (POST) {
+    row_params<S, V>(a.post_gamma, 1.f, d, l, ga);
 #pragma unroll
-  for (int i = 0; i < E; ++i) gs[i] *= a.scale;
-  if constexpr (POST) row_params<S, V>(a.post_gamma, 1.f, d, l, pg);
-  float acc[NS][E];
+    for (int i = 0; i < E; ++i) gs[i] *= a.scale * ga[i];
+  } else {
 #pragma unroll
-  for (int k = 0; k < NS; ++k)
+    for (int i = 0; i < E; ++i) gs[i] *= a.scale;
+  }
+  row_params<S, V>(a.gamma, 1.f, d, l, ga);
+  // A, C (in LDS where WIDE), B, D
+  float acc[NR > 0 ? NR : 1][E];
+#pragma unroll
+  for (int k = 0; k < NR; ++k)
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[k][i] = 0.f;
+  constexpr int AT_B = WIDE ? 0 : 2, AT_D = AT_B + 1;
+  auto wide_at = [&](int sum, int half) -> f32x4& { return wide[(sum * 2 * V + half) * S::LANES + l]; };
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int h = 0; h < 4 * V; ++h) wide[h * S::LANES + l] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // adds x y to A (0) or C (1)
+  auto add = [&](int sum, const float (&x)[E], const float (&y)[E]) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int h = 0; h < 2 * V; ++h) {
+        f32x4 v = wide_at(sum, h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(x[4 * h + e], y[4 * h + e], v[e]);
+        wide_at(sum, h) = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[sum][i] = fmaf(x[i], y[i], acc[sum][i]);
+    }
+  };
   const float inv_d = 1.f / float(d);
   const int64_t step = int64_t(gridDim.x) * S::GROUPS;
   int64_t t = int64_t(blockIdx.x) * S::GROUPS + group;
@@ -263,7 +297,7 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
       r_b = live ? a.rstd_b[u] : 0.f;
     }
   };
-  load(t);
+  if (AHEAD) load(t);
   R reduce;
   // v = gamma dy -> its gradient through the norm whose normalised row is xh
   auto through = [&](float (&v)[E], const float (&xh)[E], float r) {
@@ -285,6 +319,7 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
   };
   for (int64_t t0 = int64_t(blockIdx.x) * S::GROUPS; t0 < a.n; t0 += step, t += step) {
     float g[E], xh[E], total[E], bh[E];
+    if (!AHEAD) load(t);
     const float rsv = r_s, rbv = r_b;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -295,23 +330,23 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
       bh[i] = rb.at(i);
       if (POST) bh[i] = in ? (LAYER ? bh[i] - mu_b : bh[i]) * rbv : 0.f;
     }
-    load(t + step);
+    if (AHEAD) load(t + step);
     const bool live = t < a.n;
     if (a.dh != nullptr) {
+      add(0, g, xh);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        acc[0][i] = fmaf(g[i], xh[i], acc[0][i]);
-        if (LAYER) acc[1][i] += g[i];
+        if constexpr (LAYER) acc[AT_B][i] += g[i];
         g[i] *= ga[i];
       }
       through(g, xh, rsv);
 #pragma unroll
       for (int i = 0; i < E; ++i) total[i] += S::col(i, l) < d ? g[i] : 0.f;
     }
+    add(1, total, bh);
+    if constexpr (LAYER) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      acc[LAYER ? 2 : 1][i] = fmaf(total[i], bh[i], acc[LAYER ? 2 : 1][i]);
-      if (LAYER) acc[NS - 1][i] += total[i];
+      for (int i = 0; i < E; ++i) acc[AT_D][i] += total[i];
     }
     auto store = [&](void* to, int64_t ld, const float (&v)[E]) {
       if (to == nullptr || !live) return;
@@ -328,10 +363,7 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
     store(a.dres, a.lddr, total);
     if (a.db == nullptr) continue;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      total[i] *= gs[i];
-      if constexpr (POST) total[i] *= pg[i];
-    }
+    for (int i = 0; i < E; ++i) total[i] *= gs[i];
     if constexpr (POST) through(total, bh, rbv);
     store(a.db, a.lddb, total);
   }
@@ -345,7 +377,7 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
     }
     __syncthreads();
     if (group > 0) return;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < S::GROUPS - 1; ++w)
 #pragma unroll
       for (int k = 0; k < NS; ++k)
@@ -360,7 +392,9 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_bwd_kernel(NormBa
       const int c = (j * S::LANES + l) * 8;
       float p[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = acc[k][8 * j + e];
+      for (int e = 0; e < 8; ++e)
+        p[e] = !WIDE ? acc[k % (NR > 0 ? NR : 1)][8 * j + e]
+               : k < 2 ? wide_at(k, 2 * j + e / 4)[e % 4] : acc[NR > 0 ? (k - 2) % NR : 0][8 * j + e];
       if (c < d) st8(o + k * int64_t(d) + c, d - c, p);
     }
 }
@@ -396,7 +430,7 @@ __global__ __launch_bounds__(256) void block_norm_params_kernel(const float* __r
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[k] += acc[k][i][cx];
   }
-  const float A = v[0], B = sums == 4 ? v[1] : 0.f, C = sums == 4 ? v[2] : v[1], D = sums == 4 ? v[3] : 0.f;
+  const float A = v[0], C = v[1], B = v[2], D = v[3];
   const float w = g.scale * (g.gate != nullptr ? g.gate[c] : 1.f);
   if (g.dgamma != nullptr) g.dgamma[c] = A;
   if (g.dbeta != nullptr) g.dbeta[c] = B;
@@ -408,11 +442,20 @@ __global__ __launch_bounds__(256) void block_norm_params_kernel(const float* __r
                                    : C);
 }
 
-// Workgroups of the backward kernel: at least four tokens to a group of waves, so that the shares stay a small
-// part of the traffic.
+// Shapes of the backward kernel: up to 2048 channels a lane holds eight, so that more waves are resident.
+template <class F>
+lrc_status with_bwd_shape(int64_t d, F f) {
+  using std::integral_constant;
+  if (d > 512 && d <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  if (d > 1024 && d <= 1536) return f(integral_constant<int, 3>{}, integral_constant<int, 1>{});
+  if (d > 1536 && d <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  return with_any_row_shape(d, f);
+}
+// Workgroups of the backward kernel: at least four tokens to a group of lanes, so that the shares stay a small part
+// of the traffic.
 int64_t bwd_groups(int64_t n, int64_t d) {
-  const int64_t at_once = d <= 1024 ? 4 : d <= 2048 ? 2 : 1, most = d <= 512 ? 1280 : d <= 2048 ? 768 : 512;
-  return std::max<int64_t>(1, std::min<int64_t>(most, cdiv(n, 4 * at_once)));
+  const int64_t at_once = d <= 128 ? 16 : d <= 256 ? 8 : d <= 512 ? 4 : d <= 1024 ? 2 : 1;
+  return std::max<int64_t>(1, std::min<int64_t>(d <= 2048 ? 1024 : 512, cdiv(n, 4 * at_once)));
 }
 
 bool sizes_ok(int64_t n, int64_t d) { return n >= 0 && n < (int64_t(1) << 31) && d >= 1 && d <= ROW_MAX; }
@@ -420,13 +463,13 @@ bool kind_ok(int k) { return k == LRC_NORM_LAYER || k == LRC_NORM_RMS; }
 
 // f(waves, pieces, LAYER, POST) as compile-time constants
 template <class F>
-lrc_status with_norm(int64_t d, int kind, bool post, F f) {
-  using std::false_type;
-  using std::true_type;
-  return with_row_shape(d, [&](auto w, auto v) -> lrc_status {
+auto with_norm(int kind, bool post, F f) {
+  return [=](auto w, auto v) -> lrc_status {
+    using std::false_type;
+    using std::true_type;
     if (kind == LRC_NORM_LAYER) return post ? f(w, v, true_type{}, true_type{}) : f(w, v, true_type{}, false_type{});
     return post ? f(w, v, false_type{}, true_type{}) : f(w, v, false_type{}, false_type{});
-  });
+  };
 }
 
 template <class T>
@@ -434,28 +477,28 @@ lrc_status forward(hipStream_t st, const NormForward& a, int kind, bool post) {
   const double cells = double(a.n) * double(a.d);
   const int streams = 1 + (a.res != nullptr) + (a.s != nullptr) + (a.h != nullptr);
   ProfScope scope("block_norm_kernel", st, 16.0 * cells, cells * double(streams * sizeof(T) + (a.q != nullptr)));
-  return with_norm(a.d, kind, post, [&](auto w, auto v, auto layer, auto after) -> lrc_status {
+  return with_any_row_shape(a.d, with_norm(kind, post, [&](auto w, auto v, auto layer, auto after) -> lrc_status {
     constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
     using S = RowShape<T, WPR, V>;
     const unsigned grid = unsigned(std::min<int64_t>(cdiv(a.n, S::GROUPS), 2048 / std::max(1, WPR / 4)));
     block_norm_kernel<T, WPR, V, decltype(layer)::value, decltype(after)::value><<<grid, S::THREADS, 0, st>>>(a);
     LRC_LAUNCHED();
     return LRC_OK;
-  });
+  }));
 }
 
 template <class T>
 lrc_status backward(hipStream_t st, const NormBackward& a, int kind, bool post) {
   const double cells = double(a.n) * double(a.d);
   ProfScope scope("block_norm_bwd_kernel", st, 30.0 * cells, 6.0 * cells * sizeof(T));
-  return with_norm(a.d, kind, post, [&](auto w, auto v, auto layer, auto after) -> lrc_status {
+  return with_bwd_shape(a.d, with_norm(kind, post, [&](auto w, auto v, auto layer, auto after) -> lrc_status {
     constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
     using S = RowShape<T, WPR, V>;
     block_norm_bwd_kernel<T, WPR, V, decltype(layer)::value, decltype(after)::value>
         <<<unsigned(bwd_groups(a.n, a.d)), S::THREADS, 0, st>>>(a);
     LRC_LAUNCHED();
     return LRC_OK;
-  });
+  }));
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ lrc_status quantize(hipStream_t st, const T* x, int64_t n, int64_t d, int64_t ld
     LRC_LAUNCHED();
     return LRC_OK;
   }
-  return with_row_shape(d, [&](auto w, auto v) -> lrc_status {
+  return with_any_row_shape(d, [&](auto w, auto v) -> lrc_status {
     constexpr int WPR = decltype(w)::value, V = decltype(v)::value;
     using S = RowShape<T, WPR, V>;
     const unsigned grid = unsigned(std::min<int64_t>(cdiv(n, S::GROUPS), 2048 / std::max(1, WPR / 4)));

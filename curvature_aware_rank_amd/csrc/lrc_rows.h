@@ -1,6 +1,6 @@
 // Token rows held in registers: shapes, loads and sums shared by the norm and quantisation kernels.
 //
-// WPR waves share a token, each lane holds 8 V of its channels.  Lane l holds channels
+// WPR waves share a token (WPR <= 0: 2^-WPR tokens share a wave), each lane holds 8 V of its channels.  Lane l holds channels
 // 8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint block; pieces are 16-byte
 // accesses at any alignment, the last one of a ragged row is short.
 #pragma once
@@ -26,6 +26,21 @@ __device__ __forceinline__ float wave_sum(float v) {
   const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
 }
+// The same over 16, 32 or all 64 lanes that share a token.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if (LANES >= 64) return wave_sum(v);
+  auto dpp = [](float x, auto ctrl) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v += dpp(v, std::integral_constant<int, 0xb1>{});
+  v += dpp(v, std::integral_constant<int, 0x4e>{});
+  v += dpp(v, std::integral_constant<int, 0x141>{});
+  v += dpp(v, std::integral_constant<int, 0x140>{});
+  if (LANES == 16) return v;
+  const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+}
 // The mean from the sum of x_j / 2 d, which no finite token overflows; it ends at the largest number.
 __device__ __forceinline__ float mean_of(float half) {
   const float m = 2.f * half;
@@ -34,12 +49,13 @@ __device__ __forceinline__ float mean_of(float half) {
 
 constexpr int ROW_MAX = 16384;        // widest row held in registers
 
-constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }   // tokens of a workgroup at a time
-constexpr int row_threads(int wpr) { return 64 * wpr * row_groups(wpr); }
+constexpr int row_lanes(int wpr) { return wpr > 0 ? 64 * wpr : 64 >> -wpr; }
+constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : wpr > 0 ? 4 / wpr : 4 << -wpr; }   // tokens of a workgroup at a time
+constexpr int row_threads(int wpr) { return row_lanes(wpr) * row_groups(wpr); }
 
 template <class T, int WPR, int V>
 struct RowShape {
-  static constexpr int E = 8 * V, LANES = 64 * WPR, GROUPS = row_groups(WPR), THREADS = row_threads(WPR);
+  static constexpr int E = 8 * V, LANES = row_lanes(WPR), GROUPS = row_groups(WPR), THREADS = row_threads(WPR);
   static __device__ __forceinline__ int col(int i, int l) {
     return ((i >> 3) * LANES + l) * 8 + (i & 7);
   }
@@ -132,20 +148,24 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int wav
   }
 }
 
-// Largest of a magnitude over the wave, in every lane (as wave_sum; magnitudes as integers).
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+// Largest of a magnitude over the lanes that share a token, in each of them (as lanes_sum; magnitudes as integers).
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   v = max_of_8(v);
   v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xf, 0xf, true)));
+  if (LANES == 16) return v;
   const auto rows = __builtin_amdgcn_permlane16_swap(v, v, false, false);
   v = max(uint32_t(rows[0]), uint32_t(rows[1]));
+  if (LANES == 32) return v;
   const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return max(uint32_t(halves[0]), uint32_t(halves[1]));
 }
-// largest over the token's WPR waves (`red` as in row_sums)
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return lanes_max<64>(v); }
+// largest over the token's waves (`red` as in row_sums)
 template <int WPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int wave_in_row, int lane, int group) {
-  v = wave_max(v);
-  if (WPR == 1) return v;
+  v = lanes_max<row_lanes(WPR) < 64 ? row_lanes(WPR) : 64>(v);
+  if (WPR <= 1) return v;
   if (lane == 0) red[group * WPR + wave_in_row] = v;
   __syncthreads();
 #pragma unroll
@@ -234,6 +254,15 @@ lrc_status with_row_shape(int64_t d, F f) {
   if (d <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
   if (d <= 12288) return f(integral_constant<int, 8>{}, integral_constant<int, 3>{});
   return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+}
+
+// The same with narrow rows in 16 or 32 lanes.
+template <class F>
+lrc_status with_any_row_shape(int64_t d, F f) {
+  using std::integral_constant;
+  if (d <= 128) return f(integral_constant<int, -2>{}, integral_constant<int, 1>{});
+  if (d <= 256) return f(integral_constant<int, -1>{}, integral_constant<int, 1>{});
+  return with_row_shape(d, f);
 }
 
 }  // namespace lrc
