@@ -8,7 +8,8 @@
 // rounding to bf16 left out; dx is one product whose k runs over dg Wg and then du Wu, dWg and dWu one each whose k
 // runs over the tokens twice, the left-out piece first (a gradient so carries 16 bits of dz and no more than its own
 // rounding).  Sums fp32 throughout.
-// fp32: the products are those of the linear layer (fp32 instructions, or six of bf16 pieces), the gate an
+// Few tokens, both types: the weights are streamed once (lrc_pair.h).
+// fp32 otherwise: the products are those of the linear layer (fp32 instructions, or six of bf16 pieces), the gate an
 // elementwise pass: the products take 10 to 100 times as long.
 #include "lrc_operand.h"
 #include "lrc_pair.h"
@@ -189,6 +190,10 @@ lrc_status gated_bf16(hipStream_t st, GatedArgs& a, void* ws) {
 }
 
 lrc_status gated_f32(hipStream_t st, GatedArgs& a, void* ws) {
+  if (gemm::stream_f32_pair(a.n, a.di) && a.ep.codes == nullptr)
+    return gemm::few_rows<float, FP32, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
+                                          a.di, a.ep, a.co, 4.0 * double(a.n) * double(a.df) * double(a.di),
+                                          4.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df));
   const GatedRoom room = forward_room(ws, LRC_F32, a.n, a.di, a.df);
   const size_t inner = lrc_linear_workspace(LRC_F32, a.n, a.di, a.df);
   // g and u go where they are kept, else to the workspace

@@ -134,6 +134,15 @@ struct RowPiece<BF16> {
   }
 };
 template <>
+struct RowPiece<FP32> {   // an instruction takes one of a lane's four k steps; any order of k serves both operands
+  using T = uint32_t;
+  using Acc = f32x4;
+  static constexpr int K = 16;
+  static __device__ __forceinline__ Acc mma(const u32x4& w, const u32x4& x, Acc c) {
+    return Block<16>::mma_f32(__builtin_bit_cast(f32x4, w), __builtin_bit_cast(f32x4, x), c);
+  }
+};
+template <>
 struct RowPiece<INT8> {
   using T = uint8_t;
   using Acc = i32x4;
@@ -161,7 +170,8 @@ __device__ __forceinline__ u32x4 row_piece(const T* p, int left) {
 }
 
 // OWN (integers, at most OWN_TOKENS): x is the tokens themselves, in the type of y, and every workgroup quantises them
-// into LDS while its first weights are on the way: a launch less (one token 4096 -> 11008: @@).
+// into LDS while its first weights are on the way: a launch less (one token 4096 -> 11008 12.4 us a call
+// against 15.1).
 constexpr int OWN_TOKENS = 4, OWN_ROOM = 16384;
 
 template <class TO, int NW>
@@ -325,6 +335,8 @@ inline bool stream_bf16_pair(int64_t n, int64_t N, int64_t K) {
   if (n > 64 || K % 8 != 0) return n <= 64;
   return n <= 8 || (n <= 32 && N * K <= (int64_t(1) << 22));
 }
+
+inline bool stream_f32_pair(int64_t n, int64_t K) { return n <= 8 || (n <= 64 && n * K <= (int64_t(1) << 16)); }
 
 // n <= 64; own: x is the tokens themselves (own_tokens)
 template <class TO, Element EL, int W>
