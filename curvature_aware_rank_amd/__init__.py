@@ -824,7 +824,7 @@ def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: s
     u = x Wu^T for the backward pass: "z" in full, "checkpoint" in 8 bits, "none" not at all.
 
     Returns (h, saved, info): saved is (g, u), ((codes, exps), (codes, exps)) or None; info (int32 (1,), sticky
-    LRC_ENONFINITE) is None unless given or save is "checkpoint"."""
+    LRC_ENONFINITE of a checkpoint's g or u) is None unless given."""
     x, ldx = _rows(x, "x")
     dt, dev = _dtype_code(x), x.device
     n, d_in = x.shape
@@ -842,7 +842,7 @@ def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: s
         kept = _new_checkpoint(n, d_ff, dev), _new_checkpoint(n, d_ff, dev)
     elif save != "none":
         raise ValueError("save is none, z or checkpoint")
-    if save == "checkpoint" or info is not None:
+    if info is not None:
         info = _info(info, dev)
     ws = _workspace(lib.lrc_gated_linear_workspace(dt, n, d_in, d_ff), dev)
     _run("lrc_gated_linear", dev, lib.lrc_gated_linear, _ptr(x), dt, n, d_in, d_ff, ldx, _ptr(Wg), _ptr(Wu), ldw, code,

@@ -537,7 +537,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
   // (the accumulators' first index is a constant in each call, so that they stay in registers)
-  static_assert(FM * MF == 64 || FM * MF == 16, "a wave holds 64 or 16 rows");
+  static_assert(FM * MF == 64 || FM * MF == 32 || FM * MF == 16, "a wave holds 64, 32 or 16 rows");
   constexpr int HALF_ROWS = ER / MF;
   emit(acc[0], acc[HALF_ROWS - 1], 0);
   if constexpr (FM * MF == 64) emit(acc[HALF_ROWS], acc[2 * HALF_ROWS - 1], 1);

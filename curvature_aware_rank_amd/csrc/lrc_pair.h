@@ -83,11 +83,11 @@ inline Plan plan_rows(int64_t M, int64_t N, int64_t K, bool pair) {
   double cost;
   return plan_gemm(M, pair ? 2 * N : N, K, 1, 64, cost);
 }
-// bytes of the tiles in the workspace; those of a pair's checkpoint pass through it unless tiles are large
+// bytes of the tiles in the workspace; those of a pair's checkpoint pass through it where tiles are tiny
 inline size_t rows_workspace(int64_t M, int64_t N, int64_t K, bool pair) {
   const Plan p = plan_rows(M, N, K, pair);
   if (!pair) return plan_bytes(p, M, N);
-  return p.tg.splits > 1 || p.tile != LARGE ? 2 * size_t(p.tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
+  return p.tg.splits > 1 || p.tile == TINY ? 2 * size_t(p.tg.splits) * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
 }
 
 template <class TO, Element EL, bool PAIR>
@@ -96,15 +96,25 @@ lrc_status rows_product(hipStream_t st, const char* name, GemmOperand A, GemmOpe
                         double bytes) {
   Plan p = plan_rows(M, N, K, PAIR);
   TileGrid& tg = p.tg;
-  tg.hold = PAIR && ep.codes != nullptr && p.tile != LARGE;
+  tg.hold = PAIR && ep.codes != nullptr && p.tile == TINY;
   const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
   if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
   ProfScope scope(name, st, flops, bytes);
   const unsigned g = unsigned(grid);
   if (p.tile == LARGE)
     rows_product_kernel<TO, 4, 2, 4, 8, 2, EL, PAIR><<<g, 512, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
-  else if (p.tile == SMALL)
-    rows_product_kernel<TO, 2, 2, 4, 4, 2, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+  else if (p.tile == SMALL) {
+    // A checkpoint's blocks need waves with 64 channels of each weight (4051 x 832 -> 2816 57 us; through the workspace
+    // and a second launch 82); otherwise square ones read fewer fragments.
+    if constexpr (PAIR && EL == BF16) {
+      if (ep.codes != nullptr && tg.splits == 1)
+        rows_product_kernel<TO, 4, 1, 2, 8, 2, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+      else
+        rows_product_kernel<TO, 2, 2, 4, 4, 2, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+    } else {
+      rows_product_kernel<TO, 2, 2, 4, 4, 2, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
+    }
+  }
   else
     rows_product_kernel<TO, 4, 1, 1, 4, 4, EL, PAIR><<<g, 256, 0, st>>>(A, B, M, N, K, tg, ep, co, partial);
   LRC_LAUNCHED();

@@ -237,7 +237,9 @@ def test_gated(lrc, dtype, n, d_in, d_ff, layout):
         a = base.act(g, name)
         e = (LIP * e_g + 8 * U * np.abs(g)) * (np.abs(u) + e_u) + np.abs(a) * e_u + 4 * U * np.abs(a * u)
         for save in ["none", "z", "checkpoint"]:
-            h, kept, info = lrc.lrc_gated_linear(lay(x, layout), lay(wg, layout), lay(wu, "packed"), act=name, save=save)
+            f = flag() if save == "checkpoint" else None
+            h, kept, info = lrc.lrc_gated_linear(lay(x, layout), lay(wg, layout), lay(wu, "packed"), act=name, save=save,
+                                                 info=f)
             check(h, a * u, e + half * (np.abs(a * u) + e) + TINY, ("h", name, save))
             if save == "z":
                 check(kept[0], g, e_g + half * (np.abs(g) + e_g) + TINY, "g")
@@ -269,7 +271,7 @@ def test_gated_exact_on_small_integers(lrc, dtype, n, d_in, d_ff):
     h, kept, _ = lrc.lrc_gated_linear(x, wg, wu, act="relu", save="z")
     assert torch.equal(h, (g.clamp_min(0) * u).to(dtype))
     assert torch.equal(kept[0], g.to(dtype)) and torch.equal(kept[1], u.to(dtype))
-    h, kept, info = lrc.lrc_gated_linear(x, wg, wu, act="none", save="checkpoint")
+    h, kept, info = lrc.lrc_gated_linear(x, wg, wu, act="none", save="checkpoint", info=flag())
     assert torch.equal(h, (g * u).to(dtype)) and int(info.cpu()) == 0
     for held, z in zip(kept, (g, u)):
         for p, q in zip(held, lrc.lrc_pack_activations(z.float())[:2]):
@@ -405,7 +407,7 @@ def test_gated_nonfinite_entries(lrc, dtype, n, d):
     dg, du = dh.double() * 3, dh.double() * 2
     assert same(got[0], dg) and same(got[1], du) and same(got[2], dg @ w.double() + du @ w.double())
     assert same(got[3], dg.T.contiguous() @ x.double()) and same(got[4], du.T.contiguous() @ x.double())
-    h, kept, info = lrc.lrc_gated_linear(x, w, w, act="none", save="checkpoint")
+    h, kept, info = lrc.lrc_gated_linear(x, w, w, act="none", save="checkpoint", info=flag())
     z = x.double() @ w.double().T
     assert same(h, z * z) and int(info.cpu()) == lrc.LRC_ENONFINITE
     clean = [t for t in range(n) if t not in (7, 9)]
@@ -686,7 +688,7 @@ def test_step_of_a_block(lrc):
     g1, g2, g3, gate = vec(), vec(), vec(), 0.5 * vec()
     s1, h1, st1, _, _ = lrc.lrc_block_norm(b, res, gate=gate, pre=(g1, None))
     h1k = lrc.lrc_pack_activations(h1)[:2]
-    a, kept, info = lrc.lrc_gated_linear(h1, wg, wu, save="checkpoint")
+    a, kept, info = lrc.lrc_gated_linear(h1, wg, wu, save="checkpoint", info=flag())
     ak = lrc.lrc_pack_activations(a)[:2]
     y, _, _ = lrc.lrc_linear(a, wd)
     s2, h2, st2, _, _ = lrc.lrc_block_norm(y, s1, post=(g2, None), scale=0.7, pre=(g3, None))
