@@ -574,13 +574,16 @@ def _rows(t, name, n=None, d=None, dtype=None, device=None):
     _dev(t, name)
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
-    rows, cols = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {len(shape)}")
+    rows, cols = shape
     if (n is not None and rows != n) or (d is not None and cols != d):
-        raise ValueError(f"{name} must have shape {(n, d)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {(n, d)}, got {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if cols and t.is_contiguous():
+        return t, cols
     s0, s1 = t.stride()
     if rows <= 1 or cols == 0:
         return t if s1 == 1 or cols <= 1 else t.contiguous(), max(cols, 1)
@@ -605,7 +608,7 @@ def _vector(t, name, n, device):
     if t is None:
         return None
     _dev(t, name)
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != device:
+    if t.dtype != torch.float32 or t.shape != (n,) or t.device != device:
         raise ValueError(f"{name} must be fp32 of shape ({n},) on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.contiguous()
 
@@ -854,7 +857,7 @@ def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: s
 def lrc_gated_linear_backward(dh: torch.Tensor, x, Wg: torch.Tensor, Wu: torch.Tensor, g, u, act: str = "silu",
                               need_dx: bool = True, need_dw: bool = True, dw_dtype=None):
     """Gradients of lrc_gated_linear.  dh: (n_tokens, d_ff); x: the input (n_tokens, d_in) like dh, or its (codes, exps)
-    checkpoint (may be None without need_dw); Wg, Wu: (d_ff, d_in); g, u: as kept, both in full or both as (codes, exps).
+    checkpoint (may be None without need_dw); Wg, Wu: (d_ff, d_in); g, u: as kept, both in full or both as pairs.
 
     Returns (dg, du, dx, dWg, dWu): dg = dh * u * act'(g) and du = dh * act(g), the output-gradient streams of the two
     projections, dx (n_tokens, d_in), dWg and dWu (d_ff, d_in) in dw_dtype (default dh's; torch.float32 allowed); None
@@ -1050,8 +1053,8 @@ def lrc_block_norm(b: torch.Tensor, residual=None, kind: str = "rms", eps: float
 
 def lrc_block_norm_backward(dh, ds, s, b, stats, kind: str = "rms", post=None, gate=None, scale: float = 1.0, pre=None,
                             need_dresidual: bool = True, need_db: bool = True, need_dparams: bool = True):
-    """Gradients of lrc_block_norm.  dh, ds: gradients of h and s, (n_tokens, d), one of them may be None; s, b: as in the
-    forward pass (s may be None without dh); stats, kind, post, gate, scale, pre: those of the forward pass.
+    """Gradients of lrc_block_norm.  dh, ds: gradients of h and s, (n_tokens, d), one of them may be None; s, b: as in
+    the forward pass (s may be None without dh); stats, kind, post, gate, scale, pre: those of the forward pass.
 
     Returns (dresidual, db, dgamma, dbeta, dpost_gamma, dpost_beta, dgate): the first two like dh, the others fp32 (d,);
     None where not needed or where the forward pass had no such parameter (a gamma or beta that was None included)."""
@@ -1071,8 +1074,8 @@ def lrc_block_norm_backward(dh, ds, s, b, stats, kind: str = "rms", post=None, g
     pg, pb = _norm_params(post, "post", d, dev, rms)
     ga, be = _norm_params(pre, "pre", d, dev, rms)
     gate = _vector(gate, "gate", d, dev)
-    if len(stats) != 4:
-        raise ValueError("stats is (mean_b, rstd_b, mean_s, rstd_s)")
+    if stats is None or len(stats) != 4:
+        raise ValueError("stats is (mean_b, rstd_b, mean_s, rstd_s) of a forward pass without quantize")
     names = ("mean_b", "rstd_b", "mean_s", "rstd_s")
     used = (post is not None and not rms, post is not None, dh is not None and not rms, dh is not None)
     stats = [_vector(v, nm, n, dev) if use else None for v, nm, use in zip(stats, names, used)]

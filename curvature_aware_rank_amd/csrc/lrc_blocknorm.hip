@@ -517,7 +517,7 @@ extern "C" lrc_status lrc_block_norm(const void* b, lrc_dtype dt, int64_t n_toke
   if ((s != nullptr && lds < d) || (h != nullptr && ldh < d) || (q != nullptr && ldq < d)) return LRC_EINVAL;
   if ((q == nullptr) != (qscale == nullptr) || (!post && (post_gamma != nullptr || post_beta != nullptr)))
     return LRC_EINVAL;
-  if (kind == LRC_NORM_RMS && beta != nullptr) return LRC_EINVAL;
+  if (kind == LRC_NORM_RMS && (beta != nullptr || post_beta != nullptr)) return LRC_EINVAL;
   if (n_tokens == 0) return LRC_OK;
   if (b == nullptr || (s == nullptr && h == nullptr && q == nullptr)) return LRC_EINVAL;
   const NormForward a = {b,   residual, n_tokens, ldb, ldr, int(d), post_gamma, post_beta, gate,   gamma, beta, scale,

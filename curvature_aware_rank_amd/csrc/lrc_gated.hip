@@ -191,8 +191,8 @@ lrc_status gated_bf16(hipStream_t st, GatedArgs& a, void* ws) {
 
 lrc_status gated_f32(hipStream_t st, GatedArgs& a, void* ws) {
   if (gemm::stream_f32_pair(a.n, a.di) && a.ep.codes == nullptr)
-    return gemm::few_rows<float, FP32, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
-                                          a.di, a.ep, a.co, 4.0 * double(a.n) * double(a.df) * double(a.di),
+    return gemm::few_rows<float, FP32, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n,
+                                          a.df, a.di, a.ep, a.co, 4.0 * double(a.n) * double(a.df) * double(a.di),
                                           4.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df));
   const GatedRoom room = forward_room(ws, LRC_F32, a.n, a.di, a.df);
   const size_t inner = lrc_linear_workspace(LRC_F32, a.n, a.di, a.df);
@@ -351,10 +351,10 @@ lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
     GemmSegments seg;
     seg.count = 2;
     seg.pa = seg.pb = 1u << 2;   // the second segment takes the second planes
+    const double bytes = 2.0 * (2.0 * double(a.n) * a.df + 2.0 * double(a.df) * a.di + double(a.n) * a.di);
     LRC_TRY((gemm_bf16<uint16_t, K_ROWS, K_COLS>(st, "gated_dx_kernel", {dg, f8, apart(dg, du)},
                                                  {wg, ldw, apart(wg, wu)}, a.n, a.di, a.df, seg, ep, room.partial,
-                                                 nullptr, 2 * product,
-                                                 2.0 * (2.0 * double(a.n) * a.df + 2.0 * double(a.df) * a.di + double(a.n) * a.di))));
+                                                 nullptr, 2 * product, bytes)));
   }
   if (!dw) return LRC_OK;
   Epilogue ep;

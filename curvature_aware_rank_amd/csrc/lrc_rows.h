@@ -1,7 +1,7 @@
 // Token rows held in registers: shapes, loads and sums shared by the norm and quantisation kernels.
 //
-// WPR waves share a token (WPR <= 0: 2^-WPR tokens share a wave), each lane holds 8 V of its channels.  Lane l holds channels
-// 8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint block; pieces are 16-byte
+// WPR waves share a token (WPR <= 0: 2^-WPR tokens share a wave), each lane holds 8 V of its channels.
+// Lane l holds channels 8 (k LANES + l) .. + 7 of piece k, so eight lanes hold one checkpoint block; pieces are 16-byte
 // accesses at any alignment, the last one of a ragged row is short.
 #pragma once
 
@@ -50,7 +50,8 @@ __device__ __forceinline__ float mean_of(float half) {
 constexpr int ROW_MAX = 16384;        // widest row held in registers
 
 constexpr int row_lanes(int wpr) { return wpr > 0 ? 64 * wpr : 64 >> -wpr; }
-constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : wpr > 0 ? 4 / wpr : 4 << -wpr; }   // tokens of a workgroup at a time
+// tokens of a workgroup at a time
+constexpr int row_groups(int wpr) { return wpr >= 4 ? 1 : wpr > 0 ? 4 / wpr : 4 << -wpr; }
 constexpr int row_threads(int wpr) { return row_lanes(wpr) * row_groups(wpr); }
 
 template <class T, int WPR, int V>

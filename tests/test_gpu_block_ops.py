@@ -393,7 +393,7 @@ def test_gated_weight_gradient_keeps_the_bits_of_dz(lrc, act, n, d_in, d_ff):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n,d", [(200, 72), (1300, 904)])
+@pytest.mark.parametrize("n,d", [(200, 72), (1300, 904), (4100, 2104)])
 def test_gated_nonfinite_entries(lrc, dtype, n, d):
     """NaN and infinities give what the plain products give, and stay in their rows."""
     ones = lambda *s: torch.ones(*s, dtype=dtype)   # noqa: E731
@@ -915,7 +915,7 @@ def test_refusals(lrc):
            lambda: lrc.lrc_block_norm(x, gate=v[:63]), lambda: lrc.lrc_block_norm(x, need_s=False, need_h=False),
            lambda: lrc.lrc_block_norm(x, x.bfloat16()),
            lambda: lrc.lrc_block_norm_backward(None, None, x, x, st), lambda: lrc.lrc_block_norm_backward(x, None, None, x, st),
-           lambda: lrc.lrc_block_norm_backward(x, None, x, x, st[:3]),
+           lambda: lrc.lrc_block_norm_backward(x, None, x, x, st[:3]), lambda: lrc.lrc_block_norm_backward(x, x, x, x, None),
            lambda: lrc.lrc_block_norm_backward(x, None, x, x, st, kind="layer"),
            lambda: lrc.lrc_block_norm_backward(x, None, x, None, st, gate=v)]
     for k, call in enumerate(bad):
