@@ -6,6 +6,9 @@
 // A token lies in the registers of 1 to 8 waves (lrc_rows.h): b and the residual are read once, s and h written
 // once, the statistics of both norms are taken from registers in between (values centred before they are squared).
 // The next token's loads are in flight while the present one is worked on.
+// Bound by memory: forward 65536 x 4096 bf16, both norms, 445 us (2.15 GB, 4.8 TB/s), backward 32768 x 4096 308 us
+// (1.61 GB, 5.2 TB/s) and 9 for the shares' sums; one token 4.4 us, a launch.  Rows of no whole 16-byte pieces reach
+// 2 to 3 TB/s (334 or 5114 bf16 channels): every piece straddles two, and the last one is read element by element.
 // Backward: all parameter gradients follow from four column sums over the tokens,
 //   A = sum dh s^, B = sum dh, C = sum t b^, D = sum t      (^: normalised; b^ = b without a post-norm)
 //   dgamma = A, dbeta = B, dpost_gamma = scale gate C, dpost_beta = scale gate D,
