@@ -230,8 +230,8 @@ GatedRoom backward_room(void* ws, int dt, int64_t n, int64_t di, int64_t df) {
     if (df % 8 != 0) r.dz = cv.take<uint16_t>(size_t(2) * n * f8);
     r.x = cv.take<uint16_t>(size_t(n) * i8);
     if (di % 8 != 0) r.wg = cv.take<uint16_t>(size_t(2) * df * i8);
-    r.partial = cv.take<float>(std::max(gemm_segments_workspace(n, di, df, K_ROWS, K_COLS, 2),
-                                        gemm_weight_pair_workspace(df, di, n)) / 4);
+    const size_t px = gemm_segments_workspace(n, di, df, K_ROWS, K_COLS, 2), pw = gemm_weight_pair_workspace(df, di, n);
+    r.partial = cv.take<float>((gemm_gradients_joined(n, di, df) ? px + pw : std::max(px, pw)) / 4);
   }
   r.bytes = cv.bytes();
   return r;
@@ -346,28 +346,35 @@ lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
   }
   LRC_TRY(gate_backward<uint16_t>(st, a, room, dw, jobs));
   const double product = 2.0 * double(a.n) * double(a.df) * double(a.di);
+  const double xbytes = 2.0 * (2.0 * double(a.n) * a.df + 2.0 * double(a.df) * a.di + double(a.n) * a.di);
+  const double wbytes = 2.0 * (4.0 * double(a.n) * a.df + double(a.n) * a.di + 2.0 * double(a.df) * a.di);
+  // dx: the second segment takes the second planes
+  const GemmOperand G = {dg, f8, apart(dg, du)}, W = {wg, ldw, apart(wg, wu)};
+  Epilogue epx, epw;
+  epx.y = a.dx;
+  epx.ldy = a.lddx;
+  const GemmOperand A1 = {dg, f8, apart(dg, room.low)}, A2 = {du, f8, apart(du, room.low + plane)}, B = {x, ldx, 0};
+  epw.y = a.dWg;
+  epw.y2 = a.dWu;
+  epw.ldy = a.lddw;
+  if (a.dx != nullptr && dw && gemm_gradients_joined(a.n, a.di, a.df)) {
+    auto go = [&](auto tag) {
+      return gemm_gradients<decltype(tag)>(st, "gated_grads_kernel", G, W, A1, A2, B, a.n, a.di, a.df, epx, epw,
+                                           room.partial, 6 * product, xbytes + wbytes);
+    };
+    return a.dw_dt == LRC_F32 ? go(float{}) : go(uint16_t{});
+  }
   if (a.dx != nullptr) {
-    Epilogue ep;
-    ep.y = a.dx;
-    ep.ldy = a.lddx;
     GemmSegments seg;
     seg.count = 2;
-    seg.pa = seg.pb = 1u << 2;   // the second segment takes the second planes
-    const double bytes = 2.0 * (2.0 * double(a.n) * a.df + 2.0 * double(a.df) * a.di + double(a.n) * a.di);
-    LRC_TRY((gemm_bf16<uint16_t, K_ROWS, K_COLS>(st, "gated_dx_kernel", {dg, f8, apart(dg, du)},
-                                                 {wg, ldw, apart(wg, wu)}, a.n, a.di, a.df, seg, ep, room.partial,
-                                                 nullptr, 2 * product, bytes)));
+    seg.pa = seg.pb = 1u << 2;
+    LRC_TRY((gemm_bf16<uint16_t, K_ROWS, K_COLS>(st, "gated_dx_kernel", G, W, a.n, a.di, a.df, seg, epx, room.partial,
+                                                 nullptr, 2 * product, xbytes)));
   }
   if (!dw) return LRC_OK;
-  Epilogue ep;
-  ep.y = a.dWg;
-  ep.y2 = a.dWu;
-  ep.ldy = a.lddw;
-  const GemmOperand A1 = {dg, f8, apart(dg, room.low)}, A2 = {du, f8, apart(du, room.low + plane)}, B = {x, ldx, 0};
-  const double bytes = 2.0 * (4.0 * double(a.n) * a.df + double(a.n) * a.di + 2.0 * double(a.df) * a.di);
   auto go = [&](auto tag) {
-    return gemm_weight_pair<decltype(tag)>(st, "gated_dw_kernel", A1, A2, B, a.df, a.di, a.n, ep, room.partial,
-                                           4 * product, bytes);
+    return gemm_weight_pair<decltype(tag)>(st, "gated_dw_kernel", A1, A2, B, a.df, a.di, a.n, epw, room.partial,
+                                           4 * product, wbytes);
   };
   return a.dw_dt == LRC_F32 ? go(float{}) : go(uint16_t{});
 }

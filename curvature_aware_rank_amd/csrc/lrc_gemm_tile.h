@@ -247,12 +247,18 @@ __device__ __forceinline__ void tile_at(int64_t i, int64_t nm, int64_t nn, int64
 // one launch (the second one's A is co.B, its y ep.y2).
 // PAIR: the tile holds BN / 2 channels of each of two weights; a wave's first FN MF / 2 columns are the
 // first one's, the others the same channels of the second.
+// block: the workgroup's place in the product's grid.
+template <int BYTES, int I>
+__device__ __forceinline__ uint8_t* stage_room() {   // the same for all products of a kernel
+  __shared__ __attribute__((aligned(1024))) uint8_t room[BYTES];
+  return room;
+}
 template <class TO, int KA, int KB, int MF, int WM, int WN, int FM, int FN, int KS, int NST, int SEG, Element EL,
           bool PAIR = false>
 __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N, int64_t K,
                                           const GemmSegments& seg, const TileGrid& tg, const Epilogue& ep,
                                           float* __restrict__ partial, const int32_t* __restrict__ skip,
-                                          const Companion& co = Companion{}) {
+                                          const Companion& co, int block) {
   constexpr int NW = WM * WN, BM = WM * FM * MF, BN = WN * FN * MF;
   constexpr int AB = BM * KS * 2, STB = (BM + BN) * KS * 2;
   constexpr int ES = EL == FP32 ? 4 : 2;
@@ -261,18 +267,18 @@ __device__ __forceinline__ void gemm_tile(const GemmOperand& A, const GemmOperan
   using SB = Stager<KB, BN, NW, KS, MF, ES, HW>;
   constexpr int L = SA::LOADS + SB::LOADS;      // loads of a wave per stage
   // one LDS object per stage, so that a read of one stage does not wait for the loads of others
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[STB], sb1[STB], sb2[NST > 2 ? STB : 16],
-      sb3[NST > 3 ? STB : 16];
+  uint8_t *const sb0 = stage_room<STB, 0>(), *const sb1 = stage_room<STB, 1>();
+  uint8_t* const sb2 = NST > 2 ? stage_room<(NST > 2 ? STB : 16), 2>() : nullptr;
+  uint8_t* const sb3 = NST > 3 ? stage_room<(NST > 3 ? STB : 16), 3>() : nullptr;
   constexpr int ER = FM * MF < 32 ? FM * MF : 32;   // rows a wave finishes at a time
   constexpr int PART = ER * FN * MF * 4;
   constexpr int FIT = STB / PART;               // of them in a stage buffer
   static_assert(NST >= 2 && NST <= 4 && KS % 32 == 0 && FIT >= 1 && FIT * NST >= NW, "the epilogue rows fit the stage buffers");
 
   if (skip != nullptr && *skip != 0) return;
-  const int b = blockIdx.x;
-  const int local = b / NXCD;
+  const int local = block / NXCD;
   const int split = local / tg.per_xcd;
-  const int64_t ti = int64_t(b % NXCD) * tg.per_xcd + local % tg.per_xcd;
+  const int64_t ti = int64_t(block % NXCD) * tg.per_xcd + local % tg.per_xcd;
   if (ti >= tg.tiles) return;
   const bool other = SEG == 2 && ti >= tg.half;   // of two products, the second
   int64_t tm, tn;

@@ -22,7 +22,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void rows_product_kernel(GemmOpera
                                                                        int64_t N, int64_t K, TileGrid tg, Epilogue ep,
                                                                        Companion co, float* __restrict__ partial) {
   gemm_tile<TO, K_ROWS, K_ROWS, 16, WM, WN, FM, FN, 64, NST, false, EL, PAIR>(A, B, M, N, K, GemmSegments{}, tg, ep,
-                                                                              partial, nullptr, co);
+                                                                              partial, nullptr, co, blockIdx.x);
 }
 
 // Sum of the splits' tiles in split order (integers: exact in any), then the epilogue.  One lane per

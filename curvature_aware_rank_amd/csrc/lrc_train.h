@@ -344,6 +344,13 @@ template <class TO>
 lrc_status gemm_weight_pair(hipStream_t st, const char* name, GemmOperand A1, GemmOperand A2, GemmOperand B, int64_t M,
                             int64_t N, int64_t K, const Epilogue& ep, float* partial, double flops, double bytes);
 size_t gemm_weight_pair_workspace(int64_t M, int64_t N, int64_t K);
+// These and dx = Ax Bx (two planes each, one after the other) in one launch, where both take the smallest tiles: the
+// results are those of the two calls.  `partial`: the workspaces of both.
+bool gemm_gradients_joined(int64_t n, int64_t di, int64_t df);
+template <class TO>
+lrc_status gemm_gradients(hipStream_t st, const char* name, GemmOperand Ax, GemmOperand Bx, GemmOperand A1,
+                          GemmOperand A2, GemmOperand B, int64_t n, int64_t di, int64_t df, const Epilogue& epx,
+                          const Epilogue& epw, float* partial, double flops, double bytes);
 // workspace of a product of `count` segments
 size_t gemm_segments_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, int count);
 // estimates in microseconds of an fp32 product, on fp32 operands and on ones split in three
