@@ -4,12 +4,12 @@
 //
 // bf16 forward: one product whose tiles hold as many channels of Wg as of Wu (lrc_gemm_tile.h), so x is staged once
 // for both and act(g) u is formed from the accumulators; g and u reach memory only where they are kept.
-// (8192 x 4096 x 11008: forward 1180 us; backward dz 199 us, memory, 5.4 TB/s; dx 1230, dWg and dWu 2520: the matrix
-// pipes, busy 61 to 66 % of the cycles at 1.75 to 1.85 GHz, 1190 TFLOP/s.)
+// (8192 x 4096 x 11008: forward 1180 us; backward dz 199 us, memory, 5.4 TB/s; dx, dWg and dWu 3700, 1200 TFLOP/s:
+// the matrix pipes, busy 61 to 66 % of the cycles at 1.75 to 1.85 GHz.)
 // bf16 backward: one pass writes dg and du (the output-gradient streams of the two projections) and what their
 // rounding to bf16 left out; dx is one product whose k runs over dg Wg and then du Wu, dWg and dWu one each whose k
 // runs over the tokens twice, the left-out piece first (a gradient so carries 16 bits of dz and no more than its own
-// rounding).  Sums fp32 throughout.
+// rounding); all three in one launch where their tiles are of one kind.  Sums fp32 throughout.
 // Few tokens, both types: the weights are streamed once (lrc_pair.h).
 // fp32 otherwise: the products are those of the linear layer (fp32 instructions, or six of bf16 pieces), the gate an
 // elementwise pass: the products take 10 to 100 times as long.

@@ -46,31 +46,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_weight_pair_kernel(GemmO
                                                                        blockIdx.x);
 }
 
-// Both on the smallest tiles in one launch, the weight gradients first: dx does not wait for them, and the two
-// seldom fill the chip alone (1000 x 521 -> 303 14.7 us for 9.7 and 14.4 in a row).
+// f(matrix instruction's edge, waves, a wave's fragments, stage, stages) of a tile whose B runs along columns
+template <int V>
+using I = std::integral_constant<int, V>;
+template <int TILE, class F>
+__device__ __forceinline__ void with_cols_tile(F f) {
+  if constexpr (TILE == LARGE)
+    f(I<32>{}, I<4>{}, I<2>{}, I<2>{}, I<4>{}, I<32>{}, I<4>{});
+  else if constexpr (TILE == SMALL)
+    f(I<16>{}, I<2>{}, I<2>{}, I<4>{}, I<4>{}, I<64>{}, I<2>{});
+  else
+    f(I<16>{}, I<4>{}, I<1>{}, I<1>{}, I<4>{}, I<64>{}, I<4>{});
+}
+// Both in one launch: dx does not wait for the weight gradients, and neither often fills the chip to its end.  The
+// product with the longer tiles goes first (1000 x 521 -> 303 33 -> 27 us a call, 8192 x 1024 -> 4096 500 -> 463, 6144 x 3584
+// -> 4736 1350 -> 1240, 8192 x 4096 -> 11008 3970 -> 3910).
 struct Product {
   GemmOperand A, B;
   int64_t M, N, K;
   TileGrid tg;
   Epilogue ep;
   float* partial;
-  unsigned groups() const { return unsigned(int64_t(NXCD) * tg.per_xcd * tg.splits); }
+  int64_t groups() const { return int64_t(NXCD) * tg.per_xcd * tg.splits; }
 };
-template <class TO>
-__global__ __launch_bounds__(256, 2) void gemm_gradients_kernel(Product w, GemmOperand A2, Product x) {
-  const int block = blockIdx.x, first = NXCD * w.tg.per_xcd * w.tg.splits;
+template <class TO, int TILE>
+__global__ __launch_bounds__(TILE == LARGE ? 512 : 256, 2) void gemm_gradients_kernel(Product w, GemmOperand A2,
+                                                                                      Product x, int x0, int w0) {
+  const int block = blockIdx.x;
   GemmSegments seg;
   seg.count = 2;
-  if (block < first) {
+  if (w0 < x0 ? block < x0 : block >= w0) {
     seg.pa = 1u;
     Companion co;
     co.B = A2;
-    gemm_tile<TO, K_COLS, K_COLS, 16, 4, 1, 1, 4, 64, 4, 2, BF16>(w.A, w.B, w.M, w.N, w.K, seg, w.tg, w.ep, w.partial,
-                                                                  nullptr, co, block);
+    auto go = [&](auto mf, auto wm, auto wn, auto fm, auto fn, auto ks, auto nst) {
+      gemm_tile<TO, K_COLS, K_COLS, mf, wm, wn, fm, fn, ks, nst, 2, BF16>(w.A, w.B, w.M, w.N, w.K, seg, w.tg, w.ep,
+                                                                          w.partial, nullptr, co, block - w0);
+    };
+    with_cols_tile<TILE>(go);
   } else {
     seg.pa = seg.pb = 1u << 2;
-    gemm_tile<uint16_t, K_ROWS, K_COLS, 16, 4, 1, 1, 4, 64, 4, 1, BF16>(x.A, x.B, x.M, x.N, x.K, seg, x.tg, x.ep,
-                                                                        x.partial, nullptr, Companion{}, block - first);
+    auto go = [&](auto mf, auto wm, auto wn, auto fm, auto fn, auto ks, auto nst) {
+      gemm_tile<uint16_t, K_ROWS, K_COLS, mf, wm, wn, fm, fn, ks, nst, 1, BF16>(
+          x.A, x.B, x.M, x.N, x.K, seg, x.tg, x.ep, x.partial, nullptr, Companion{}, block - x0);
+    };
+    with_cols_tile<TILE>(go);
   }
 }
 
@@ -258,21 +278,35 @@ template lrc_status gemm_weight_pair<float>(hipStream_t, const char*, GemmOperan
 template lrc_status gemm_weight_pair<uint16_t>(hipStream_t, const char*, GemmOperand, GemmOperand, GemmOperand, int64_t,
                                                int64_t, int64_t, const Epilogue&, float*, double, double);
 
-bool gemm_gradients_joined(int64_t n, int64_t di, int64_t df) {
+static Plan plan_dx(int64_t n, int64_t di, int64_t df) {
   double cost;
-  return plan_gemm(n, di, df, 2, large_stage(K_ROWS, K_COLS), cost).tile == TINY && plan_weight_pair(df, di, n).tile == TINY;
+  return plan_gemm(n, di, df, 2, large_stage(K_ROWS, K_COLS), cost);
+}
+bool gemm_gradients_joined(int64_t n, int64_t di, int64_t df) {
+  return plan_dx(n, di, df).tile == plan_weight_pair(df, di, n).tile;
 }
 template <class TO>
 lrc_status gemm_gradients(hipStream_t st, const char* name, GemmOperand Ax, GemmOperand Bx, GemmOperand A1,
                           GemmOperand A2, GemmOperand B, int64_t n, int64_t di, int64_t df, const Epilogue& epx,
                           const Epilogue& epw, float* partial, double flops, double bytes) {
-  double cost;
-  const Plan px = plan_gemm(n, di, df, 2, large_stage(K_ROWS, K_COLS), cost), pw = plan_weight_pair(df, di, n);
+  const Plan px = plan_dx(n, di, df), pw = plan_weight_pair(df, di, n);
   const Product x = {Ax, Bx, n, di, df, px.tg, epx, partial};
   const Product w = {A1, B, df, di, n, pw.tg, epw, partial + plan_bytes(px, n, di) / 4};
-  if (int64_t(x.groups()) + w.groups() >= (int64_t(1) << 31)) return LRC_EINVAL;
+  const int64_t grid = x.groups() + w.groups();
+  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
+  const bool x_first = px.tg.steps_per_split > pw.tg.steps_per_split;
+  const int x0 = x_first ? 0 : int(w.groups()), w0 = x_first ? int(x.groups()) : 0;
   ProfScope scope(name, st, flops, bytes);
-  gemm_gradients_kernel<TO><<<w.groups() + x.groups(), 256, 0, st>>>(w, A2, x);
+  auto go = [&](auto tile) {
+    constexpr int TILE = decltype(tile)::value;
+    gemm_gradients_kernel<TO, TILE><<<unsigned(grid), TILE == LARGE ? 512 : 256, 0, st>>>(w, A2, x, x0, w0);
+  };
+  if (px.tile == LARGE)
+    go(I<LARGE>{});
+  else if (px.tile == SMALL)
+    go(I<SMALL>{});
+  else
+    go(I<TINY>{});
   LRC_LAUNCHED();
   if (px.tg.splits > 1) LRC_TRY(gemm_finish<uint16_t>(st, x.partial, px.tg.splits, n, di, epx, nullptr));
   return pw.tg.splits == 1 ? LRC_OK : gemm_finish<TO>(st, w.partial, pw.tg.splits, 2 * df, di, epw, nullptr);

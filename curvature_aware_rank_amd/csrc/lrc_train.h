@@ -344,7 +344,7 @@ template <class TO>
 lrc_status gemm_weight_pair(hipStream_t st, const char* name, GemmOperand A1, GemmOperand A2, GemmOperand B, int64_t M,
                             int64_t N, int64_t K, const Epilogue& ep, float* partial, double flops, double bytes);
 size_t gemm_weight_pair_workspace(int64_t M, int64_t N, int64_t K);
-// These and dx = Ax Bx (two planes each, one after the other) in one launch, where both take the smallest tiles: the
+// These and dx = Ax Bx (two planes each, one after the other) in one launch, where both take tiles of one kind: the
 // results are those of the two calls.  `partial`: the workspaces of both.
 bool gemm_gradients_joined(int64_t n, int64_t di, int64_t df);
 template <class TO>

@@ -356,6 +356,22 @@ def test_gated_backward_exact_on_small_integers(lrc, dtype, n, d_in, d_ff, held)
     assert some[2] is None and all(torch.equal(some[k], got[k]) for k in (0, 1, 3, 4))
 
 
+@pytest.mark.parametrize("n,d_in,d_ff", [(300, 200, 136), (64, 1000, 72), (1, 8, 8), (4096, 1536, 1024), (8192, 512, 4096),
+                                         (4100, 1540, 1030), (2048, 5632, 1024), (2050, 5637, 1026)])
+def test_gated_backward_joined_products(lrc, n, d_in, d_ff):
+    """All products of a bf16 block in one launch, on each kind of tile, with and without splits: the bits of each
+    gradient asked for alone, whose kernels the tests above hold to the formulas."""
+    r = gen(n + d_in)
+    make = lambda *s: torch.randn(*s, generator=r).bfloat16().to(dev())   # noqa: E731
+    dh, g, u, x, wg, wu = make(n, d_ff), make(n, d_ff), make(n, d_ff), make(n, d_in), make(d_ff, d_in), make(d_ff, d_in)
+    for dw_dtype in (torch.bfloat16, torch.float32):
+        call = lambda **k: lrc.lrc_gated_linear_backward(dh, x, wg, wu, g, u, dw_dtype=dw_dtype, **k)   # noqa: E731
+        full, only_w, only_x = call(), call(need_dx=False), call(need_dw=False)
+        assert all(torch.isfinite(t).all() for t in full)
+        assert all(torch.equal(full[k], only_w[k]) for k in (0, 1, 3, 4))
+        assert all(torch.equal(full[k], only_x[k]) for k in (0, 1, 2))
+
+
 def test_gated_backward_against_differences(lrc):
     n, d, f = 5, 24, 40
     x, dh = stream(n, d, torch.float32, 1), stream(n, f, torch.float32, 2)
