@@ -167,13 +167,12 @@ struct GatedArgs {
   gemm::Companion co;
 };
 
-lrc_status gated_bf16(hipStream_t st, GatedArgs& a, void* ws) {
+lrc_status gated_bf16(hipStream_t st, GatedArgs& a, const GatedRoom& room) {
   const double flops = 4.0 * double(a.n) * double(a.df) * double(a.di);
   const double bytes = 2.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df);
   if (gemm::stream_bf16_pair(a.n, a.df, a.di) && a.ep.codes == nullptr)
     return gemm::few_rows<uint16_t, BF16, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
                                              a.di, a.ep, a.co, flops, bytes);
-  const GatedRoom room = forward_room(ws, LRC_BF16, a.n, a.di, a.df);
   GemmOperand x = {static_cast<const uint16_t*>(a.x), a.ldx, 0}, g = {static_cast<const uint16_t*>(a.Wg), a.ldw, 0},
               u = {static_cast<const uint16_t*>(a.Wu), a.ldw, 0};
   if (a.di % 8 != 0) {
@@ -191,12 +190,11 @@ lrc_status gated_bf16(hipStream_t st, GatedArgs& a, void* ws) {
                                                   flops, bytes);
 }
 
-lrc_status gated_f32(hipStream_t st, GatedArgs& a, void* ws) {
+lrc_status gated_f32(hipStream_t st, GatedArgs& a, const GatedRoom& room) {
   if (gemm::stream_f32_pair(a.n, a.di) && a.ep.codes == nullptr)
     return gemm::few_rows<float, FP32, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n,
                                           a.df, a.di, a.ep, a.co, 4.0 * double(a.n) * double(a.df) * double(a.di),
                                           4.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df));
-  const GatedRoom room = forward_room(ws, LRC_F32, a.n, a.di, a.df);
   const size_t inner = lrc_linear_workspace(LRC_F32, a.n, a.di, a.df);
   // g and u go where they are kept, else to the workspace
   float *g = static_cast<float*>(a.ep.z), *u = static_cast<float*>(a.co.z);
@@ -230,8 +228,7 @@ GatedRoom backward_room(void* ws, int dt, int64_t n, int64_t di, int64_t df) {
     if (df % 8 != 0) r.dz = cv.take<uint16_t>(size_t(2) * n * f8);
     r.x = cv.take<uint16_t>(size_t(n) * i8);
     if (di % 8 != 0) r.wg = cv.take<uint16_t>(size_t(2) * df * i8);
-    const size_t px = gemm_segments_workspace(n, di, df, K_ROWS, K_COLS, 2), pw = gemm_weight_pair_workspace(df, di, n);
-    r.partial = cv.take<float>((gemm_gradients_joined(n, di, df) ? px + pw : std::max(px, pw)) / 4);
+    r.partial = cv.take<float>(gemm_gradients_workspace(n, di, df) / 4);
   }
   r.bytes = cv.bytes();
   return r;
@@ -299,8 +296,7 @@ lrc_status gate_backward(hipStream_t st, const GatedBack& a, const GatedRoom& ro
   return LRC_OK;
 }
 
-lrc_status gated_back_f32(hipStream_t st, const GatedBack& a, void* ws) {
-  const GatedRoom room = backward_room(ws, LRC_F32, a.n, a.di, a.df);
+lrc_status gated_back_f32(hipStream_t st, const GatedBack& a, const GatedRoom& room) {
   LRC_TRY(gate_backward<float>(st, a, room, false, OperandJobs{}));
   auto grads = [&](const void* dz, const void* W, void* dW, bool add) -> lrc_status {
     if (a.dx == nullptr && dW == nullptr) return LRC_OK;
@@ -317,8 +313,7 @@ int64_t apart(const uint16_t* from, const uint16_t* to) {
   return (reinterpret_cast<intptr_t>(to) - reinterpret_cast<intptr_t>(from)) / 2;
 }
 
-lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
-  const GatedRoom room = backward_room(ws, LRC_BF16, a.n, a.di, a.df);
+lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, const GatedRoom& room) {
   const bool dw = a.dWg != nullptr, held = a.x == nullptr;
   const int64_t f8 = round8(a.df), i8 = round8(a.di), plane = a.n * f8;
   const uint16_t *dg = static_cast<const uint16_t*>(a.dg), *du = static_cast<const uint16_t*>(a.du);
@@ -357,26 +352,13 @@ lrc_status gated_back_bf16(hipStream_t st, const GatedBack& a, void* ws) {
   epw.y = a.dWg;
   epw.y2 = a.dWu;
   epw.ldy = a.lddw;
-  if (a.dx != nullptr && dw && gemm_gradients_joined(a.n, a.di, a.df)) {
-    auto go = [&](auto tag) {
-      return gemm_gradients<decltype(tag)>(st, "gated_grads_kernel", G, W, A1, A2, B, a.n, a.di, a.df, epx, epw,
-                                           room.partial, 6 * product, xbytes + wbytes);
-    };
-    return a.dw_dt == LRC_F32 ? go(float{}) : go(uint16_t{});
-  }
-  if (a.dx != nullptr) {
-    GemmSegments seg;
-    seg.count = 2;
-    seg.pa = seg.pb = 1u << 2;
-    LRC_TRY((gemm_bf16<uint16_t, K_ROWS, K_COLS>(st, "gated_dx_kernel", G, W, a.n, a.di, a.df, seg, epx, room.partial,
-                                                 nullptr, 2 * product, xbytes)));
-  }
-  if (!dw) return LRC_OK;
+  if (a.dx == nullptr && !dw) return LRC_OK;
   auto go = [&](auto tag) {
-    return gemm_weight_pair<decltype(tag)>(st, "gated_dw_kernel", A1, A2, B, a.df, a.di, a.n, epw, room.partial,
-                                           4 * product, wbytes);
+    return gemm_gradients<decltype(tag)>(st, "gated_grads_kernel", G, W, A1, A2, B, a.n, a.di, a.df, epx, epw,
+                                         room.partial, (a.dx ? 2 * product : 0) + (dw ? 4 * product : 0),
+                                         (a.dx ? xbytes : 0) + (dw ? wbytes : 0));
   };
-  return a.dw_dt == LRC_F32 ? go(float{}) : go(uint16_t{});
+  return dw && a.dw_dt == LRC_F32 ? go(float{}) : go(uint16_t{});
 }
 
 bool act_ok(int a) { return a >= LRC_ACT_NONE && a <= LRC_ACT_SILU; }
@@ -408,8 +390,8 @@ extern "C" lrc_status lrc_gated_linear(const void* x, lrc_dtype dt, int64_t n_to
   if (n_tokens == 0) return LRC_OK;
   if (x == nullptr || Wg == nullptr || Wu == nullptr || h == nullptr) return LRC_EINVAL;
   if (!in_place(x, ldx, d_in, dt) || !in_place(Wg, ldw, d_in, dt) || !in_place(Wu, ldw, d_in, dt)) return LRC_EINVAL;
-  const size_t need = lrc_gated_linear_workspace(dt, n_tokens, d_in, d_ff);
-  if (ws_bytes < need || (need > 0 && ws == nullptr)) return LRC_EWORKSPACE;
+  const GatedRoom room = forward_room(ws, dt, n_tokens, d_in, d_ff);
+  if (ws_bytes < room.bytes || (room.bytes > 0 && ws == nullptr)) return LRC_EWORKSPACE;
   GatedArgs a = {n_tokens, d_in, d_ff, x, ldx, Wg, Wu, ldw, {}, {}};
   a.ep.act = act;
   a.ep.y = h;
@@ -424,7 +406,7 @@ extern "C" lrc_status lrc_gated_linear(const void* x, lrc_dtype dt, int64_t n_to
   a.ep.nb = cdiv(d_ff, CKB);
   a.ep.info = info;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return dt == LRC_BF16 ? gated_bf16(st, a, ws) : gated_f32(st, a, ws);
+  return dt == LRC_BF16 ? gated_bf16(st, a, room) : gated_f32(st, a, room);
 }
 
 extern "C" size_t lrc_gated_linear_backward_workspace(lrc_dtype dt, int64_t n_tokens, int64_t d_in, int64_t d_ff) {
@@ -462,9 +444,9 @@ extern "C" lrc_status lrc_gated_linear_backward(const void* dh, lrc_dtype dt, in
   if (!in_place(dg, d_ff, d_ff, dt) || !in_place(du, d_ff, d_ff, dt)) return LRC_EINVAL;
   if (dx != nullptr && (!in_place(Wg, ldw, d_in, dt) || !in_place(Wu, ldw, d_in, dt))) return LRC_EINVAL;
   if (dw && x != nullptr && !in_place(x, ldx, d_in, dt)) return LRC_EINVAL;
-  const size_t need = lrc_gated_linear_backward_workspace(dt, n_tokens, d_in, d_ff);
-  if (ws_bytes < need || (need > 0 && ws == nullptr)) return LRC_EWORKSPACE;
+  const GatedRoom room = backward_room(ws, dt, n_tokens, d_in, d_ff);
+  if (ws_bytes < room.bytes || (room.bytes > 0 && ws == nullptr)) return LRC_EWORKSPACE;
   const GatedBack a = {n_tokens, d_in, d_ff, dh, lddh, Wg, Wu, ldw, x, ldx, xcodes, xexps, act, g, u, ldz, gcodes,
                        gexps, ucodes, uexps, dg, du, dx, lddx, dWg, dWu, int(dw_dt), lddw};
-  return dt == LRC_BF16 ? gated_back_bf16(st, a, ws) : gated_back_f32(st, a, ws);
+  return dt == LRC_BF16 ? gated_back_bf16(st, a, room) : gated_back_f32(st, a, room);
 }

@@ -24,6 +24,8 @@
 // a second kernel adds them in split order and runs the epilogue (bit-reproducible).
 #include "lrc_gemm_tile.h"
 
+#include <cmath>
+
 namespace lrc {
 namespace gemm {
 
@@ -35,17 +37,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_bf16_kernel(GemmOperand 
   gemm_tile<TO, KA, KB, MF, WM, WN, FM, FN, KS, NST, SEG, EL>(A, B, M, N, K, seg, tg, ep, partial, skip, Companion{},
                                                            blockIdx.x);
 }
-template <class TO, int MF, int WM, int WN, int FM, int FN, int KS, int NST>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_weight_pair_kernel(GemmOperand A1, GemmOperand A2, GemmOperand B,
-                                                                           int64_t M, int64_t N, int64_t K,
-                                                                           GemmSegments seg, TileGrid tg, Epilogue ep,
-                                                                           float* __restrict__ partial) {
-  Companion co;
-  co.B = A2;
-  gemm_tile<TO, K_COLS, K_COLS, MF, WM, WN, FM, FN, KS, NST, 2, BF16>(A1, B, M, N, K, seg, tg, ep, partial, nullptr, co,
-                                                                       blockIdx.x);
-}
-
 // f(matrix instruction's edge, waves, a wave's fragments, stage, stages) of a tile whose B runs along columns
 template <int V>
 using I = std::integral_constant<int, V>;
@@ -59,8 +50,8 @@ __device__ __forceinline__ void with_cols_tile(F f) {
     f(I<16>{}, I<4>{}, I<1>{}, I<1>{}, I<4>{}, I<64>{}, I<4>{});
 }
 // Both in one launch: dx does not wait for the weight gradients, and neither often fills the chip to its end.  The
-// product with the longer tiles goes first (1000 x 521 -> 303 33 -> 27 us a call, 8192 x 1024 -> 4096 500 -> 463, 6144 x 3584
-// -> 4736 1350 -> 1240, 8192 x 4096 -> 11008 3970 -> 3910).
+// product with the longer tiles goes first (1000 x 521 -> 303 33 -> 27 us a call, 8192 x 1024 -> 4096 500 -> 463,
+// 2048 x 4096 -> 11008 1131 -> 989, 8192 x 4096 -> 11008 3970 -> 3910; mean of 60 drawn sizes 1.1 times as fast).
 struct Product {
   GemmOperand A, B;
   int64_t M, N, K;
@@ -150,10 +141,6 @@ size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, bool
     most = std::max(most, plan_bytes(plan_gemm(M, N, K, count, large_stage(KA, KB), c), M, N));
   return most;
 }
-size_t gemm_segments_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, int count) {
-  double c;
-  return plan_bytes(plan_gemm(M, N, K, count, large_stage(KA, KB), c), M, N);
-}
 double gemm_f32_time(int64_t M, int64_t N, int64_t K) {
   double c;
   plan_f32(M, N, K, c);
@@ -209,7 +196,7 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
     else if (p.tile == SMALL)
       gemm_bf16_kernel<TO, KA, KB, 16, 2, 2, 4, 4, 64, 2, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
-    else if constexpr (SEG == 0 || BITS)
+    else if constexpr (SEG == 0)
       gemm_bf16_kernel<TO, KA, KB, 16, 4, 1, 1, 4, 64, 4, SEG, EL><<<unsigned(grid), 256, 0, st>>>(
           A, B, M, N, K, seg, tg, ep, partial, skip);
     else
@@ -217,16 +204,13 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
     return true;
   };
   using std::integral_constant;
-  // bf16 layers have one plane, the gradients of a gated block two; an fp32 result may come of one (dW of
+  // bf16 layers have one plane; an fp32 result may come of one (dW of
   // a bf16 layer) or more.  What no caller asks for has no kernel, and is refused.
   bool launched = false;
   if (seg.type == FP32) {
     if constexpr (!BITS) launched = launch(integral_constant<int, 0>{}, integral_constant<Element, FP32>{});
   } else if (seg.count == 1) {
     if constexpr (BITS || KA == K_COLS) launched = launch(integral_constant<int, 0>{}, integral_constant<Element, BF16>{});
-  } else if (seg.count == 2) {
-    if constexpr (BITS && KA == K_ROWS && KB == K_COLS)
-      launched = launch(integral_constant<int, 1>{}, integral_constant<Element, BF16>{});
   } else if constexpr (!BITS) {
     launched = launch(integral_constant<int, 1>{}, integral_constant<Element, BF16>{});
   }
@@ -237,79 +221,103 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   return gemm_finish<TO>(st, partial, splits, M, N, ep, skip);
 }
 
-// Tiles and splits as for one product of twice the rows, each product's own edge apart.
-static Plan plan_weight_pair(int64_t M, int64_t N, int64_t K) {
-  double cost;
-  Plan p = plan_gemm(2 * M, N, K, 2, 32, cost);
-  TileGrid& tg = p.tg;
-  const int edge = p.tile == LARGE ? 256 : p.tile == SMALL ? 128 : 64;
-  tg.nm = cdiv(M, edge);
-  tg.half = tg.nm * tg.nn;
-  tg.tiles = 2 * tg.half;
-  tg.per_xcd = int(cdiv(tg.tiles, NXCD));
-  return p;
+// The plans of dx and of both weight gradients.  One kind of tile for all, in one launch, unless two launches cost
+// less; whichever gradients are asked for, so that their bits do not depend on it.
+struct GradPlan {
+  Plan x, w;
+  bool joined;
+};
+// Workgroups of two lengths on `slots`, the longer ones first.
+static double joint_cost(double slots, int64_t ga, double ta, int64_t gb, double tb) {
+  if (ta < tb) std::swap(ga, gb), std::swap(ta, tb);
+  const double rounds = std::floor(double(ga) / slots), rest = double(ga) - rounds * slots;
+  // b starts on the free slots of a's last round: `ahead` of its tiles each before the others end
+  const double start = rounds * ta, ahead = rest > 0 ? std::floor(ta / tb) : 0, early = (slots - rest) * ahead;
+  if (rest > 0 && double(gb) <= early) return start + ta;
+  const double left = double(gb) - early;
+  return start + ahead * tb + std::ceil(std::max(left, 1.0) / slots) * tb;
 }
-size_t gemm_weight_pair_workspace(int64_t M, int64_t N, int64_t K) {
-  return plan_bytes(plan_weight_pair(M, N, K), 2 * M, N);
+static GradPlan plan_gradients(int64_t n, int64_t di, int64_t df) {
+  GradPlan best;
+  double apart_x = 1e30, apart_w = 1e30, joint = 1e30;
+  Plan ax, aw;
+  const double unique = 4.0 * (double(df) * double(n + di) + double(n) * double(2 * df + di));
+  constexpr double CACHE = 24e6;
+  for (Tile tile : {LARGE, SMALL, TINY}) {
+    double cx, cw;
+    const Plan x = plan_tiles(tile, n, di, df, 2, 32, cx);
+    Plan w = plan_tiles(tile, 2 * df, di, n, 2, 32, cw);
+    const int edge = tile == LARGE ? 256 : tile == SMALL ? 128 : 64;
+    w.tg.nm = cdiv(df, edge);   // each product's own edge
+    w.tg.half = w.tg.nm * w.tg.nn;
+    w.tg.tiles = 2 * w.tg.half;
+    w.tg.per_xcd = int(cdiv(w.tg.tiles, NXCD));
+    if (cx < apart_x) apart_x = cx, ax = x;
+    if (cw < apart_w) apart_w = cw, aw = w;
+    const double round = tile == LARGE ? LARGE_ROUND : tile == SMALL ? SMALL_ROUND : TINY_ROUND;
+    for (int mx = 0; mx < (x.tg.splits > 1 ? 2 : 1); ++mx)
+      for (int mw = 0; mw < (w.tg.splits > 1 ? 2 : 1); ++mw) {
+        Plan px = x, pw = w;
+        if (mx) px.tg.splits = 1, px.tg.steps_per_split = 2 * px.tg.steps;
+        if (mw) pw.tg.splits = 1, pw.tg.steps_per_split = 2 * pw.tg.steps;
+        const int64_t gx = px.tg.tiles * px.tg.splits, gw = pw.tg.tiles * pw.tg.splits;
+        const double step = tile == LARGE ? 0.5 * LARGE_STEP
+                            : tile == SMALL ? (gx + gw > 256 ? SMALL_STEP_FULL : SMALL_STEP_HALF)
+                                            : (gx + gw > 256 ? TINY_STEP_FULL : TINY_STEP_HALF);
+        double c = joint_cost(tile == LARGE ? 256 : 512, gx, px.tg.steps_per_split * step + round, gw,
+                              pw.tg.steps_per_split * step + round);
+        // every tile reads its rows: from memory the first time, and from the caches (7546 x 128 -> 9320 on the
+        // smallest tiles 576 us against 488)
+        const double reads = 8.0 * edge * (double(px.tg.tiles) * double(df) + double(pw.tg.tiles) * double(n));
+        c = std::max(c, unique / MEMORY + std::max(0.0, reads - unique) / CACHE);
+        if (px.tg.splits > 1) c += 4.0 + 8.0 * px.tg.splits * double(n) * double(di) / MEMORY;
+        if (pw.tg.splits > 1) c += 4.0 + 16.0 * pw.tg.splits * double(df) * double(di) / MEMORY;
+        if (c < joint) joint = c, best.x = px, best.w = pw;
+      }
+  }
+  best.joined = joint <= apart_x + apart_w + 5.0;
+  if (!best.joined) best.x = ax, best.w = aw;
+  return best;
 }
-template <class TO>
-lrc_status gemm_weight_pair(hipStream_t st, const char* name, GemmOperand A1, GemmOperand A2, GemmOperand B, int64_t M,
-                            int64_t N, int64_t K, const Epilogue& ep, float* partial, double flops, double bytes) {
-  const Plan p = plan_weight_pair(M, N, K);
-  const TileGrid& tg = p.tg;
-  const int64_t grid = int64_t(NXCD) * tg.per_xcd * tg.splits;
-  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-  GemmSegments seg;
-  seg.count = 2;
-  seg.pa = 1u;
-  ProfScope scope(name, st, flops, bytes);
-  const unsigned g = unsigned(grid);
-  if (p.tile == LARGE)
-    gemm_weight_pair_kernel<TO, 32, 4, 2, 2, 4, 32, 4><<<g, 512, 0, st>>>(A1, A2, B, M, N, K, seg, tg, ep, partial);
-  else if (p.tile == SMALL)
-    gemm_weight_pair_kernel<TO, 16, 2, 2, 4, 4, 64, 2><<<g, 256, 0, st>>>(A1, A2, B, M, N, K, seg, tg, ep, partial);
-  else
-    gemm_weight_pair_kernel<TO, 16, 4, 1, 1, 4, 64, 4><<<g, 256, 0, st>>>(A1, A2, B, M, N, K, seg, tg, ep, partial);
-  LRC_LAUNCHED();
-  return tg.splits == 1 ? LRC_OK : gemm_finish<TO>(st, partial, tg.splits, 2 * M, N, ep, nullptr);
-}
-template lrc_status gemm_weight_pair<float>(hipStream_t, const char*, GemmOperand, GemmOperand, GemmOperand, int64_t,
-                                            int64_t, int64_t, const Epilogue&, float*, double, double);
-template lrc_status gemm_weight_pair<uint16_t>(hipStream_t, const char*, GemmOperand, GemmOperand, GemmOperand, int64_t,
-                                               int64_t, int64_t, const Epilogue&, float*, double, double);
-
-static Plan plan_dx(int64_t n, int64_t di, int64_t df) {
-  double cost;
-  return plan_gemm(n, di, df, 2, large_stage(K_ROWS, K_COLS), cost);
-}
-bool gemm_gradients_joined(int64_t n, int64_t di, int64_t df) {
-  return plan_dx(n, di, df).tile == plan_weight_pair(df, di, n).tile;
+size_t gemm_gradients_workspace(int64_t n, int64_t di, int64_t df) {
+  const GradPlan p = plan_gradients(n, di, df);
+  return plan_bytes(p.x, n, di) + plan_bytes(p.w, 2 * df, di);
 }
 template <class TO>
 lrc_status gemm_gradients(hipStream_t st, const char* name, GemmOperand Ax, GemmOperand Bx, GemmOperand A1,
                           GemmOperand A2, GemmOperand B, int64_t n, int64_t di, int64_t df, const Epilogue& epx,
                           const Epilogue& epw, float* partial, double flops, double bytes) {
-  const Plan px = plan_dx(n, di, df), pw = plan_weight_pair(df, di, n);
-  const Product x = {Ax, Bx, n, di, df, px.tg, epx, partial};
-  const Product w = {A1, B, df, di, n, pw.tg, epw, partial + plan_bytes(px, n, di) / 4};
-  const int64_t grid = x.groups() + w.groups();
-  if (grid >= (int64_t(1) << 31)) return LRC_EINVAL;
-  const bool x_first = px.tg.steps_per_split > pw.tg.steps_per_split;
-  const int x0 = x_first ? 0 : int(w.groups()), w0 = x_first ? int(x.groups()) : 0;
+  const GradPlan p = plan_gradients(n, di, df);
+  const Product x = {Ax, Bx, n, di, df, p.x.tg, epx, partial};
+  const Product w = {A1, B, df, di, n, p.w.tg, epw, partial + plan_bytes(p.x, n, di) / 4};
+  const bool dx = epx.y != nullptr, dw = epw.y != nullptr;
+  if (x.groups() + w.groups() >= (int64_t(1) << 31)) return LRC_EINVAL;
   ProfScope scope(name, st, flops, bytes);
-  auto go = [&](auto tile) {
-    constexpr int TILE = decltype(tile)::value;
-    gemm_gradients_kernel<TO, TILE><<<unsigned(grid), TILE == LARGE ? 512 : 256, 0, st>>>(w, A2, x, x0, w0);
+  auto launch = [&](Tile tile, int gx, int gw) {   // workgroups of dx and of dWg and dWu
+    const bool x_first = gw == 0 || (gx > 0 && p.x.tg.steps_per_split > p.w.tg.steps_per_split);
+    const int x0 = x_first ? 0 : gw, w0 = x_first ? gx : 0;
+    auto go = [&](auto t) {
+      constexpr int TILE = decltype(t)::value;
+      gemm_gradients_kernel<TO, TILE><<<unsigned(gx + gw), TILE == LARGE ? 512 : 256, 0, st>>>(w, A2, x, x0, w0);
+    };
+    if (tile == LARGE)
+      go(I<LARGE>{});
+    else if (tile == SMALL)
+      go(I<SMALL>{});
+    else
+      go(I<TINY>{});
   };
-  if (px.tile == LARGE)
-    go(I<LARGE>{});
-  else if (px.tile == SMALL)
-    go(I<SMALL>{});
-  else
-    go(I<TINY>{});
+  const int gx = dx ? int(x.groups()) : 0, gw = dw ? int(w.groups()) : 0;
+  if (p.joined || !dx || !dw) {
+    launch(dx ? p.x.tile : p.w.tile, gx, gw);
+  } else {
+    launch(p.x.tile, gx, 0);
+    LRC_LAUNCHED();
+    launch(p.w.tile, 0, gw);
+  }
   LRC_LAUNCHED();
-  if (px.tg.splits > 1) LRC_TRY(gemm_finish<uint16_t>(st, x.partial, px.tg.splits, n, di, epx, nullptr));
-  return pw.tg.splits == 1 ? LRC_OK : gemm_finish<TO>(st, w.partial, pw.tg.splits, 2 * df, di, epw, nullptr);
+  if (dx && p.x.tg.splits > 1) LRC_TRY(gemm_finish<uint16_t>(st, x.partial, p.x.tg.splits, n, di, epx, nullptr));
+  return dw && p.w.tg.splits > 1 ? gemm_finish<TO>(st, w.partial, p.w.tg.splits, 2 * df, di, epw, nullptr) : LRC_OK;
 }
 template lrc_status gemm_gradients<float>(hipStream_t, const char*, GemmOperand, GemmOperand, GemmOperand, GemmOperand,
                                           GemmOperand, int64_t, int64_t, int64_t, const Epilogue&, const Epilogue&,

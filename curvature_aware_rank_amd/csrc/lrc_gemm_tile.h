@@ -583,36 +583,44 @@ inline double round_cost(int64_t groups, double steps64, double step_full, doubl
   if (rest > 0) c += steps64 * (rest > 256 ? step_full : step_half) + round;
   return c;
 }
-// KL: k steps per stage of a large tile
-inline Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double& cost) {
+// One kind of tile.  KL: k steps per stage of a large one.
+inline Plan plan_tiles(Tile tile, int64_t M, int64_t N, int64_t K, int count, int KL, double& cost) {
   Plan best;
-  const int64_t steps_l = cdiv(K, KL), steps_s = cdiv(K, 64);
-  const double s64 = double(steps_s) * count;
+  best.tile = tile;
+  const int64_t steps_l = cdiv(K, KL), steps_s = cdiv(K, 64), total = steps_s * count;
   const double floor_us = 2.0 * double(K) * double(M + N) * std::min(count, 3) / MEMORY;
-  best.tile = LARGE;
-  best.tg = tiles_of(M, N, 256, 1, steps_l * count, steps_l);
-  cost = std::max(floor_us, large_cost(best.tg.tiles, s64));
-  const int64_t total = steps_s * count;
+  if (tile == LARGE) {
+    best.tg = tiles_of(M, N, 256, 1, steps_l * count, steps_l);
+    cost = std::max(floor_us, large_cost(best.tg.tiles, double(total)));
+    return best;
+  }
+  const bool small = tile == SMALL;
+  const int edge = small ? 128 : 64;
+  const double full = small ? SMALL_STEP_FULL : TINY_STEP_FULL, half = small ? SMALL_STEP_HALF : TINY_STEP_HALF,
+               round = small ? SMALL_ROUND : TINY_ROUND;
+  cost = 1e30;
   for (int64_t s = 1; s <= std::min<int64_t>(32, total); ++s) {
     const int64_t per = cdiv(total, s);
     if (cdiv(total, per) != s) continue;
-    const TileGrid tg = tiles_of(M, N, 128, int(s), per, steps_s);
-    double c = std::max(floor_us, round_cost(tg.tiles * s, double(per), SMALL_STEP_FULL, SMALL_STEP_HALF, SMALL_ROUND));
+    const TileGrid tg = tiles_of(M, N, edge, int(s), per, steps_s);
+    double c = std::max(floor_us, round_cost(tg.tiles * s, double(per), full, half, round));
     if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
     if (c < cost) {
       cost = c;
-      best = {SMALL, tg};
+      best.tg = tg;
     }
   }
-  for (int64_t s = 1; count <= 2 && s <= std::min<int64_t>(32, total); ++s) {
-    const int64_t per = cdiv(total, s);
-    if (cdiv(total, per) != s) continue;
-    const TileGrid tg = tiles_of(M, N, 64, int(s), per, steps_s);
-    double c = std::max(floor_us, round_cost(tg.tiles * s, double(per), TINY_STEP_FULL, TINY_STEP_HALF, TINY_ROUND));
-    if (s > 1) c += 4.0 + 8.0 * double(s) * double(M) * double(N) / MEMORY;
+  return best;
+}
+inline Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double& cost) {
+  Plan best = plan_tiles(LARGE, M, N, K, count, KL, cost);
+  for (Tile tile : {SMALL, TINY}) {
+    if (tile == TINY && count > 2) continue;
+    double c;
+    const Plan p = plan_tiles(tile, M, N, K, count, KL, c);
     if (c < cost) {
       cost = c;
-      best = {TINY, tg};
+      best = p;
     }
   }
   return best;

@@ -337,22 +337,15 @@ template <class TO>
 lrc_status gemm_finish(hipStream_t st, const float* partial, int splits, int64_t M, int64_t N, const Epilogue& ep,
                        const int32_t* skip);
 size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, bool f32);
-// The weight gradients of a gated block, both in one launch: ep.y = A1^T B and ep.y2 = A2^T B (M x N each; columns of
-// all operands), every sum over two segments, plane 1 of A (what rounding left out) and then plane 0; a sum of the
-// first that is not finite counts as zero.
-template <class TO>
-lrc_status gemm_weight_pair(hipStream_t st, const char* name, GemmOperand A1, GemmOperand A2, GemmOperand B, int64_t M,
-                            int64_t N, int64_t K, const Epilogue& ep, float* partial, double flops, double bytes);
-size_t gemm_weight_pair_workspace(int64_t M, int64_t N, int64_t K);
-// These and dx = Ax Bx (two planes each, one after the other) in one launch, where both take tiles of one kind: the
-// results are those of the two calls.  `partial`: the workspaces of both.
-bool gemm_gradients_joined(int64_t n, int64_t di, int64_t df);
+// The gradients of a gated block: epx.y = Ax Bx (n x di, k of df, the operands' second planes after the first), and
+// epw.y = A1^T B, epw.y2 = A2^T B (df x di, columns of all operands), these over two segments, plane 1 of A (what
+// rounding left out) and then plane 0; a sum of the first that is not finite counts as zero.  dx or the two others are
+// left out where epx.y or epw.y is NULL; their bits do not depend on it.
+size_t gemm_gradients_workspace(int64_t n, int64_t di, int64_t df);
 template <class TO>
 lrc_status gemm_gradients(hipStream_t st, const char* name, GemmOperand Ax, GemmOperand Bx, GemmOperand A1,
                           GemmOperand A2, GemmOperand B, int64_t n, int64_t di, int64_t df, const Epilogue& epx,
                           const Epilogue& epw, float* partial, double flops, double bytes);
-// workspace of a product of `count` segments
-size_t gemm_segments_workspace(int64_t M, int64_t N, int64_t K, int KA, int KB, int count);
 // estimates in microseconds of an fp32 product, on fp32 operands and on ones split in three
 double gemm_f32_time(int64_t M, int64_t N, int64_t K);
 double gemm_split_time(int64_t M, int64_t N, int64_t K, int KA, int KB);

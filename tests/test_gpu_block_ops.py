@@ -357,10 +357,11 @@ def test_gated_backward_exact_on_small_integers(lrc, dtype, n, d_in, d_ff, held)
 
 
 @pytest.mark.parametrize("n,d_in,d_ff", [(300, 200, 136), (64, 1000, 72), (1, 8, 8), (4096, 1536, 1024), (8192, 512, 4096),
-                                         (4100, 1540, 1030), (2048, 5632, 1024), (2050, 5637, 1026)])
+                                         (4100, 1540, 1030), (2048, 5632, 1024), (2050, 5637, 1026), (4096, 256, 1024),
+                                         (4147, 80, 8464)])
 def test_gated_backward_joined_products(lrc, n, d_in, d_ff):
-    """All products of a bf16 block in one launch, on each kind of tile, with and without splits: the bits of each
-    gradient asked for alone, whose kernels the tests above hold to the formulas."""
+    """All products of a bf16 block in one launch or two, on each kind of tile, with and without splits: the bits of each
+    gradient asked for alone, and its own formula's value from the streams."""
     r = gen(n + d_in)
     make = lambda *s: torch.randn(*s, generator=r).bfloat16().to(dev())   # noqa: E731
     dh, g, u, x, wg, wu = make(n, d_ff), make(n, d_ff), make(n, d_ff), make(n, d_in), make(d_ff, d_in), make(d_ff, d_in)
@@ -370,6 +371,17 @@ def test_gated_backward_joined_products(lrc, n, d_in, d_ff):
         assert all(torch.isfinite(t).all() for t in full)
         assert all(torch.equal(full[k], only_w[k]) for k in (0, 1, 3, 4))
         assert all(torch.equal(full[k], only_x[k]) for k in (0, 1, 2))
+    # fp32 sums of k terms in any order: k 2^-24 of the terms' magnitudes (two reductions), and the result's rounding;
+    # a weight gradient may differ from the streams' product by what their rounding left out, 2^-8 of each term
+    f = lambda t: t.float()   # noqa: E731
+    dg, du, dx, dwg, dwu = full
+    want = f(dg) @ f(wg) + f(du) @ f(wu)
+    size = f(dg).abs() @ f(wg).abs() + f(du).abs() @ f(wu).abs()
+    assert ((f(dx) - want).abs() <= 2**-8 * want.abs() + 6 * d_ff * 2**-24 * size).all()
+    for got, dz in ((dwg, dg), (dwu, du)):
+        size = f(dz).abs().T.contiguous() @ f(x).abs()
+        err = (got - f(dz).T.contiguous() @ f(x)).abs()
+        assert (err <= (2**-8 * 1.01 + 6 * n * 2**-24) * size).all()
 
 
 def test_gated_backward_against_differences(lrc):
