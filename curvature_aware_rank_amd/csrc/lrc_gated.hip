@@ -4,8 +4,8 @@
 //
 // bf16 forward: one product whose tiles hold as many channels of Wg as of Wu (lrc_gemm_tile.h), so x is staged once
 // for both and act(g) u is formed from the accumulators; g and u reach memory only where they are kept.
-// (8192 x 4096 x 11008: forward 1180 us; backward dz 199 us, memory, 5.4 TB/s; dx, dWg and dWu 3700, 1200 TFLOP/s:
-// the matrix pipes, busy 61 to 66 % of the cycles at 1.75 to 1.85 GHz.)
+// (8192 x 4096 x 11008: forward 1180 us; backward dz 199 us, memory, 5.4 TB/s; dx, dWg and dWu 3650, 1220 TFLOP/s:
+// the matrix pipes, busy 65 % of the cycles at 1.79 GHz.)
 // bf16 backward: one pass writes dg and du (the output-gradient streams of the two projections) and what their
 // rounding to bf16 left out; dx is one product whose k runs over dg Wg and then du Wu, dWg and dWu one each whose k
 // runs over the tokens twice, the left-out piece first (a gradient so carries 16 bits of dz and no more than its own
@@ -171,8 +171,8 @@ lrc_status gated_bf16(hipStream_t st, GatedArgs& a, const GatedRoom& room) {
   const double flops = 4.0 * double(a.n) * double(a.df) * double(a.di);
   const double bytes = 2.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df);
   if (gemm::stream_bf16_pair(a.n, a.df, a.di) && a.ep.codes == nullptr)
-    return gemm::few_rows<uint16_t, BF16, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n, a.df,
-                                             a.di, a.ep, a.co, flops, bytes);
+    return gemm::few_rows<uint16_t, BF16, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n,
+                                             a.df, a.di, a.ep, a.co, flops, bytes);
   GemmOperand x = {static_cast<const uint16_t*>(a.x), a.ldx, 0}, g = {static_cast<const uint16_t*>(a.Wg), a.ldw, 0},
               u = {static_cast<const uint16_t*>(a.Wu), a.ldw, 0};
   if (a.di % 8 != 0) {

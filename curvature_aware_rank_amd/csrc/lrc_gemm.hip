@@ -51,7 +51,7 @@ __device__ __forceinline__ void with_cols_tile(F f) {
 }
 // Both in one launch: dx does not wait for the weight gradients, and neither often fills the chip to its end.  The
 // product with the longer tiles goes first (1000 x 521 -> 303 33 -> 27 us a call, 8192 x 1024 -> 4096 500 -> 463,
-// 2048 x 4096 -> 11008 1131 -> 989, 8192 x 4096 -> 11008 3970 -> 3910; mean of 60 drawn sizes 1.1 times as fast).
+// 2048 x 4096 -> 11008 1131 -> 989, 8192 x 4096 -> 11008 3970 -> 3910; mean of 60 drawn sizes 1.13 times as fast).
 struct Product {
   GemmOperand A, B;
   int64_t M, N, K;
@@ -204,8 +204,8 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
     return true;
   };
   using std::integral_constant;
-  // bf16 layers have one plane; an fp32 result may come of one (dW of
-  // a bf16 layer) or more.  What no caller asks for has no kernel, and is refused.
+  // bf16 layers have one plane; an fp32 result may come of one (dW of a bf16 layer) or more.  What no caller asks for
+  // has no kernel, and is refused.
   bool launched = false;
   if (seg.type == FP32) {
     if constexpr (!BITS) launched = launch(integral_constant<int, 0>{}, integral_constant<Element, FP32>{});
