@@ -191,7 +191,7 @@ lrc_status gated_bf16(hipStream_t st, GatedArgs& a, const GatedRoom& room) {
 }
 
 lrc_status gated_f32(hipStream_t st, GatedArgs& a, const GatedRoom& room) {
-  if (gemm::stream_f32_pair(a.n, a.di) && a.ep.codes == nullptr)
+  if (gemm::stream_f32_pair(a.n, a.df, a.di) && a.ep.codes == nullptr)
     return gemm::few_rows<float, FP32, 2>(st, "gated_rows_kernel", a.x, a.ldx, false, a.Wg, a.ldw, a.Wu, a.ldw, a.n,
                                           a.df, a.di, a.ep, a.co, 4.0 * double(a.n) * double(a.df) * double(a.di),
                                           4.0 * (double(a.n) * a.di + 2.0 * double(a.df) * a.di + double(a.n) * a.df));

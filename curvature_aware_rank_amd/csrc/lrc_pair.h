@@ -355,7 +355,15 @@ inline bool stream_bf16_pair(int64_t n, int64_t N, int64_t K) {
   return n <= 8 || (n <= 32 && N * K <= (int64_t(1) << 22));
 }
 
-inline bool stream_f32_pair(int64_t n, int64_t K) { return n <= 8 || (n <= 64 && n * K <= (int64_t(1) << 16)); }
+// fp32, two weights, rows / the linear layer's two products: 4096 -> 1024 35 / 33 at 17 tokens, 52 / 34 at 33; with more
+// channels, whose waves fill the chip, 11008 -> 4096 90 / 114 at 16, 117 / 115 at 24, 4096 -> 4096 38 / 51 at 32,
+// 55 / 52 at 33; rows that the products would lay out anew, 2999 -> 5001 76 / 112 at 64, 3957 -> 19 43 / 59.
+inline bool stream_f32_pair(int64_t n, int64_t N, int64_t K) {
+  const int64_t x = n * K;
+  if (n > 64) return false;
+  if (n <= 8 || x <= (int64_t(1) << 16) || (K % 4 != 0 && x <= (int64_t(1) << 18))) return true;
+  return N >= 2048 && (n <= 16 || (n <= 32 && x <= (int64_t(1) << 17)));
+}
 
 // n <= 64; own: x is the tokens themselves (own_tokens)
 template <class TO, Element EL, int W>

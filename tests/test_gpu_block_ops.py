@@ -261,7 +261,8 @@ def test_gated(lrc, dtype, n, d_in, d_ff, layout):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n,d_in,d_ff", [(1, 3000, 500), (8, 4096, 640), (9, 4096, 640), (33, 2048, 520), (96, 2040, 1032),
-                                         (300, 1500, 1032), (1500, 264, 1030), (4096, 160, 2056), (3900, 1100, 1500)])
+                                         (300, 1500, 1032), (1500, 264, 1030), (4096, 160, 2056), (3900, 1100, 1500),
+                                         (12, 9000, 2056), (29, 4096, 2051), (64, 3999, 40)])
 def test_gated_exact_on_small_integers(lrc, dtype, n, d_in, d_ff):
     """Small integers: g, u and their product are integers below 2^24, exact in any order; h is the rounded integer."""
     r = gen(n)
