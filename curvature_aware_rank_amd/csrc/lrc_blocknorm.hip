@@ -193,14 +193,15 @@ __global__ __launch_bounds__(row_threads(WPR)) void block_norm_kernel(NormForwar
       }
     }
     if (a.q == nullptr) continue;
-    // codes of h as it is in T, the bits of the quantiser of a written h
+    // codes of h as it is in T, the bits of the quantiser of a written h (places without a token count for nothing: with
+    // eps = 0 they hold 0 / 0)
     uint32_t m = 0;
     float p[V][8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        p[k][e] = S::col(8 * k + e, l) < d ? round_to(v[8 * k + e], static_cast<const T*>(nullptr)) : 0.f;
+        p[k][e] = live && S::col(8 * k + e, l) < d ? round_to(v[8 * k + e], static_cast<const T*>(nullptr)) : 0.f;
       m = mag8(p[k], m, bad);
     }
     const float qs = token_step(reduce.largest(m, red, wave, lane, group));
