@@ -128,3 +128,116 @@ def test_gated_weight_gradient_of_nonfinite_inputs(lrc, n, d_in, d_ff, dw_dtype)
         assert torch.equal(torch.nan_to_num(dw[:, ~clean], 9.0, 8.0, 7.0), torch.nan_to_num(plain, 9.0, 8.0, 7.0))
         want = dz.T @ x[:, clean].double()
         assert ((dw[:, clean] - want).abs() <= rel * want.abs()).all()
+
+
+# ----------------------------------------------------------------------------- every shape of a row
+# a ragged and a full width of the shapes that a token may have in registers: 32 lanes, 2 waves (backward 3 and 4), 8 waves
+ROW_WIDTHS = [200, 256, 1030, 1536, 1540, 2048, 4100, 5120, 8192]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", ROW_WIDTHS)
+@pytest.mark.parametrize("layout", ["packed", "offset"])
+def test_quantize_tokens_row_shapes(lrc, dtype, d, layout):
+    ops.test_quantize_tokens_bit_exact(lrc, dtype, 5, d, layout)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", ROW_WIDTHS)
+@pytest.mark.parametrize("kind", ops.KINDS)
+def test_block_norm_row_shapes(lrc, dtype, d, kind):
+    ops.test_block_norm(lrc, dtype, 5, d, kind)
+
+
+# the widths, and several workgroups of uneven counts of tokens (rows past 8192 channels keep two of the sums in LDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", [*((5, d) for d in ROW_WIDTHS), (70, 1536), (45, 2048), (30, 5120), (41, 8200), (37, 11008),
+                                 (18, 16384)])
+@pytest.mark.parametrize("kind", ops.KINDS)
+def test_block_norm_backward_row_shapes(lrc, dtype, n, d, kind):
+    ops.test_block_norm_backward(lrc, dtype, n, d, kind)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", [(1, 1), (5, 2), (65, 65), (300, 300), (9, 1000), (70, 1024), (5, 2050), (3, 4096), (3, 8200),
+                                 (4, 11008), (2, 16384), *((6, d) for d in ROW_WIDTHS)])
+@pytest.mark.parametrize("kind", ops.KINDS)
+def test_block_norm_statistics_of_the_block(lrc, dtype, n, d, kind):
+    """The post-norm's mean and 1 / spread as values, also where h is not asked for."""
+    b, res, post, gate, _ = ops.norm_inputs(n, d, dtype, kind, n + d)
+    eps = float(torch.tensor(1e-5))
+    _, _, e_mean, e_rstd = ops.standardise(ops.f64(b), 0 * ops.f64(b), kind, eps)
+    mean, rstd = ops.ref._moments(ops.f64(b), kind, eps)
+    post = tuple(ops.on(*post))
+    for need_h in (True, False):
+        stats = lrc.lrc_block_norm(*ops.on(b, res), kind=kind, eps=1e-5, post=post, gate=gate.to(dev()), need_h=need_h)[2]
+        ops.check(stats[1], rstd, e_rstd + ops.TINY, "rstd_b")
+        if kind == "layer":
+            ops.check(stats[0], mean, e_mean + ops.TINY, "mean_b")
+
+
+# More tokens than the widest launch holds at once, for every shape: a workgroup takes several, its loads a token ahead.
+LONG = [(33000, 24), (16700, 200), (8300, 300), (8200, 1000), (2100, 1030), (4200, 1536), (4200, 2048), (2100, 4096),
+        (1100, 4100), (1050, 8200), (1030, 16384)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", LONG)
+@pytest.mark.parametrize("kind", ops.KINDS)
+def test_block_norm_many_tokens(lrc, dtype, n, d, kind):
+    """A token's results do not depend on the others: the bits of calls on a few tokens each."""
+    b, res, post, gate, pre = ops.norm_inputs(n, d, dtype, kind, n + d)
+    b, res, dh, ds = ops.on(b, res, stream(n, d, dtype, 7, 0.01), stream(n, d, dtype, 8, 0.01))
+    opt = dict(kind=kind, post=tuple(ops.on(*post)), gate=gate.to(dev()), scale=0.75, pre=tuple(ops.on(*pre)))
+    s, h, stats, _, _ = lrc.lrc_block_norm(b, res, **opt)
+    _, _, _, q, info = lrc.lrc_block_norm(b, res, quantize=True, info=ops.flag(), **opt)
+    wq, ws, _ = lrc.lrc_quantize_tokens(h)
+    assert torch.equal(q[0], wq) and torch.equal(q[1], ws) and int(info.cpu()) == 0
+    dr, db, *_ = lrc.lrc_block_norm_backward(dh, ds, s, b, stats, **opt)
+    some = slice(0, None, 97)
+    few = lambda t: None if t is None else t[some].contiguous()   # noqa: E731
+    s2, h2, stats2, _, _ = lrc.lrc_block_norm(few(b), few(res), **opt)
+    for p, w in zip((s, h, *stats), (s2, h2, *stats2)):
+        assert p is w is None or torch.equal(few(p), w)
+    dr2, db2, *_ = lrc.lrc_block_norm_backward(few(dh), few(ds), s2, few(b), stats2, **opt)
+    assert torch.equal(few(dr), dr2) and torch.equal(few(db), db2)
+    p2, s2, _ = lrc.lrc_quantize_tokens(few(h))
+    assert torch.equal(few(wq), p2) and torch.equal(few(ws), s2)
+    # and all the others: every token again in the opposite order, where it meets another workgroup
+    flip = lambda t: t.flip(0).contiguous()   # noqa: E731
+    s2, h2, _, _, _ = lrc.lrc_block_norm(flip(b), flip(res), **opt)
+    assert torch.equal(s2, flip(s)) and torch.equal(h2, flip(h))
+    dr2, db2, *_ = lrc.lrc_block_norm_backward(flip(dh), flip(ds), flip(s), flip(b),
+                                               tuple(None if t is None else flip(t) for t in stats), **opt)
+    assert torch.equal(dr2, flip(dr)) and torch.equal(db2, flip(db))
+
+
+@pytest.mark.parametrize("n,d", LONG)
+@pytest.mark.parametrize("kind", ops.KINDS)
+def test_block_norm_many_tokens_sums(lrc, n, d, kind):
+    """The parameters' gradients over many workgroups, each with several tokens, fp32, from the call's own total
+    gradient.  Sums of n terms (n + 12) u, and three roundings a term."""
+    b, res, post, gate, pre = ops.norm_inputs(n, d, torch.float32, kind, n + d)
+    b, res, dh, ds = ops.on(b, res, stream(n, d, torch.float32, 7, 0.01), stream(n, d, torch.float32, 8, 0.01))
+    post, pre, gate = tuple(ops.on(*post)), tuple(ops.on(*pre)), gate.to(dev())
+    opt = dict(kind=kind, post=post, gate=gate, scale=0.75, pre=pre)
+    s, _, stats, _, _ = lrc.lrc_block_norm(b, res, **opt)
+    t, _, dgamma, dbeta, dpost_gamma, dpost_beta, dgate = lrc.lrc_block_norm_backward(dh, ds, s, b, stats, **opt)
+    mb, rb, ms, rs = (torch.zeros(n, device=dev()) if v is None else v for v in stats)
+    hat = lambda v, m, r: (v.double() - m.double()[:, None]) * r.double()[:, None]   # noqa: E731
+    # normalised values, two roundings of a difference whose terms may be larger than it, one of the product
+    size = lambda v, m, r: (v.double().abs() + m.double().abs()[:, None]) * r.double()[:, None]   # noqa: E731
+    w = (0.75 * gate).double()
+    cases = [(dgamma, dh.double() * hat(s, ms, rs), dh.double().abs() * size(s, ms, rs), 1.0)]
+    C = t.double() * hat(b, mb, rb), t.double().abs() * size(b, mb, rb)
+    cases.append((dpost_gamma, *C, w))
+    along = post[0].double() * C[0]
+    if kind == "layer":
+        cases += [(dbeta, dh.double(), dh.double().abs(), 1.0), (dpost_beta, t.double(), t.double().abs(), w)]
+        along = along + post[1].double() * t.double()
+    cases.append((dgate, along, post[0].double().abs() * C[1]
+                  + (post[1].double().abs() * t.double().abs() if kind == "layer" else 0), torch.tensor(0.75).double()))
+    for got, terms, sizes, scale in cases:
+        want = terms.sum(0) * scale
+        bound = ((n + 12) * terms.abs().sum(0) + 4 * sizes.sum(0)) * ops.U * abs(scale) + 4 * ops.U * want.abs() + ops.TINY
+        assert ((got.double() - want).abs() <= bound).all()
