@@ -568,9 +568,8 @@ def _run(where, device, fn, *args):
         raise LrcError(st, where)
 
 
-def _rows(t, name, n=None, d=None, dtype=None, device=None):
-    """Check a 2-D GPU tensor (its dtype, its device and, where given, its n rows and d columns)
-    and return (tensor, leading dim); rows that are not contiguous or overlap are copied."""
+def _check_rows(t, name, n=None, d=None, dtype=None, device=None):
+    """Check a 2-D GPU tensor (its dtype, its device and, where given, its n rows and d columns) and return its shape."""
     _dev(t, name)
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -582,6 +581,12 @@ def _rows(t, name, n=None, d=None, dtype=None, device=None):
         raise ValueError(f"{name} must have shape {(n, d)}, got {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return shape
+
+
+def _rows(t, name, n=None, d=None, dtype=None, device=None):
+    """_check_rows, and (tensor, leading dim); rows that are not contiguous or overlap are copied."""
+    rows, cols = _check_rows(t, name, n, d, dtype, device)
     if cols and t.is_contiguous():
         return t, cols
     s0, s1 = t.stride()
@@ -809,15 +814,21 @@ def _in_pieces(t, ld):
     return t.clone(memory_format=torch.contiguous_format), t.shape[1]
 
 
-def _pair_of_weights(Wg, Wu, d_ff, d_in, dtype, device, read):
-    """(Wg, Wu, leading dim) of two weights of one shape and, where the products read them, one pitch."""
+def _pair_of_weights(Wg, Wu, d_ff, d_in, dtype, device, read=True):
+    """(Wg, Wu, leading dim, d_ff, d_in) of two weights of one shape, which the products read at one pitch; what is not
+    read is only checked."""
+    if not read:
+        d_ff, d_in = _check_rows(Wg, "Wg", d_ff, d_in, dtype, device)
+        _check_rows(Wu, "Wu", d_ff, d_in, dtype, device)
+        return None, None, max(d_in, 1), d_ff, d_in
     Wg, ldw = _rows(Wg, "Wg", d_ff, d_in, dtype, device)
-    Wu, ldu = _rows(Wu, "Wu", Wg.shape[0], Wg.shape[1], dtype, Wg.device)
-    if read and dtype == torch.bfloat16:
+    d_ff, d_in = Wg.shape
+    Wu, ldu = _rows(Wu, "Wu", d_ff, d_in, dtype, device)
+    if dtype == torch.bfloat16:
         (Wg, ldw), (Wu, ldu) = _in_pieces(Wg, ldw), _in_pieces(Wu, ldu)
     if ldw != ldu:
-        Wg, Wu, ldw = Wg.contiguous(), Wu.contiguous(), max(Wg.shape[1], 1)
-    return Wg, Wu, ldw
+        Wg, Wu, ldw = Wg.contiguous(), Wu.contiguous(), max(d_in, 1)
+    return Wg, Wu, ldw, d_ff, d_in
 
 
 def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", save: str = "none",
@@ -831,8 +842,7 @@ def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: s
     x, ldx = _rows(x, "x")
     dt, dev = _dtype_code(x), x.device
     n, d_in = x.shape
-    Wg, Wu, ldw = _pair_of_weights(Wg, Wu, None, d_in, x.dtype, dev, True)
-    d_ff = Wg.shape[0]
+    Wg, Wu, ldw, d_ff, _ = _pair_of_weights(Wg, Wu, None, d_in, x.dtype, dev)
     if x.dtype == torch.bfloat16:
         x, ldx = _in_pieces(x, ldx)
     code = _act_code(act)
@@ -865,8 +875,7 @@ def lrc_gated_linear_backward(dh: torch.Tensor, x, Wg: torch.Tensor, Wu: torch.T
     dh, lddh = _rows(dh, "dh")
     dt, dev = _dtype_code(dh), dh.device
     n, d_ff = dh.shape
-    Wg, Wu, ldw = _pair_of_weights(Wg, Wu, d_ff, None, dh.dtype, dev, need_dx)
-    d_in = Wg.shape[1]
+    Wg, Wu, ldw, _, d_in = _pair_of_weights(Wg, Wu, d_ff, None, dh.dtype, dev, need_dx)
     code = _act_code(act)
     if need_dw and x is None:
         raise ValueError("dWg and dWu need x or its checkpoint")

@@ -241,3 +241,17 @@ def test_block_norm_many_tokens_sums(lrc, n, d, kind):
         want = terms.sum(0) * scale
         bound = ((n + 12) * terms.abs().sum(0) + 4 * sizes.sum(0)) * ops.U * abs(scale) + 4 * ops.U * want.abs() + ops.TINY
         assert ((got.double() - want).abs() <= bound).all()
+
+
+def test_gated_backward_does_not_copy_weights_it_does_not_read(lrc):
+    """Without dx the two weights only say how many input channels there are, whatever their pitches."""
+    n, d_in, d_ff = 8, 4096, 8192
+    bf = dict(dtype=torch.bfloat16, device=dev())
+    wg, wu = torch.ones(d_ff, d_in, **bf), torch.ones(d_ff, d_in + 8, **bf)[:, :d_in]
+    dh, g, u, x = (torch.ones(n, d, **bf) for d in (d_ff, d_ff, d_ff, d_in))
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    dg, du, dx, dwg, _ = lrc.lrc_gated_linear_backward(dh, x, wg, wu, g, u, act="none", need_dx=False, need_dw=False)
+    assert dx is None and dwg is None and (dg == 1).all() and (du == 1).all()
+    assert torch.cuda.max_memory_allocated() - before < wu.numel()      # half of what a copy of one takes
