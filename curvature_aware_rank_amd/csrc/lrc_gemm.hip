@@ -212,7 +212,8 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
   } else if (seg.count == 1) {
     if constexpr (BITS || KA == K_COLS) launched = launch(integral_constant<int, 0>{}, integral_constant<Element, BF16>{});
   } else if constexpr (!BITS) {
-    launched = launch(integral_constant<int, 1>{}, integral_constant<Element, BF16>{});
+    if (seg.count == 3 || seg.count == 6)   // the counts that the workspace is sized for
+      launched = launch(integral_constant<int, 1>{}, integral_constant<Element, BF16>{});
   }
   if (!launched) return LRC_EINVAL;
   LRC_LAUNCHED();

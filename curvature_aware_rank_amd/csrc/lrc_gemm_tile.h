@@ -615,7 +615,7 @@ inline Plan plan_tiles(Tile tile, int64_t M, int64_t N, int64_t K, int count, in
 inline Plan plan_gemm(int64_t M, int64_t N, int64_t K, int count, int KL, double& cost) {
   Plan best = plan_tiles(LARGE, M, N, K, count, KL, cost);
   for (Tile tile : {SMALL, TINY}) {
-    if (tile == TINY && count > 2) continue;
+    if (tile == TINY && count > 1) continue;   // no such tiles over several segments (the gradients plan theirs apart)
     double c;
     const Plan p = plan_tiles(tile, M, N, K, count, KL, c);
     if (c < cost) {
