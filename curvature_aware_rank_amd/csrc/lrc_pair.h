@@ -213,9 +213,8 @@ __device__ __forceinline__ void quantize_own(const TO* x, int64_t ldx, int n, in
   __syncthreads();
 }
 
-// (Six waves on a SIMD where a wave has 16 tokens: three workgroups on a unit, 688 of them in one go rather than two.)
 template <class TO, Element EL, int W, int G, int NW, bool OWN>
-__global__ __launch_bounds__(64 * NW, G == 1 ? 6 : 1) void few_rows_kernel(const void* __restrict__ x, int64_t ldx,
+__global__ __launch_bounds__(64 * NW) void few_rows_kernel(const void* __restrict__ x, int64_t ldx,
                                                            const typename RowPiece<EL>::T* __restrict__ W0, int64_t ld0,
                                                            const typename RowPiece<EL>::T* __restrict__ W1, int64_t ld1,
                                                            int n, int64_t N, int K, Epilogue ep, Companion co) {
