@@ -807,7 +807,7 @@ def lrc_linear_backward(dy: torch.Tensor, x, W: torch.Tensor, act: str = "none",
 
 def _in_pieces(t, ld):
     """(tensor, leading dim) of an operand the products read where it lies: rows that could be whole 16-byte
-    pieces are, at a pitch below 2^22 bytes; a tensor laid out otherwise is copied."""
+    pieces are, at a pitch of at most 2^22 bytes; a tensor laid out otherwise is copied."""
     size = t.element_size()
     if t.shape[1] * size % 16 or (t.data_ptr() % 16 == 0 and ld * size % 16 == 0 and ld * size <= 1 << 22):
         return t, ld
@@ -836,6 +836,9 @@ def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: s
     """h = act(x Wg^T) * (x Wu^T), the gate and up projection of a gated feed-forward block.  x: (n_tokens, d_in), Wg,
     Wu: (d_ff, d_in), all bf16 or all fp32; act: none, relu, gelu (exact) or silu.  save keeps g = x Wg^T and
     u = x Wu^T for the backward pass: "z" in full, "checkpoint" in 8 bits, "none" not at all.
+
+    Every call copies weights whose pitches differ and, in bf16, operands whose rows are whole 16-byte pieces but do not
+    start on 16 bytes (or lie more than 2^22 bytes apart): lay weights out once.
 
     Returns (h, saved, info): saved is (g, u), ((codes, exps), (codes, exps)) or None; info (int32 (1,), sticky
     LRC_ENONFINITE of a checkpoint's g or u) is None unless given."""
@@ -867,7 +870,8 @@ def lrc_gated_linear(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: s
 def lrc_gated_linear_backward(dh: torch.Tensor, x, Wg: torch.Tensor, Wu: torch.Tensor, g, u, act: str = "silu",
                               need_dx: bool = True, need_dw: bool = True, dw_dtype=None):
     """Gradients of lrc_gated_linear.  dh: (n_tokens, d_ff); x: the input (n_tokens, d_in) like dh, or its (codes, exps)
-    checkpoint (may be None without need_dw); Wg, Wu: (d_ff, d_in); g, u: as kept, both in full or both as pairs.
+    checkpoint (may be None without need_dw); Wg, Wu: (d_ff, d_in), not read without need_dx; g, u: as kept, both in
+    full or both as pairs.  Copies as in lrc_gated_linear.
 
     Returns (dg, du, dx, dWg, dWu): dg = dh * u * act'(g) and du = dh * act(g), the output-gradient streams of the two
     projections, dx (n_tokens, d_in), dWg and dWu (d_ff, d_in) in dw_dtype (default dh's; torch.float32 allowed); None
@@ -956,7 +960,8 @@ def lrc_int8_linear(x, W, bias=None, act: str = "none", residual=None, dtype=Non
     """y = act(x W^T + bias) + residual in 8-bit integers.  x: (n_tokens, d_in) bf16 or fp32, quantised within the call,
     or the (codes, scale) pair of lrc_quantize_tokens or lrc_block_norm; W: the (codes (d_out, d_in) int8, scale
     (d_out,)) pair of lrc_quantize_rows; bias: (d_out,) fp32; residual: (n_tokens, d_out) like y; act: none, relu, gelu
-    or silu.  y has x's dtype; for a pair `dtype` (bf16 unless given).
+    or silu.  y has x's dtype; for a pair `dtype` (bf16 unless given).  Every call copies codes whose rows are whole
+    16-byte pieces but do not start on 16 bytes (or lie more than 2^22 bytes apart): lay weights out once.
 
     Returns (y, info): info (int32 (1,), sticky LRC_ENONFINITE of x) is None unless given."""
     x, ldx, xc, ldxc, xs, n, d_in, dtype, dev = _int8_tokens(x, dtype)

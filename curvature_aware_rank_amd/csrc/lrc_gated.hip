@@ -9,10 +9,14 @@
 // bf16 backward: one pass writes dg and du (the output-gradient streams of the two projections) and what their
 // rounding to bf16 left out; dx is one product whose k runs over dg Wg and then du Wu, dWg and dWu one each whose k
 // runs over the tokens twice, the left-out piece first (a gradient so carries 16 bits of dz and no more than its own
-// rounding); all three in one launch where their tiles are of one kind.  Sums fp32 throughout.
+// rounding); all three in one launch where their tiles are of one kind.  Sums fp32 throughout.  dx takes the streams
+// as they are returned, as the linear layer's does: it is the gradient that belongs to them, and the left-out pieces
+// would add a third to the products' time.  Its error is 1.4 times that of one rounding.
 // Few tokens, both types: the weights are streamed once (lrc_pair.h).
-// fp32 otherwise: the products are those of the linear layer (fp32 instructions, or six of bf16 pieces), the gate an
-// elementwise pass: the products take 10 to 100 times as long.
+// fp32 otherwise: the products are those of the linear layer (fp32 instructions, or six of bf16 pieces), each laying
+// out x for itself, the gate an elementwise pass.  1024 x 4096 x 2 x 11008: forward 1450 us (products 2 x 604 of it,
+// operands 2 x 76, gate 25), 128 TFLOP/s; backward 2500 (products 2 x 1107, operands 2 x 103, dz 46), 148 TFLOP/s; the
+// library's fp32 product reaches 154 at 8192^3.
 #include "lrc_operand.h"
 #include "lrc_pair.h"
 

@@ -50,8 +50,9 @@ __device__ __forceinline__ void with_cols_tile(F f) {
     f(I<16>{}, I<4>{}, I<1>{}, I<1>{}, I<4>{}, I<64>{}, I<4>{});
 }
 // Both in one launch: dx does not wait for the weight gradients, and neither often fills the chip to its end.  The
-// product with the longer tiles goes first (1000 x 521 -> 303 33 -> 27 us a call, 8192 x 1024 -> 4096 500 -> 463,
-// 2048 x 4096 -> 11008 1131 -> 989, 8192 x 4096 -> 11008 3970 -> 3910; mean of 60 drawn sizes 1.13 times as fast).
+// product with the longer tiles goes first.  One launch / two, us a call: 300 x 136 -> 264 12.6 / 20.8, 1000 x 521 -> 303
+// 22.9 / 31.2, 1813 x 11016 -> 144 78 / 129, 8192 x 1024 -> 4096 475 / 509, 2048 x 4096 -> 11008 985 / 1116,
+// 8192 x 4096 -> 11008 3998 / 3989.
 struct Product {
   GemmOperand A, B;
   int64_t M, N, K;
@@ -223,7 +224,10 @@ lrc_status gemm_bf16(hipStream_t st, const char* name, GemmOperand A, GemmOperan
 }
 
 // The plans of dx and of both weight gradients.  One kind of tile for all, in one launch, unless two launches cost
-// less; whichever gradients are asked for, so that their bits do not depend on it.
+// less; whichever gradients are asked for, so that their bits do not depend on it.  A second launch costs SECOND_LAUNCH
+// or more (8 us at 300 x 136 -> 264).  Two it is where a product's split of k saves more: 7546 x 128 -> 9320 487 us
+// against 498 in one (4147 x 80 -> 8464 230 against 226).  The estimate is wrong where the weight gradients have few
+// tokens to sum: 288 x 4384 -> 768 44 in one, 37 in two, 512 x 4096 -> 11008 367 and 359.
 struct GradPlan {
   Plan x, w;
   bool joined;
@@ -238,6 +242,7 @@ static double joint_cost(double slots, int64_t ga, double ta, int64_t gb, double
   const double left = double(gb) - early;
   return start + ahead * tb + std::ceil(std::max(left, 1.0) / slots) * tb;
 }
+constexpr double SECOND_LAUNCH = 5.0;
 static GradPlan plan_gradients(int64_t n, int64_t di, int64_t df) {
   GradPlan best;
   double apart_x = 1e30, apart_w = 1e30, joint = 1e30;
@@ -276,7 +281,7 @@ static GradPlan plan_gradients(int64_t n, int64_t di, int64_t df) {
         if (c < joint) joint = c, best.x = px, best.w = pw;
       }
   }
-  best.joined = joint <= apart_x + apart_w + 5.0;
+  best.joined = joint <= apart_x + apart_w + SECOND_LAUNCH;
   if (!best.joined) best.x = ax, best.w = aw;
   return best;
 }

@@ -11,8 +11,9 @@ namespace {
 constexpr int QT = 256;
 
 // ---- the quantiser --------------------------------------------------------------------
-// A token in registers, read once (wider ones: two passes).  Bound by memory: 65536 x 4096 bf16 166 us (4.85 TB/s),
-// 8192 x 4096 22.6; 32 tokens 4.2, a launch.  `dq`: columns written,
+// A token in registers, read once (wider ones: two passes).  Bound by memory: 65536 x 4096 bf16 161 us (5.0 TB/s), what a
+// copy reaches; 8192 x 4096 22.5 in a row of its own calls, 24.1 on inputs that no cache holds (4.2 TB/s, the launch's
+// start and end are 4 of it), 28 to 34 traced behind a product; 32 tokens 4.0, a launch.  `dq`: columns written,
 // zeros behind the d that exist.
 template <class T, int WPR, int V>
 __global__ __launch_bounds__(row_threads(WPR)) void quantize_tokens_kernel(const T* __restrict__ x, int64_t ldx,

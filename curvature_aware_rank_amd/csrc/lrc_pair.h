@@ -189,8 +189,9 @@ __device__ __forceinline__ u32x4 row_piece(const T* p, int left) {
 }
 
 // OWN (integers, at most OWN_TOKENS): x is the tokens themselves, in the type of y, and every workgroup quantises them
-// into LDS while its first weights are on the way: a launch less (one token 4096 -> 11008 12.4 us a call
-// against 15.1).
+// into LDS while its first weights are on the way: a launch less, but each token's codes delay the workgroup.  One
+// launch / two, us a call: one token 1024 -> 4096 5.6 / 8.5, 4096 -> 4096 6.9 / 9.4, 4096 -> 11008 11.4 / 15.2,
+// 8192 -> 4096 10.1 / 12.2; four 1024 -> 4096 6.8 / 8.5, 4096 -> 4096 9.8 / 10.0, 4096 -> 11008 17 / 16.
 constexpr int OWN_TOKENS = 4, OWN_ROOM = 16384;
 
 template <class TO, int NW>
@@ -331,7 +332,9 @@ __global__ __launch_bounds__(64 * NW) void few_rows_kernel(const void* __restric
 
 // waves of a workgroup of up to 16 tokens: with few channels more waves share the k of each
 inline int few_waves(int64_t N) { return cdiv(N, 16) <= 256 ? 16 : 8; }
-// whether the few tokens are quantised by the product itself
+// Whether the few tokens are quantised by the product itself: where their codes fit the LDS room and a thread has at
+// most eight channels of a token (quantize_own loads a token in one go).  Wider rows take the quantiser's launch: one
+// token 11008 -> 4096 17.5 us, 8192 -> 28672 45.
 inline bool own_tokens(int64_t n, int64_t N, int64_t K) {
   return n <= OWN_TOKENS && n * ((K + 63) & ~int64_t(63)) <= OWN_ROOM && K <= 512 * few_waves(N);
 }
@@ -347,8 +350,11 @@ inline bool stream_int8(int64_t n, int64_t N, int64_t K, bool pair) {
   const double x = double(cdiv(N, 16)) * double(n) * double(K);
   return x <= (plan_rows(n, N, K / 2, pair).tg.splits > 1 ? 75e6 : pair ? 16e6 : 24e6);
 }
-// bf16, two weights: 4096 -> 11008 32.0 / 30.6 at 8 tokens, 11008 -> 4096 32.2 / 35.5 at 8, 36.9 / 35.8 at 17,
-// 1024 -> 4096 6.8 / 6.8 at 32.
+// bf16, two weights, rows / tiles (weights not in the caches).  Up to 8 tokens rows lose little where many channels fill
+// the chip with tiles and gain more elsewhere: at 8 4096 -> 11008 39.7 / 38.9, 2048 -> 5632 14.8 / 14.0, 8192 -> 28672
+// 169 / 165, 11008 -> 4096 39.3 / 43.1, 4096 -> 4096 16.1 / 19.4; at one 36.0 / 38.6, 14.1 / 13.8, 156 / 165, 37.5 / 42.8,
+// 15.0 / 19.5.  More tokens: 4096 -> 11008 43.2 / 39.3 at 16, 11008 -> 4096 42.5 / 43.6 at 16 and 52 / 44 at 24,
+// 1024 -> 4096 7.6 / 7.5 at 32.
 inline bool stream_bf16_pair(int64_t n, int64_t N, int64_t K) {
   if (n > 64 || K % 8 != 0) return n <= 64;
   return n <= 8 || (n <= 32 && N * K <= (int64_t(1) << 22));
