@@ -568,8 +568,10 @@ def _run(where, device, fn, *args):
         raise LrcError(st, where)
 
 
-def _check_rows(t, name, n=None, d=None, dtype=None, device=None):
-    """Check a 2-D GPU tensor (its dtype, its device and, where given, its n rows and d columns) and return its shape."""
+def _rows(t, name, n=None, d=None, dtype=None, device=None, read=True):
+    """Check a 2-D GPU tensor (its dtype, its device and, where given, its n rows and d columns)
+    and return (tensor, leading dim); rows that are not contiguous or overlap are copied if they
+    are read."""
     _dev(t, name)
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -581,14 +583,10 @@ def _check_rows(t, name, n=None, d=None, dtype=None, device=None):
         raise ValueError(f"{name} must have shape {(n, d)}, got {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return shape
-
-
-def _rows(t, name, n=None, d=None, dtype=None, device=None):
-    """_check_rows, and (tensor, leading dim); rows that are not contiguous or overlap are copied."""
-    rows, cols = _check_rows(t, name, n, d, dtype, device)
     if cols and t.is_contiguous():
         return t, cols
+    if not read:
+        return t, max(cols, 1)
     s0, s1 = t.stride()
     if rows <= 1 or cols == 0:
         return t if s1 == 1 or cols <= 1 else t.contiguous(), max(cols, 1)
@@ -817,13 +815,11 @@ def _in_pieces(t, ld):
 def _pair_of_weights(Wg, Wu, d_ff, d_in, dtype, device, read=True):
     """(Wg, Wu, leading dim, d_ff, d_in) of two weights of one shape, which the products read at one pitch; what is not
     read is only checked."""
-    if not read:
-        d_ff, d_in = _check_rows(Wg, "Wg", d_ff, d_in, dtype, device)
-        _check_rows(Wu, "Wu", d_ff, d_in, dtype, device)
-        return None, None, max(d_in, 1), d_ff, d_in
-    Wg, ldw = _rows(Wg, "Wg", d_ff, d_in, dtype, device)
+    Wg, ldw = _rows(Wg, "Wg", d_ff, d_in, dtype, device, read)
     d_ff, d_in = Wg.shape
-    Wu, ldu = _rows(Wu, "Wu", d_ff, d_in, dtype, device)
+    Wu, ldu = _rows(Wu, "Wu", d_ff, d_in, dtype, device, read)
+    if not read:
+        return None, None, ldw, d_ff, d_in
     if dtype == torch.bfloat16:
         (Wg, ldw), (Wu, ldu) = _in_pieces(Wg, ldw), _in_pieces(Wu, ldu)
     if ldw != ldu:
